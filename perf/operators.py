@@ -166,7 +166,7 @@ def prepare(case, seed):
     if op == "backward":
         st["dy"] = (_activations(g, M, N) * 1e-2).to(dt)
         # what the forward kept: round(x.down^T), the rank padded as the library pads it
-        h = (st["x"].double() @ st["down"].to(dt).double().t()).to(dt)
+        h = _round16(st["x"].double() @ st["down"].to(dt).double().t(), dt)
         st["h"] = torch.zeros(M, _rank_pad(r), dtype=dt, device="cuda")
         st["h"][:, :r] = h
         del st["wq"]
@@ -185,6 +185,14 @@ def _round_e4m3(v):
     e = (torch.frexp(v.abs())[1] - 1).clamp(min=-6)
     step = torch.ldexp(torch.ones_like(v), e - 3)
     return torch.round(v / step) * step
+
+
+def _round16(v, dt):
+    """v (64 bits) to the nearest value of a 16-bit type, ties to even, in one rounding."""
+    bits, low = (11, -14) if dt == torch.float16 else (8, -126)
+    e = (torch.frexp(v.abs())[1] - 1).clamp(min=low)
+    step = torch.ldexp(torch.ones_like(v), e - (bits - 1))
+    return (torch.round(v / step) * step).to(dt)
 
 
 def _padded(x, R, C):
@@ -246,7 +254,7 @@ def _plain_forward(st):
     v, s = _row_quantized(x)
     w = st["wq"].float() * _spread(st["ws"], *st["wq"].shape)
     # in 64 bits: h is rounded to 16 bits before its second product
-    h = (x.double() @ st["down"].to(c).double().t()).to(c).float()
+    h = _round16(x.double() @ st["down"].to(c).double().t(), c).float()
     y = _rows_value(v, s) @ w.t() + st["scale"] * (h @ st["up"].to(c).float().t())
     if "bias" in st:
         y = y + st["bias"].float()
@@ -259,7 +267,7 @@ def _plain_backward(st):
     down, up = st["down"].to(c).float(), st["up"].to(c).float()
     v, s = _row_quantized(dy)
     w = st["wqt"].float().t() * _spread(st["ws"], dy.shape[1], x.shape[1])
-    gh = (st["scale"] * (dy.double() @ up.double())).to(c).float()
+    gh = _round16(st["scale"] * (dy.double() @ up.double()), c).float()
     dx = _rows_value(v, s) @ w + gh @ down
     dd = gh.t() @ x.float()
     du = st["scale"] * (dy.float().t() @ st["h"][:, :r].float())
@@ -358,6 +366,17 @@ def _codes64(v):
     return torch.copysign(val[code], v)
 
 
+def _nearest16(v, dt):
+    """v to the nearest of the 16-bit values around its torch conversion (which rounds through 32 bits)."""
+    mid = v.to(dt).view(torch.int16)
+    best = mid.view(dt).double()
+    for d in (-1, 1):
+        near = (mid + d).view(dt).double()
+        off, was = (near - v).abs(), (best - v).abs()
+        best = torch.where((off < was) | ((off == was) & (mid % 2 != 0)), near, best)
+    return best
+
+
 def _exact_rows(x):
     """(dequantized values, code values, scales [kb, M]) of rows in groups of 128."""
     M, K = x.shape
@@ -430,12 +449,12 @@ def exact(case, seed):
     if op == "forward":
         xv, _, _ = _exact_rows(st["x"])
         y = torch.mm(xv, _exact_weight(st["wq"], st["ws"]).t())
-        h = torch.mm(st["x"].double(), down.t()).to(c).double()
+        h = _nearest16(torch.mm(st["x"].double(), down.t()), c)
         y = torch.addmm(y, h, up.t(), alpha=st["scale"])
         return y + st["bias"].double() if "bias" in st else y
     w = _exact_weight(st["wqt"].t().contiguous(), st["ws"])
     gv, _, _ = _exact_rows(st["dy"])
-    gh = (st["scale"] * torch.mm(st["dy"].double(), up)).to(c).double()
+    gh = _nearest16(st["scale"] * torch.mm(st["dy"].double(), up), c)
     dx = torch.addmm(torch.mm(gv, w), gh, down)
     dd = torch.mm(gh.t(), st["x"].double())
     du = st["scale"] * torch.mm(st["dy"].double().t(), st["h"][:, :case["r"]].double())
