@@ -400,6 +400,79 @@ int lyc_dora_linear_fwd(const void* x, int x_dt, const void* w, int w_dt, const 
                         int64_t K, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * 8-bit base weight: the frozen W of a LoRA layer held as OCP e4m3 codes with
+ * one fp32 scale per 128 x 128 tile, activations quantized per token in groups
+ * of 128 features, the product accumulated in fp32.
+ *
+ * Quantization, per group (128 consecutive features of a row, or a 128 x 128
+ * tile; the last group of an axis may be shorter):
+ *   s = max(amax, 2^-100) / 448          amax = max |x| over the group; fp32 division
+ *   q = e4m3(x / s)                      the exact quotient rounded once, ties to even
+ * A group that holds an infinity or a NaN gets an infinite or NaN scale and
+ * NaN codes.  A code c stands for the value c * s.
+ *
+ * lyc_fp8_quantize_rows: x [M][K] -> codes q [M][K] (1 byte each) and scales
+ *   s [ceil(K/128)][M], group index first (the order the product reads).
+ * lyc_fp8_quantize_weight: w [N][K] -> scales s [ceil(N/128)][ceil(K/128)] and
+ *   codes q [N][K] and/or the transposed codes q_t [K][N] that the backward
+ *   reads (either may be NULL, not both; q_t needs N a multiple of 16).
+ *  - K a multiple of 16 (at most 2^20), M <= 2^28, N * K <= 2^38; x, w, q, q_t
+ *    16-byte aligned (LYC_ERR_UNSUPPORTED).  Outputs must not overlap inputs or
+ *    each other (LYC_ERR_INVALID_ARG).  No workspace.
+ *
+ * lyc_fp8_linear_fwd: y = round_out( sum_kb s_x[kb][m] s_w[n/128][kb] *
+ *   sum_{k in kb} q_x[m][k] q_w[n][k] + b[n] ) over the groups kb of 128: each
+ *   group's sum is one fp32 MFMA, added by one fp32 fused multiply-add per
+ *   group; one final rounding.  y_dt is the caller's choice, and so is the
+ *   bias's dtype (8-bit operands enter no dtype policy).
+ */
+int lyc_fp8_quantize_rows(const void* x, int x_dt, void* q, float* s, int64_t M, int64_t K, void* stream);
+int lyc_fp8_quantize_weight(const void* w, int w_dt, void* q, void* q_t, float* s, int64_t N, int64_t K,
+                            void* stream);
+int lyc_fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int lyc_fp8_linear_fwd(const void* q_x, const float* s_x, const void* q_w, const float* s_w, const void* bias,
+                       int bias_dt, void* y, int y_dt, int64_t M, int64_t N, int64_t K, void* workspace,
+                       size_t workspace_bytes, void* stream);
+/*
+ * The LoRA-bypass forward over an 8-bit base weight:
+ *   y = round_out( Q(x).Q(W)^T + scale * round_c(x_c.down_c^T).up_c^T + b )
+ * where Q(x) is x quantized in the call (lyc_fp8_quantize_rows of x as stored)
+ * and Q(W) the caller's codes and scales.  The bypass is lyc_lora_linear_fwd's,
+ * on x itself: the same exactly rounded h_r, folded into the same fp32
+ * accumulators.  The dtype policy runs over (x, b, down, up).  rank == 0: no
+ * bypass.  Arguments, stream, workspace and errors as lyc_lora_linear_fwd,
+ * with q_w [N][K] and s_w in place of W; K a multiple of 16.
+ * lyc_fp8_lora_workspace_layout: where the call leaves h_r [M][h_ld] in the
+ * compute dtype (columns >= rank are zero), as lyc_lora_workspace_layout.
+ */
+int lyc_fp8_lora_linear_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int bias_dt,
+                                       int down_dt, int up_dt, size_t* bytes);
+int lyc_fp8_lora_workspace_layout(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int bias_dt, int down_dt,
+                                  int up_dt, size_t* h_offset, int64_t* h_ld);
+int lyc_fp8_lora_linear_fwd(const void* x, int x_dt, const void* q_w, const float* s_w, const void* bias, int bias_dt,
+                            const void* down, int down_dt, const void* up, int up_dt, int64_t rank, double scale,
+                            void* y, int y_dt, int64_t M, int64_t N, int64_t K, void* workspace,
+                            size_t workspace_bytes, void* stream);
+/*
+ * Its backward (W and the bias frozen; quantization passes the gradient
+ * straight through):
+ *   gh_r  = round_c( scale * dy_c . up_c )
+ *   dx    = round_x( Q(dy).Q(W) + gh_r . down_c )      dy quantized in the call, in groups of 128 along N
+ *   dDown = round_down( gh_r^T . x_c ),  dUp = round_up( scale * dy_c^T . h_r )
+ * q_wt [K][N]: the transposed codes (read only when dx is wanted); s_w: the
+ * scales of W as lyc_fp8_quantize_weight wrote them.  h_r: the forward's, or
+ * NULL (recomputed), as lyc_lora_linear_bwd_saved.  Everything else as
+ * lyc_lora_linear_bwd (`want` bits 1 | 2 | 4, and 16 when h_r is given), with K
+ * and N multiples of 16.  dy must be 16-byte aligned when dx is wanted.
+ */
+int lyc_fp8_lora_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int bias_dt,
+                                           int down_dt, int up_dt, int dy_dt, int want, size_t* bytes);
+int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const float* s_w, int bias_dt,
+                            const void* down, int down_dt, const void* up, int up_dt, const void* h_r, int64_t rank,
+                            double scale, const void* dy, int dy_dt, void* dx, void* d_down, void* d_up, int64_t M,
+                            int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Tile planner and measured pick for the LoRA forward's main contraction
  * (LyCORIS "Backend Selection" page, "Tile selection": an analytic model
  * shortlists candidates, the shortlist is timed once, best of three, and the

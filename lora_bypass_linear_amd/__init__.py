@@ -18,7 +18,9 @@ __all__ = ["F16", "BF16", "F32", "LycError", "MixedHalfError", "lib", "resolve_d
            "linear_workspace_layout", "linear_prepare", "lora_merge_workspace_size", "lora_bwd_workspace_size",
            "lora_bwd_workspace_layout", "gemm_tile", "gemm_plan", "lora_linear_tune", "tuning_save",
            "tuning_load", "tuning_clear", "tuning_count", "tuning_key", "tuning_lookup", "tuning_cache_path", "profile_begin", "profile_end",
-           "dtype_code", "torch_dtype"]
+           "dtype_code", "torch_dtype", "fp8_quantize_rows", "fp8_quantize_weight", "fp8_linear", "fp8_lora_linear",
+           "fp8_lora_saved_h", "fp8_lora_linear_backward", "fp8_linear_workspace_size", "fp8_lora_workspace_size",
+           "fp8_lora_bwd_workspace_size"]
 
 F16, BF16, F32 = 1, 2, 3
 OK, ERR_MIXED_HALF, ERR_INVALID_ARG, ERR_DTYPE_MISMATCH, ERR_UNSUPPORTED, ERR_HIP, ERR_WORKSPACE, ERR_IO, ERR_SCRATCH = range(9)
@@ -31,6 +33,7 @@ _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.environ.get("LYC_LIB") or os.path.join(_HERE, "liblyc.so")
 _lib = None
 
+E4M3 = torch.float8_e4m3fn   # the 8-bit codes (OCP e4m3)
 _CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 _TORCH = {v: k for k, v in _CODE.items()}
 
@@ -111,6 +114,22 @@ def lib():
         L.lyc_dora_linear_fwd.argtypes = [c_vp, c_int, c_vp, c_int, c_vp, c_int, c_vp, c_int, c_vp, c_int, c_vp,
                                           c_int, c_vp, c_i64, ctypes.c_double, c_vp, c_int, c_i64, c_i64, c_i64,
                                           c_vp, c_sz, c_vp]
+        L.lyc_fp8_quantize_rows.argtypes = [c_vp, c_int, c_vp, c_vp, c_i64, c_i64, c_vp]
+        L.lyc_fp8_quantize_weight.argtypes = [c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp]
+        L.lyc_fp8_linear_workspace_size.argtypes = [c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)]
+        L.lyc_fp8_linear_fwd.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_vp, c_int, c_i64, c_i64, c_i64, c_vp,
+                                         c_sz, c_vp]
+        L.lyc_fp8_lora_linear_workspace_size.argtypes = [c_i64, c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int,
+                                                         ctypes.POINTER(c_sz)]
+        L.lyc_fp8_lora_workspace_layout.argtypes = [c_i64, c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int,
+                                                    ctypes.POINTER(c_sz), ctypes.POINTER(c_i64)]
+        L.lyc_fp8_lora_linear_fwd.argtypes = [c_vp, c_int, c_vp, c_vp, c_vp, c_int, c_vp, c_int, c_vp, c_int, c_i64,
+                                              ctypes.c_double, c_vp, c_int, c_i64, c_i64, c_i64, c_vp, c_sz, c_vp]
+        L.lyc_fp8_lora_linear_bwd_workspace_size.argtypes = [c_i64, c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int,
+                                                             c_int, c_int, ctypes.POINTER(c_sz)]
+        L.lyc_fp8_lora_linear_bwd.argtypes = [c_vp, c_int, c_vp, c_vp, c_int, c_vp, c_int, c_vp, c_int, c_vp, c_i64,
+                                              ctypes.c_double, c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64,
+                                              c_vp, c_sz, c_vp]
         L.lyc_gemm_tile.argtypes = [c_i64, c_i64, c_int, ctypes.POINTER(c_int), ctypes.POINTER(c_int)]
         L.lyc_profile_begin.argtypes = [c_int]
         L.lyc_profile_end.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_int)]
@@ -127,6 +146,9 @@ def lib():
                    L.lyc_gemm_plan, L.lyc_device_rates, L.lyc_measure_device_rates, L.lyc_lora_linear_tune, L.lyc_tuning_key, L.lyc_tuning_lookup, L.lyc_tuning_save,
                    L.lyc_tuning_load, L.lyc_tuning_clear, L.lyc_tuning_count, L.lyc_dora_norms_workspace_size,
                    L.lyc_dora_norms, L.lyc_dora_linear_workspace_size, L.lyc_dora_linear_fwd,
+                   L.lyc_fp8_quantize_rows, L.lyc_fp8_quantize_weight, L.lyc_fp8_linear_workspace_size,
+                   L.lyc_fp8_linear_fwd, L.lyc_fp8_lora_linear_workspace_size, L.lyc_fp8_lora_workspace_layout,
+                   L.lyc_fp8_lora_linear_fwd, L.lyc_fp8_lora_linear_bwd_workspace_size, L.lyc_fp8_lora_linear_bwd,
                    L.lyc_gemm_tile, L.lyc_profile_begin, L.lyc_profile_end):
             fn.restype = c_int
         _lib = L
@@ -209,7 +231,7 @@ def _need_device(*ts):
             raise ValueError("lyc operands must be GPU tensors")
         if not t.is_contiguous():
             raise ValueError("lyc operands must be contiguous")
-        if t.dtype not in _CODE and t.dtype != torch.uint8:
+        if t.dtype not in _CODE and t.dtype != torch.uint8 and t.dtype != E4M3:
             raise TypeError(f"unsupported dtype {t.dtype}")
         if dev is None:
             dev = t.device
@@ -642,3 +664,172 @@ def dora_linear(x: torch.Tensor, w: torch.Tensor, down: torch.Tensor, up: torch.
                                      _ptr(magnitude), m_dt, _ptr(norms), r, float(scale), _ptr(out), dtype_code(out),
                                      M, N, K, _ptr(ws), nbytes, _stream(dev)))
     return out
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def _typed(t: Optional[torch.Tensor], dtype: torch.dtype, name: str) -> None:
+    if t is not None and t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+
+
+def _codes(q: Optional[torch.Tensor], s: Optional[torch.Tensor], q_shape, s_shape, name: str) -> None:
+    """Check codes and their scales: shapes and dtypes."""
+    _shape(q, q_shape, name)
+    _typed(q, E4M3, name)
+    _shape(s, s_shape, f"{name}'s scales")
+    _typed(s, torch.float32, f"{name}'s scales")
+
+
+def fp8_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                      s: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """e4m3 codes [M,K] of x [M,K] with one scale per row and 128 features,
+    and the scales [ceil(K/128), M]: a code c of row m, feature k stands for
+    c * s[k // 128, m]."""
+    M, K = _dims(x, 2, "x")
+    _codes(q, s, (M, K), (_blocks(K), M), "q")
+    dev = _need_device(x, q, s)
+    q = torch.empty((M, K), dtype=E4M3, device=dev) if q is None else q
+    s = torch.empty((_blocks(K), M), dtype=torch.float32, device=dev) if s is None else s
+    _check(lib().lyc_fp8_quantize_rows(_ptr(x), dtype_code(x), _ptr(q), _ptr(s), M, K, _stream(dev)))
+    return q, s
+
+
+def fp8_quantize_weight(w: torch.Tensor, transposed: bool = False):
+    """(q, s, q_t) of a weight w [N,K]: e4m3 codes [N,K], one scale per 128 x
+    128 tile [ceil(N/128), ceil(K/128)], and with ``transposed`` the codes of
+    W^T [K,N] that the backward reads (else None)."""
+    N, K = _dims(w, 2, "w")
+    dev = _need_device(w)
+    q = torch.empty((N, K), dtype=E4M3, device=dev)
+    q_t = torch.empty((K, N), dtype=E4M3, device=dev) if transposed else None
+    s = torch.empty((_blocks(N), _blocks(K)), dtype=torch.float32, device=dev)
+    _check(lib().lyc_fp8_quantize_weight(_ptr(w), dtype_code(w), _ptr(q), _ptr(q_t), _ptr(s), N, K, _stream(dev)))
+    return q, s, q_t
+
+
+def fp8_linear_workspace_size(M: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().lyc_fp8_linear_workspace_size(M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def fp8_lora_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().lyc_fp8_lora_linear_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt, ctypes.byref(n)))
+    return n.value
+
+
+def fp8_lora_bwd_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt, dy_dt, want=7) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().lyc_fp8_lora_linear_bwd_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt, dy_dt, want,
+                                                        ctypes.byref(n)))
+    return n.value
+
+
+def fp8_linear(q: torch.Tensor, s: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor,
+               bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+               out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M,N] = round_out(x.W^T + b) of quantized x (``fp8_quantize_rows``)
+    and W (``fp8_quantize_weight``), fp32 accumulation; y in ``out_dtype``."""
+    M, K = _dims(q, 2, "q")
+    N, _ = _dims(w_q, 2, "w_q")
+    _codes(q, s, (M, K), (_blocks(K), M), "q")
+    _codes(w_q, w_s, (N, K), (_blocks(N), _blocks(K)), "w_q")
+    _shape(bias, (N,), "bias")
+    _shape(out, (M, N), "out")
+    b_dt = dtype_code(bias) if bias is not None else 0
+    o_dt = dtype_code(out if out is not None else out_dtype)
+    dev = _need_device(q, s, w_q, w_s, bias, out, workspace)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    ws = _workspace(fp8_linear_workspace_size(M, N, K), dev, workspace)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().lyc_fp8_linear_fwd(_ptr(q), _ptr(s), _ptr(w_q), _ptr(w_s), _ptr(bias), b_dt, _ptr(out), o_dt, M, N,
+                                    K, _ptr(ws), nbytes, _stream(dev)))
+    return out
+
+
+def _fp8_lora_shapes(x, w_q, w_s, down, up, bias, out, transposed=False):
+    M, K = _dims(x, 2, "x")
+    N, r = _dims(up, 2, "up")
+    _codes(w_q, w_s, (K, N) if transposed else (N, K), (_blocks(N), _blocks(K)), "w_qt" if transposed else "w_q")
+    _shape(down, (r, K), "down")
+    _shape(bias, (N,), "bias")
+    _shape(out, (M, N), "out")
+    return M, N, K, r
+
+
+def fp8_lora_linear(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, down: torch.Tensor, up: torch.Tensor,
+                    scale: float, bias: Optional[torch.Tensor] = None, out: Optional[torch.Tensor] = None,
+                    workspace: Optional[torch.Tensor] = None, return_workspace: bool = False):
+    """y = round_out(Q(x).Q(W)^T + scale * round_c(x.down^T).up^T + b): the
+    LoRA forward over an 8-bit base weight (``fp8_quantize_weight``), x
+    quantized in the call, the bypass on x itself.  With ``return_workspace``
+    the workspace too (see ``fp8_lora_saved_h``)."""
+    M, N, K, r = _fp8_lora_shapes(x, w_q, w_s, down, up, bias, out)
+    x_dt, d_dt, u_dt = dtype_code(x), dtype_code(down), dtype_code(up)
+    b_dt = dtype_code(bias) if bias is not None else 0
+    _, o_dt = resolve_dtypes([x_dt] + ([b_dt] if b_dt else []) + [d_dt, u_dt])
+    _out_dtype(out, o_dt)
+    dev = _need_device(x, w_q, w_s, down, up, bias, out, workspace)
+    if out is None:
+        out = torch.empty((M, N), dtype=_TORCH[o_dt], device=dev)
+    ws = _workspace(fp8_lora_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt), dev, workspace)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().lyc_fp8_lora_linear_fwd(_ptr(x), x_dt, _ptr(w_q), _ptr(w_s), _ptr(bias), b_dt, _ptr(down), d_dt,
+                                         _ptr(up), u_dt, r, float(scale), _ptr(out), dtype_code(out), M, N, K,
+                                         _ptr(ws), nbytes, _stream(dev)))
+    return (out, ws) if return_workspace else out
+
+
+def fp8_lora_saved_h(workspace: torch.Tensor, x: torch.Tensor, down: torch.Tensor, up: torch.Tensor,
+                     bias: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The h_r [M, r_pad] that fp8_lora_linear left in ``workspace`` for these
+    operands: a view, valid until the workspace is reused."""
+    M, K = _dims(x, 2, "x")
+    N, r = _dims(up, 2, "up")
+    codes = [dtype_code(x), dtype_code(bias) if bias is not None else 0, dtype_code(down), dtype_code(up)]
+    ho, ld = ctypes.c_size_t(0), ctypes.c_int64(0)
+    _check(lib().lyc_fp8_lora_workspace_layout(M, N, K, r, *codes, ctypes.byref(ho), ctypes.byref(ld)))
+    c_dt = resolve_dtypes([c for c in codes if c])[0]
+    es = 4 if c_dt == F32 else 2
+    return workspace[ho.value: ho.value + M * ld.value * es].view(_TORCH[c_dt]).view(M, ld.value)
+
+
+def fp8_lora_linear_backward(x: torch.Tensor, w_qt: torch.Tensor, w_s: torch.Tensor, down: torch.Tensor,
+                             up: torch.Tensor, scale: float, dy: torch.Tensor,
+                             bias_dtype: Optional[torch.dtype] = None, want_dx: bool = True, want_ddown: bool = True,
+                             want_dup: bool = True, workspace: Optional[torch.Tensor] = None,
+                             h: Optional[torch.Tensor] = None):
+    """Gradients (dx, d_down, d_up) of ``fp8_lora_linear`` for dy, each in its
+    leaf's dtype (None where not wanted).  ``w_qt``: the transposed codes [K,N]
+    (``fp8_quantize_weight(w, transposed=True)``), ``w_s`` the scales of W.
+    ``h``: optional h_r the forward left (``fp8_lora_saved_h``)."""
+    M, N, K, r = _fp8_lora_shapes(x, w_qt, w_s, down, up, None, None, transposed=True)
+    _shape(dy, (M, N), "dy")
+    dev = _need_device(x, w_qt, w_s, down, up, dy, workspace, h)
+    x_dt, d_dt, u_dt, g_dt = (dtype_code(t) for t in (x, down, up, dy))
+    b_dt = _CODE[bias_dtype] if bias_dtype is not None else 0
+    c_dt = resolve_dtypes([x_dt] + ([b_dt] if b_dt else []) + [d_dt, u_dt, g_dt])[0]
+    if h is not None:
+        ld = ctypes.c_int64(0)
+        _check(lib().lyc_fp8_lora_workspace_layout(M, N, K, r, x_dt, c_dt, d_dt, u_dt, None,
+                                                   ctypes.byref(ld)))
+        _shape(h, (M, ld.value), "h")
+        _typed(h, _TORCH[c_dt], "h")
+    want = (BWD_DX if want_dx else 0) | (BWD_DDOWN if want_ddown else 0) | (BWD_DUP if want_dup else 0) | \
+        (BWD_H if h is not None else 0)
+    dx = torch.empty((M, K), dtype=x.dtype, device=dev) if want_dx else None
+    dd = torch.empty((r, K), dtype=down.dtype, device=dev) if want_ddown else None
+    du = torch.empty((N, r), dtype=up.dtype, device=dev) if want_dup else None
+    ws = _workspace(fp8_lora_bwd_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt, g_dt, want), dev, workspace)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    # an empty output still has to be passed (non-NULL) to be "wanted"
+    p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr() if t.numel() else 256)
+    _check(lib().lyc_fp8_lora_linear_bwd(_ptr(x), x_dt, _ptr(w_qt), _ptr(w_s), b_dt, _ptr(down), d_dt, _ptr(up), u_dt,
+                                         _ptr(h), r, float(scale), _ptr(dy), g_dt, p(dx), p(dd), p(du), M, N, K,
+                                         _ptr(ws), nbytes, _stream(dev)))
+    return dx, dd, du

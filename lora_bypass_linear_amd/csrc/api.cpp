@@ -14,6 +14,7 @@
 #include <vector>
 
 #include "bwd.h"
+#include "fp8.h"
 #include "kernels.h"
 #include "merge.h"
 #include "tune.h"
@@ -59,16 +60,27 @@ struct Problem {
     // (fp32 W) and its split and row norms, from lyc_linear_prepare or an
     // earlier forward with the same W, shapes and dtypes
     bool w_prepared = false;
+    // the base weight as e4m3 codes with one scale per 128 x 128 tile: it has
+    // no operand dtype of its own (w_dt 0) and x is quantized in the call
+    bool w8 = false;
 };
+
+// limits the 8-bit kernels add: 16-byte rows of codes, 32-bit offsets of a
+// scale row, tile counts that fit the scale array
+int check_w8(int64_t M, int64_t N, int64_t K) {
+    if (K % 16 != 0 || M > ((int64_t)1 << 28)) return LYC_ERR_UNSUPPORTED;
+    if ((double)N * (double)K > 274877906944.0) return LYC_ERR_UNSUPPORTED;   // 2^38
+    return LYC_OK;
+}
 
 // Shape and dtype checks shared by the size queries and the forward calls.
 int check_problem(Problem& P) {
     if (P.M < 0 || P.N < 0 || P.K < 0 || P.rank < 0) return LYC_ERR_INVALID_ARG;
-    if (!valid_dt(P.x_dt) || !valid_dt(P.w_dt)) return LYC_ERR_INVALID_ARG;
+    if (!valid_dt(P.x_dt) || (!P.w8 && !valid_dt(P.w_dt))) return LYC_ERR_INVALID_ARG;
     if (P.b_dt != 0 && !valid_dt(P.b_dt)) return LYC_ERR_INVALID_ARG;
     int dts[6], n = 0;
     dts[n++] = P.x_dt;
-    dts[n++] = P.w_dt;
+    if (!P.w8) dts[n++] = P.w_dt;
     if (P.b_dt != 0) dts[n++] = P.b_dt;
     if (P.lora) {
         if (!valid_dt(P.d_dt) || !valid_dt(P.u_dt)) return LYC_ERR_INVALID_ARG;
@@ -84,6 +96,7 @@ int check_problem(Problem& P) {
     if (P.M > MAX_DIM || P.N > MAX_DIM || P.K > MAX_K) return LYC_ERR_UNSUPPORTED;
     if (P.K % 8 != 0) return LYC_ERR_UNSUPPORTED;
     if (P.rank > MAX_RANK) return LYC_ERR_UNSUPPORTED;
+    if (P.w8 && check_w8(P.M, P.N, P.K) != LYC_OK) return LYC_ERR_UNSUPPORTED;
     if (!P.lora) P.rank = 0;
     P.r_pad = P.rank == 0 ? 0 : (P.rank <= 16 && P.c_dt != LYC_F32) ? 16 : (P.rank <= 32 ? 32 : P.rank <= 64 ? 64 : P.rank <= 128 ? 128 : 256);
     return LYC_OK;
@@ -91,7 +104,7 @@ int check_problem(Problem& P) {
 
 struct Layout {
     size_t xc = 0, wc = 0, dc = 0, dh = 0, dl = 0, uc = 0, h = 0, dnorm = 0, wh = 0, wl = 0, wnorm = 0, flagged = 0,
-           partial = 0, gain = 0, total = 0;
+           partial = 0, gain = 0, xq = 0, xs = 0, total = 0;
     // plain affine form: guard counts, one per workgroup of the contraction
     int64_t flag_slots = 0;
     bool w_split_pass = false;
@@ -116,8 +129,9 @@ Layout layout(const Problem& P) {
     Layout L;
     size_t off = 0;
     const size_t ce = esize(P.c_dt);
-    L.cast_x = P.x_dt == LYC_F32 && P.c_dt != LYC_F32;
-    L.cast_w = P.w_dt == LYC_F32 && P.c_dt != LYC_F32 && !P.w_kept;
+    // (over an 8-bit base x_c is read by the h pass only)
+    L.cast_x = P.x_dt == LYC_F32 && P.c_dt != LYC_F32 && !(P.w8 && P.r_pad == 0);
+    L.cast_w = P.w_dt == LYC_F32 && P.c_dt != LYC_F32 && !P.w_kept && !P.w8;
     if (L.cast_x) { L.xc = off; off = align256(off + (size_t)(P.M * P.K) * 2); }
     const bool split = P.c_dt != LYC_F32;   // hi/lo split of the second contraction operand
     if (P.r_pad > 0) {
@@ -136,7 +150,13 @@ Layout layout(const Problem& P) {
                                             : 1;
         L.flagged = off; off = align256(off + (size_t)L.flag_slots * sizeof(unsigned));
     }
-    if (P.lora) {
+    if (P.w8) {
+        // x's codes and scales, and the partial sums of a K-split product
+        L.xq = off; off = align256(off + (size_t)(P.M * P.K));
+        L.xs = off; off = align256(off + (size_t)P.M * (size_t)((P.K + 127) / 128) * 4);
+        L.ksplit = lyc::fp8_gemm_ksplit(P.M, P.N, P.K);
+        if (L.ksplit > 1) { L.partial = off; off = align256(off + (size_t)L.ksplit * (size_t)(P.M * P.N) * 4); }
+    } else if (P.lora) {
         // fp32 partial sums of a K-split GEMM (few output tiles), sized for
         // the largest split the planner can shortlist (a tuned pick may take it)
         L.ksplit = lyc::gemm_ksplit(P.M, P.N, P.K, P.c_dt);
@@ -207,8 +227,10 @@ hipError_t timed(int kind, hipStream_t s, F fn) {
 // else a measured pick for this device and shape, else the analytic one.
 int forward(const Problem& P, const void* x, const void* w, const void* bias, const void* down, const void* up,
             double scale, void* y, int y_dt, void* ws, size_t ws_bytes, void* stream,
-            const lyc::TuneChoice* force = nullptr, const void* mag = nullptr, const float* norms = nullptr) {
-    // (P.w_kept: w is W_c, W already rounded to the compute dtype)
+            const lyc::TuneChoice* force = nullptr, const void* mag = nullptr, const float* norms = nullptr,
+            const float* w_s = nullptr) {
+    // (P.w_kept: w is W_c, W already rounded to the compute dtype; P.w8: w is
+    // its e4m3 codes and w_s their tile scales)
     if (y_dt != P.o_dt) return LYC_ERR_DTYPE_MISMATCH;
     if ((bias == nullptr) != (P.b_dt == 0)) return LYC_ERR_INVALID_ARG;
     if (P.M == 0 || P.N == 0) return LYC_OK;
@@ -216,6 +238,8 @@ int forward(const Problem& P, const void* x, const void* w, const void* bias, co
     if (P.K > 0) {
         if (x == nullptr || w == nullptr) return LYC_ERR_INVALID_ARG;
         if (!aligned(x, 16) || !aligned(w, 16)) return LYC_ERR_UNSUPPORTED;
+        if (P.w8 && w_s == nullptr) return LYC_ERR_INVALID_ARG;
+        if (P.w8 && !aligned(w_s, 4)) return LYC_ERR_UNSUPPORTED;
     }
     if (P.w_kept && P.K > 0 && overlaps(y, (size_t)(P.M * P.N) * esize(y_dt), w, (size_t)(P.N * P.K) * esize(P.c_dt)))
         return LYC_ERR_INVALID_ARG;
@@ -299,7 +323,7 @@ int forward(const Problem& P, const void* x, const void* w, const void* bias, co
     g.post = 1.0f;
     lyc::TuneChoice tc{};
     const bool have = force ? (tc = *force, true)
-                            : lyc::tune_count() > 0 &&
+                            : !P.w8 && lyc::tune_count() > 0 &&
                                   lyc::tune_lookup(lyc::tune_key("lora_fwd", P.M, P.N, P.K, P.r_pad, P.c_dt, P.o_dt), &tc);
     // a pick is taken only if this build can run it in this workspace
     if (have && tc.ksplit >= 1 && tc.ksplit <= L.ks_max && tc.tile >= 0 && tc.tile <= 3 &&
@@ -405,6 +429,18 @@ int forward(const Problem& P, const void* x, const void* w, const void* bias, co
         g.af = up_stored ? up : (const void*)(W + L.uc);
         g.bf = W + L.h;
         g.rf = P.r_pad;
+    }
+    if (P.w8) {
+        if (P.K > 0 && timed(LYC_KERNEL_PREP, s, [&] {
+                return lyc::launch_quant_rows(
+                    lyc::QuantRowsParams{x, P.x_dt, W + L.xq, (float*)(W + L.xs), P.M, P.K}, s);
+            }) != hipSuccess)
+            return LYC_ERR_HIP;
+        g.b = W + L.xq;
+        const lyc::Fp8GemmParams q{g, (const float*)(W + L.xs), w_s, (P.K + 127) / 128, 1};
+        return timed(LYC_KERNEL_GEMM, s, [&] { return lyc::launch_fp8_gemm(P.c_dt, q, s); }) == hipSuccess
+                   ? LYC_OK
+                   : LYC_ERR_HIP;
     }
     if (timed(LYC_KERNEL_GEMM, s, [&] { return lyc::launch_gemm(P.c_dt, g, s); }) != hipSuccess) return LYC_ERR_HIP;
     return LYC_OK;
@@ -524,7 +560,8 @@ struct Bwd {
 
 struct BwdLayout {
     size_t xc = 0, gc = 0, dc = 0, dh = 0, dl = 0, uc = 0, dnorm = 0, flag_h = 0, h = 0, ut = 0, uth = 0, utl = 0,
-           unorm = 0, flag_g = 0, gh = 0, wt = 0, dt = 0, xt = 0, ght = 0, dyt = 0, ht = 0, partial = 0, total = 0;
+           unorm = 0, flag_g = 0, gh = 0, wt = 0, dt = 0, xt = 0, ght = 0, dyt = 0, ht = 0, gq = 0, gs = 0,
+           partial = 0, total = 0;
     bool cast_x = false, cast_g = false, need_h = false, need_gh = false;
     // tr_tok: dDown and dUp read x, dy, h_r and gh_r as stored, the token
     // index as their contraction rows (16-bit compute, each operand below
@@ -537,12 +574,13 @@ struct BwdLayout {
 int check_bwd(Bwd& B) {
     Problem& P = B.P;
     if (P.M < 0 || P.N < 0 || P.K < 0 || P.rank < 0 || B.want < 0 || B.want > 31) return LYC_ERR_INVALID_ARG;
-    if (!valid_dt(P.x_dt) || !valid_dt(P.w_dt) || !valid_dt(P.d_dt) || !valid_dt(P.u_dt) || !valid_dt(B.dy_dt))
+    if (!valid_dt(P.x_dt) || (!P.w8 && !valid_dt(P.w_dt)) || !valid_dt(P.d_dt) || !valid_dt(P.u_dt) ||
+        !valid_dt(B.dy_dt))
         return LYC_ERR_INVALID_ARG;
     if (P.b_dt != 0 && !valid_dt(P.b_dt)) return LYC_ERR_INVALID_ARG;
     int dts[6], n = 0;
     dts[n++] = P.x_dt;
-    dts[n++] = P.w_dt;
+    if (!P.w8) dts[n++] = P.w_dt;
     if (P.b_dt != 0) dts[n++] = P.b_dt;
     dts[n++] = P.d_dt;
     dts[n++] = P.u_dt;
@@ -553,6 +591,7 @@ int check_bwd(Bwd& B) {
     // dDown and dUp, N of dx and gh, K of h): the limit of K in the forward
     if (P.M > MAX_K || P.N > MAX_K || P.K > MAX_K) return LYC_ERR_UNSUPPORTED;
     if (P.K % 8 != 0 || P.N % 8 != 0) return LYC_ERR_UNSUPPORTED;
+    if (P.w8 && (P.N % 16 != 0 || check_w8(P.M, P.N, P.K) != LYC_OK)) return LYC_ERR_UNSUPPORTED;
     if (P.rank > MAX_RANK) return LYC_ERR_UNSUPPORTED;
     P.r_pad = P.rank == 0 ? 0 : (P.rank <= 16 && P.c_dt != LYC_F32) ? 16 : (P.rank <= 32 ? 32 : P.rank <= 64 ? 64 : P.rank <= 128 ? 128 : 256);
     B.M8 = (P.M + 7) & ~(int64_t)7;
@@ -571,7 +610,8 @@ BwdLayout bwd_layout(const Bwd& B) {
     const size_t G1 = (size_t)1 << 30;
     L.tr_tok = split && (size_t)P.M * (size_t)P.K * 2 < G1 && (size_t)P.M * (size_t)P.N * 2 < G1;
     L.cast_x = P.x_dt == LYC_F32 && P.c_dt != LYC_F32 && (L.need_h || (L.tr_tok && dd));
-    L.cast_g = B.dy_dt == LYC_F32 && P.c_dt != LYC_F32 && (L.need_gh || dx || (L.tr_tok && du));
+    // (over an 8-bit base dx's product reads dy's codes, taken from dy as stored)
+    L.cast_g = B.dy_dt == LYC_F32 && P.c_dt != LYC_F32 && (L.need_gh || (dx && !P.w8) || (L.tr_tok && du));
     auto take = [&](size_t& at, size_t bytes) { at = off; off = align256(off + bytes); };
     const size_t M = (size_t)P.M, N = (size_t)P.N, K = (size_t)P.K, R = (size_t)P.r_pad, M8 = (size_t)B.M8;
     if (L.cast_x) take(L.xc, M * K * 2);
@@ -595,7 +635,11 @@ BwdLayout bwd_layout(const Bwd& B) {
     if (dx) {
         if (!(B.want & BWD_WT)) take(L.wt, K * N * ce);
         if (P.rank > 0) take(L.dt, K * R * ce);
-        L.ks_dx = lyc::gemm_ksplit(P.M, P.K, P.N, P.c_dt);
+        if (P.w8) {
+            take(L.gq, M * N);
+            take(L.gs, M * ((N + 127) / 128) * 4);
+        }
+        L.ks_dx = P.w8 ? lyc::fp8_gemm_ksplit(P.M, P.K, P.N) : lyc::gemm_ksplit(P.M, P.K, P.N, P.c_dt);
         if (L.ks_dx > 1) part = std::max(part, (size_t)L.ks_dx * M * K * 4);
     }
     if (dd) {
@@ -621,7 +665,8 @@ BwdLayout bwd_layout(const Bwd& B) {
 
 int backward(const Bwd& B, const void* x, const void* w, const void* down, const void* up, double scale,
              const void* dy, void* dx, void* d_down, void* d_up, void* ws, size_t ws_bytes, void* stream,
-             const void* w_t = nullptr, const void* h_r = nullptr) {
+             const void* w_t = nullptr, const void* h_r = nullptr, const float* w_s = nullptr) {
+    // (P.w8: w_t is W^T's e4m3 codes [K][N] and w_s the tile scales of W)
     const Problem& P = B.P;
     if (!(scale == scale) || scale > 3.4e38 || scale < -3.4e38) return LYC_ERR_INVALID_ARG;
     const bool wdx = B.want & BWD_DX, wdd = B.want & BWD_DDOWN, wdu = B.want & BWD_DUP;
@@ -637,6 +682,8 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
         return LYC_ERR_INVALID_ARG;
     // a caller-kept W_c^T [K][N] is read in place by the dx GEMM: 16-byte rows
     if (wt_given && use_w && !aligned(w_t, 16)) return LYC_ERR_UNSUPPORTED;
+    if (P.w8 && use_w && w_s == nullptr) return LYC_ERR_INVALID_ARG;
+    if (P.w8 && use_w && !aligned(w_s, 4)) return LYC_ERR_UNSUPPORTED;
     // the forward's h_r [M][r_pad], read in place by dUp (16-byte rows)
     const bool h_given = B.want & BWD_H;
     const bool use_h = h_given && wdu && r > 0 && M > 0 && N > 0;
@@ -647,7 +694,7 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
     if ((wdx && ndx > 0 && dx == nullptr) || (wdd && ndd > 0 && d_down == nullptr) || (wdu && ndu > 0 && d_up == nullptr))
         return LYC_ERR_INVALID_ARG;
     // alignment: rows read in place by the contractions need 16 bytes
-    const bool x_in_place = use_x && P.x_dt == P.c_dt, dy_in_place = use_dy && B.dy_dt == P.c_dt;
+    const bool x_in_place = use_x && P.x_dt == P.c_dt, dy_in_place = use_dy && (B.dy_dt == P.c_dt || (P.w8 && wdx));
     if ((x_in_place && !aligned(x, 16)) || (dy_in_place && !aligned(dy, 16))) return LYC_ERR_UNSUPPORTED;
     if ((w && !aligned(w, esize(P.w_dt))) || (down && !aligned(down, esize(P.d_dt))) ||
         (up && !aligned(up, esize(P.u_dt))) || (x && !aligned(x, esize(P.x_dt))) ||
@@ -657,15 +704,15 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
         (wdu && d_up && !aligned(d_up, esize(P.u_dt))))
         return LYC_ERR_UNSUPPORTED;
     // the gradients overlap neither the inputs nor each other
-    const void* ins[7] = {x, w, down, up, dy, wt_given ? w_t : nullptr, use_h ? h_r : nullptr};
-    const size_t nin[7] = {(size_t)(M * K) * esize(P.x_dt), (size_t)(N * K) * esize(P.w_dt),
+    const void* ins[8] = {x, w, down, up, dy, wt_given ? w_t : nullptr, use_h ? h_r : nullptr, w_s};
+    const size_t nin[8] = {(size_t)(M * K) * esize(P.x_dt), (size_t)(N * K) * esize(P.w_dt),
                            (size_t)(r * K) * esize(P.d_dt), (size_t)(N * r) * esize(P.u_dt),
-                           (size_t)(M * N) * esize(B.dy_dt), (size_t)(K * N) * esize(P.c_dt),
-                           (size_t)(M * P.r_pad) * esize(P.c_dt)};
+                           (size_t)(M * N) * esize(B.dy_dt), (size_t)(K * N) * (P.w8 ? 1 : esize(P.c_dt)),
+                           (size_t)(M * P.r_pad) * esize(P.c_dt), (size_t)((N + 127) / 128 * ((K + 127) / 128)) * 4};
     void* outs[3] = {wdx ? dx : nullptr, wdd ? d_down : nullptr, wdu ? d_up : nullptr};
     const size_t nout[3] = {ndx, ndd, ndu};
     for (int i = 0; i < 3; ++i) {
-        for (int j = 0; j < 7; ++j)
+        for (int j = 0; j < 8; ++j)
             if (overlaps(outs[i], nout[i], ins[j], nin[j])) return LYC_ERR_INVALID_ARG;
         for (int j = i + 1; j < 3; ++j)
             if (overlaps(outs[i], nout[i], outs[j], nout[j])) return LYC_ERR_INVALID_ARG;
@@ -788,7 +835,20 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
         g.ksplit = L.ks_dx;
         g.partial = L.ks_dx > 1 ? (float*)(W + L.partial) : nullptr;
         g.vec_store = (K % 4 == 0) && aligned(dx, P.x_dt == LYC_F32 ? 16 : 8);
-        if (!gemm(g)) return LYC_ERR_HIP;
+        if (P.w8) {
+            if (N > 0 && timed(LYC_KERNEL_PREP, s, [&] {
+                    return lyc::launch_quant_rows(
+                        lyc::QuantRowsParams{dy, B.dy_dt, W + L.gq, (float*)(W + L.gs), M, N}, s);
+                }) != hipSuccess)
+                return LYC_ERR_HIP;
+            g.b = W + L.gq;
+            // the scale of W^T's tile (k / 128, n / 128) is W's of (n / 128, k / 128)
+            const lyc::Fp8GemmParams q{g, (const float*)(W + L.gs), w_s, 1, (K + 127) / 128};
+            if (timed(LYC_KERNEL_GEMM, s, [&] { return lyc::launch_fp8_gemm(P.c_dt, q, s); }) != hipSuccess)
+                return LYC_ERR_HIP;
+        } else if (!gemm(g)) {
+            return LYC_ERR_HIP;
+        }
     }
 
     // dDown = round_down(gh_r^T . x_c), over the tokens
@@ -1161,6 +1221,176 @@ int lyc_lora_merge_fwd(const void* w, int w_dt, const void* down, int down_dt, c
     if (st != LYC_OK) return st;
     if (!valid_dt(out_dt)) return LYC_ERR_INVALID_ARG;
     return merge(G, w, down, up, scale, out, out_dt, workspace, workspace_bytes, stream);
+}
+
+// ---- 8-bit base weight --------------------------------------------------------------
+
+int lyc_fp8_quantize_rows(const void* x, int x_dt, void* q, float* s, int64_t M, int64_t K, void* stream) {
+    if (M < 0 || K < 0 || !valid_dt(x_dt)) return LYC_ERR_INVALID_ARG;
+    if (M > MAX_DIM || K > MAX_K || check_w8(M, 0, K) != LYC_OK) return LYC_ERR_UNSUPPORTED;
+    if (M == 0 || K == 0) return LYC_OK;
+    if (x == nullptr || q == nullptr || s == nullptr) return LYC_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(s, 4)) return LYC_ERR_UNSUPPORTED;
+    const size_t nx = (size_t)(M * K) * esize(x_dt), nq = (size_t)(M * K), ns = (size_t)(M * ((K + 127) / 128)) * 4;
+    if (overlaps(q, nq, x, nx) || overlaps(s, ns, x, nx) || overlaps(s, ns, q, nq)) return LYC_ERR_INVALID_ARG;
+    (void)hipGetLastError();
+    hipStream_t st = (hipStream_t)stream;
+    return timed(LYC_KERNEL_PREP, st, [&] {
+               return lyc::launch_quant_rows(lyc::QuantRowsParams{x, x_dt, q, s, M, K}, st);
+           }) == hipSuccess
+               ? LYC_OK
+               : LYC_ERR_HIP;
+}
+
+int lyc_fp8_quantize_weight(const void* w, int w_dt, void* q, void* q_t, float* s, int64_t N, int64_t K,
+                            void* stream) {
+    if (N < 0 || K < 0 || !valid_dt(w_dt)) return LYC_ERR_INVALID_ARG;
+    if (N > MAX_DIM || K > MAX_K || check_w8(0, N, K) != LYC_OK) return LYC_ERR_UNSUPPORTED;
+    if (N == 0 || K == 0) return LYC_OK;
+    if (w == nullptr || s == nullptr || (q == nullptr && q_t == nullptr)) return LYC_ERR_INVALID_ARG;
+    if (q_t != nullptr && N % 16 != 0) return LYC_ERR_UNSUPPORTED;
+    if (!aligned(w, 16) || !aligned(q, 16) || !aligned(q_t, 16) || !aligned(s, 4)) return LYC_ERR_UNSUPPORTED;
+    const size_t nw = (size_t)(N * K) * esize(w_dt), nq = (size_t)(N * K),
+                 ns = (size_t)((N + 127) / 128 * ((K + 127) / 128)) * 4;
+    if (overlaps(q, nq, w, nw) || overlaps(q_t, nq, w, nw) || overlaps(s, ns, w, nw) || overlaps(q, nq, q_t, nq) ||
+        overlaps(s, ns, q, nq) || overlaps(s, ns, q_t, nq))
+        return LYC_ERR_INVALID_ARG;
+    (void)hipGetLastError();
+    hipStream_t st = (hipStream_t)stream;
+    return timed(LYC_KERNEL_PREP, st, [&] {
+               return lyc::launch_quant_tiles(lyc::QuantTilesParams{w, w_dt, q, q_t, s, N, K}, st);
+           }) == hipSuccess
+               ? LYC_OK
+               : LYC_ERR_HIP;
+}
+
+// shape checks of the product of two quantized operands
+static int check_fp8_linear(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0) return LYC_ERR_INVALID_ARG;
+    if (M > MAX_DIM || N > MAX_DIM || K > MAX_K) return LYC_ERR_UNSUPPORTED;
+    return check_w8(M, N, K);
+}
+
+int lyc_fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+    const int st = check_fp8_linear(M, N, K);
+    if (st != LYC_OK) return st;
+    const int ks = lyc::fp8_gemm_ksplit(M, N, K);
+    if (bytes) *bytes = ks > 1 ? align256((size_t)ks * (size_t)(M * N) * 4) : 0;
+    return LYC_OK;
+}
+
+int lyc_fp8_linear_fwd(const void* q_x, const float* s_x, const void* q_w, const float* s_w, const void* bias,
+                       int bias_dt, void* y, int y_dt, int64_t M, int64_t N, int64_t K, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+    const int st = check_fp8_linear(M, N, K);
+    if (st != LYC_OK) return st;
+    if (!valid_dt(y_dt) || (bias_dt != 0 && !valid_dt(bias_dt))) return LYC_ERR_INVALID_ARG;
+    if ((bias == nullptr) != (bias_dt == 0)) return LYC_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return LYC_OK;
+    if (y == nullptr) return LYC_ERR_INVALID_ARG;
+    if (K > 0 && (q_x == nullptr || s_x == nullptr || q_w == nullptr || s_w == nullptr)) return LYC_ERR_INVALID_ARG;
+    if (K > 0 && (!aligned(q_x, 16) || !aligned(q_w, 16) || !aligned(s_x, 4) || !aligned(s_w, 4)))
+        return LYC_ERR_UNSUPPORTED;
+    if ((bias && !aligned(bias, esize(bias_dt))) || !aligned(y, esize(y_dt))) return LYC_ERR_UNSUPPORTED;
+    const size_t ny = (size_t)(M * N) * esize(y_dt);
+    if (overlaps(y, ny, q_x, (size_t)(M * K)) || overlaps(y, ny, q_w, (size_t)(N * K)) ||
+        overlaps(y, ny, s_x, (size_t)(M * ((K + 127) / 128)) * 4) ||
+        overlaps(y, ny, s_w, (size_t)((N + 127) / 128 * ((K + 127) / 128)) * 4) ||
+        (bias && overlaps(y, ny, bias, (size_t)N * esize(bias_dt))))
+        return LYC_ERR_INVALID_ARG;
+    const int ks = lyc::fp8_gemm_ksplit(M, N, K);
+    const size_t need = ks > 1 ? align256((size_t)ks * (size_t)(M * N) * 4) : 0;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
+        return LYC_ERR_WORKSPACE;
+    (void)hipGetLastError();
+    hipStream_t s = (hipStream_t)stream;
+    lyc::Fp8GemmParams q{};
+    q.g.a = q_w;
+    q.g.b = q_x;
+    q.g.M = M;
+    q.g.N = N;
+    q.g.K = K;
+    q.g.scale = 1.0f;
+    q.g.bias = bias;
+    q.g.bias_dt = bias_dt;
+    q.g.y = y;
+    q.g.y_dt = y_dt;
+    q.g.ksplit = ks;
+    q.g.partial = ks > 1 ? (float*)workspace : nullptr;
+    q.g.vec_store = (N % 4 == 0) && aligned(y, y_dt == LYC_F32 ? 16 : 8);
+    q.sx = s_x;
+    q.sw = s_w;
+    q.sw_n = (K + 127) / 128;
+    q.sw_k = 1;
+    // (no fold: any compute dtype's instance)
+    return timed(LYC_KERNEL_GEMM, s, [&] { return lyc::launch_fp8_gemm(LYC_BF16, q, s); }) == hipSuccess ? LYC_OK
+                                                                                                         : LYC_ERR_HIP;
+}
+
+static Problem fp8_problem(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int bias_dt, int down_dt,
+                           int up_dt) {
+    Problem P{true, M, N, K, rank, x_dt, 0, bias_dt, down_dt, up_dt, 0, 0, 0};
+    P.w8 = true;
+    return P;
+}
+
+int lyc_fp8_lora_linear_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int bias_dt,
+                                       int down_dt, int up_dt, size_t* bytes) {
+    Problem P = fp8_problem(M, N, K, rank, x_dt, bias_dt, down_dt, up_dt);
+    const int st = check_problem(P);
+    if (st != LYC_OK) return st;
+    if (bytes) *bytes = layout(P).total;
+    return LYC_OK;
+}
+
+int lyc_fp8_lora_workspace_layout(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int bias_dt, int down_dt,
+                                  int up_dt, size_t* h_offset, int64_t* h_ld) {
+    Problem P = fp8_problem(M, N, K, rank, x_dt, bias_dt, down_dt, up_dt);
+    const int st = check_problem(P);
+    if (st != LYC_OK) return st;
+    if (h_offset) *h_offset = layout(P).h;
+    if (h_ld) *h_ld = P.r_pad;
+    return LYC_OK;
+}
+
+int lyc_fp8_lora_linear_fwd(const void* x, int x_dt, const void* q_w, const float* s_w, const void* bias, int bias_dt,
+                            const void* down, int down_dt, const void* up, int up_dt, int64_t rank, double scale,
+                            void* y, int y_dt, int64_t M, int64_t N, int64_t K, void* workspace,
+                            size_t workspace_bytes, void* stream) {
+    Problem P = fp8_problem(M, N, K, rank, x_dt, bias_dt, down_dt, up_dt);
+    const int st = check_problem(P);
+    if (st != LYC_OK) return st;
+    if (!valid_dt(y_dt)) return LYC_ERR_INVALID_ARG;
+    if (!(scale == scale) || scale > 3.4e38 || scale < -3.4e38) return LYC_ERR_INVALID_ARG;
+    return forward(P, x, q_w, bias, down, up, scale, y, y_dt, workspace, workspace_bytes, stream, nullptr, nullptr,
+                   nullptr, s_w);
+}
+
+static Bwd fp8_bwd(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int bias_dt, int down_dt, int up_dt,
+                   int dy_dt, int want) {
+    // (the transposed codes are always the caller's: BWD_WT)
+    return Bwd{fp8_problem(M, N, K, rank, x_dt, bias_dt, down_dt, up_dt), dy_dt, want < 0 ? want : want | BWD_WT, 0};
+}
+
+int lyc_fp8_lora_linear_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int bias_dt,
+                                           int down_dt, int up_dt, int dy_dt, int want, size_t* bytes) {
+    Bwd B = fp8_bwd(M, N, K, rank, x_dt, bias_dt, down_dt, up_dt, dy_dt, want);
+    const int st = check_bwd(B);
+    if (st != LYC_OK) return st;
+    if (bytes) *bytes = bwd_layout(B).total;
+    return LYC_OK;
+}
+
+int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const float* s_w, int bias_dt,
+                            const void* down, int down_dt, const void* up, int up_dt, const void* h_r, int64_t rank,
+                            double scale, const void* dy, int dy_dt, void* dx, void* d_down, void* d_up, int64_t M,
+                            int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+    const int want = (dx ? BWD_DX : 0) | (d_down ? BWD_DDOWN : 0) | (d_up ? BWD_DUP : 0) | (h_r ? BWD_H : 0);
+    Bwd B = fp8_bwd(M, N, K, rank, x_dt, bias_dt, down_dt, up_dt, dy_dt, want);
+    const int st = check_bwd(B);
+    if (st != LYC_OK) return st;
+    return backward(B, x, nullptr, down, up, scale, dy, dx, d_down, d_up, workspace, workspace_bytes, stream, q_wt,
+                    h_r, s_w);
 }
 
 int lyc_resolve_dtypes(const int* operand_dtypes, int n, int* compute, int* output) {

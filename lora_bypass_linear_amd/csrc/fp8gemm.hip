@@ -1,0 +1,363 @@
+// fp8gemm.hip -- the product over an 8-bit base weight on gfx950 MFMA:
+//
+//   y[m][n] = round_out( scale * (h_r . up_c^T)[m][n]
+//                        + sum_kb sx[kb][m] * sw[n/128][kb] * sum_{k in kb} qx[m][k] qw[n][k]  + b[n] )
+//
+// with qx, qw e4m3 codes and one fp32 scale per row group and per weight tile
+// of 128.  A K step of the tiles is 128 bytes of every row, exactly one scale
+// block: one v_mfma_f32_16x16x128 from a zero accumulator gives the block's
+// sum, and one fp32 FMA per element adds it, times the block's two scales, to
+// the running sum.  The W side is the MFMA's A operand (a wave's rows share
+// one tile scale), the x side its B operand (a lane's column m has one row
+// scale), so the product of scales is one value per lane and 16-row block of
+// x.
+//
+// Two instances of the block's sum.  The 8-bit MFMA aligns the products of
+// every 8 consecutive k to the largest of them and keeps about 15 bits below
+// it (a product 2^-16 of its neighbour vanishes; across the groups of 8 it
+// sums in fp32): 1.6e-5 of a result's norm on normal data, a fifteenth of
+// fp16's rounding and a hundredth of bf16's, so 16-bit outputs take it.  fp32
+// outputs take EXACT: the codes widened to fp16, which holds every e4m3 value,
+// and summed by 16-bit MFMAs in fp32 at half the rate.
+//  The LoRA fold runs first in the same pipeline with 16-bit (or fp32)
+// MFMAs, as in gemm.hip.
+#include <algorithm>
+
+#include "fp8.h"
+#include "gemm_tile.h"
+#include "kernels.h"
+#include "lyc_device.h"
+
+namespace lyc {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+// the sum over one 128-element block: 32 codes of A and of B per lane (bytes
+// 16 g .. 16 g + 15 and 64 + 16 g .. of the block for lane group g = lane / 16;
+// both sides take the same, so every k meets its own)
+__device__ __forceinline__ f32x4 block_dot(i32x4 a0, i32x4 a1, i32x4 b0, i32x4 b1) {
+    const i32x8 a = __builtin_shufflevector(a0, a1, 0, 1, 2, 3, 4, 5, 6, 7);
+    const i32x8 b = __builtin_shufflevector(b0, b1, 0, 1, 2, 3, 4, 5, 6, 7);
+    return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(a, b, f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
+}
+
+// 8 codes widened to fp16 (exact)
+__device__ __forceinline__ i32x4 widen8(int lo, int hi) {
+    i32x4 o;
+    o[0] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, false));
+    o[1] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(lo, 1.0f, true));
+    o[2] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, false));
+    o[3] = __builtin_bit_cast(int, __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(hi, 1.0f, true));
+    return o;
+}
+
+// A block's operand fragment: 32 codes a lane, as loaded or widened
+template <bool EXACT>
+struct Frag8 {
+    i32x4 v[2];
+    __device__ __forceinline__ void set(i32x4 a, i32x4 b) { v[0] = a; v[1] = b; }
+};
+template <>
+struct Frag8<true> {
+    i32x4 v[4];
+    __device__ __forceinline__ void set(i32x4 a, i32x4 b) {
+        v[0] = widen8(a[0], a[1]);
+        v[1] = widen8(a[2], a[3]);
+        v[2] = widen8(b[0], b[1]);
+        v[3] = widen8(b[2], b[3]);
+    }
+};
+template <bool EXACT>
+__device__ __forceinline__ f32x4 block_sum(const Frag8<EXACT>& a, const Frag8<EXACT>& b) {
+    if constexpr (EXACT) {
+        f32x4 t = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) t = CF16::step(a.v[i], b.v[i], t);
+        return t;
+    } else {
+        return block_dot(a.v[0], a.v[1], b.v[0], b.v[1]);
+    }
+}
+
+// A tile whose stages also hold a K step's scales: 64 floats per wave, waves
+// 0 .. TM/64-1 the rows' scales, the next wave the tile scales of the TN/128
+// (at least one) weight blocks.
+template <int TN_, int TM_, int WN_, int WM_, int NS_>
+struct Tile8 : Tile<TN_, TM_, WN_, WM_, NS_, 128> {
+    using B = Tile<TN_, TM_, WN_, WM_, NS_, 128>;
+    static constexpr int DATA = B::STAGE;
+    static constexpr int STAGE = DATA + B::NW * 256;
+    static constexpr int Q = B::Q + 1;   // loads per wave per step
+    static_assert(B::TM / 64 + 1 <= B::NW, "a wave for the tile scales");
+    static_assert(NS_ * STAGE + TN_ * 4 <= 160 * 1024, "LDS");
+};
+using Tile8L = Tile8<256, 256, 128, 64, 2>;
+using Tile8M = Tile8<128, 128, 64, 64, 4>;
+using Tile8S = Tile8<64, 64, 32, 32, 4>;
+
+template <class CT, class TL, bool ROWS, bool EXACT>
+__global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, int tiles_n, int tiles_m, int group_m) {
+    const GemmParams& p = pp.g;
+    __shared__ __attribute__((aligned(16))) char smem[TL::NS * TL::STAGE + TL::TN * 4];
+    float* sbias = (float*)(smem + TL::NS * TL::STAGE);
+    constexpr int FN = TL::FN, FM = TL::FM, NS = TL::NS;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wn = wave % TL::WAVES_N, wm = wave / TL::WAVES_N;
+    int tn, tm;
+    tile_coords(blockIdx.x, gridDim.x, tiles_n, tiles_m, group_m, tn, tm);
+    const int64_t n0 = (int64_t)tn * TL::TN, m0 = (int64_t)tm * TL::TM;
+    const int rows_a = (int)((p.N - n0) < TL::TN ? (p.N - n0) : TL::TN);
+    const int rows_b = (int)((p.M - m0) < TL::TM ? (p.M - m0) : TL::TM);
+
+    f32x4 acc[FN][FM];
+#pragma unroll
+    for (int i = 0; i < FN; ++i)
+#pragma unroll
+        for (int j = 0; j < FM; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    // steps: the fold's (with K split 0), then this split's K blocks
+    const uint32_t fbytes = (uint32_t)(p.rf * CT::es), kbytes = (uint32_t)p.K;
+    const int KM = (int)((kbytes + 127) / 128);
+    const int per = (KM + (int)gridDim.y - 1) / (int)gridDim.y;
+    const int k0 = (int)blockIdx.y * per;
+    const int nmain = KM - k0 < per ? (KM - k0 > 0 ? KM - k0 : 0) : per;
+    const int RF = blockIdx.y == 0 ? (int)((fbytes + 127) / 128) : 0;
+    const int KT = RF + nmain;
+    const char* fa = (const char*)p.af + n0 * fbytes;
+    const char* fb = (const char*)p.bf + m0 * fbytes;
+    const char* ma = (const char*)p.a + n0 * kbytes;
+    const char* mb = (const char*)p.b + m0 * kbytes;
+    Loader<TL> lf, lm;
+    lf.init(fbytes, fbytes, wave, lane);
+    lm.init(kbytes, kbytes, wave, lane);
+    // this wave's part of a step's scales (a row's, or a weight tile's)
+    const bool is_w = wave == TL::TM / 64;
+    const int64_t nblk = (p.N + FP8_BLOCK - 1) / FP8_BLOCK, nb0 = n0 / FP8_BLOCK;
+    uint32_t soff = OOB;
+    if (wave < TL::TM / 64) {
+        if (wave * 64 + lane < rows_b) soff = (uint32_t)(wave * 64 + lane) * 4;
+    } else if (is_w) {
+        if (lane < (TL::TN + 127) / 128 && nb0 + lane < nblk) soff = (uint32_t)(lane * pp.sw_n) * 4;
+    }
+    const uint32_t srange = is_w ? (uint32_t)((TL::TN + 127) / 128 * pp.sw_n + 1) * 4 : (uint32_t)rows_b * 4;
+
+    // loads of step s into its stage; past the last step entirely out of range,
+    // so that every step issues the same number of loads
+    auto issue = [&](int s) {
+        char* st = smem + (s % NS) * TL::STAGE;
+        const bool fold = s < RF;
+        const auto ra = make_rsrc(fold ? fa : ma, (uint32_t)rows_a * (fold ? fbytes : kbytes));
+        const auto rb = make_rsrc(fold ? fb : mb, (uint32_t)rows_b * (fold ? fbytes : kbytes));
+        Loader<TL> l;
+        l.va = fold ? lf.va : lm.va;
+        l.vb = fold ? lf.vb : lm.vb;
+        l.sa = fold ? lf.sa : lm.sa;
+        l.sb = fold ? lf.sb : lm.sb;
+        const uint32_t row_bytes = s < KT ? (fold ? fbytes : kbytes) : 0u;
+        const int64_t kb = fold ? s : s - RF + k0;
+        l.issue(st, ra, rb, row_bytes, (uint32_t)kb * 128u, wave, lane);
+        const float* sp = is_w ? pp.sw + nb0 * pp.sw_n + kb * pp.sw_k : pp.sx + kb * p.M + m0;
+        const bool on = !fold && s < KT;
+        const auto rs = make_rsrc(on ? sp : pp.sw, on ? srange : 0u);
+        auto* dst = (__attribute__((address_space(3))) void*)(st + TL::DATA + wave * 256);
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 4, soff, 0, 0, 0);
+    };
+
+    float bv = 0.f;
+    if (p.bias != nullptr && p.ksplit <= 1 && tid < TL::TN)
+        bv = n0 + tid < p.N ? load_as_f32(p.bias, p.bias_dt, n0 + tid) : 0.f;
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) issue(s);
+    if (tid < TL::TN) sbias[tid] = bv;
+
+    const int g = lane >> 4, r = lane & 15;
+    auto begin = [&](int kt) -> const char* {
+        wait_vm<(NS - 2) * TL::Q>();   // step kt has landed (this wave's share)
+        lds_barrier();                 // ... every wave's, and step kt-1's stage is free
+        issue(kt + NS - 1);
+        return smem + (kt % NS) * TL::STAGE;
+    };
+    for (int kt = 0; kt < RF; ++kt) {
+        const char* st = begin(kt);
+        const char* sb = st + TL::TN * TL::BKB;
+#pragma unroll
+        for (int sub = 0; sub < 2; ++sub) {
+            i32x4 a[FN], b[FM];
+#pragma unroll
+            for (int i = 0; i < FN; ++i) a[i] = *(const i32x4*)(st + lds_at<TL>(wn * TL::WN + i * 16 + r, sub * 4 + g));
+#pragma unroll
+            for (int j = 0; j < FM; ++j) b[j] = *(const i32x4*)(sb + lds_at<TL>(wm * TL::WM + j * 16 + r, sub * 4 + g));
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[i][j] = CT::step(a[i], b[j], acc[i][j]);
+        }
+    }
+    if (RF > 0) {
+#pragma unroll
+        for (int i = 0; i < FN; ++i)
+#pragma unroll
+            for (int j = 0; j < FM; ++j) acc[i][j] *= p.scale;
+    }
+    for (int kt = RF; kt < KT; ++kt) {
+        const char* st = begin(kt);
+        const char* sb = st + TL::TN * TL::BKB;
+        const float* sc = (const float*)(st + TL::DATA);
+        const float sw = sc[TL::TM + (wn * TL::WN) / FP8_BLOCK];
+        Frag8<EXACT> b[FM];
+        float sj[FM];
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int row = wm * TL::WM + j * 16 + r;
+            b[j].set(*(const i32x4*)(sb + lds_at<TL>(row, g)), *(const i32x4*)(sb + lds_at<TL>(row, 4 + g)));
+            sj[j] = sc[row] * sw;
+        }
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            const int row = wn * TL::WN + i * 16 + r;
+            Frag8<EXACT> a;
+            a.set(*(const i32x4*)(st + lds_at<TL>(row, g)), *(const i32x4*)(st + lds_at<TL>(row, 4 + g)));
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                const f32x4 t = block_sum<EXACT>(a, b[j]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t[e], sj[j], acc[i][j][e]);
+            }
+        }
+    }
+    wait_vm<0>();   // the out-of-range loads past the last step still write LDS
+    __syncthreads();
+
+    if (p.ksplit > 1) {
+        float* part = p.partial + (int64_t)blockIdx.y * p.M * p.N;
+#pragma unroll
+        for (int i = 0; i < FN; ++i) {
+            const int64_t nb = n0 + wn * TL::WN + i * 16 + 4 * g;
+#pragma unroll
+            for (int j = 0; j < FM; ++j) {
+                const int64_t m = m0 + wm * TL::WM + j * 16 + r;
+                if (m >= p.M) continue;
+                float* dst = part + m * p.N + nb;
+                if (p.vec_store && nb + 3 < p.N) {
+                    *(f32x4*)dst = acc[i][j];
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        if (nb + e < p.N) dst[e] = acc[i][j][e];
+                }
+            }
+        }
+        return;
+    }
+    float biasv[FN * 4] = {};
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+        const f32x4 b4 = *(const f32x4*)(sbias + wn * TL::WN + i * 16 + 4 * g);
+        biasv[4 * i] = b4[0]; biasv[4 * i + 1] = b4[1]; biasv[4 * i + 2] = b4[2]; biasv[4 * i + 3] = b4[3];
+    }
+    if constexpr (ROWS) {
+        epilogue_rows<TL, 2, false>(p, smem, acc, biasv, biasv, n0, m0, wave, lane, wn, wm);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < FN; ++i) {
+        const int64_t nb = n0 + wn * TL::WN + i * 16 + 4 * g;
+#pragma unroll
+        for (int j = 0; j < FM; ++j) {
+            const int64_t m = m0 + wm * TL::WM + j * 16 + r;
+            if (m >= p.M) continue;
+            if (p.y_dt == DT_F32 && p.vec_store && nb + 3 < p.N) {
+                f32x4 v = acc[i][j];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) v[e] += biasv[4 * i + e];
+                *(f32x4*)((float*)p.y + m * p.N + nb) = v;
+                continue;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float v = acc[i][j][e] + biasv[4 * i + e];
+                if (nb + e >= p.N) continue;
+                const int64_t at = m * p.N + nb + e;
+                if (p.y_dt == DT_F32) ((float*)p.y)[at] = v;
+                else ((uint16_t*)p.y)[at] = p.y_dt == DT_F16 ? f32_to_f16(v) : f32_to_bf16(v);
+            }
+        }
+    }
+}
+
+enum { T8_L, T8_M, T8_S };
+
+// Output tile and K split: the fewest rounds of workgroups over the device's
+// CUs, weighted by the tile's area and a penalty for its operand re-reads,
+// plus the partial sums' round trip of a split.
+static void fp8_pick(int64_t M, int64_t N, int64_t K, int* tile, int* ksplit) {
+    struct C { int id, tn, tm, per_cu; double pen; };
+    const C cands[] = {{T8_L, 256, 256, 1, 1.0}, {T8_M, 128, 128, 1, 1.3}, {T8_S, 64, 64, 2, 2.0}};
+    const double cus = (double)device_rates().cus;
+    const int64_t ksteps = (K + 127) / 128;
+    double best = 1e300;
+    *tile = T8_S;
+    *ksplit = 1;
+    for (const C& c : cands) {
+        const double tiles = (double)((N + c.tn - 1) / c.tn) * (double)((M + c.tm - 1) / c.tm);
+        for (int ks = 1; ks <= 8; ks *= 2) {
+            if (ks > 1 && (ks > ksteps / 2 || (double)M * N * 4.0 * ks > 32.0 * 1024 * 1024)) continue;
+            const double steps = (double)((ksteps + ks - 1) / ks);
+            const double rounds = std::ceil(tiles * ks / cus);
+            // a step of 256 x 256 x 128 takes about 1 us
+            double t = rounds * steps * (c.tn * c.tm / 65536.0) * c.pen;
+            if (ks > 1) t += (double)M * N * 4.0 * (ks + 1) / 4e6 + 4.0;
+            if (t < best) { best = t; *tile = c.id; *ksplit = ks; }
+        }
+    }
+}
+
+int fp8_gemm_ksplit(int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0 || K <= 0) return 1;
+    int t, ks;
+    fp8_pick(M, N, K, &t, &ks);
+    return ks;
+}
+
+template <class CT, class TL>
+static hipError_t run8(const Fp8GemmParams& p, hipStream_t s) {
+    const int64_t tiles_n = (p.g.N + TL::TN - 1) / TL::TN, tiles_m = (p.g.M + TL::TM - 1) / TL::TM;
+    if (tiles_n * tiles_m >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    const int ks = p.g.ksplit > 1 ? p.g.ksplit : 1;
+    const dim3 grid((unsigned)(tiles_n * tiles_m), ks);
+    const bool rows = ks == 1 && (p.g.N * 2) % 16 == 0 && ((uintptr_t)p.g.y & 15) == 0;
+    if (p.g.y_dt == DT_F32)
+        hipLaunchKernelGGL((fp8_gemm_kernel<CT, TL, false, true>), grid, dim3(TL::NT), 0, s, p, (int)tiles_n,
+                           (int)tiles_m, 4);
+    else if (rows)
+        hipLaunchKernelGGL((fp8_gemm_kernel<CT, TL, true, false>), grid, dim3(TL::NT), 0, s, p, (int)tiles_n,
+                           (int)tiles_m, 4);
+    else
+        hipLaunchKernelGGL((fp8_gemm_kernel<CT, TL, false, false>), grid, dim3(TL::NT), 0, s, p, (int)tiles_n,
+                           (int)tiles_m, 4);
+    if (ks > 1) {
+        const hipError_t e = hipGetLastError();
+        return e != hipSuccess ? e : launch_gemm_reduce(p.g, s);
+    }
+    return hipGetLastError();
+}
+
+template <class CT>
+static hipError_t run8_ct(const Fp8GemmParams& p, int t, hipStream_t s) {
+    if (t == T8_L) return run8<CT, Tile8L>(p, s);
+    if (t == T8_M) return run8<CT, Tile8M>(p, s);
+    return run8<CT, Tile8S>(p, s);
+}
+
+hipError_t launch_fp8_gemm(int c_dt, const Fp8GemmParams& p, hipStream_t s) {
+    if (p.g.M <= 0 || p.g.N <= 0) return hipSuccess;
+    int t, ks;
+    fp8_pick(p.g.M, p.g.N, p.g.K, &t, &ks);
+    if (p.g.ksplit > 1 && p.g.partial == nullptr) return hipErrorInvalidValue;
+    if (c_dt == DT_F16) return run8_ct<CF16>(p, t, s);
+    if (c_dt == DT_BF16) return run8_ct<CBF16>(p, t, s);
+    return run8_ct<CF32>(p, t, s);
+}
+
+}  // namespace lyc
