@@ -473,6 +473,29 @@ int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const flo
                             int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Orthogonalized update (the step an optimizer takes with a factor's or a
+ * dense weight's gradient or momentum in place of the gradient itself): the
+ * Newton-Schulz iteration
+ *   X0 = G / (|G|_F + eps)
+ *   X <- a X + (b A + c A^2) X,  A = X X^T      `steps` times, over the short side of G [R][C]
+ * which maps every singular value s to s p(s^2) per step, p(l) = a + b l +
+ * c l^2, and keeps the singular vectors (a = 3.4445, b = -4.775, c = 2.0315
+ * take 5 steps to bring them near 1).  Products are summed in fp32 from
+ * operands split into 16-bit pieces (22 bits for a 16-bit G, 24 for an fp32
+ * one); out has G's dtype, rounded once.
+ *  - g, out [R][C] row-major, element alignment; out may be g itself, any
+ *    other overlap is LYC_ERR_INVALID_ARG.
+ *  - R, C <= 2^20, min(R, C) <= 16384, R * C <= 2^31 (LYC_ERR_UNSUPPORTED).
+ *    1 <= steps <= 32, |a|, |b|, |c| < 1e6, 0 <= eps < 1e6
+ *    (LYC_ERR_INVALID_ARG).  A zero G gives zeros; one that holds a NaN or an
+ *    infinity gives NaN.
+ *  - Workspace: lyc_orthogonalize_workspace_size bytes, 256-byte aligned.
+ */
+int lyc_orthogonalize_workspace_size(int64_t R, int64_t C, int dt, size_t* bytes);
+int lyc_orthogonalize(const void* g, int dt, void* out, int64_t R, int64_t C, int steps, double a, double b, double c,
+                      double eps, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * Tile planner and measured pick for the LoRA forward's main contraction
  * (LyCORIS "Backend Selection" page, "Tile selection": an analytic model
  * shortlists candidates, the shortlist is timed once, best of three, and the

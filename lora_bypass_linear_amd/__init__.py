@@ -20,7 +20,7 @@ __all__ = ["F16", "BF16", "F32", "LycError", "MixedHalfError", "lib", "resolve_d
            "tuning_load", "tuning_clear", "tuning_count", "tuning_key", "tuning_lookup", "tuning_cache_path", "profile_begin", "profile_end",
            "dtype_code", "torch_dtype", "fp8_quantize_rows", "fp8_quantize_weight", "fp8_linear", "fp8_lora_linear",
            "fp8_lora_saved_h", "fp8_lora_linear_backward", "fp8_linear_workspace_size", "fp8_lora_workspace_size",
-           "fp8_lora_bwd_workspace_size"]
+           "fp8_lora_bwd_workspace_size", "orthogonalize", "orthogonalize_workspace_size"]
 
 F16, BF16, F32 = 1, 2, 3
 OK, ERR_MIXED_HALF, ERR_INVALID_ARG, ERR_DTYPE_MISMATCH, ERR_UNSUPPORTED, ERR_HIP, ERR_WORKSPACE, ERR_IO, ERR_SCRATCH = range(9)
@@ -130,6 +130,9 @@ def lib():
         L.lyc_fp8_lora_linear_bwd.argtypes = [c_vp, c_int, c_vp, c_vp, c_int, c_vp, c_int, c_vp, c_int, c_vp, c_i64,
                                               ctypes.c_double, c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64,
                                               c_vp, c_sz, c_vp]
+        c_d = ctypes.c_double
+        L.lyc_orthogonalize_workspace_size.argtypes = [c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]
+        L.lyc_orthogonalize.argtypes = [c_vp, c_int, c_vp, c_i64, c_i64, c_int, c_d, c_d, c_d, c_d, c_vp, c_sz, c_vp]
         L.lyc_gemm_tile.argtypes = [c_i64, c_i64, c_int, ctypes.POINTER(c_int), ctypes.POINTER(c_int)]
         L.lyc_profile_begin.argtypes = [c_int]
         L.lyc_profile_end.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_int)]
@@ -149,7 +152,7 @@ def lib():
                    L.lyc_fp8_quantize_rows, L.lyc_fp8_quantize_weight, L.lyc_fp8_linear_workspace_size,
                    L.lyc_fp8_linear_fwd, L.lyc_fp8_lora_linear_workspace_size, L.lyc_fp8_lora_workspace_layout,
                    L.lyc_fp8_lora_linear_fwd, L.lyc_fp8_lora_linear_bwd_workspace_size, L.lyc_fp8_lora_linear_bwd,
-                   L.lyc_gemm_tile, L.lyc_profile_begin, L.lyc_profile_end):
+                   L.lyc_orthogonalize_workspace_size, L.lyc_orthogonalize, L.lyc_gemm_tile, L.lyc_profile_begin, L.lyc_profile_end):
             fn.restype = c_int
         _lib = L
     return _lib
@@ -833,3 +836,31 @@ def fp8_lora_linear_backward(x: torch.Tensor, w_qt: torch.Tensor, w_s: torch.Ten
                                          _ptr(h), r, float(scale), _ptr(dy), g_dt, p(dx), p(dd), p(du), M, N, K,
                                          _ptr(ws), nbytes, _stream(dev)))
     return dx, dd, du
+
+
+def orthogonalize_workspace_size(R: int, C: int, dt: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().lyc_orthogonalize_workspace_size(R, C, dt, ctypes.byref(n)))
+    return n.value
+
+
+def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),
+                  eps: float = 1e-7, out: Optional[torch.Tensor] = None,
+                  workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The update g [R,C] (a LoRA factor's or a dense weight's gradient or
+    momentum) with its singular values brought near 1: ``steps`` Newton-Schulz
+    steps X <- a X + (b A + c A^2) X, A = X X^T over the short side, from
+    X = g / (|g| + eps).  ``out`` may be ``g`` itself."""
+    R, C = _dims(g, 2, "g")
+    _shape(out, (R, C), "out")
+    a, b, c = (float(v) for v in coefficients)
+    dt = dtype_code(g)
+    _out_dtype(out, dt)
+    dev = _need_device(g, out, workspace)
+    if out is None:
+        out = torch.empty_like(g)
+    ws = _workspace(orthogonalize_workspace_size(R, C, dt), dev, workspace)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().lyc_orthogonalize(_ptr(g), dt, _ptr(out), R, C, int(steps), a, b, c, float(eps), _ptr(ws), nbytes,
+                                   _stream(dev)))
+    return out

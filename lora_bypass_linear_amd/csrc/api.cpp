@@ -17,6 +17,7 @@
 #include "fp8.h"
 #include "kernels.h"
 #include "merge.h"
+#include "ortho.h"
 #include "tune.h"
 
 namespace {
@@ -1391,6 +1392,44 @@ int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const flo
     if (st != LYC_OK) return st;
     return backward(B, x, nullptr, down, up, scale, dy, dx, d_down, d_up, workspace, workspace_bytes, stream, q_wt,
                     h_r, s_w);
+}
+
+// ---- orthogonalized update ------------------------------------------------------------
+
+static int check_ortho(int64_t R, int64_t C, int dt) {
+    if (R < 0 || C < 0 || !valid_dt(dt)) return LYC_ERR_INVALID_ARG;
+    if (R > MAX_K || C > MAX_K || std::min(R, C) > 16384 || (double)R * (double)C > 2147483648.0)
+        return LYC_ERR_UNSUPPORTED;
+    return LYC_OK;
+}
+
+int lyc_orthogonalize_workspace_size(int64_t R, int64_t C, int dt, size_t* bytes) {
+    const int st = check_ortho(R, C, dt);
+    if (st != LYC_OK) return st;
+    if (bytes) *bytes = lyc::ortho_workspace(R, C, dt);
+    return LYC_OK;
+}
+
+int lyc_orthogonalize(const void* g, int dt, void* out, int64_t R, int64_t C, int steps, double a, double b, double c,
+                      double eps, void* workspace, size_t workspace_bytes, void* stream) {
+    const int st = check_ortho(R, C, dt);
+    if (st != LYC_OK) return st;
+    if (steps < 1 || steps > lyc::ORTHO_MAX_STEPS) return LYC_ERR_INVALID_ARG;
+    for (double v : {a, b, c, eps})
+        if (!(v > -1e6 && v < 1e6)) return LYC_ERR_INVALID_ARG;
+    if (eps < 0) return LYC_ERR_INVALID_ARG;
+    if (R == 0 || C == 0) return LYC_OK;
+    if (g == nullptr || out == nullptr) return LYC_ERR_INVALID_ARG;
+    if (!aligned(g, esize(dt)) || !aligned(out, esize(dt))) return LYC_ERR_UNSUPPORTED;
+    const size_t n = (size_t)(R * C) * esize(dt), need = lyc::ortho_workspace(R, C, dt);
+    if (out != g && overlaps(out, n, g, n)) return LYC_ERR_INVALID_ARG;
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
+        return LYC_ERR_WORKSPACE;
+    if (overlaps(workspace, need, g, n) || overlaps(workspace, need, out, n)) return LYC_ERR_INVALID_ARG;
+    (void)hipGetLastError();
+    hipStream_t s = (hipStream_t)stream;
+    const lyc::OrthoParams p{g, dt, out, R, C, steps, a, b, c, eps, (char*)workspace};
+    return timed(LYC_KERNEL_GEMM, s, [&] { return lyc::launch_ortho(p, s); }) == hipSuccess ? LYC_OK : LYC_ERR_HIP;
 }
 
 int lyc_resolve_dtypes(const int* operand_dtypes, int n, int* compute, int* output) {
