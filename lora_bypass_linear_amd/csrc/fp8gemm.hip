@@ -167,19 +167,23 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
     float bv = 0.f;
     if (p.bias != nullptr && p.ksplit <= 1 && tid < TL::TN)
         bv = n0 + tid < p.N ? load_as_f32(p.bias, p.bias_dt, n0 + tid) : 0.f;
-#pragma unroll
-    for (int s = 0; s < NS - 1; ++s) issue(s);
-    if (tid < TL::TN) sbias[tid] = bv;
-
     const int g = lane >> 4, r = lane & 15;
-    auto begin = [&](int kt) -> const char* {
-        wait_vm<(NS - 2) * TL::Q>();   // step kt has landed (this wave's share)
-        lds_barrier();                 // ... every wave's, and step kt-1's stage is free
-        issue(kt + NS - 1);
-        return smem + (kt % NS) * TL::STAGE;
+#pragma unroll
+    for (int s = 0; s < NS; ++s) issue(s);
+    if (tid < TL::TN) sbias[tid] = bv;
+    wait_vm<(NS - 1) * TL::Q>();
+    lds_barrier();
+    // Invariant at the head of step kt: its stage has landed for every wave,
+    // and the steps up to kt+NS-1 have been issued.  next(kt), once the wave
+    // holds all it needs of stage kt in registers: step kt+1 has landed and
+    // stage kt is free for step kt+NS.
+    auto next = [&]() {
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+        wait_vm<(NS - 2) * TL::Q>();
+        lds_barrier();
     };
     for (int kt = 0; kt < RF; ++kt) {
-        const char* st = begin(kt);
+        const char* st = smem + (kt % NS) * TL::STAGE;
         const char* sb = st + TL::TN * TL::BKB;
 #pragma unroll
         for (int sub = 0; sub < 2; ++sub) {
@@ -193,6 +197,8 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
 #pragma unroll
                 for (int j = 0; j < FM; ++j) acc[i][j] = CT::step(a[i], b[j], acc[i][j]);
         }
+        next();
+        issue(kt + NS);
     }
     if (RF > 0) {
 #pragma unroll
@@ -200,30 +206,128 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
 #pragma unroll
             for (int j = 0; j < FM; ++j) acc[i][j] *= p.scale;
     }
-    for (int kt = RF; kt < KT; ++kt) {
-        const char* st = begin(kt);
-        const char* sb = st + TL::TN * TL::BKB;
+    const int row_a = wn * TL::WN + r, row_b = wm * TL::WM + r;
+    auto load_frag = [&](Frag8<EXACT>& f, const char* base, int row) {
+        f.set(*(const i32x4*)(base + lds_at<TL>(row, g)), *(const i32x4*)(base + lds_at<TL>(row, 4 + g)));
+    };
+    auto load_scales = [&](float (&sj)[FM], const char* st) {
         const float* sc = (const float*)(st + TL::DATA);
         const float sw = sc[TL::TM + (wn * TL::WN) / FP8_BLOCK];
-        Frag8<EXACT> b[FM];
-        float sj[FM];
 #pragma unroll
-        for (int j = 0; j < FM; ++j) {
-            const int row = wm * TL::WM + j * 16 + r;
-            b[j].set(*(const i32x4*)(sb + lds_at<TL>(row, g)), *(const i32x4*)(sb + lds_at<TL>(row, 4 + g)));
-            sj[j] = sc[row] * sw;
+        for (int j = 0; j < FM; ++j) sj[j] = sc[row_b + j * 16] * sw;
+    };
+    if constexpr (EXACT || FN < 4) {
+        for (int kt = RF; kt < KT; ++kt) {
+            const char* st = smem + (kt % NS) * TL::STAGE;
+            Frag8<EXACT> b[FM];
+            float sj[FM];
+            load_scales(sj, st);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) load_frag(b[j], st + TL::TN * TL::BKB, row_b + j * 16);
+#pragma unroll
+            for (int i = 0; i < FN; ++i) {
+                Frag8<EXACT> a;
+                load_frag(a, st, row_a + i * 16);
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    const f32x4 t = block_sum<EXACT>(a, b[j]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t[e], sj[j], acc[i][j][e]);
+                }
+            }
+            next();
+            issue(kt + NS);
         }
+    } else if (KT > RF) {
+        // One K step by hand.  A fragments go through a ring of four, read two
+        // rows of blocks ahead; a row's MFMAs are followed by the FMAs of the
+        // row before, so that the matrix pipe and the vector pipe both have
+        // work.  The last two rows of blocks run column by column after the
+        // barrier: they need registers only, and each column's B fragment is
+        // refilled for the next step as soon as it is used, with a share of
+        // the loads of step kt+NS.
+        Frag8<false> a[4], b[FM];
+        float sj[FM], sn[FM];
+        auto fma4 = [&](f32x4& c, const f32x4& t, float sc) {
 #pragma unroll
-        for (int i = 0; i < FN; ++i) {
-            const int row = wn * TL::WN + i * 16 + r;
-            Frag8<EXACT> a;
-            a.set(*(const i32x4*)(st + lds_at<TL>(row, g)), *(const i32x4*)(st + lds_at<TL>(row, 4 + g)));
+            for (int e = 0; e < 4; ++e) c[e] = __builtin_fmaf(t[e], sc, c[e]);
+        };
+        {
+            const char* st = smem + (RF % NS) * TL::STAGE;
+            load_scales(sj, st);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) load_frag(b[j], st + TL::TN * TL::BKB, row_b + j * 16);
+            load_frag(a[0], st, row_a);
+            load_frag(a[1], st, row_a + 16);
+        }
+        const auto ra = make_rsrc(ma, (uint32_t)rows_a * kbytes);
+        const auto rb = make_rsrc(mb, (uint32_t)rows_b * kbytes);
+        using LD = Loader<TL>;
+        constexpr int QL = LD::QA + LD::QB;
+        for (int kt = RF; kt < KT; ++kt) {
+            const char* st = smem + (kt % NS) * TL::STAGE;
+            const char* nx = smem + ((kt + 1) % NS) * TL::STAGE;
+            f32x4 t[2][FM];
+#pragma unroll
+            for (int i = 0; i < FN - 2; ++i) {
+                load_frag(a[(i + 2) & 3], st, row_a + (i + 2) * 16);
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    t[i & 1][j] = block_sum<false>(a[i & 3], b[j]);
+                    if (i > 0) fma4(acc[i - 1][j], t[(i - 1) & 1][j], sj[j]);
+                }
+                // an MFMA, then the four FMAs of one column of the row before
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+#pragma unroll
+                for (int j = 0; j < FM; ++j) {
+                    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+                    if (i > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            }
+            next();
+            // (steps past the last are out of range; fold steps are all before)
+            const int s = kt + NS;
+            const int64_t kb = s - RF + k0;
+            const uint32_t kb0 = (uint32_t)kb * 128u, row_bytes = s < KT ? kbytes : 0u;
+            const bool ok = kb0 + 128u <= row_bytes || kb0 + LD::chunk16(lane) < row_bytes;
+            char* wr = smem + (s % NS) * TL::STAGE;
+            const float* sp = is_w ? pp.sw + nb0 * pp.sw_n + kb * pp.sw_k : pp.sx + kb * p.M + m0;
+            const auto rs = make_rsrc(s < KT ? sp : pp.sw, s < KT ? srange : 0u);
+            load_scales(sn, nx);
+            load_frag(a[FN & 3], nx, row_a);
+            load_frag(a[(FN + 1) & 3], nx, row_a + 16);
+            f32x4 u[2][2];
 #pragma unroll
             for (int j = 0; j < FM; ++j) {
-                const f32x4 t = block_sum<EXACT>(a, b[j]);
 #pragma unroll
-                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(t[e], sj[j], acc[i][j][e]);
+                for (int q = 0; q < QL; ++q) {
+                    if (q * FM / QL != j) continue;
+                    auto* dst = (__attribute__((address_space(3))) void*)(wr + (wave + q * TL::NW) * 1024);
+                    const bool is_a = q < LD::QA;
+                    const uint32_t v = is_a ? lm.va + (uint32_t)q * lm.sa : lm.vb + (uint32_t)(q - LD::QA) * lm.sb;
+                    if (is_a) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, dst, 16, ok ? v : OOB, (int)kb0, 0, 0);
+                    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, dst, 16, ok ? v : OOB, (int)kb0, 0, 0);
+                }
+                u[j & 1][0] = block_sum<false>(a[(FN - 2) & 3], b[j]);
+                fma4(acc[FN - 3][j], t[(FN - 3) & 1][j], sj[j]);
+                u[j & 1][1] = block_sum<false>(a[(FN - 1) & 3], b[j]);
+                if (j > 0) {
+                    fma4(acc[FN - 2][j - 1], u[(j - 1) & 1][0], sj[j - 1]);
+                    fma4(acc[FN - 1][j - 1], u[(j - 1) & 1][1], sj[j - 1]);
+                }
+                load_frag(b[j], nx + TL::TN * TL::BKB, row_b + j * 16);
+                __builtin_amdgcn_sched_barrier(0);
             }
+            {
+                auto* dst = (__attribute__((address_space(3))) void*)(wr + TL::DATA + wave * 256);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 4, soff, 0, 0, 0);
+            }
+            fma4(acc[FN - 2][FM - 1], u[(FM - 1) & 1][0], sj[FM - 1]);
+            fma4(acc[FN - 1][FM - 1], u[(FM - 1) & 1][1], sj[FM - 1]);
+#pragma unroll
+            for (int j = 0; j < FM; ++j) sj[j] = sn[j];
+            static_assert(FN % 4 == 0, "the ring starts over each step");
         }
     }
     wait_vm<0>();   // the out-of-range loads past the last step still write LDS
