@@ -210,20 +210,24 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
     auto load_frag = [&](Frag8<EXACT>& f, const char* base, int row) {
         f.set(*(const i32x4*)(base + lds_at<TL>(row, g)), *(const i32x4*)(base + lds_at<TL>(row, 4 + g)));
     };
+    // a step's row scales and this wave's tile scale
     auto load_scales = [&](float (&sj)[FM], const char* st) {
         const float* sc = (const float*)(st + TL::DATA);
-        const float sw = sc[TL::TM + (wn * TL::WN) / FP8_BLOCK];
 #pragma unroll
-        for (int j = 0; j < FM; ++j) sj[j] = sc[row_b + j * 16] * sw;
+        for (int j = 0; j < FM; ++j) sj[j] = sc[row_b + j * 16];
+        return sc[TL::TM + (wn * TL::WN) / FP8_BLOCK];
     };
     if constexpr (EXACT || FN < 4) {
         for (int kt = RF; kt < KT; ++kt) {
             const char* st = smem + (kt % NS) * TL::STAGE;
             Frag8<EXACT> b[FM];
             float sj[FM];
-            load_scales(sj, st);
+            const float sw = load_scales(sj, st);
 #pragma unroll
-            for (int j = 0; j < FM; ++j) load_frag(b[j], st + TL::TN * TL::BKB, row_b + j * 16);
+            for (int j = 0; j < FM; ++j) {
+                load_frag(b[j], st + TL::TN * TL::BKB, row_b + j * 16);
+                sj[j] *= sw;
+            }
 #pragma unroll
             for (int i = 0; i < FN; ++i) {
                 Frag8<EXACT> a;
@@ -254,9 +258,12 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
         };
         {
             const char* st = smem + (RF % NS) * TL::STAGE;
-            load_scales(sj, st);
+            const float sw = load_scales(sj, st);
 #pragma unroll
-            for (int j = 0; j < FM; ++j) load_frag(b[j], st + TL::TN * TL::BKB, row_b + j * 16);
+            for (int j = 0; j < FM; ++j) {
+                load_frag(b[j], st + TL::TN * TL::BKB, row_b + j * 16);
+                sj[j] *= sw;
+            }
             load_frag(a[0], st, row_a);
             load_frag(a[1], st, row_a + 16);
         }
@@ -294,7 +301,7 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
             char* wr = smem + (s % NS) * TL::STAGE;
             const float* sp = is_w ? pp.sw + nb0 * pp.sw_n + kb * pp.sw_k : pp.sx + kb * p.M + m0;
             const auto rs = make_rsrc(s < KT ? sp : pp.sw, s < KT ? srange : 0u);
-            load_scales(sn, nx);
+            const float swn = load_scales(sn, nx);
             load_frag(a[FN & 3], nx, row_a);
             load_frag(a[(FN + 1) & 3], nx, row_a + 16);
             f32x4 u[2][2];
@@ -326,7 +333,7 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
             fma4(acc[FN - 2][FM - 1], u[(FM - 1) & 1][0], sj[FM - 1]);
             fma4(acc[FN - 1][FM - 1], u[(FM - 1) & 1][1], sj[FM - 1]);
 #pragma unroll
-            for (int j = 0; j < FM; ++j) sj[j] = sn[j];
+            for (int j = 0; j < FM; ++j) sj[j] = sn[j] * swn;
             static_assert(FN % 4 == 0, "the ring starts over each step");
         }
     }
@@ -390,6 +397,144 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
     }
 }
 
+// ---- few token rows: one workgroup per 16 NF output features ----------------------
+// All of K in one workgroup, wave w of the NW taking the w-th share of the
+// 128-byte blocks, its fragments and scales read straight from global memory D
+// blocks ahead (every weight byte is used once); the waves' sums meet in LDS
+// in wave order, wave 0's with the fold.  Bound by the weight's bytes: x's
+// rows, read by every workgroup from L2, cost as much again per 16 features,
+// so NF = 2 where that still leaves a workgroup per CU.
+template <class CT, int MT, int NF, int D, int NW, bool EXACT>
+__global__ __launch_bounds__(64 * NW) void fp8_skinny_kernel(Fp8GemmParams pp) {
+    const GemmParams& p = pp.g;
+    __shared__ __attribute__((aligned(16))) f32x4 red[NW][NF][MT][64];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * NF);
+    const uint32_t kb = (uint32_t)p.K;
+    const int nrows = (int)(p.N - n0 < 16 * NF ? p.N - n0 : 16 * NF);
+    const auto rw = make_rsrc_uniform((const char*)p.a + n0 * kb, (uint32_t)nrows * kb);
+    const auto rx = make_rsrc_uniform(p.b, (uint32_t)p.M * kb);
+    const int blocks = (int)((kb + 127) / 128);
+    const auto rs = make_rsrc_uniform(pp.sx, (uint32_t)(blocks * p.M) * 4);
+    const float* sw = pp.sw + n0 / FP8_BLOCK * pp.sw_n;   // (16 NF features lie in one tile)
+    f32x4 acc[NF][MT];
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[f][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+
+    if (wave == 0 && p.rf > 0) {
+        const uint32_t fb = (uint32_t)(p.rf * CT::es), lo = (uint32_t)g * 16;
+        const auto ru = make_rsrc_uniform((const char*)p.af + n0 * fb, (uint32_t)nrows * fb);
+        const auto rh = make_rsrc_uniform(p.bf, (uint32_t)p.M * fb);
+        for (uint32_t k = 0; k < fb; k += 64) {
+            i32x4 hb[MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) hb[t] = buf_load16(rh, k + lo < fb ? (uint32_t)(16 * t + r) * fb + k + lo : OOB);
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                const i32x4 ua = buf_load16(ru, k + lo < fb ? (uint32_t)(16 * f + r) * fb + k + lo : OOB);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) acc[f][t] = CT::step(ua, hb[t], acc[f][t]);
+            }
+        }
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int t = 0; t < MT; ++t) acc[f][t] *= p.scale;
+    }
+
+    // ring slot u holds block s0 + u (mod D); past the share's end everything
+    // is sent out of range and reads zeros
+    const int s0 = blocks * wave / NW, s1 = blocks * (wave + 1) / NW;
+    const int se = s0 + ((s1 - s0 + D - 1) / D) * D;
+    i32x4 wa[D][NF][2], xa[D][MT][2];
+    float sx[D][MT], sv[D];
+    auto load = [&](int u, int b) {
+        const bool on = b < s1;
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const uint32_t k = (uint32_t)b * 128 + (uint32_t)(h * 64 + g * 16);
+            const bool in = on && k < kb;
+#pragma unroll
+            for (int f = 0; f < NF; ++f) wa[u][f][h] = buf_load16(rw, in ? (uint32_t)(16 * f + r) * kb + k : OOB);
+#pragma unroll
+            for (int t = 0; t < MT; ++t) xa[u][t][h] = buf_load16(rx, in ? (uint32_t)(16 * t + r) * kb + k : OOB);
+        }
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            sx[u][t] = __builtin_bit_cast(float, __builtin_amdgcn_raw_buffer_load_b32(
+                rs, on && 16 * t + r < p.M ? (uint32_t)(b * p.M + 16 * t + r) * 4 : OOB, 0, 0));
+        sv[u] = sw[(on ? b : 0) * pp.sw_k];
+    };
+#pragma unroll
+    for (int u = 0; u < D; ++u) load(u, s0 + u);
+    for (int sb = s0; sb < se; sb += D) {
+#pragma unroll
+        for (int u = 0; u < D; ++u) {
+            Frag8<EXACT> fx[MT];
+            float sc[MT];
+#pragma unroll
+            for (int t = 0; t < MT; ++t) {
+                fx[t].set(xa[u][t][0], xa[u][t][1]);
+                sc[t] = sx[u][t] * sv[u];
+            }
+#pragma unroll
+            for (int f = 0; f < NF; ++f) {
+                Frag8<EXACT> fw;
+                fw.set(wa[u][f][0], wa[u][f][1]);
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    const f32x4 v = block_sum<EXACT>(fw, fx[t]);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) acc[f][t][e] = __builtin_fmaf(v[e], sc[t], acc[f][t][e]);
+                }
+            }
+            load(u, sb + u + D);
+        }
+    }
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) red[wave][f][t][lane] = acc[f][t];
+    __syncthreads();
+    // wave w < NF MT adds up and stores block (f, t) = (w / MT, w % MT)
+    if (wave >= NF * MT) return;
+    const int f = wave / MT, t = wave % MT;
+    f32x4 sum = red[0][f][t][lane];
+#pragma unroll
+    for (int w = 1; w < NW; ++w) sum += red[w][f][t][lane];
+    const int64_t nb = n0 + 16 * f + 4 * g, m = 16 * t + r;
+    if (m >= p.M) return;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        if (nb + e >= p.N) continue;
+        const float v = sum[e] + (p.bias != nullptr ? load_as_f32(p.bias, p.bias_dt, nb + e) : 0.f);
+        const int64_t at = m * p.N + nb + e;
+        if (p.y_dt == DT_F32) ((float*)p.y)[at] = v;
+        else ((uint16_t*)p.y)[at] = p.y_dt == DT_F16 ? f32_to_f16(v) : f32_to_bf16(v);
+    }
+}
+
+// the few-row kernel's limits: 32 rows, 32-bit offsets
+static bool fp8_skinny(int64_t M, int64_t K) {
+    return M >= 1 && M <= 32 && K > 0 && 32 * K < ((int64_t)1 << 31);
+}
+
+template <class CT, int MT, int NF, bool EXACT>
+static hipError_t run_skinny8(const Fp8GemmParams& p, hipStream_t s) {
+    hipLaunchKernelGGL((fp8_skinny_kernel<CT, MT, NF, 4, 8, EXACT>), dim3((unsigned)((p.g.N + 16 * NF - 1) / (16 * NF))),
+                       dim3(512), 0, s, p);
+    return hipGetLastError();
+}
+template <class CT, bool EXACT>
+static hipError_t run_skinny8_ct(const Fp8GemmParams& p, hipStream_t s) {
+    const bool wide = p.g.N >= 32 * device_rates().cus;
+    if (p.g.M <= 16) return wide ? run_skinny8<CT, 1, 2, EXACT>(p, s) : run_skinny8<CT, 1, 1, EXACT>(p, s);
+    return wide ? run_skinny8<CT, 2, 2, EXACT>(p, s) : run_skinny8<CT, 2, 1, EXACT>(p, s);
+}
+
 enum { T8_L, T8_M, T8_S };
 
 // Output tile and K split: the fewest rounds of workgroups over the device's
@@ -418,7 +563,7 @@ static void fp8_pick(int64_t M, int64_t N, int64_t K, int* tile, int* ksplit) {
 }
 
 int fp8_gemm_ksplit(int64_t M, int64_t N, int64_t K) {
-    if (M <= 0 || N <= 0 || K <= 0) return 1;
+    if (M <= 0 || N <= 0 || K <= 0 || fp8_skinny(M, K)) return 1;
     int t, ks;
     fp8_pick(M, N, K, &t, &ks);
     return ks;
@@ -456,6 +601,12 @@ static hipError_t run8_ct(const Fp8GemmParams& p, int t, hipStream_t s) {
 
 hipError_t launch_fp8_gemm(int c_dt, const Fp8GemmParams& p, hipStream_t s) {
     if (p.g.M <= 0 || p.g.N <= 0) return hipSuccess;
+    if (p.g.ksplit <= 1 && fp8_skinny(p.g.M, p.g.K)) {
+        const bool exact = p.g.y_dt == DT_F32;
+        if (c_dt == DT_F16) return exact ? run_skinny8_ct<CF16, true>(p, s) : run_skinny8_ct<CF16, false>(p, s);
+        if (c_dt == DT_BF16) return exact ? run_skinny8_ct<CBF16, true>(p, s) : run_skinny8_ct<CBF16, false>(p, s);
+        return exact ? run_skinny8_ct<CF32, true>(p, s) : run_skinny8_ct<CF32, false>(p, s);
+    }
     int t, ks;
     fp8_pick(p.g.M, p.g.N, p.g.K, &t, &ks);
     if (p.g.ksplit > 1 && p.g.partial == nullptr) return hipErrorInvalidValue;
