@@ -8,6 +8,7 @@ nothing here falls back to another implementation.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 from typing import Optional, Sequence, Tuple
 
@@ -197,7 +198,7 @@ def _shape(t: Optional[torch.Tensor], shape, name: str) -> None:
     written) out of bounds: every shape is checked here before any call."""
     if t is None:
         return
-    if tuple(t.shape) != tuple(int(s) for s in shape):
+    if t.shape != tuple(shape) and tuple(t.shape) != tuple(int(s) for s in shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(int(s) for s in shape)}")
 
 
@@ -713,6 +714,27 @@ def fp8_quantize_weight(w: torch.Tensor, transposed: bool = False):
     return q, s, q_t
 
 
+# What a call's shape and dtypes alone decide (output dtype, workspace bytes),
+# looked up once per shape and device instead of on every call.
+@functools.lru_cache(maxsize=4096)
+def _fp8_linear_plan(dev, M, N, K) -> int:
+    return fp8_linear_workspace_size(M, N, K)
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp8_lora_plan(dev, M, N, K, r, x_dt, b_dt, d_dt, u_dt) -> Tuple[int, int]:
+    _, o_dt = resolve_dtypes([x_dt] + ([b_dt] if b_dt else []) + [d_dt, u_dt])
+    return o_dt, fp8_lora_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt)
+
+
+@functools.lru_cache(maxsize=4096)
+def _fp8_lora_bwd_plan(dev, M, N, K, r, x_dt, b_dt, d_dt, u_dt, g_dt, want) -> Tuple[int, int, int]:
+    c_dt, _ = resolve_dtypes([x_dt] + ([b_dt] if b_dt else []) + [d_dt, u_dt, g_dt])
+    ld = ctypes.c_int64(0)
+    _check(lib().lyc_fp8_lora_workspace_layout(M, N, K, r, x_dt, c_dt, d_dt, u_dt, None, ctypes.byref(ld)))
+    return c_dt, ld.value, fp8_lora_bwd_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt, g_dt, want)
+
+
 def fp8_linear_workspace_size(M: int, N: int, K: int) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().lyc_fp8_linear_workspace_size(M, N, K, ctypes.byref(n)))
@@ -748,7 +770,7 @@ def fp8_linear(q: torch.Tensor, s: torch.Tensor, w_q: torch.Tensor, w_s: torch.T
     dev = _need_device(q, s, w_q, w_s, bias, out, workspace)
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
-    ws = _workspace(fp8_linear_workspace_size(M, N, K), dev, workspace)
+    ws = _workspace(_fp8_linear_plan(dev, M, N, K), dev, workspace)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib().lyc_fp8_linear_fwd(_ptr(q), _ptr(s), _ptr(w_q), _ptr(w_s), _ptr(bias), b_dt, _ptr(out), o_dt, M, N,
                                     K, _ptr(ws), nbytes, _stream(dev)))
@@ -775,12 +797,12 @@ def fp8_lora_linear(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, down:
     M, N, K, r = _fp8_lora_shapes(x, w_q, w_s, down, up, bias, out)
     x_dt, d_dt, u_dt = dtype_code(x), dtype_code(down), dtype_code(up)
     b_dt = dtype_code(bias) if bias is not None else 0
-    _, o_dt = resolve_dtypes([x_dt] + ([b_dt] if b_dt else []) + [d_dt, u_dt])
-    _out_dtype(out, o_dt)
     dev = _need_device(x, w_q, w_s, down, up, bias, out, workspace)
+    o_dt, need = _fp8_lora_plan(dev, M, N, K, r, x_dt, b_dt, d_dt, u_dt)
+    _out_dtype(out, o_dt)
     if out is None:
         out = torch.empty((M, N), dtype=_TORCH[o_dt], device=dev)
-    ws = _workspace(fp8_lora_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt), dev, workspace)
+    ws = _workspace(need, dev, workspace)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib().lyc_fp8_lora_linear_fwd(_ptr(x), x_dt, _ptr(w_q), _ptr(w_s), _ptr(bias), b_dt, _ptr(down), d_dt,
                                          _ptr(up), u_dt, r, float(scale), _ptr(out), dtype_code(out), M, N, K,
@@ -816,19 +838,16 @@ def fp8_lora_linear_backward(x: torch.Tensor, w_qt: torch.Tensor, w_s: torch.Ten
     dev = _need_device(x, w_qt, w_s, down, up, dy, workspace, h)
     x_dt, d_dt, u_dt, g_dt = (dtype_code(t) for t in (x, down, up, dy))
     b_dt = _CODE[bias_dtype] if bias_dtype is not None else 0
-    c_dt = resolve_dtypes([x_dt] + ([b_dt] if b_dt else []) + [d_dt, u_dt, g_dt])[0]
-    if h is not None:
-        ld = ctypes.c_int64(0)
-        _check(lib().lyc_fp8_lora_workspace_layout(M, N, K, r, x_dt, c_dt, d_dt, u_dt, None,
-                                                   ctypes.byref(ld)))
-        _shape(h, (M, ld.value), "h")
-        _typed(h, _TORCH[c_dt], "h")
     want = (BWD_DX if want_dx else 0) | (BWD_DDOWN if want_ddown else 0) | (BWD_DUP if want_dup else 0) | \
         (BWD_H if h is not None else 0)
+    c_dt, r_pad, need = _fp8_lora_bwd_plan(dev, M, N, K, r, x_dt, b_dt, d_dt, u_dt, g_dt, want)
+    if h is not None:
+        _shape(h, (M, r_pad), "h")
+        _typed(h, _TORCH[c_dt], "h")
     dx = torch.empty((M, K), dtype=x.dtype, device=dev) if want_dx else None
     dd = torch.empty((r, K), dtype=down.dtype, device=dev) if want_ddown else None
     du = torch.empty((N, r), dtype=up.dtype, device=dev) if want_dup else None
-    ws = _workspace(fp8_lora_bwd_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt, g_dt, want), dev, workspace)
+    ws = _workspace(need, dev, workspace)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     # an empty output still has to be passed (non-NULL) to be "wanted"
     p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr() if t.numel() else 256)
@@ -836,6 +855,11 @@ def fp8_lora_linear_backward(x: torch.Tensor, w_qt: torch.Tensor, w_s: torch.Ten
                                          _ptr(h), r, float(scale), _ptr(dy), g_dt, p(dx), p(dd), p(du), M, N, K,
                                          _ptr(ws), nbytes, _stream(dev)))
     return dx, dd, du
+
+
+@functools.lru_cache(maxsize=4096)
+def _ortho_plan(dev, R, C, dt) -> int:
+    return orthogonalize_workspace_size(R, C, dt)
 
 
 def orthogonalize_workspace_size(R: int, C: int, dt: int) -> int:
@@ -859,7 +883,7 @@ def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients: Sequence[float]
     dev = _need_device(g, out, workspace)
     if out is None:
         out = torch.empty_like(g)
-    ws = _workspace(orthogonalize_workspace_size(R, C, dt), dev, workspace)
+    ws = _workspace(_ortho_plan(dev, R, C, dt), dev, workspace)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     _check(lib().lyc_orthogonalize(_ptr(g), dt, _ptr(out), R, C, int(steps), a, b, c, float(eps), _ptr(ws), nbytes,
                                    _stream(dev)))

@@ -324,6 +324,493 @@ __global__ __launch_bounds__(256) void ns_reduce_kernel(NsParams p) {
     }
 }
 
+// ---- thin updates (a LoRA factor's): the iteration on the n x n side -----------------
+//
+// For n <= 128 one step's work is small and its launches and passes over X
+// are not.  Every matrix of the iteration is a polynomial of the first A, so
+// they commute, and several steps need X only at their ends:
+//   P = a I + b A + c A^2,   Q <- P Q,   A <- P A P,     then X <- Q X.
+// One workgroup runs a segment of steps on A in LDS; one pass over X applies
+// Q, and takes the next segment's Gram matrix while X is there.  A's rounding
+// errors grow by a^2 a step against its small eigenvalues (twice as fast as
+// X's own), so a segment has at most 3 steps with two pieces (its errors stay
+// near 1e-5 of the result, a hundredth of a 16-bit rounding; all 5 steps in
+// one segment measured 1e-4 and more), and one step with three.
+//   ns_chunk_kernel  Gram matrix of X / X <- Q X with it / the last X <- Q X
+//   ns_sum_kernel    the workgroups' Gram matrices added up (n > 32)
+//   ns_iter_kernel   a segment of steps; the first one scales by 1 / (|G| + eps),
+//                    |G|^2 being the trace
+
+constexpr int NS_SEG = 3;
+constexpr int NS_THIN = 128;
+constexpr int NS_EMPTY = -100000;   // exponent of a workgroup that saw zeros only
+
+template <int NPAD>
+struct ThinShape {
+    static constexpr int NW = NPAD == 128 ? 8 : 4, NT = NW * 64;
+    static constexpr int CW = NPAD == 16 ? 256 : NPAD == 32 ? 128 : 64;   // columns a chunk
+    static constexpr int LD = CW + 8;            // LDS row: consecutive rows four banks on
+    static constexpr int KR = NPAD < 32 ? 32 : NPAD;   // rows an MFMA step reads (zeros past NPAD)
+    static constexpr int IB = NPAD / 16, WC = NW / IB, CB = CW / 16 / WC;
+    static constexpr int PT = NPAD * CW / NT;    // elements a thread loads
+    static constexpr int GT = NPAD == 16 ? 1 : IB * IB / NW;   // Gram tiles a wave
+    static constexpr bool KSPLIT = NPAD == 16;   // one Gram tile: the waves share its columns
+    static_assert(CB == 4 && PT == 16, "a chunk's shares");
+};
+
+struct ThinParams {
+    const void* g;      // raw source [R][C] (src 0: wide, 1: tall)
+    int src, dt;        // 2: x, fp32 [n][ldx]
+    int64_t n, m, ldx;
+    float* x;
+    const uint16_t* q;  // pieces [NP][NPAD][KR], scaled
+    const double* fac;  // X' = fac * 2^e * (q . pieces)
+    float* part;        // a Gram matrix per workgroup, [NPAD][NPAD]
+    int* exps;          // which stands for 2^(2 e) times its values
+    float sx;           // the power of two that scales X after the first segment
+    void* out;          // [R][C]
+    int tall;
+};
+
+__device__ __forceinline__ int exponent_of(uint32_t abs_bits) { return (int)(abs_bits >> 23) - 127; }
+
+// 8 consecutive rows of one column of an LDS tile [row][LD]: the transposing
+// read of lyc_device.h's frag_t, rows LD elements apart
+template <int LD>
+__device__ __forceinline__ i32x4 thin_frag_t(const uint16_t* t, int row0, int col0, int lane) {
+    typedef short s4 __attribute__((ext_vector_type(4)));
+    typedef __attribute__((address_space(3))) s4 lds_s4;
+    const int G = lane >> 4, j = lane & 15;
+    const uint16_t* p = t + (row0 + 8 * G + (j >> 2)) * LD + col0 + 4 * (j & 3);
+    const s4 a = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(__attribute__((address_space(3))) uint16_t*)p);
+    const s4 b =
+        __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(__attribute__((address_space(3))) uint16_t*)(p + 4 * LD));
+    const i32x2 ai = __builtin_bit_cast(i32x2, a), bi = __builtin_bit_cast(i32x2, b);
+    return i32x4{ai[0], ai[1], bi[0], bi[1]};
+}
+
+// the piece products whose orders add up to at most NP - 1, small ones first
+template <int NP>
+__device__ __forceinline__ f32x4 piece_step(const i32x4 (&a)[NP], const i32x4 (&b)[NP], f32x4 c) {
+#pragma unroll
+    for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+        for (int k = 0; k <= o; ++k) c = Pieces<NP>::CT::step(a[k], b[o - k], c);
+    return c;
+}
+
+enum { THIN_GRAM = 0, THIN_BOTH = 1, THIN_OUT = 2 };
+
+template <int NPAD, int NP, int MODE>
+__global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParams p) {
+    using S = ThinShape<NPAD>;
+    constexpr int LD = S::LD, CW = S::CW, KS = S::KR / 32;
+    __shared__ __attribute__((aligned(16))) uint16_t xs[NP][S::KR * LD];
+    __shared__ uint32_t wmax[S::NW];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int ib = wave % S::IB, cb0 = wave / S::IB * S::CB;
+    if constexpr (S::KR > NPAD) {
+        for (int i = tid; i < (S::KR - NPAD) * LD; i += S::NT)
+#pragma unroll
+            for (int k = 0; k < NP; ++k) xs[k][NPAD * LD + i] = 0;
+    }
+    i32x4 q[KS][NP];
+    double fac = 0;
+    if constexpr (MODE != THIN_GRAM) {
+#pragma unroll
+        for (int s = 0; s < KS; ++s)
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+                q[s][k] = *(const i32x4*)(p.q + ((int64_t)k * NPAD + ib * 16 + r) * S::KR + s * 32 + g * 8);
+        fac = *p.fac;
+    }
+    f32x4 gacc[S::GT];
+#pragma unroll
+    for (int t = 0; t < S::GT; ++t) gacc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    int erun = MODE == THIN_GRAM && p.src != 2 ? NS_EMPTY : -exponent_of(__builtin_bit_cast(uint32_t, p.sx));
+
+    const int64_t chunks = (p.m + CW - 1) / CW;
+    for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
+        const int64_t c0 = ch * CW;
+        // the chunk, 16 elements a thread, consecutive threads along the stored rows
+        float v[S::PT];
+        int at[S::PT];
+        uint32_t raw[S::PT];
+#pragma unroll
+        for (int u = 0; u < S::PT; ++u) {
+            const int idx = tid + u * S::NT;
+            const int row = p.src == 1 ? idx % NPAD : idx / CW, col = p.src == 1 ? idx / NPAD : idx % CW;
+            at[u] = row * LD + col;
+            const bool in = row < p.n && c0 + col < p.m;
+            const int64_t e = p.src == 1 ? (c0 + col) * p.n + row : row * (p.src == 2 ? p.ldx : p.m) + c0 + col;
+            raw[u] = 0;
+            if (in) {
+                if (p.src == 2) raw[u] = ((const uint32_t*)p.x)[e];
+                else if (p.dt == DT_F32) raw[u] = ((const uint32_t*)p.g)[e];
+                else raw[u] = ((const uint16_t*)p.g)[e];
+            }
+        }
+        uint32_t mx = 0;
+#pragma unroll
+        for (int u = 0; u < S::PT; ++u) {
+            if (p.src == 2 || p.dt == DT_F32) v[u] = __builtin_bit_cast(float, raw[u]);
+            else v[u] = p.dt == DT_F16 ? f16_to_f32((uint16_t)raw[u]) : bf16_to_f32((uint16_t)raw[u]);
+            const uint32_t b = __builtin_bit_cast(uint32_t, v[u]) & 0x7FFFFFFFu;
+            mx = b > mx ? b : mx;
+        }
+        // a raw chunk is scaled by 2^-e, its largest magnitude to [2^11, 2^12)
+        // (fp16 pieces' low bits stay normal); subnormal maxima count as 2^-126
+        int e = -exponent_of(__builtin_bit_cast(uint32_t, p.sx));
+        if (p.src != 2) {
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) {
+                const uint32_t o = (uint32_t)__shfl_xor((int)mx, d);
+                mx = o > mx ? o : mx;
+            }
+            if (lane == 0) wmax[wave] = mx;
+            __syncthreads();
+#pragma unroll
+            for (int w = 0; w < S::NW; ++w) mx = wmax[w] > mx ? wmax[w] : mx;
+            if (mx == 0) {
+                e = 0;
+            } else {
+                const int top = exponent_of(mx < 0x00800000u ? 0x00800000u : mx);
+                e = top - 11;
+            }
+        }
+        if constexpr (MODE == THIN_GRAM) {
+            if (mx == 0 && p.src != 2) {
+                __syncthreads();   // (wmax is read by all before the next chunk writes it)
+                continue;          // zeros add nothing
+            }
+            if (p.src != 2) {
+                if (erun == NS_EMPTY) erun = e;
+                else if (e > erun) {
+                    const float f = __builtin_ldexpf(1.f, 2 * (erun - e) < -126 ? -126 : 2 * (erun - e));
+#pragma unroll
+                    for (int t = 0; t < S::GT; ++t) gacc[t] *= f;
+                    erun = e;
+                }
+                e = erun;
+            }
+        }
+        __syncthreads();   // the previous chunk's tile has been read
+#pragma unroll
+        for (int u = 0; u < S::PT; ++u) {
+            uint16_t o[NP];
+            Pieces<NP>::split(__builtin_ldexpf(v[u], -e), o);
+#pragma unroll
+            for (int k = 0; k < NP; ++k) xs[k][at[u]] = o[k];
+        }
+        __syncthreads();
+
+        if constexpr (MODE != THIN_GRAM) {
+            const float f = (float)__builtin_ldexp(fac, e);
+            f32x4 acc[S::CB];
+#pragma unroll
+            for (int c = 0; c < S::CB; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int s = 0; s < KS; ++s)
+#pragma unroll
+                for (int c = 0; c < S::CB; ++c) {
+                    i32x4 x[NP];
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) x[k] = thin_frag_t<LD>(xs[k], s * 32, (cb0 + c) * 16, lane);
+                    if (MODE == THIN_OUT && p.tall) acc[c] = piece_step<NP>(q[s], x, acc[c]);
+                    else acc[c] = piece_step<NP>(x, q[s], acc[c]);
+                }
+            if constexpr (MODE == THIN_OUT) {
+#pragma unroll
+                for (int c = 0; c < S::CB; ++c) {
+                    // wide: row i of the block, 4 consecutive columns; tall: the other way round
+                    const int64_t i = ib * 16 + (p.tall ? 4 * g : r), cc = c0 + (cb0 + c) * 16 + (p.tall ? r : 4 * g);
+#pragma unroll
+                    for (int el = 0; el < 4; ++el) {
+                        const int64_t ie = p.tall ? i + el : i, ce = p.tall ? cc : cc + el;
+                        if (ie >= p.n || ce >= p.m) continue;
+                        const int64_t o = p.tall ? ce * p.n + ie : ie * p.m + ce;
+                        const float val = acc[c][el] * f;
+                        if (p.dt == DT_F32) ((float*)p.out)[o] = val;
+                        else ((uint16_t*)p.out)[o] = p.dt == DT_F16 ? f32_to_f16(val) : f32_to_bf16(val);
+                    }
+                }
+                continue;
+            } else {
+                __syncthreads();   // the tile has been read: X' takes its place
+#pragma unroll
+                for (int c = 0; c < S::CB; ++c) {
+                    const int i = ib * 16 + r, cc = (cb0 + c) * 16 + 4 * g;
+                    acc[c] *= f;
+                    if (i < p.n) *(f32x4*)(p.x + i * p.ldx + c0 + cc) = acc[c];
+                    uint16_t o[4][NP];
+#pragma unroll
+                    for (int el = 0; el < 4; ++el) Pieces<NP>::split(acc[c][el] * p.sx, o[el]);
+#pragma unroll
+                    for (int k = 0; k < NP; ++k)
+                        *(i32x2*)&xs[k][i * LD + cc] = i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16),
+                                                             (int)((uint32_t)o[2][k] | (uint32_t)o[3][k] << 16)};
+                }
+                __syncthreads();
+            }
+        }
+        if constexpr (MODE != THIN_OUT) {
+            constexpr int GK = CW / 32 / (S::KSPLIT ? S::NW : 1);
+#pragma unroll
+            for (int s = 0; s < GK; ++s) {
+                const int ks = S::KSPLIT ? wave * GK + s : s;
+                const int gi = S::KSPLIT ? 0 : wave % S::IB;
+                i32x4 a[NP];
+#pragma unroll
+                for (int k = 0; k < NP; ++k) a[k] = *(const i32x4*)&xs[k][(gi * 16 + r) * LD + ks * 32 + g * 8];
+#pragma unroll
+                for (int t = 0; t < S::GT; ++t) {
+                    const int gj = S::KSPLIT ? 0 : wave / S::IB * S::GT + t;
+                    i32x4 b[NP];
+#pragma unroll
+                    for (int k = 0; k < NP; ++k) b[k] = *(const i32x4*)&xs[k][(gj * 16 + r) * LD + ks * 32 + g * 8];
+                    gacc[t] = piece_step<NP>(a, b, gacc[t]);
+                }
+            }
+        }
+    }
+    if constexpr (MODE != THIN_OUT) {
+        if constexpr (S::KSPLIT) {
+            __syncthreads();   // the last chunk's tile has been read
+            f32x4* red = (f32x4*)&xs[0][0];
+            red[wave * 64 + lane] = gacc[0];
+            __syncthreads();
+            gacc[0] = red[lane];
+#pragma unroll
+            for (int w = 1; w < S::NW; ++w) gacc[0] += red[w * 64 + lane];
+            if (wave != 0) return;
+        }
+        const int gi = S::KSPLIT ? 0 : wave % S::IB;
+#pragma unroll
+        for (int t = 0; t < S::GT; ++t) {
+            const int gj = S::KSPLIT ? 0 : wave / S::IB * S::GT + t;
+            *(f32x4*)(p.part + ((int64_t)blockIdx.x * NPAD + gj * 16 + r) * NPAD + gi * 16 + 4 * g) = gacc[t];
+        }
+        if (tid == 0) p.exps[blockIdx.x] = erun;
+    }
+}
+
+// the largest of the slots' exponents
+__device__ __forceinline__ int top_exponent(const int* exps, int slots) {
+    int e = NS_EMPTY;
+    for (int i = threadIdx.x & 63; i < slots; i += 64) e = exps[i] > e ? exps[i] : e;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_xor(e, d);
+        e = o > e ? o : e;
+    }
+    return e;
+}
+__device__ __forceinline__ float slot_weight(int e, int top) {
+    const int d = 2 * (e - top);
+    return d < -126 ? 0.f : __builtin_ldexpf(1.f, d);
+}
+
+// sum[j] = sum over the slots of 2^(2 (e - top)) part[slot][j], four floats a
+// thread; 8 threads share an element's slots and add up in thread order
+__global__ __launch_bounds__(256) void ns_sum_kernel(const float* part, const int* exps, int slots, int quads, float* sum,
+                                                     int* top_out) {
+    __shared__ __attribute__((aligned(16))) f32x4 red[8][32];
+    const int tid = threadIdx.x, e = tid & 31, h = tid >> 5;
+    const int top = top_exponent(exps, slots);
+    const int at = (int)blockIdx.x * 32 + e;
+    f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (at < quads)
+        for (int k = h; k < slots; k += 8) s += *(const f32x4*)(part + ((int64_t)k * quads + at) * 4) * slot_weight(exps[k], top);
+    red[h][e] = s;
+    __syncthreads();
+    if (h == 0 && at < quads) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) s += red[k][e];
+        *(f32x4*)(sum + (int64_t)at * 4) = s;
+        if (blockIdx.x == 0 && tid == 0) *top_out = top;
+    }
+}
+
+struct IterParams {
+    const float* part;   // [slots][NPAD][NPAD]; one slot: the sum, its exponent in exps[0]
+    const int* exps;
+    int slots, steps, first;
+    float a, b, c;
+    double eps;
+    float sA[NS_SEG], sP[NS_SEG], sT[NS_SEG], sQ[NS_SEG];   // powers of two that keep each matrix inside fp16
+    uint16_t* q;         // pieces [NP][NPAD][KR]
+    double* fac;
+};
+
+// One workgroup: the Gram matrix, then `steps` steps on it; Q out as pieces.
+// Masters in registers (MFMA layout), operands as pieces in LDS: all matrices
+// are symmetric, so each serves as either operand row by row.
+template <int NPAD, int NP>
+__global__ __launch_bounds__(NPAD >= 64 ? 1024 : NPAD == 32 ? 256 : 64) void ns_iter_kernel(IterParams p) {
+    constexpr int NT = NPAD >= 64 ? 1024 : NPAD == 32 ? 256 : 64, IB = NPAD / 16;
+    constexpr int TW = NPAD == 128 ? 2 : 1;   // tiles per wave along each side
+    constexpr int WB = IB / TW;               // waves along a side
+    constexpr int KR = ThinShape<NPAD>::KR, LD = KR + 8, KS = KR / 32;
+    constexpr int BUFS = NP == 2 ? 2 : 1;
+    __shared__ __attribute__((aligned(16))) uint16_t buf[BUFS][NP][NPAD * LD];
+    __shared__ float diag[NPAD];
+    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
+    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int wi = wave % WB, wj = wave / WB;
+    typedef f32x4 M[TW][TW];
+    auto row_of = [&](int ti) { return (wi * TW + ti) * 16 + 4 * g; };   // first of 4 rows
+    auto col_of = [&](int tj) { return (wj * TW + tj) * 16 + r; };
+
+    // zero the columns an MFMA step reads past NPAD
+    if constexpr (KR > NPAD) {
+        for (int i = tid; i < BUFS * NP * NPAD * LD; i += NT) ((uint16_t*)buf)[i] = 0;
+        __syncthreads();
+    }
+    const int top = top_exponent(p.exps, p.slots);
+    M A, Q;
+#pragma unroll
+    for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+        for (int tj = 0; tj < TW; ++tj) {
+            f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 16
+            for (int k = 0; k < p.slots; ++k)
+                s += *(const f32x4*)(p.part + ((int64_t)k * NPAD + col_of(tj)) * NPAD + row_of(ti)) *
+                     slot_weight(p.exps[k], top);
+            A[ti][tj] = s;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if (row_of(ti) + e == col_of(tj)) diag[col_of(tj)] = s[e];
+        }
+    // A's true size: 2^(2 top) A; the first segment divides by (|G| + eps)^2
+    double inv = 1.0;
+    if (p.first) {
+        __syncthreads();
+        double tr = 0;
+        for (int i = lane; i < NPAD; i += 64) tr += (double)diag[i];
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) tr += __shfl_xor(tr, d);
+        const double norm = top == NS_EMPTY ? 0.0 : __builtin_ldexp(__builtin_sqrt(tr), top);
+        inv = 1.0 / (norm + p.eps);
+    }
+    const double half = top == NS_EMPTY ? 0.0 : __builtin_ldexp(inv, top);
+    const float fA = (float)(half * half);
+#pragma unroll
+    for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+        for (int tj = 0; tj < TW; ++tj) A[ti][tj] *= fA;
+
+    auto put = [&](int b, const M& m, float scale) {
+#pragma unroll
+        for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TW; ++tj) {
+                uint16_t o[4][NP];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) Pieces<NP>::split(m[ti][tj][e] * scale, o[e]);
+#pragma unroll
+                for (int k = 0; k < NP; ++k)
+                    *(i32x2*)&buf[b][k][col_of(tj) * LD + row_of(ti)] =
+                        i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16),
+                              (int)((uint32_t)o[2][k] | (uint32_t)o[3][k] << 16)};
+            }
+    };
+    auto product = [&](int bu, int bv, float scale, M& out) {
+#pragma unroll
+        for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TW; ++tj) out[ti][tj] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            i32x4 u[TW][NP], v[TW][NP];
+#pragma unroll
+            for (int t = 0; t < TW; ++t)
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    u[t][k] = *(const i32x4*)&buf[bu][k][((wi * TW + t) * 16 + r) * LD + s * 32 + g * 8];
+                    v[t][k] = *(const i32x4*)&buf[bv][k][((wj * TW + t) * 16 + r) * LD + s * 32 + g * 8];
+                }
+#pragma unroll
+            for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+                for (int tj = 0; tj < TW; ++tj) out[ti][tj] = piece_step<NP>(u[ti], v[tj], out[ti][tj]);
+        }
+#pragma unroll
+        for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TW; ++tj) out[ti][tj] *= scale;
+    };
+
+    for (int k = 0; k < p.steps; ++k) {
+        M P;
+        put(0, A, p.sA[k]);
+        __syncthreads();
+        product(0, 0, 1.f / (p.sA[k] * p.sA[k]), P);
+#pragma unroll
+        for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TW; ++tj)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    float v = p.c * P[ti][tj][e] + p.b * A[ti][tj][e];
+                    if (row_of(ti) + e == col_of(tj)) v += p.a;
+                    P[ti][tj][e] = v;
+                }
+        const bool more = k + 1 < p.steps;
+        if constexpr (NP == 2) {
+            if (k > 0 || more) {
+                put(1, P, p.sP[k]);
+                __syncthreads();
+            }
+            if (more) product(0, 1, 1.f / (p.sA[k] * p.sP[k]), A);   // T = A P
+            if (k > 0) {
+                __syncthreads();   // buffer 0 has been read
+                put(0, Q, p.sQ[k - 1]);
+                __syncthreads();
+                product(0, 1, 1.f / (p.sQ[k - 1] * p.sP[k]), Q);
+            }
+            if (more) {
+                __syncthreads();
+                put(0, A, p.sT[k]);
+                __syncthreads();
+                M T;
+                product(0, 1, 1.f / (p.sT[k] * p.sP[k]), T);   // P A P
+#pragma unroll
+                for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+                    for (int tj = 0; tj < TW; ++tj) A[ti][tj] = T[ti][tj];
+                __syncthreads();
+            }
+        }
+        if (k == 0) {
+#pragma unroll
+            for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+                for (int tj = 0; tj < TW; ++tj) Q[ti][tj] = P[ti][tj];
+        }
+    }
+    const float sq = p.sQ[p.steps - 1];
+#pragma unroll
+    for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+        for (int tj = 0; tj < TW; ++tj) {
+            uint16_t o[4][NP];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) Pieces<NP>::split(Q[ti][tj][e] * sq, o[e]);
+#pragma unroll
+            for (int k = 0; k < NP; ++k)
+                *(i32x2*)(p.q + ((int64_t)k * NPAD + col_of(tj)) * KR + row_of(ti)) =
+                    i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16),
+                          (int)((uint32_t)o[2][k] | (uint32_t)o[3][k] << 16)};
+        }
+    if constexpr (KR > NPAD) {
+        for (int i = tid; i < NP * NPAD * (KR - NPAD); i += NT)
+            p.q[(i / (KR - NPAD)) * KR + NPAD + i % (KR - NPAD)] = 0;
+    }
+    if (tid == 0) *p.fac = inv / (double)sq;
+}
+
 // ---- host ----------------------------------------------------------------------------------
 
 static int64_t up8(int64_t v) { return (v + 7) & ~(int64_t)7; }
@@ -342,6 +829,29 @@ static void ns_plan(int64_t I, int64_t J, int64_t K, int* tile, int* ksplit) {
     ks = std::min<int64_t>(ks, steps / 4);
     ks = std::min<int64_t>(ks, 64);
     *ksplit = ks > 1 ? (int)ks : 1;
+}
+
+// powers of two that keep a matrix of the given spectral norm inside fp16
+// (elements are at most the norm)
+static double pow2_under(double bound) {
+    return std::ldexp(1.0, std::max(-100, std::min(15, (int)std::floor(15.0 - std::log2(std::max(bound, 1e-30))))));
+}
+// [0, top] -> the next A's largest eigenvalue, max |p| and max |l p| there
+static void poly_bounds(const OrthoParams& p, double top, double* next, double* pmax, double* tmax) {
+    *next = *pmax = *tmax = 0.0;
+    for (int i = 0; i <= 512; ++i) {
+        const double l = top * i / 512.0, q = p.a + l * (p.b + l * p.c);
+        *pmax = std::max(*pmax, std::fabs(q));
+        *tmax = std::max(*tmax, std::fabs(l * q));
+        *next = std::max(*next, l * q * q);
+    }
+    // between the sampled points, and the products' rounding
+    *next *= 1.02;
+    *pmax *= 1.02;
+    *tmax *= 1.02;
+    if (!(*next < 1e30)) *next = 1e30;
+    if (!(*pmax < 1e30)) *pmax = 1e30;
+    if (!(*tmax < 1e30)) *tmax = 1e30;
 }
 
 struct NsLayout {
@@ -373,7 +883,6 @@ static NsLayout ns_layout(int64_t R, int64_t C, int dt) {
     L.total = off;
     return L;
 }
-size_t ortho_workspace(int64_t R, int64_t C, int dt) { return R > 0 && C > 0 ? ns_layout(R, C, dt).total : 0; }
 
 template <int NP, bool TR>
 static hipError_t ns_product(NsParams p, hipStream_t s) {
@@ -404,31 +913,18 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
     A = Planes{(uint16_t*)(W + L.A), L.ldn, n * L.ldn};
     P = Planes{(uint16_t*)(W + L.P), L.ldn, n * L.ldn};
 
-    // power-of-two scales that keep every element inside fp16: elements are at
-    // most the spectral norm, which the scalar map s -> s p(s^2) bounds
-    // (A's eigenvalues lie in [0, top])
-    double top = 1.0, sx = 1.0, pmax = 0.0;
-    double topx = 1.0;
+    // power-of-two scales that keep every element inside fp16
+    double top = 1.0, topx = 1.0, pmax = 0.0, next, pm, tm, sx = 1.0, sa = 1.0, sp = 1.0;
     for (int k = 0; k < p.steps; ++k) {
-        double next = 0.0;
-        for (int i = 0; i <= 512; ++i) {
-            const double l = top * i / 512.0, q = p.a + l * (p.b + l * p.c);
-            pmax = std::max(pmax, std::fabs(q));
-            next = std::max(next, l * q * q);
-        }
-        next *= 1.02;   // between the sampled points, and the products' rounding
-        if (!(next < 1e30)) next = 1e30;
+        poly_bounds(p, top, &next, &pm, &tm);
+        pmax = std::max(pmax, pm);
         top = next;
         topx = std::max(topx, top);
     }
-    auto pow2_under = [](double bound) {   // the largest power of two with scale * bound <= 2^15
-        return std::ldexp(1.0, std::min(15, (int)std::floor(15.0 - std::log2(std::max(bound, 1e-30)))));
-    };
-    double sa = 1.0, sp = 1.0;
     if (NP == 2) {
         sx = pow2_under(std::sqrt(topx));
         sa = pow2_under(topx);
-        sp = pow2_under(std::max(pmax, 1e-30));
+        sp = pow2_under(pmax);
     }
 
     hipLaunchKernelGGL(ns_norm_kernel, dim3(NORM_WGS), dim3(256), 0, s, p.g, p.dt, p.R * p.C, part);
@@ -488,9 +984,133 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
     return hipSuccess;
 }
 
+struct ThinLayout {
+    size_t part, exps, sum, top, q, fac, x, total;
+    int64_t npad, kr, ldx;
+    int wgs;
+};
+static ThinLayout thin_layout(int64_t R, int64_t C, int dt) {
+    const size_t np = dt == DT_F32 ? 3 : 2;
+    const int64_t n = std::min(R, C), m = std::max(R, C);
+    ThinLayout L{};
+    L.npad = n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
+    L.kr = std::max<int64_t>(L.npad, 32);
+    const int64_t cw = L.npad == 16 ? 256 : L.npad == 32 ? 128 : 64;
+    const int64_t chunks = (m + cw - 1) / cw;
+    L.ldx = chunks * cw;
+    // (few enough Gram matrices that adding them up stays short)
+    L.wgs = (int)std::min<int64_t>(chunks, L.npad <= 32 ? 32 : 64);
+    size_t off = 0;
+    auto take = [&](size_t& at, size_t bytes) { at = off; off = up256(off + bytes); };
+    take(L.part, (size_t)L.wgs * (size_t)(L.npad * L.npad) * 4);
+    take(L.exps, (size_t)L.wgs * 4);
+    take(L.sum, (size_t)(L.npad * L.npad) * 4);
+    take(L.top, 4);
+    take(L.q, np * (size_t)(L.npad * L.kr) * 2);
+    take(L.fac, 8);
+    take(L.x, (size_t)(n * L.ldx) * 4);
+    L.total = off;
+    return L;
+}
+
+template <int NPAD, int NP>
+static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
+    using S = ThinShape<NPAD>;
+    const ThinLayout L = thin_layout(p.R, p.C, p.dt);
+    char* W = p.ws;
+    ThinParams t{};
+    t.g = p.g;
+    t.tall = p.R > p.C;
+    t.src = t.tall ? 1 : 0;
+    t.dt = p.dt;
+    t.n = std::min(p.R, p.C);
+    t.m = std::max(p.R, p.C);
+    t.ldx = L.ldx;
+    t.x = (float*)(W + L.x);
+    t.q = (const uint16_t*)(W + L.q);
+    t.fac = (const double*)(W + L.fac);
+    t.part = (float*)(W + L.part);
+    t.exps = (int*)(W + L.exps);
+    t.out = p.out;
+    double topx = 1.0, top = 1.0, next, pm, tm;
+    for (int k = 0; k < p.steps; ++k) {
+        poly_bounds(p, top, &next, &pm, &tm);
+        top = next;
+        topx = std::max(topx, top);
+    }
+    // (bf16 pieces have fp32's range)
+    t.sx = NP == 2 ? (float)pow2_under(std::sqrt(topx)) : 1.0f;
+    const int seg = NP == 2 ? NS_SEG : 1, segs = (p.steps + seg - 1) / seg;
+    const int64_t chunks = L.ldx / S::CW;
+    hipLaunchKernelGGL((ns_chunk_kernel<NPAD, NP, THIN_GRAM>), dim3(L.wgs), dim3(S::NT), 0, s, t);
+    hipError_t e = hipGetLastError();
+    top = 1.0;
+    int done = 0;
+    for (int k = 0; k < segs && e == hipSuccess; ++k) {
+        IterParams q{};
+        q.part = t.part;
+        q.exps = t.exps;
+        q.slots = L.wgs;
+        if (NPAD > 32) {
+            const int quads = NPAD * NPAD / 4;
+            hipLaunchKernelGGL(ns_sum_kernel, dim3((quads + 31) / 32), dim3(256), 0, s, t.part, t.exps, L.wgs, quads,
+                               (float*)(W + L.sum), (int*)(W + L.top));
+            if ((e = hipGetLastError()) != hipSuccess) break;
+            q.part = (const float*)(W + L.sum);
+            q.exps = (const int*)(W + L.top);
+            q.slots = 1;
+        }
+        q.steps = (p.steps - done + (segs - k) - 1) / (segs - k);
+        done += q.steps;
+        q.first = k == 0;
+        q.a = (float)p.a;
+        q.b = (float)p.b;
+        q.c = (float)p.c;
+        q.eps = p.eps;
+        double qmax = 1.0;
+        for (int i = 0; i < q.steps; ++i) {
+            poly_bounds(p, top, &next, &pm, &tm);
+            qmax *= pm;
+            q.sA[i] = NP == 2 ? (float)pow2_under(top) : 1.0f;
+            q.sP[i] = NP == 2 ? (float)pow2_under(pm) : 1.0f;
+            q.sT[i] = NP == 2 ? (float)pow2_under(tm) : 1.0f;
+            q.sQ[i] = NP == 2 ? (float)pow2_under(qmax) : 1.0f;
+            top = next;
+        }
+        q.q = (uint16_t*)(W + L.q);
+        q.fac = (double*)(W + L.fac);
+        hipLaunchKernelGGL((ns_iter_kernel<NPAD, NP>), dim3(1), dim3(NPAD >= 64 ? 1024 : NPAD == 32 ? 256 : 64), 0, s, q);
+        if ((e = hipGetLastError()) != hipSuccess) break;
+        if (k + 1 < segs) {
+            hipLaunchKernelGGL((ns_chunk_kernel<NPAD, NP, THIN_BOTH>), dim3(L.wgs), dim3(S::NT), 0, s, t);
+        } else {
+            hipLaunchKernelGGL((ns_chunk_kernel<NPAD, NP, THIN_OUT>), dim3((unsigned)std::min<int64_t>(chunks, 1024)),
+                               dim3(S::NT), 0, s, t);
+        }
+        e = hipGetLastError();
+        t.src = 2;
+    }
+    return e;
+}
+
+template <int NP>
+static hipError_t ns_run(const OrthoParams& p, hipStream_t s) {
+    const int64_t n = std::min(p.R, p.C);
+    if (n <= 16) return ns_thin<16, NP>(p, s);
+    if (n <= 32) return ns_thin<32, NP>(p, s);
+    if (n <= 64) return ns_thin<64, NP>(p, s);
+    if (n <= NS_THIN) return ns_thin<128, NP>(p, s);
+    return ns_direct<NP>(p, s);
+}
+
+size_t ortho_workspace(int64_t R, int64_t C, int dt) {
+    if (R <= 0 || C <= 0) return 0;
+    return std::min(R, C) <= NS_THIN ? thin_layout(R, C, dt).total : ns_layout(R, C, dt).total;
+}
+
 hipError_t launch_ortho(const OrthoParams& p, hipStream_t s) {
     if (p.R <= 0 || p.C <= 0) return hipSuccess;
-    return p.dt == DT_F32 ? ns_direct<3>(p, s) : ns_direct<2>(p, s);
+    return p.dt == DT_F32 ? ns_run<3>(p, s) : ns_run<2>(p, s);
 }
 
 }  // namespace lyc
