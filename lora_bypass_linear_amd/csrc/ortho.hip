@@ -361,6 +361,7 @@ struct ThinShape {
 struct ThinParams {
     const void* g;      // raw source [R][C] (src 0: wide, 1: tall)
     int src, dt;        // 2: x, fp32 [n][ldx]
+    int vec;            // 8-element runs of the source are whole and 16-byte aligned
     int64_t n, m, ldx;
     float* x;
     const uint16_t* q;  // pieces [NP][NPAD][KR], scaled
@@ -433,29 +434,57 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
     const int64_t chunks = (p.m + CW - 1) / CW;
     for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
         const int64_t c0 = ch * CW;
-        // the chunk, 16 elements a thread, consecutive threads along the stored rows
+        // the chunk, 16 elements a thread: two runs of 8 along the stored rows
+        // where those are whole 16-byte pieces (vec), else single elements
         float v[S::PT];
-        int at[S::PT];
-        uint32_t raw[S::PT];
+        int row0[2], col0[2];   // of the runs
 #pragma unroll
-        for (int u = 0; u < S::PT; ++u) {
-            const int idx = tid + u * S::NT;
-            const int row = p.src == 1 ? idx % NPAD : idx / CW, col = p.src == 1 ? idx / NPAD : idx % CW;
-            at[u] = row * LD + col;
-            const bool in = row < p.n && c0 + col < p.m;
-            const int64_t e = p.src == 1 ? (c0 + col) * p.n + row : row * (p.src == 2 ? p.ldx : p.m) + c0 + col;
-            raw[u] = 0;
-            if (in) {
-                if (p.src == 2) raw[u] = ((const uint32_t*)p.x)[e];
-                else if (p.dt == DT_F32) raw[u] = ((const uint32_t*)p.g)[e];
-                else raw[u] = ((const uint16_t*)p.g)[e];
+        for (int h = 0; h < 2; ++h) {
+            const int t8 = tid + h * S::NT;
+            row0[h] = p.src == 1 ? t8 % (NPAD / 8) * 8 : t8 / (CW / 8);
+            col0[h] = p.src == 1 ? t8 / (NPAD / 8) : t8 % (CW / 8) * 8;
+        }
+        const bool f32 = p.src == 2 || p.dt == DT_F32;
+        const auto rs = make_rsrc(p.src == 2 ? (const void*)p.x : p.g,
+                                  (uint32_t)(p.src == 2 ? p.n * p.ldx * 4 : p.n * p.m * (f32 ? 4 : 2)));
+        const uint32_t ld = (uint32_t)(p.src == 1 ? p.n : p.src == 2 ? p.ldx : p.m);
+        // byte offset of an element, out of range where there is none
+        auto offset = [&](int row, int col) -> uint32_t {
+            if (row >= p.n || c0 + col >= p.m) return OOB;
+            return (p.src == 1 ? (uint32_t)(c0 + col) * ld + (uint32_t)row : (uint32_t)row * ld + (uint32_t)(c0 + col)) *
+                   (f32 ? 4u : 2u);
+        };
+        auto widen = [&](uint32_t b) { return p.dt == DT_F16 ? f16_to_f32((uint16_t)b) : bf16_to_f32((uint16_t)b); };
+        if (p.vec) {
+            i32x4 raw[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const uint32_t o = offset(row0[h], col0[h]);
+                raw[h][0] = buf_load16(rs, o);
+                raw[h][1] = buf_load16(rs, f32 ? o + 16 : OOB);
             }
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int u = 0; u < 8; ++u) {
+                    const uint32_t w = (uint32_t)raw[h][0][u >> 1];
+                    const float half = widen((u & 1) ? w >> 16 : w);
+                    v[8 * h + u] = f32 ? __builtin_bit_cast(float, (uint32_t)raw[h][u >> 2][u & 3]) : half;
+                }
+        } else {
+            uint32_t raw[S::PT];
+#pragma unroll
+            for (int u = 0; u < S::PT; ++u) {
+                const uint32_t o = offset(row0[u >> 3] + (p.src == 1 ? u & 7 : 0), col0[u >> 3] + (p.src == 1 ? 0 : u & 7));
+                raw[u] = f32 ? (uint32_t)__builtin_amdgcn_raw_buffer_load_b32(rs, o, 0, 0)
+                             : (uint32_t)(uint16_t)__builtin_amdgcn_raw_buffer_load_b16(rs, o, 0, 0);
+            }
+#pragma unroll
+            for (int u = 0; u < S::PT; ++u) v[u] = f32 ? __builtin_bit_cast(float, raw[u]) : widen(raw[u]);
         }
         uint32_t mx = 0;
 #pragma unroll
         for (int u = 0; u < S::PT; ++u) {
-            if (p.src == 2 || p.dt == DT_F32) v[u] = __builtin_bit_cast(float, raw[u]);
-            else v[u] = p.dt == DT_F16 ? f16_to_f32((uint16_t)raw[u]) : bf16_to_f32((uint16_t)raw[u]);
             const uint32_t b = __builtin_bit_cast(uint32_t, v[u]) & 0x7FFFFFFFu;
             mx = b > mx ? b : mx;
         }
@@ -496,12 +525,27 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
             }
         }
         __syncthreads();   // the previous chunk's tile has been read
+        {
+            // 2^-e in two factors (e reaches past fp32's exponents)
+            const float f1 = __builtin_ldexpf(1.f, -(e / 2)), f2 = __builtin_ldexpf(1.f, -(e - e / 2));
 #pragma unroll
-        for (int u = 0; u < S::PT; ++u) {
-            uint16_t o[NP];
-            Pieces<NP>::split(__builtin_ldexpf(v[u], -e), o);
+            for (int h = 0; h < 2; ++h) {
+                uint16_t o[8][NP];
 #pragma unroll
-            for (int k = 0; k < NP; ++k) xs[k][at[u]] = o[k];
+                for (int u = 0; u < 8; ++u) Pieces<NP>::split(v[8 * h + u] * f1 * f2, o[u]);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    if (p.src == 1) {
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) xs[k][(row0[h] + u) * LD + col0[h]] = o[u][k];
+                    } else {
+                        i32x4 w;
+#pragma unroll
+                        for (int u = 0; u < 4; ++u) w[u] = (int)((uint32_t)o[2 * u][k] | (uint32_t)o[2 * u + 1][k] << 16);
+                        *(i32x4*)&xs[k][row0[h] * LD + col0[h]] = w;
+                    }
+                }
+            }
         }
         __syncthreads();
 
@@ -1040,6 +1084,7 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
     }
     // (bf16 pieces have fp32's range)
     t.sx = NP == 2 ? (float)pow2_under(std::sqrt(topx)) : 1.0f;
+    t.vec = (t.tall ? t.n : t.m) % 8 == 0 && ((uintptr_t)p.g & 15) == 0;
     const int seg = NP == 2 ? NS_SEG : 1, segs = (p.steps + seg - 1) / seg;
     const int64_t chunks = L.ldx / S::CW;
     hipLaunchKernelGGL((ns_chunk_kernel<NPAD, NP, THIN_GRAM>), dim3(L.wgs), dim3(S::NT), 0, s, t);
@@ -1089,6 +1134,7 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
         }
         e = hipGetLastError();
         t.src = 2;
+        t.vec = 1;
     }
     return e;
 }
