@@ -337,9 +337,11 @@ __global__ __launch_bounds__(256) void ns_reduce_kernel(NsParams p) {
 // near 1e-5 of the result, a hundredth of a 16-bit rounding; all 5 steps in
 // one segment measured 1e-4 and more), and one step with three.
 //   ns_chunk_kernel  Gram matrix of X / X <- Q X with it / the last X <- Q X
-//   ns_sum_kernel    the workgroups' Gram matrices added up (n > 32)
-//   ns_iter_kernel   a segment of steps; the first one scales by 1 / (|G| + eps),
+//   Iter             a segment of steps; the first one scales by 1 / (|G| + eps),
 //                    |G|^2 being the trace
+//                    (a kernel of its own: run by the last workgroup of the one
+//                    before, behind a device-wide fence, it took 2 us more)
+//   ns_sum_kernel    the workgroups' Gram matrices added up (n > 32)
 
 constexpr int NS_SEG = 3;
 constexpr int NS_THIN = 128;
@@ -400,6 +402,257 @@ __device__ __forceinline__ f32x4 piece_step(const i32x4 (&a)[NP], const i32x4 (&
     return c;
 }
 
+struct IterParams {
+    const float* part;   // Gram matrices [slots][NPAD][NPAD], standing for 2^(2 e) times their values
+    const int* exps;     // e of each
+    int slots, steps, first;
+    float a, b, c;
+    double eps;
+    float sA[NS_SEG], sP[NS_SEG], sT[NS_SEG], sQ[NS_SEG];   // powers of two that keep each matrix inside fp16
+    uint16_t* q;         // pieces [NP][NPAD][KR]
+    double* fac;
+};
+
+// the largest of the slots' exponents
+__device__ __forceinline__ int top_exponent(const int* exps, int slots) {
+    int e = NS_EMPTY;
+    for (int i = threadIdx.x & 63; i < slots; i += 64) e = exps[i] > e ? exps[i] : e;
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) {
+        const int o = __shfl_xor(e, d);
+        e = o > e ? o : e;
+    }
+    return e;
+}
+__device__ __forceinline__ float slot_weight(int e, int top) {
+    const int d = 2 * (e - top);
+    return d < -126 ? 0.f : __builtin_ldexpf(1.f, d);
+}
+
+// A segment on the n x n side, by one workgroup: waves WB (WB + 1) / 2 hold the
+// blocks on and below the diagonal (every matrix is symmetric), masters in
+// registers in MFMA layout; operands go to LDS whole, as pieces, a block and
+// its mirror image, and serve as either operand row by row.
+constexpr int iter_threads(int npad) { return npad == 16 ? 64 : npad == 32 ? 192 : 640; }
+
+template <int NPAD, int NP>
+struct Iter {
+    static constexpr int IB = NPAD / 16;
+    static constexpr int TW = NPAD == 128 ? 2 : 1;   // tiles per wave along each side
+    static constexpr int WB = IB / TW, WAVES = WB * (WB + 1) / 2;
+    static_assert(WAVES * 64 == iter_threads(NPAD), "launch");
+    static constexpr int KR = NPAD < 32 ? 32 : NPAD, LD = KR + 8, KS = KR / 32;
+    static constexpr int BUFS = NP == 2 ? 2 : 1;
+    static constexpr int LDS = BUFS * NP * NPAD * LD * 2;   // bytes
+    typedef f32x4 M[TW][TW];
+
+    uint16_t* buf;   // [BUFS][NP][NPAD * LD]
+    int lane, g, r, wi, wj;
+
+    __device__ __forceinline__ int row_of(int ti) const { return (wi * TW + ti) * 16 + 4 * g; }   // first of 4 rows
+    __device__ __forceinline__ int col_of(int tj) const { return (wj * TW + tj) * 16 + r; }
+    __device__ __forceinline__ uint16_t* at(int b, int k) const { return buf + (b * NP + k) * NPAD * LD; }
+
+    __device__ __forceinline__ void put(int b, const M& m, float scale) const {
+#pragma unroll
+        for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TW; ++tj) {
+                uint16_t o[4][NP];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) Pieces<NP>::split(m[ti][tj][e] * scale, o[e]);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    *(i32x2*)(at(b, k) + col_of(tj) * LD + row_of(ti)) =
+                        i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16),
+                              (int)((uint32_t)o[2][k] | (uint32_t)o[3][k] << 16)};
+                    if (wi != wj) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) at(b, k)[(row_of(ti) + e) * LD + col_of(tj)] = o[e][k];
+                    }
+                }
+            }
+    }
+    __device__ __forceinline__ void product(int bu, int bv, float scale, M& out) const {
+#pragma unroll
+        for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TW; ++tj) out[ti][tj] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int s = 0; s < KS; ++s) {
+            i32x4 u[TW][NP], v[TW][NP];
+#pragma unroll
+            for (int t = 0; t < TW; ++t)
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    u[t][k] = *(const i32x4*)(at(bu, k) + ((wi * TW + t) * 16 + r) * LD + s * 32 + g * 8);
+                    v[t][k] = *(const i32x4*)(at(bv, k) + ((wj * TW + t) * 16 + r) * LD + s * 32 + g * 8);
+                }
+#pragma unroll
+            for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+                for (int tj = 0; tj < TW; ++tj) out[ti][tj] = piece_step<NP>(u[ti], v[tj], out[ti][tj]);
+        }
+#pragma unroll
+        for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TW; ++tj) out[ti][tj] *= scale;
+    }
+
+    // all of the workgroup's WAVES * 64 threads
+    __device__ void run(const IterParams& p, char* lds, float* diag) {
+        constexpr int nt = WAVES * 64;
+        const int tid = threadIdx.x;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        lane = tid & 63;
+        g = lane >> 4;
+        r = lane & 15;
+        buf = (uint16_t*)lds;
+        wi = 0;
+        while ((wi + 1) * (wi + 2) / 2 <= wave) ++wi;
+        wj = wave - wi * (wi + 1) / 2;
+        // zero the columns an MFMA step reads past NPAD
+        if constexpr (KR > NPAD) {
+            for (int i = tid; i < BUFS * NP * NPAD * LD; i += nt) buf[i] = 0;
+            __syncthreads();
+        }
+        const int top = top_exponent(p.exps, p.slots);
+        M A, Q;
+#pragma unroll
+        for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TW; ++tj) {
+                const int64_t o = (int64_t)col_of(tj) * NPAD + row_of(ti);
+                f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 16
+                for (int k = 0; k < p.slots; ++k)
+                    s += *(const f32x4*)(p.part + (int64_t)k * NPAD * NPAD + o) * slot_weight(p.exps[k], top);
+                A[ti][tj] = s;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (row_of(ti) + e == col_of(tj)) diag[col_of(tj)] = s[e];
+            }
+        // A's true size is 2^(2 top) times its values; the first segment divides by (|G| + eps)^2
+        double inv = 1.0;
+        if (p.first) {
+            __syncthreads();
+            double tr = 0;
+            for (int i = lane; i < NPAD; i += 64) tr += (double)diag[i];
+#pragma unroll
+            for (int d = 1; d < 64; d <<= 1) tr += __shfl_xor(tr, d);
+            const double norm = top == NS_EMPTY ? 0.0 : __builtin_ldexp(__builtin_sqrt(tr), top);
+            inv = 1.0 / (norm + p.eps);
+        }
+        const double half = top == NS_EMPTY ? 0.0 : __builtin_ldexp(inv, top);
+        const float fA = (float)(half * half);
+#pragma unroll
+        for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TW; ++tj) A[ti][tj] *= fA;
+
+        for (int k = 0; k < p.steps; ++k) {
+            M P;
+            put(0, A, p.sA[k]);
+            __syncthreads();
+            product(0, 0, 1.f / (p.sA[k] * p.sA[k]), P);
+#pragma unroll
+            for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+                for (int tj = 0; tj < TW; ++tj)
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        float v = p.c * P[ti][tj][e] + p.b * A[ti][tj][e];
+                        if (row_of(ti) + e == col_of(tj)) v += p.a;
+                        P[ti][tj][e] = v;
+                    }
+            const bool more = k + 1 < p.steps;
+            if constexpr (NP == 2) {
+                if (k > 0 || more) {
+                    put(1, P, p.sP[k]);
+                    __syncthreads();
+                }
+                if (more) product(0, 1, 1.f / (p.sA[k] * p.sP[k]), A);   // T = A P
+                if (k > 0) {
+                    __syncthreads();   // buffer 0 has been read
+                    put(0, Q, p.sQ[k - 1]);
+                    __syncthreads();
+                    product(0, 1, 1.f / (p.sQ[k - 1] * p.sP[k]), Q);
+                }
+                if (more) {
+                    __syncthreads();
+                    put(0, A, p.sT[k]);
+                    __syncthreads();
+                    product(0, 1, 1.f / (p.sT[k] * p.sP[k]), A);   // P A P
+                    __syncthreads();
+                }
+            }
+            if (k == 0) {
+#pragma unroll
+                for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+                    for (int tj = 0; tj < TW; ++tj) Q[ti][tj] = P[ti][tj];
+            }
+        }
+        const float sq = p.sQ[p.steps - 1];
+#pragma unroll
+        for (int ti = 0; ti < TW; ++ti)
+#pragma unroll
+            for (int tj = 0; tj < TW; ++tj) {
+                uint16_t o[4][NP];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) Pieces<NP>::split(Q[ti][tj][e] * sq, o[e]);
+#pragma unroll
+                for (int k = 0; k < NP; ++k) {
+                    uint16_t* q = p.q + (int64_t)k * NPAD * KR;
+                    *(i32x2*)(q + col_of(tj) * KR + row_of(ti)) =
+                        i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16),
+                              (int)((uint32_t)o[2][k] | (uint32_t)o[3][k] << 16)};
+                    if (wi != wj) {
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) q[(row_of(ti) + e) * KR + col_of(tj)] = o[e][k];
+                    }
+                }
+            }
+        if constexpr (KR > NPAD) {
+            for (int i = tid; i < NP * NPAD * (KR - NPAD); i += nt)
+                p.q[(i / (KR - NPAD)) * KR + NPAD + i % (KR - NPAD)] = 0;
+        }
+        if (tid == 0) *p.fac = inv / (double)sq;
+    }
+};
+
+// sum = the Gram matrices added up at the largest exponent, four floats a
+// thread; 8 threads share an element's slots, added in thread order
+__global__ __launch_bounds__(256) void ns_sum_kernel(const float* part, const int* exps, int slots, int quads, float* sum,
+                                                     int* top_out) {
+    __shared__ __attribute__((aligned(16))) f32x4 red[8][32];
+    const int tid = threadIdx.x, e = tid & 31, h = tid >> 5;
+    const int top = top_exponent(exps, slots);
+    const int at = (int)blockIdx.x * 32 + e;
+    f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+    if (at < quads) {
+#pragma unroll 8
+        for (int k = h; k < slots; k += 8) s += *(const f32x4*)(part + ((int64_t)k * quads + at) * 4) * slot_weight(exps[k], top);
+    }
+    red[h][e] = s;
+    __syncthreads();
+    if (h == 0 && at < quads) {
+#pragma unroll
+        for (int k = 1; k < 8; ++k) s += red[k][e];
+        *(f32x4*)(sum + (int64_t)at * 4) = s;
+        if (blockIdx.x == 0 && tid == 0) *top_out = top;
+    }
+}
+
+template <int NPAD, int NP>
+__global__ __launch_bounds__(iter_threads(NPAD)) void ns_iter_kernel(IterParams p) {
+    using I = Iter<NPAD, NP>;
+    __shared__ __attribute__((aligned(16))) char lds[I::LDS];
+    __shared__ float diag[NPAD];
+    I it;
+    it.run(p, lds, diag);
+}
+
 enum { THIN_GRAM = 0, THIN_BOTH = 1, THIN_OUT = 2 };
 
 template <int NPAD, int NP, int MODE>
@@ -441,8 +694,10 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int t8 = tid + h * S::NT;
-            row0[h] = p.src == 1 ? t8 % (NPAD / 8) * 8 : t8 / (CW / 8);
-            col0[h] = p.src == 1 ? t8 / (NPAD / 8) : t8 % (CW / 8) * 8;
+            // (tall: 16 consecutive stored rows a group of lanes, so that the
+            // transposed LDS writes fall on few common banks)
+            row0[h] = p.src == 1 ? (t8 >> 4) % (NPAD / 8) * 8 : t8 / (CW / 8);
+            col0[h] = p.src == 1 ? t8 / (2 * NPAD) * 16 + (t8 & 15) : t8 % (CW / 8) * 8;
         }
         const bool f32 = p.src == 2 || p.dt == DT_F32;
         const auto rs = make_rsrc(p.src == 2 ? (const void*)p.x : p.g,
@@ -627,232 +882,16 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
             gacc[0] = red[lane];
 #pragma unroll
             for (int w = 1; w < S::NW; ++w) gacc[0] += red[w * 64 + lane];
-            if (wave != 0) return;
         }
         const int gi = S::KSPLIT ? 0 : wave % S::IB;
 #pragma unroll
         for (int t = 0; t < S::GT; ++t) {
             const int gj = S::KSPLIT ? 0 : wave / S::IB * S::GT + t;
-            *(f32x4*)(p.part + ((int64_t)blockIdx.x * NPAD + gj * 16 + r) * NPAD + gi * 16 + 4 * g) = gacc[t];
+            if (!S::KSPLIT || wave == 0)
+                *(f32x4*)(p.part + ((int64_t)blockIdx.x * NPAD + gj * 16 + r) * NPAD + gi * 16 + 4 * g) = gacc[t];
         }
         if (tid == 0) p.exps[blockIdx.x] = erun;
     }
-}
-
-// the largest of the slots' exponents
-__device__ __forceinline__ int top_exponent(const int* exps, int slots) {
-    int e = NS_EMPTY;
-    for (int i = threadIdx.x & 63; i < slots; i += 64) e = exps[i] > e ? exps[i] : e;
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) {
-        const int o = __shfl_xor(e, d);
-        e = o > e ? o : e;
-    }
-    return e;
-}
-__device__ __forceinline__ float slot_weight(int e, int top) {
-    const int d = 2 * (e - top);
-    return d < -126 ? 0.f : __builtin_ldexpf(1.f, d);
-}
-
-// sum[j] = sum over the slots of 2^(2 (e - top)) part[slot][j], four floats a
-// thread; 8 threads share an element's slots and add up in thread order
-__global__ __launch_bounds__(256) void ns_sum_kernel(const float* part, const int* exps, int slots, int quads, float* sum,
-                                                     int* top_out) {
-    __shared__ __attribute__((aligned(16))) f32x4 red[8][32];
-    const int tid = threadIdx.x, e = tid & 31, h = tid >> 5;
-    const int top = top_exponent(exps, slots);
-    const int at = (int)blockIdx.x * 32 + e;
-    f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
-    if (at < quads)
-        for (int k = h; k < slots; k += 8) s += *(const f32x4*)(part + ((int64_t)k * quads + at) * 4) * slot_weight(exps[k], top);
-    red[h][e] = s;
-    __syncthreads();
-    if (h == 0 && at < quads) {
-#pragma unroll
-        for (int k = 1; k < 8; ++k) s += red[k][e];
-        *(f32x4*)(sum + (int64_t)at * 4) = s;
-        if (blockIdx.x == 0 && tid == 0) *top_out = top;
-    }
-}
-
-struct IterParams {
-    const float* part;   // [slots][NPAD][NPAD]; one slot: the sum, its exponent in exps[0]
-    const int* exps;
-    int slots, steps, first;
-    float a, b, c;
-    double eps;
-    float sA[NS_SEG], sP[NS_SEG], sT[NS_SEG], sQ[NS_SEG];   // powers of two that keep each matrix inside fp16
-    uint16_t* q;         // pieces [NP][NPAD][KR]
-    double* fac;
-};
-
-// One workgroup: the Gram matrix, then `steps` steps on it; Q out as pieces.
-// Masters in registers (MFMA layout), operands as pieces in LDS: all matrices
-// are symmetric, so each serves as either operand row by row.
-template <int NPAD, int NP>
-__global__ __launch_bounds__(NPAD >= 64 ? 1024 : NPAD == 32 ? 256 : 64) void ns_iter_kernel(IterParams p) {
-    constexpr int NT = NPAD >= 64 ? 1024 : NPAD == 32 ? 256 : 64, IB = NPAD / 16;
-    constexpr int TW = NPAD == 128 ? 2 : 1;   // tiles per wave along each side
-    constexpr int WB = IB / TW;               // waves along a side
-    constexpr int KR = ThinShape<NPAD>::KR, LD = KR + 8, KS = KR / 32;
-    constexpr int BUFS = NP == 2 ? 2 : 1;
-    __shared__ __attribute__((aligned(16))) uint16_t buf[BUFS][NP][NPAD * LD];
-    __shared__ float diag[NPAD];
-    const int tid = threadIdx.x, lane = tid & 63, g = lane >> 4, r = lane & 15;
-    const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wi = wave % WB, wj = wave / WB;
-    typedef f32x4 M[TW][TW];
-    auto row_of = [&](int ti) { return (wi * TW + ti) * 16 + 4 * g; };   // first of 4 rows
-    auto col_of = [&](int tj) { return (wj * TW + tj) * 16 + r; };
-
-    // zero the columns an MFMA step reads past NPAD
-    if constexpr (KR > NPAD) {
-        for (int i = tid; i < BUFS * NP * NPAD * LD; i += NT) ((uint16_t*)buf)[i] = 0;
-        __syncthreads();
-    }
-    const int top = top_exponent(p.exps, p.slots);
-    M A, Q;
-#pragma unroll
-    for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-        for (int tj = 0; tj < TW; ++tj) {
-            f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 16
-            for (int k = 0; k < p.slots; ++k)
-                s += *(const f32x4*)(p.part + ((int64_t)k * NPAD + col_of(tj)) * NPAD + row_of(ti)) *
-                     slot_weight(p.exps[k], top);
-            A[ti][tj] = s;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (row_of(ti) + e == col_of(tj)) diag[col_of(tj)] = s[e];
-        }
-    // A's true size: 2^(2 top) A; the first segment divides by (|G| + eps)^2
-    double inv = 1.0;
-    if (p.first) {
-        __syncthreads();
-        double tr = 0;
-        for (int i = lane; i < NPAD; i += 64) tr += (double)diag[i];
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) tr += __shfl_xor(tr, d);
-        const double norm = top == NS_EMPTY ? 0.0 : __builtin_ldexp(__builtin_sqrt(tr), top);
-        inv = 1.0 / (norm + p.eps);
-    }
-    const double half = top == NS_EMPTY ? 0.0 : __builtin_ldexp(inv, top);
-    const float fA = (float)(half * half);
-#pragma unroll
-    for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-        for (int tj = 0; tj < TW; ++tj) A[ti][tj] *= fA;
-
-    auto put = [&](int b, const M& m, float scale) {
-#pragma unroll
-        for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-            for (int tj = 0; tj < TW; ++tj) {
-                uint16_t o[4][NP];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) Pieces<NP>::split(m[ti][tj][e] * scale, o[e]);
-#pragma unroll
-                for (int k = 0; k < NP; ++k)
-                    *(i32x2*)&buf[b][k][col_of(tj) * LD + row_of(ti)] =
-                        i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16),
-                              (int)((uint32_t)o[2][k] | (uint32_t)o[3][k] << 16)};
-            }
-    };
-    auto product = [&](int bu, int bv, float scale, M& out) {
-#pragma unroll
-        for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-            for (int tj = 0; tj < TW; ++tj) out[ti][tj] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-        for (int s = 0; s < KS; ++s) {
-            i32x4 u[TW][NP], v[TW][NP];
-#pragma unroll
-            for (int t = 0; t < TW; ++t)
-#pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    u[t][k] = *(const i32x4*)&buf[bu][k][((wi * TW + t) * 16 + r) * LD + s * 32 + g * 8];
-                    v[t][k] = *(const i32x4*)&buf[bv][k][((wj * TW + t) * 16 + r) * LD + s * 32 + g * 8];
-                }
-#pragma unroll
-            for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-                for (int tj = 0; tj < TW; ++tj) out[ti][tj] = piece_step<NP>(u[ti], v[tj], out[ti][tj]);
-        }
-#pragma unroll
-        for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-            for (int tj = 0; tj < TW; ++tj) out[ti][tj] *= scale;
-    };
-
-    for (int k = 0; k < p.steps; ++k) {
-        M P;
-        put(0, A, p.sA[k]);
-        __syncthreads();
-        product(0, 0, 1.f / (p.sA[k] * p.sA[k]), P);
-#pragma unroll
-        for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-            for (int tj = 0; tj < TW; ++tj)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    float v = p.c * P[ti][tj][e] + p.b * A[ti][tj][e];
-                    if (row_of(ti) + e == col_of(tj)) v += p.a;
-                    P[ti][tj][e] = v;
-                }
-        const bool more = k + 1 < p.steps;
-        if constexpr (NP == 2) {
-            if (k > 0 || more) {
-                put(1, P, p.sP[k]);
-                __syncthreads();
-            }
-            if (more) product(0, 1, 1.f / (p.sA[k] * p.sP[k]), A);   // T = A P
-            if (k > 0) {
-                __syncthreads();   // buffer 0 has been read
-                put(0, Q, p.sQ[k - 1]);
-                __syncthreads();
-                product(0, 1, 1.f / (p.sQ[k - 1] * p.sP[k]), Q);
-            }
-            if (more) {
-                __syncthreads();
-                put(0, A, p.sT[k]);
-                __syncthreads();
-                M T;
-                product(0, 1, 1.f / (p.sT[k] * p.sP[k]), T);   // P A P
-#pragma unroll
-                for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-                    for (int tj = 0; tj < TW; ++tj) A[ti][tj] = T[ti][tj];
-                __syncthreads();
-            }
-        }
-        if (k == 0) {
-#pragma unroll
-            for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-                for (int tj = 0; tj < TW; ++tj) Q[ti][tj] = P[ti][tj];
-        }
-    }
-    const float sq = p.sQ[p.steps - 1];
-#pragma unroll
-    for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-        for (int tj = 0; tj < TW; ++tj) {
-            uint16_t o[4][NP];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) Pieces<NP>::split(Q[ti][tj][e] * sq, o[e]);
-#pragma unroll
-            for (int k = 0; k < NP; ++k)
-                *(i32x2*)(p.q + ((int64_t)k * NPAD + col_of(tj)) * KR + row_of(ti)) =
-                    i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16),
-                          (int)((uint32_t)o[2][k] | (uint32_t)o[3][k] << 16)};
-        }
-    if constexpr (KR > NPAD) {
-        for (int i = tid; i < NP * NPAD * (KR - NPAD); i += NT)
-            p.q[(i / (KR - NPAD)) * KR + NPAD + i % (KR - NPAD)] = 0;
-    }
-    if (tid == 0) *p.fac = inv / (double)sq;
 }
 
 // ---- host ----------------------------------------------------------------------------------
@@ -1043,7 +1082,7 @@ static ThinLayout thin_layout(int64_t R, int64_t C, int dt) {
     const int64_t chunks = (m + cw - 1) / cw;
     L.ldx = chunks * cw;
     // (few enough Gram matrices that adding them up stays short)
-    L.wgs = (int)std::min<int64_t>(chunks, L.npad <= 32 ? 32 : 64);
+    L.wgs = (int)std::min<int64_t>(chunks, L.npad <= 32 ? 32 : 128);
     size_t off = 0;
     auto take = [&](size_t& at, size_t bytes) { at = off; off = up256(off + bytes); };
     take(L.part, (size_t)L.wgs * (size_t)(L.npad * L.npad) * 4);
@@ -1087,8 +1126,7 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
     t.vec = (t.tall ? t.n : t.m) % 8 == 0 && ((uintptr_t)p.g & 15) == 0;
     const int seg = NP == 2 ? NS_SEG : 1, segs = (p.steps + seg - 1) / seg;
     const int64_t chunks = L.ldx / S::CW;
-    hipLaunchKernelGGL((ns_chunk_kernel<NPAD, NP, THIN_GRAM>), dim3(L.wgs), dim3(S::NT), 0, s, t);
-    hipError_t e = hipGetLastError();
+    hipError_t e = hipSuccess;
     top = 1.0;
     int done = 0;
     for (int k = 0; k < segs && e == hipSuccess; ++k) {
@@ -1096,15 +1134,6 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
         q.part = t.part;
         q.exps = t.exps;
         q.slots = L.wgs;
-        if (NPAD > 32) {
-            const int quads = NPAD * NPAD / 4;
-            hipLaunchKernelGGL(ns_sum_kernel, dim3((quads + 31) / 32), dim3(256), 0, s, t.part, t.exps, L.wgs, quads,
-                               (float*)(W + L.sum), (int*)(W + L.top));
-            if ((e = hipGetLastError()) != hipSuccess) break;
-            q.part = (const float*)(W + L.sum);
-            q.exps = (const int*)(W + L.top);
-            q.slots = 1;
-        }
         q.steps = (p.steps - done + (segs - k) - 1) / (segs - k);
         done += q.steps;
         q.first = k == 0;
@@ -1124,17 +1153,30 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
         }
         q.q = (uint16_t*)(W + L.q);
         q.fac = (double*)(W + L.fac);
-        hipLaunchKernelGGL((ns_iter_kernel<NPAD, NP>), dim3(1), dim3(NPAD >= 64 ? 1024 : NPAD == 32 ? 256 : 64), 0, s, q);
+        // the Gram matrix of X (and X <- Q X of the segment before), then this segment's Q
+        if (k == 0) hipLaunchKernelGGL((ns_chunk_kernel<NPAD, NP, THIN_GRAM>), dim3(L.wgs), dim3(S::NT), 0, s, t);
+        else hipLaunchKernelGGL((ns_chunk_kernel<NPAD, NP, THIN_BOTH>), dim3(L.wgs), dim3(S::NT), 0, s, t);
         if ((e = hipGetLastError()) != hipSuccess) break;
-        if (k + 1 < segs) {
-            hipLaunchKernelGGL((ns_chunk_kernel<NPAD, NP, THIN_BOTH>), dim3(L.wgs), dim3(S::NT), 0, s, t);
-        } else {
-            hipLaunchKernelGGL((ns_chunk_kernel<NPAD, NP, THIN_OUT>), dim3((unsigned)std::min<int64_t>(chunks, 1024)),
-                               dim3(S::NT), 0, s, t);
+        if constexpr (NPAD > 32) {
+            const int quads = NPAD * NPAD / 4;
+            hipLaunchKernelGGL(ns_sum_kernel, dim3(quads / 32), dim3(256), 0, s, t.part, t.exps, L.wgs, quads,
+                               (float*)(W + L.sum), (int*)(W + L.top));
+            if ((e = hipGetLastError()) != hipSuccess) break;
+            q.part = (const float*)(W + L.sum);
+            q.exps = (const int*)(W + L.top);
+            q.slots = 1;
         }
+        hipLaunchKernelGGL((ns_iter_kernel<NPAD, NP>), dim3(1), dim3(iter_threads(NPAD)), 0, s, q);
+        if ((e = hipGetLastError()) != hipSuccess) break;
+        if (k > 0) {
+            t.src = 2;
+            t.vec = 1;
+        }
+    }
+    if (e == hipSuccess) {
+        hipLaunchKernelGGL((ns_chunk_kernel<NPAD, NP, THIN_OUT>), dim3((unsigned)std::min<int64_t>(chunks, 1024)),
+                           dim3(S::NT), 0, s, t);
         e = hipGetLastError();
-        t.src = 2;
-        t.vec = 1;
     }
     return e;
 }
