@@ -392,14 +392,18 @@ __device__ __forceinline__ i32x4 thin_frag_t(const uint16_t* t, int row0, int co
     return i32x4{ai[0], ai[1], bi[0], bi[1]};
 }
 
-// the piece products whose orders add up to at most NP - 1, small ones first
-template <int NP>
-__device__ __forceinline__ f32x4 piece_step(const i32x4 (&a)[NP], const i32x4 (&b)[NP], f32x4 c) {
+// c[i][j] += a[i] . b[j] over the piece products whose orders add up to at
+// most NP - 1, small ones first; consecutive MFMAs go to different tiles
+template <int NP, int I, int J>
+__device__ __forceinline__ void piece_mma(const i32x4 (&a)[I][NP], const i32x4 (&b)[J][NP], f32x4 (&c)[I][J]) {
 #pragma unroll
     for (int o = NP - 1; o >= 0; --o)
 #pragma unroll
-        for (int k = 0; k <= o; ++k) c = Pieces<NP>::CT::step(a[k], b[o - k], c);
-    return c;
+        for (int k = 0; k <= o; ++k)
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+#pragma unroll
+                for (int j = 0; j < J; ++j) c[i][j] = Pieces<NP>::CT::step(a[i][k], b[j][o - k], c[i][j]);
 }
 
 struct IterParams {
@@ -488,10 +492,7 @@ struct Iter {
                     u[t][k] = *(const i32x4*)(at(bu, k) + ((wi * TW + t) * 16 + r) * LD + s * 32 + g * 8);
                     v[t][k] = *(const i32x4*)(at(bv, k) + ((wj * TW + t) * 16 + r) * LD + s * 32 + g * 8);
                 }
-#pragma unroll
-            for (int ti = 0; ti < TW; ++ti)
-#pragma unroll
-                for (int tj = 0; tj < TW; ++tj) out[ti][tj] = piece_step<NP>(u[ti], v[tj], out[ti][tj]);
+            piece_mma<NP>(u, v, out);
         }
 #pragma unroll
         for (int ti = 0; ti < TW; ++ti)
@@ -669,19 +670,19 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
 #pragma unroll
             for (int k = 0; k < NP; ++k) xs[k][NPAD * LD + i] = 0;
     }
-    i32x4 q[KS][NP];
+    i32x4 q[KS][1][NP];
     double fac = 0;
     if constexpr (MODE != THIN_GRAM) {
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
             for (int k = 0; k < NP; ++k)
-                q[s][k] = *(const i32x4*)(p.q + ((int64_t)k * NPAD + ib * 16 + r) * S::KR + s * 32 + g * 8);
+                q[s][0][k] = *(const i32x4*)(p.q + ((int64_t)k * NPAD + ib * 16 + r) * S::KR + s * 32 + g * 8);
         fac = *p.fac;
     }
-    f32x4 gacc[S::GT];
+    f32x4 gacc[1][S::GT];
 #pragma unroll
-    for (int t = 0; t < S::GT; ++t) gacc[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int t = 0; t < S::GT; ++t) gacc[0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
     int erun = MODE == THIN_GRAM && p.src != 2 ? NS_EMPTY : -exponent_of(__builtin_bit_cast(uint32_t, p.sx));
 
     const int64_t chunks = (p.m + CW - 1) / CW;
@@ -773,7 +774,7 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
                 else if (e > erun) {
                     const float f = __builtin_ldexpf(1.f, 2 * (erun - e) < -126 ? -126 : 2 * (erun - e));
 #pragma unroll
-                    for (int t = 0; t < S::GT; ++t) gacc[t] *= f;
+                    for (int t = 0; t < S::GT; ++t) gacc[0][t] *= f;
                     erun = e;
                 }
                 e = erun;
@@ -806,19 +807,21 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
 
         if constexpr (MODE != THIN_GRAM) {
             const float f = (float)__builtin_ldexp(fac, e);
-            f32x4 acc[S::CB];
+            f32x4 acc[S::CB][1];
 #pragma unroll
-            for (int c = 0; c < S::CB; ++c) acc[c] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int c = 0; c < S::CB; ++c) acc[c][0] = f32x4{0.f, 0.f, 0.f, 0.f};
 #pragma unroll
             for (int s = 0; s < KS; ++s)
+            {
+                i32x4 x[S::CB][NP];
 #pragma unroll
-                for (int c = 0; c < S::CB; ++c) {
-                    i32x4 x[NP];
+                for (int c = 0; c < S::CB; ++c)
 #pragma unroll
-                    for (int k = 0; k < NP; ++k) x[k] = thin_frag_t<LD>(xs[k], s * 32, (cb0 + c) * 16, lane);
-                    if (MODE == THIN_OUT && p.tall) acc[c] = piece_step<NP>(q[s], x, acc[c]);
-                    else acc[c] = piece_step<NP>(x, q[s], acc[c]);
-                }
+                    for (int k = 0; k < NP; ++k) x[c][k] = thin_frag_t<LD>(xs[k], s * 32, (cb0 + c) * 16, lane);
+                // (tall: the transposed tile, 4 consecutive i a lane)
+                if (MODE == THIN_OUT && p.tall) piece_mma<NP>(q[s], x, *(f32x4(*)[1][S::CB])&acc);
+                else piece_mma<NP>(x, q[s], acc);
+            }
             if constexpr (MODE == THIN_OUT) {
 #pragma unroll
                 for (int c = 0; c < S::CB; ++c) {
@@ -829,7 +832,7 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
                         const int64_t ie = p.tall ? i + el : i, ce = p.tall ? cc : cc + el;
                         if (ie >= p.n || ce >= p.m) continue;
                         const int64_t o = p.tall ? ce * p.n + ie : ie * p.m + ce;
-                        const float val = acc[c][el] * f;
+                        const float val = acc[c][0][el] * f;
                         if (p.dt == DT_F32) ((float*)p.out)[o] = val;
                         else ((uint16_t*)p.out)[o] = p.dt == DT_F16 ? f32_to_f16(val) : f32_to_bf16(val);
                     }
@@ -840,11 +843,11 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
 #pragma unroll
                 for (int c = 0; c < S::CB; ++c) {
                     const int i = ib * 16 + r, cc = (cb0 + c) * 16 + 4 * g;
-                    acc[c] *= f;
-                    if (i < p.n) *(f32x4*)(p.x + i * p.ldx + c0 + cc) = acc[c];
+                    acc[c][0] *= f;
+                    if (i < p.n) *(f32x4*)(p.x + i * p.ldx + c0 + cc) = acc[c][0];
                     uint16_t o[4][NP];
 #pragma unroll
-                    for (int el = 0; el < 4; ++el) Pieces<NP>::split(acc[c][el] * p.sx, o[el]);
+                    for (int el = 0; el < 4; ++el) Pieces<NP>::split(acc[c][0][el] * p.sx, o[el]);
 #pragma unroll
                     for (int k = 0; k < NP; ++k)
                         *(i32x2*)&xs[k][i * LD + cc] = i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16),
@@ -859,17 +862,16 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
             for (int s = 0; s < GK; ++s) {
                 const int ks = S::KSPLIT ? wave * GK + s : s;
                 const int gi = S::KSPLIT ? 0 : wave % S::IB;
-                i32x4 a[NP];
+                i32x4 a[1][NP], b[S::GT][NP];
 #pragma unroll
-                for (int k = 0; k < NP; ++k) a[k] = *(const i32x4*)&xs[k][(gi * 16 + r) * LD + ks * 32 + g * 8];
+                for (int k = 0; k < NP; ++k) a[0][k] = *(const i32x4*)&xs[k][(gi * 16 + r) * LD + ks * 32 + g * 8];
 #pragma unroll
                 for (int t = 0; t < S::GT; ++t) {
                     const int gj = S::KSPLIT ? 0 : wave / S::IB * S::GT + t;
-                    i32x4 b[NP];
 #pragma unroll
-                    for (int k = 0; k < NP; ++k) b[k] = *(const i32x4*)&xs[k][(gj * 16 + r) * LD + ks * 32 + g * 8];
-                    gacc[t] = piece_step<NP>(a, b, gacc[t]);
+                    for (int k = 0; k < NP; ++k) b[t][k] = *(const i32x4*)&xs[k][(gj * 16 + r) * LD + ks * 32 + g * 8];
                 }
+                piece_mma<NP>(a, b, gacc);
             }
         }
     }
@@ -877,18 +879,18 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
         if constexpr (S::KSPLIT) {
             __syncthreads();   // the last chunk's tile has been read
             f32x4* red = (f32x4*)&xs[0][0];
-            red[wave * 64 + lane] = gacc[0];
+            red[wave * 64 + lane] = gacc[0][0];
             __syncthreads();
-            gacc[0] = red[lane];
+            gacc[0][0] = red[lane];
 #pragma unroll
-            for (int w = 1; w < S::NW; ++w) gacc[0] += red[w * 64 + lane];
+            for (int w = 1; w < S::NW; ++w) gacc[0][0] += red[w * 64 + lane];
         }
         const int gi = S::KSPLIT ? 0 : wave % S::IB;
 #pragma unroll
         for (int t = 0; t < S::GT; ++t) {
             const int gj = S::KSPLIT ? 0 : wave / S::IB * S::GT + t;
             if (!S::KSPLIT || wave == 0)
-                *(f32x4*)(p.part + ((int64_t)blockIdx.x * NPAD + gj * 16 + r) * NPAD + gi * 16 + 4 * g) = gacc[t];
+                *(f32x4*)(p.part + ((int64_t)blockIdx.x * NPAD + gj * 16 + r) * NPAD + gi * 16 + 4 * g) = gacc[0][t];
         }
         if (tid == 0) p.exps[blockIdx.x] = erun;
     }
