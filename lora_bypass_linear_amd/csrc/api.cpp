@@ -113,9 +113,18 @@ struct Layout {
     bool cast_x = false, cast_w = false;
 };
 
+// up to 2^24 products of one wave per element, within the launch's grid (300
+// rows, rank 16 over 1040: 5 us against the split contraction's 31)
+bool hdot_few(int64_t M, int64_t r_pad, int64_t K) {
+    return M * r_pad <= 4 * 65535 && (double)M * (double)r_pad * (double)K <= 16777216.0;
+}
+
 // h for few token rows: one wave per element (fp64 dots), in place of the
 // split contraction, whose single workgroup would walk all of K
 bool hdot_path(const Problem& P) {
+    // (over an 8-bit base also for more rows while the dots are few: the split
+    // contraction's workgroups, one per 16 or more rows, do not fill the device)
+    if (P.w8 && P.r_pad > 0 && P.K > 0 && hdot_few(P.M, P.r_pad, P.K)) return true;
     return P.lora && P.r_pad > 0 && P.K > 0 && P.M <= 128 && (double)P.M * (double)P.r_pad * (double)P.K <= 33554432.0;
 }
 
@@ -564,6 +573,7 @@ struct BwdLayout {
            unorm = 0, flag_g = 0, gh = 0, wt = 0, dt = 0, xt = 0, ght = 0, dyt = 0, ht = 0, gq = 0, gs = 0,
            partial = 0, total = 0;
     bool cast_x = false, cast_g = false, need_h = false, need_gh = false;
+    bool gh_dot = false;   // gh one wave per element (8-bit base, few dots): no split of up^T, a count per workgroup
     // tr_tok: dDown and dUp read x, dy, h_r and gh_r as stored, the token
     // index as their contraction rows (16-bit compute, each operand below
     // 1 GiB); else they read transposed copies.  dx reads W^T and down^T copies.
@@ -625,10 +635,11 @@ BwdLayout bwd_layout(const Bwd& B) {
         take(L.h, M * R * ce);
     }
     if (L.need_gh) {
+        L.gh_dot = P.w8 && P.N > 0 && hdot_few(P.M, P.r_pad, P.N);
         take(L.ut, R * N * ce);
-        if (split) { take(L.uth, R * N * ce); take(L.utl, R * N * ce); }
+        if (split && !L.gh_dot) { take(L.uth, R * N * ce); take(L.utl, R * N * ce); }
         take(L.unorm, R * 2 * sizeof(double));
-        take(L.flag_g, sizeof(unsigned));
+        take(L.flag_g, (L.gh_dot ? (size_t)lyc::hdot_workgroups(P.M, P.r_pad) : 1) * sizeof(unsigned));
         take(L.gh, M * R * ce);
     }
     size_t part = 0;
@@ -793,27 +804,43 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
         if (!transpose(W, P.c_dt, 0, 0, W + L.gh, P.r_pad, M)) return LYC_ERR_HIP;
     } else if (L.need_gh && M > 0) {
         if (!transpose(up, P.u_dt, N, r, W + L.ut, N, P.r_pad)) return LYC_ERR_HIP;
-        if (split && timed(LYC_KERNEL_PREP, s, [&] {
-                return lyc::launch_rownorm(W + L.ut, P.c_dt, P.r_pad, N, W + L.uth, W + L.utl,
-                                           (double2*)(W + L.unorm), (unsigned*)(W + L.flag_g), s);
-            }) != hipSuccess)
-            return LYC_ERR_HIP;
-        lyc::XrParams gp{};
-        gp.x = ga;
-        gp.b = W + (split ? L.uth : L.ut);
-        gp.b_lo = split ? (const void*)(W + L.utl) : nullptr;
-        gp.b_full = W + L.ut;
-        gp.bnorm = (const double2*)(W + L.unorm);
-        gp.M = M;
-        gp.Nc = P.r_pad;
-        gp.K = N;
-        gp.guard = split ? 1 : 0;
-        gp.flagged = (unsigned*)(W + L.flag_g);
-        gp.mode = lyc::XR_H;
-        gp.out = W + L.gh;
-        gp.ld_out = P.r_pad;
-        gp.scale = scale;
-        if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_xr(P.c_dt, gp, s); }) != hipSuccess) return LYC_ERR_HIP;
+        if (L.gh_dot) {
+            lyc::HdotParams hq{};
+            hq.x = ga;
+            hq.down = W + L.ut;
+            hq.M = M;
+            hq.K = N;
+            hq.rank = r;
+            hq.r_pad = P.r_pad;
+            hq.vec = aligned(ga, 16) ? 1 : 0;   // (N is a multiple of 16)
+            hq.out = W + L.gh;
+            hq.flagged = (unsigned*)(W + L.flag_g);
+            hq.scale = scale;
+            if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_hdot(P.c_dt, hq, s); }) != hipSuccess)
+                return LYC_ERR_HIP;
+        } else {
+            if (split && timed(LYC_KERNEL_PREP, s, [&] {
+                    return lyc::launch_rownorm(W + L.ut, P.c_dt, P.r_pad, N, W + L.uth, W + L.utl,
+                                               (double2*)(W + L.unorm), (unsigned*)(W + L.flag_g), s);
+                }) != hipSuccess)
+                return LYC_ERR_HIP;
+            lyc::XrParams gp{};
+            gp.x = ga;
+            gp.b = W + (split ? L.uth : L.ut);
+            gp.b_lo = split ? (const void*)(W + L.utl) : nullptr;
+            gp.b_full = W + L.ut;
+            gp.bnorm = (const double2*)(W + L.unorm);
+            gp.M = M;
+            gp.Nc = P.r_pad;
+            gp.K = N;
+            gp.guard = split ? 1 : 0;
+            gp.flagged = (unsigned*)(W + L.flag_g);
+            gp.mode = lyc::XR_H;
+            gp.out = W + L.gh;
+            gp.ld_out = P.r_pad;
+            gp.scale = scale;
+            if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_xr(P.c_dt, gp, s); }) != hipSuccess) return LYC_ERR_HIP;
+        }
     }
 
     // dx = round_x(dy_c . W_c + gh_r . down_c): the forward's GEMM with W^T, the fold over down^T

@@ -1076,7 +1076,10 @@ __global__ __launch_bounds__(256) void hdot_kernel(HdotParams p) {
             a = __shfl(a, 0, 64);
             n += 6;
             const double u = 0x1p-53, g = (double)n * u / (1.0 - (double)n * u);
-            const double E = g * a * (1.0 + 2.0 * g) + 0x1p-1060;
+            const double E0 = g * a * (1.0 + 2.0 * g) + 0x1p-1060;
+            // (a scale other than 1 adds its own rounding)
+            s *= p.scale;
+            const double E = p.scale == 1.0 ? E0 : __builtin_fabs(p.scale) * E0 + 0x1p-52 * __builtin_fabs(s);
             bool cross;
             if constexpr (CT::dt == DT_F32) cross = (float)(s - E) != (float)(s + E);
             else cross = round16<CT>(s - E) != round16<CT>(s + E);
@@ -1112,7 +1115,7 @@ __global__ __launch_bounds__(256) void hdot_kernel(HdotParams p) {
                     S = t;
                     C = (C + Co) + err;
                 }
-                v = __shfl(S, 0, 64) + __shfl(C, 0, 64);
+                v = p.scale * (__shfl(S, 0, 64) + __shfl(C, 0, 64));
             }
         }
         if (lane == 0) {

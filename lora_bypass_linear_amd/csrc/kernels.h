@@ -131,6 +131,7 @@ struct HdotParams {
     int vec;             // rows 16-byte aligned and K * es a multiple of 16: 16-byte loads
     void* out;           // h [M][r_pad]
     unsigned* flagged;   // [hdot_workgroups(M, r_pad)]
+    double scale = 1.0;  // the value rounded is scale times the dot
 };
 int64_t hdot_workgroups(int64_t M, int64_t r_pad);
 hipError_t launch_hdot(int c_dt, const HdotParams& p, hipStream_t s);
