@@ -50,6 +50,20 @@ struct Pieces<3> {
     }
 };
 
+// c[i][j] += a[i] . b[j] over the piece products whose orders add up to at
+// most NP - 1, small ones first; consecutive MFMAs go to different tiles
+template <int NP, int I, int J>
+__device__ __forceinline__ void piece_mma(const i32x4 (&a)[I][NP], const i32x4 (&b)[J][NP], f32x4 (&c)[I][J]) {
+#pragma unroll
+    for (int o = NP - 1; o >= 0; --o)
+#pragma unroll
+        for (int k = 0; k <= o; ++k)
+#pragma unroll
+            for (int i = 0; i < I; ++i)
+#pragma unroll
+                for (int j = 0; j < J; ++j) c[i][j] = Pieces<NP>::CT::step(a[i][k], b[j][o - k], c[i][j]);
+}
+
 // A matrix as pieces: [rows][ld] per piece, ld a multiple of 8, zero past cols
 struct Planes {
     uint16_t* p;
@@ -58,15 +72,44 @@ struct Planes {
 
 // ---- the norm and the first split --------------------------------------------------
 
-constexpr int NORM_WGS = 256;
+constexpr int NORM_WGS = 512;
 
-__global__ __launch_bounds__(256) void ns_norm_kernel(const void* g, int dt, int64_t n, double* part) {
+// 16 elements from `at` of the flat matrix of n elements as fp32 (zeros past
+// it): 16-byte loads where vec (the matrix 16-byte aligned, 16 elements left)
+__device__ __forceinline__ void load16_f32(const void* g, int dt, int64_t at, int64_t n, bool vec, float (&v)[16]) {
+    if (vec && at + 16 <= n) {
+        i32x4 w[4];
+        const i32x4* src = (const i32x4*)((const char*)g + at * (dt == DT_F32 ? 4 : 2));
+#pragma unroll
+        for (int i = 0; i < 2; ++i) w[i] = src[i];
+        if (dt == DT_F32) {
+#pragma unroll
+            for (int i = 2; i < 4; ++i) w[i] = src[i];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) v[e] = __builtin_bit_cast(float, (uint32_t)w[e >> 2][e & 3]);
+        } else {
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const uint32_t u = (uint32_t)w[e >> 3][(e >> 1) & 3];
+                const uint16_t h = (uint16_t)((e & 1) ? u >> 16 : u);
+                v[e] = dt == DT_F16 ? f16_to_f32(h) : bf16_to_f32(h);
+            }
+        }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 16; ++e) v[e] = at + e < n ? load_as_f32(g, dt, at + e) : 0.f;
+    }
+}
+
+__global__ __launch_bounds__(256) void ns_norm_kernel(const void* g, int dt, int64_t n, int vec, double* part) {
     __shared__ double red[4];
     const int tid = threadIdx.x;
     double s = 0;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + tid; i < n; i += (int64_t)NORM_WGS * 256) {
-        const double v = (double)load_as_f32(g, dt, i);
-        s += v * v;
+    for (int64_t i = ((int64_t)blockIdx.x * 256 + tid) * 16; i < n; i += (int64_t)NORM_WGS * 256 * 16) {
+        float v[16];
+        load16_f32(g, dt, i, n, vec, v);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s = __builtin_fma((double)v[e], (double)v[e], s);
     }
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
@@ -86,18 +129,51 @@ __device__ __forceinline__ double ns_inverse_norm(const double* part, double eps
     return 1.0 / (__builtin_sqrt(s) + eps);
 }
 
+// x = pieces of scale * g / (|g| + eps), 8 columns a thread (rows padded to 8
+// columns with zeros)
 template <int NP>
 __global__ __launch_bounds__(256) void ns_split_kernel(const void* g, int dt, int64_t rows, int64_t cols, Planes x,
                                                        const double* part, double eps, float scale) {
-    const double inv = ns_inverse_norm(part, eps);
-    const int64_t total = rows * x.ld;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < total; i += (int64_t)gridDim.x * 256) {
-        const int64_t r = i / x.ld, c = i - r * x.ld;
-        const float v = c < cols ? (float)((double)load_as_f32(g, dt, r * cols + c) * inv) * scale : 0.f;
-        uint16_t o[NP];
-        Pieces<NP>::split(v, o);
+    // (the whole factor in 64 bits: a norm near fp32's ends has no fp32 reciprocal)
+    const double f = ns_inverse_norm(part, eps) * (double)scale;
+    const int64_t q = x.ld / 8, total = rows * q;
+    const bool vec = cols % 8 == 0 && ((uintptr_t)g & 15) == 0;
+    for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
+        const int64_t r = t / q, c = (t - r * q) * 8;
+        uint32_t raw[8];
+        if (vec) {
+            const char* src = (const char*)g + (r * cols + c) * (dt == DT_F32 ? 4 : 2);
+            const i32x4 a = *(const i32x4*)src;
+            if (dt == DT_F32) {
+                const i32x4 b = *(const i32x4*)(src + 16);
 #pragma unroll
-        for (int k = 0; k < NP; ++k) x.p[k * x.stride + i] = o[k];
+                for (int e = 0; e < 4; ++e) { raw[e] = (uint32_t)a[e]; raw[4 + e] = (uint32_t)b[e]; }
+            } else {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) raw[e] = (uint32_t)a[e >> 1] >> (16 * (e & 1)) & 0xFFFFu;
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const int64_t at = r * cols + (c + e < cols ? c + e : cols - 1);
+                const uint32_t w = dt == DT_F32 ? ((const uint32_t*)g)[at] : ((const uint16_t*)g)[at];
+                raw[e] = c + e < cols ? w : 0u;
+            }
+        }
+        uint16_t o[8][NP];
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            const float v = dt == DT_F32 ? __builtin_bit_cast(float, raw[e])
+                                         : (dt == DT_F16 ? f16_to_f32((uint16_t)raw[e]) : bf16_to_f32((uint16_t)raw[e]));
+            Pieces<NP>::split((float)((double)v * f), o[e]);
+        }
+#pragma unroll
+        for (int k = 0; k < NP; ++k) {
+            i32x4 w;
+#pragma unroll
+            for (int u = 0; u < 4; ++u) w[u] = (int)((uint32_t)o[2 * u][k] | (uint32_t)o[2 * u + 1][k] << 16);
+            *(i32x4*)(x.p + k * x.stride + r * x.ld + c) = w;
+        }
     }
 }
 
@@ -228,11 +304,11 @@ struct NsSide {
     }
 };
 
-// T x T output tile per workgroup of 4 waves (2 x 2), NS stages of one K step
-// (32 k of every piece of both sides).
-template <int NP, bool TR, int T, int NS>
-__global__ __launch_bounds__(256, NP == 2 ? 2 : 1) void ns_gemm_kernel(NsParams p, int tiles_i, int tiles_j) {
-    constexpr int NW = 4, W = T / 2, F = W / 16;
+// T x T output tile per workgroup of NW waves (2 x NW / 2), NS stages of one K
+// step (32 k of every piece of both sides).
+template <int NP, bool TR, int T, int NS, int NW>
+__global__ __launch_bounds__(64 * NW, 1) void ns_gemm_kernel(NsParams p, int tiles_i, int tiles_j) {
+    constexpr int WI = T / 2, WJ = T / (NW / 2), FI = WI / 16, FJ = WJ / 16;
     using Side = NsSide<T, NW, TR>;
     constexpr int STAGE = 2 * NP * Side::BYTES, Q = 2 * NP * Side::Q;
     static_assert(NS * STAGE <= 160 * 1024, "LDS");
@@ -258,45 +334,56 @@ __global__ __launch_bounds__(256, NP == 2 ? 2 : 1) void ns_gemm_kernel(NsParams 
             sv.issue(st + (NP + k) * Side::BYTES, k * p.v.stride * 2, s0 + kt, kt < KT, wave, lane);
         }
     };
-    f32x4 acc[F][F];
+    f32x4 acc[FI][FJ];
 #pragma unroll
-    for (int i = 0; i < F; ++i)
+    for (int i = 0; i < FI; ++i)
 #pragma unroll
-        for (int j = 0; j < F; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < FJ; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    // fragments are read one step ahead, into the other of two register sets
+    struct Frags {
+        i32x4 a[FI][NP], b[FJ][NP];
+    };
+    auto read = [&](Frags& f, int kt) {
+        const char* st = smem + (kt % NS) * STAGE;
 #pragma unroll
-    for (int s = 0; s < NS - 1; ++s) issue(s);
-    for (int kt = 0; kt < KT; ++kt) {
+        for (int k = 0; k < NP; ++k) {
+#pragma unroll
+            for (int j = 0; j < FJ; ++j) f.b[j][k] = Side::frag(st + (NP + k) * Side::BYTES, wj * WJ + j * 16, lane);
+#pragma unroll
+            for (int i = 0; i < FI; ++i) f.a[i][k] = Side::frag(st + k * Side::BYTES, wi * WI + i * 16, lane);
+        }
+    };
+    // step kt's MFMAs, from `f`; step kt+1's fragments into `nx`.  Before them:
+    // the wave holds all of stage kt, step kt+1 has landed, and stage kt is
+    // free for step kt+NS.  (Steps past the last read zeros.)
+    auto step = [&](int kt, const Frags& f, Frags& nx) {
+        __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
         wait_vm<(NS - 2) * Q>();
         lds_barrier();
-        issue(kt + NS - 1);
-        const char* st = smem + (kt % NS) * STAGE;
-        i32x4 b[NP][F];
+        issue(kt + NS);
+        read(nx, kt + 1);
+        piece_mma<NP>(f.a, f.b, acc);
+    };
+    if (KT > 0) {
+        Frags f0, f1;
 #pragma unroll
-        for (int k = 0; k < NP; ++k)
-#pragma unroll
-            for (int j = 0; j < F; ++j) b[k][j] = Side::frag(st + (NP + k) * Side::BYTES, wj * W + j * 16, lane);
-#pragma unroll
-        for (int i = 0; i < F; ++i) {
-            i32x4 a[NP];
-#pragma unroll
-            for (int k = 0; k < NP; ++k) a[k] = Side::frag(st + k * Side::BYTES, wi * W + i * 16, lane);
-            // piece products whose orders add up to at most NP - 1
-#pragma unroll
-            for (int o = NP - 1; o >= 0; --o)
-#pragma unroll
-                for (int k = 0; k <= o; ++k)
-#pragma unroll
-                    for (int j = 0; j < F; ++j) acc[i][j] = Pieces<NP>::CT::step(a[k], b[o - k][j], acc[i][j]);
+        for (int s = 0; s < NS; ++s) issue(s);
+        wait_vm<(NS - 1) * Q>();
+        lds_barrier();
+        read(f0, 0);
+        for (int kt = 0; kt < KT; kt += 2) {
+            step(kt, f0, f1);
+            step(kt + 1, f1, f0);
         }
     }
     wait_vm<0>();
     const int g = lane >> 4, r = lane & 15;
 #pragma unroll
-    for (int i = 0; i < F; ++i) {
-        const int64_t oi = i0 + wi * W + i * 16 + 4 * g;
+    for (int i = 0; i < FI; ++i) {
+        const int64_t oi = i0 + wi * WI + i * 16 + 4 * g;
 #pragma unroll
-        for (int j = 0; j < F; ++j) {
-            const int64_t oj = j0 + wj * W + j * 16 + r;
+        for (int j = 0; j < FJ; ++j) {
+            const int64_t oj = j0 + wj * WJ + j * 16 + r;
             if (oj >= p.J) continue;
             if (p.ksplit > 1) {
                 const int64_t ldp = (p.I + 3) & ~(int64_t)3;
@@ -390,20 +477,6 @@ __device__ __forceinline__ i32x4 thin_frag_t(const uint16_t* t, int row0, int co
         __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s4*)(__attribute__((address_space(3))) uint16_t*)(p + 4 * LD));
     const i32x2 ai = __builtin_bit_cast(i32x2, a), bi = __builtin_bit_cast(i32x2, b);
     return i32x4{ai[0], ai[1], bi[0], bi[1]};
-}
-
-// c[i][j] += a[i] . b[j] over the piece products whose orders add up to at
-// most NP - 1, small ones first; consecutive MFMAs go to different tiles
-template <int NP, int I, int J>
-__device__ __forceinline__ void piece_mma(const i32x4 (&a)[I][NP], const i32x4 (&b)[J][NP], f32x4 (&c)[I][J]) {
-#pragma unroll
-    for (int o = NP - 1; o >= 0; --o)
-#pragma unroll
-        for (int k = 0; k <= o; ++k)
-#pragma unroll
-            for (int i = 0; i < I; ++i)
-#pragma unroll
-                for (int j = 0; j < J; ++j) c[i][j] = Pieces<NP>::CT::step(a[i][k], b[j][o - k], c[i][j]);
 }
 
 struct IterParams {
@@ -975,8 +1048,8 @@ static hipError_t ns_product(NsParams p, hipStream_t s) {
     ns_plan(p.I, p.J, p.K, &t, &p.ksplit);
     const int ti = (int)((p.I + t - 1) / t), tj = (int)((p.J + t - 1) / t);
     const dim3 grid((unsigned)(ti * tj), (unsigned)p.ksplit);
-    if (t == 128) hipLaunchKernelGGL((ns_gemm_kernel<NP, TR, 128, 2>), grid, dim3(256), 0, s, p, ti, tj);
-    else hipLaunchKernelGGL((ns_gemm_kernel<NP, TR, 64, 3>), grid, dim3(256), 0, s, p, ti, tj);
+    if (t == 128) hipLaunchKernelGGL((ns_gemm_kernel<NP, TR, 128, NP == 2 ? 4 : 3, 8>), grid, dim3(512), 0, s, p, ti, tj);
+    else hipLaunchKernelGGL((ns_gemm_kernel<NP, TR, 64, 3, 4>), grid, dim3(256), 0, s, p, ti, tj);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.ksplit > 1) {
         const int64_t q = p.J * ((p.mode == NS_OUT ? (p.I + 3) / 4 : p.o.ld / 4));
@@ -1012,10 +1085,11 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
         sp = pow2_under(pmax);
     }
 
-    hipLaunchKernelGGL(ns_norm_kernel, dim3(NORM_WGS), dim3(256), 0, s, p.g, p.dt, p.R * p.C, part);
+    hipLaunchKernelGGL(ns_norm_kernel, dim3(NORM_WGS), dim3(256), 0, s, p.g, p.dt, p.R * p.C,
+                       ((uintptr_t)p.g & 15) == 0 ? 1 : 0, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    const int64_t wgs = std::min<int64_t>((p.R * L.ldx + 255) / 256, 2048);
+    const int64_t wgs = std::min<int64_t>((p.R * L.ldx / 8 + 255) / 256, 2048);
     hipLaunchKernelGGL(ns_split_kernel<NP>, dim3((unsigned)wgs), dim3(256), 0, s, p.g, p.dt, p.R, p.C, x[0], part, p.eps,
                        (float)sx);
     if ((e = hipGetLastError()) != hipSuccess) return e;
