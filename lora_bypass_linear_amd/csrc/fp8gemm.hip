@@ -270,11 +270,35 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
         const auto ra = make_rsrc(ma, (uint32_t)rows_a * kbytes);
         const auto rb = make_rsrc(mb, (uint32_t)rows_b * kbytes);
         using LD = Loader<TL>;
-        constexpr int QL = LD::QA + LD::QB;
+        // EARLY (long steps): the wave holds step kt's B fragments and scales in
+        // registers from its start, so that side of the stage is released by a
+        // barrier of its own and refilled while the A side is still being read:
+        // the loads, which bound the step, come in two halves over it
+        constexpr bool EARLY = FN > 4;
+        constexpr int Q0 = EARLY ? LD::QA : LD::QA + LD::QB;   // loads issued with the last columns
         for (int kt = RF; kt < KT; ++kt) {
             const char* st = smem + (kt % NS) * TL::STAGE;
             const char* nx = smem + ((kt + 1) % NS) * TL::STAGE;
             f32x4 t[2][FM];
+            // (steps past the last are out of range; fold steps are all before)
+            const int s = kt + NS;
+            const int64_t kb = s - RF + k0;
+            const uint32_t kb0 = (uint32_t)kb * 128u, row_bytes = s < KT ? kbytes : 0u;
+            const bool ok = kb0 + 128u <= row_bytes || kb0 + LD::chunk16(lane) < row_bytes;
+            char* wr = smem + (s % NS) * TL::STAGE;
+            const float* sp = is_w ? pp.sw + nb0 * pp.sw_n + kb * pp.sw_k : pp.sx + kb * p.M + m0;
+            const auto rs = make_rsrc(s < KT ? sp : pp.sw, s < KT ? srange : 0u);
+            auto load_side = [&](int q) {   // the q-th of the wave's loads of step kt+NS
+                auto* dst = (__attribute__((address_space(3))) void*)(wr + (wave + q * TL::NW) * 1024);
+                const bool is_a = q < LD::QA;
+                const uint32_t v = is_a ? lm.va + (uint32_t)q * lm.sa : lm.vb + (uint32_t)(q - LD::QA) * lm.sb;
+                if (is_a) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, dst, 16, ok ? v : OOB, (int)kb0, 0, 0);
+                else __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, dst, 16, ok ? v : OOB, (int)kb0, 0, 0);
+            };
+            auto load_scale_row = [&]() {
+                auto* dst = (__attribute__((address_space(3))) void*)(wr + TL::DATA + wave * 256);
+                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 4, soff, 0, 0, 0);
+            };
 #pragma unroll
             for (int i = 0; i < FN - 2; ++i) {
                 load_frag(a[(i + 2) & 3], st, row_a + (i + 2) * 16);
@@ -291,16 +315,18 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
                     if (i > 0) __builtin_amdgcn_sched_group_barrier(0x002, 4, 0);
                 }
                 __builtin_amdgcn_sched_barrier(0);
+                if (EARLY && i == 1) {
+                    lds_barrier();   // every wave holds its B fragments and scales
+#pragma unroll
+                    for (int q = LD::QA; q < LD::QA + LD::QB; ++q) load_side(q);
+                    load_scale_row();
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
-            next();
-            // (steps past the last are out of range; fold steps are all before)
-            const int s = kt + NS;
-            const int64_t kb = s - RF + k0;
-            const uint32_t kb0 = (uint32_t)kb * 128u, row_bytes = s < KT ? kbytes : 0u;
-            const bool ok = kb0 + 128u <= row_bytes || kb0 + LD::chunk16(lane) < row_bytes;
-            char* wr = smem + (s % NS) * TL::STAGE;
-            const float* sp = is_w ? pp.sw + nb0 * pp.sw_n + kb * pp.sw_k : pp.sx + kb * p.M + m0;
-            const auto rs = make_rsrc(s < KT ? sp : pp.sw, s < KT ? srange : 0u);
+            // as next(), the loads in flight counted in the order they go out
+            __builtin_amdgcn_s_waitcnt(0xC07F);
+            wait_vm<EARLY ? (NS - 1) * (LD::QB + 1) + (NS - 2) * LD::QA : (NS - 2) * TL::Q>();
+            lds_barrier();
             const float swn = load_scales(sn, nx);
             load_frag(a[FN & 3], nx, row_a);
             load_frag(a[(FN + 1) & 3], nx, row_a + 16);
@@ -308,14 +334,8 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
 #pragma unroll
             for (int j = 0; j < FM; ++j) {
 #pragma unroll
-                for (int q = 0; q < QL; ++q) {
-                    if (q * FM / QL != j) continue;
-                    auto* dst = (__attribute__((address_space(3))) void*)(wr + (wave + q * TL::NW) * 1024);
-                    const bool is_a = q < LD::QA;
-                    const uint32_t v = is_a ? lm.va + (uint32_t)q * lm.sa : lm.vb + (uint32_t)(q - LD::QA) * lm.sb;
-                    if (is_a) __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, dst, 16, ok ? v : OOB, (int)kb0, 0, 0);
-                    else __builtin_amdgcn_raw_ptr_buffer_load_lds(rb, dst, 16, ok ? v : OOB, (int)kb0, 0, 0);
-                }
+                for (int q = 0; q < Q0; ++q)
+                    if (q * FM / Q0 == j) load_side(q);
                 u[j & 1][0] = block_sum<false>(a[(FN - 2) & 3], b[j]);
                 fma4(acc[FN - 3][j], t[(FN - 3) & 1][j], sj[j]);
                 u[j & 1][1] = block_sum<false>(a[(FN - 1) & 3], b[j]);
@@ -326,10 +346,7 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
                 load_frag(b[j], nx + TL::TN * TL::BKB, row_b + j * 16);
                 __builtin_amdgcn_sched_barrier(0);
             }
-            {
-                auto* dst = (__attribute__((address_space(3))) void*)(wr + TL::DATA + wave * 256);
-                __builtin_amdgcn_raw_ptr_buffer_load_lds(rs, dst, 4, soff, 0, 0, 0);
-            }
+            if constexpr (!EARLY) load_scale_row();
             fma4(acc[FN - 2][FM - 1], u[(FM - 1) & 1][0], sj[FM - 1]);
             fma4(acc[FN - 1][FM - 1], u[(FM - 1) & 1][1], sj[FM - 1]);
 #pragma unroll
