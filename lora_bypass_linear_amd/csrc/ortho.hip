@@ -430,7 +430,8 @@ __global__ __launch_bounds__(256) void ns_reduce_kernel(NsParams p) {
 //                    before, behind a device-wide fence, it took 2 us more)
 //   ns_sum_kernel    the workgroups' Gram matrices added up (n > 32)
 
-constexpr int NS_SEG = 3;
+constexpr int NS_SEG = 3, NS_SEG64 = 5;
+constexpr double NS_QMAX = 1024.0;   // bound on Q's largest factor within a segment
 constexpr int NS_THIN = 128;
 constexpr int NS_EMPTY = -100000;   // exponent of a workgroup that saw zeros only
 
@@ -718,6 +719,63 @@ __global__ __launch_bounds__(256) void ns_sum_kernel(const float* part, const in
     }
 }
 
+// The segment for n <= 16 and a 16-bit G, by one wave in 64 bits, all of it in
+// registers: v_mfma_f64_16x16x4 leaves lane (r = lane % 16, g = lane / 16) the
+// elements (4 e + g, r), and takes as step s of either operand the element
+// (r, 4 s + g), which for a symmetric matrix is the same register.  A product
+// is four MFMAs and nothing else, and 64 bits leave no growth of errors to
+// stop for: five steps a segment (17 products, about 3 us).
+typedef double f64x4 __attribute__((ext_vector_type(4)));
+__global__ __launch_bounds__(64) void ns_iter64_kernel(IterParams p) {
+    constexpr int KR = ThinShape<16>::KR;
+    const int lane = threadIdx.x, g = lane >> 4, r = lane & 15;
+    const int top = top_exponent(p.exps, p.slots);
+    f64x4 A = f64x4{0, 0, 0, 0};
+#pragma unroll 8
+    for (int k = 0; k < p.slots; ++k) {
+        const double w = (double)slot_weight(p.exps[k], top);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) A[e] += w * (double)p.part[k * 256 + r * 16 + 4 * e + g];
+    }
+    double inv = 1.0;
+    if (p.first) {
+        double tr = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tr += 4 * e + g == r ? A[e] : 0.0;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) tr += __shfl_xor(tr, d);
+        inv = 1.0 / ((top == NS_EMPTY ? 0.0 : __builtin_ldexp(__builtin_sqrt(tr), top)) + p.eps);
+    }
+    const double half = top == NS_EMPTY ? 0.0 : __builtin_ldexp(inv, top);
+    A *= half * half;
+    auto product = [](const f64x4& u, const f64x4& v) {
+        f64x4 c = f64x4{0, 0, 0, 0};
+#pragma unroll
+        for (int s = 0; s < 4; ++s) c = __builtin_amdgcn_mfma_f64_16x16x4f64(u[s], v[s], c, 0, 0, 0);
+        return c;
+    };
+    f64x4 Q = f64x4{0, 0, 0, 0};
+    for (int k = 0; k < p.steps; ++k) {
+        f64x4 P = product(A, A);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) P[e] = (double)p.c * P[e] + (double)p.b * A[e] + (4 * e + g == r ? (double)p.a : 0.0);
+        Q = k == 0 ? P : product(Q, P);
+        if (k + 1 < p.steps) A = product(product(A, P), P);
+    }
+    const float sq = p.sQ[0];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+        uint16_t o[2];
+        Pieces<2>::split((float)Q[e] * sq, o);
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            p.q[(k * 16 + r) * KR + 4 * e + g] = o[k];
+            p.q[(k * 16 + r) * KR + 16 + 4 * e + g] = 0;
+        }
+    }
+    if (lane == 0) *p.fac = inv / (double)sq;
+}
+
 template <int NPAD, int NP>
 __global__ __launch_bounds__(iter_threads(NPAD)) void ns_iter_kernel(IterParams p) {
     using I = Iter<NPAD, NP>;
@@ -994,22 +1052,27 @@ static void ns_plan(int64_t I, int64_t J, int64_t K, int* tile, int* ksplit) {
 static double pow2_under(double bound) {
     return std::ldexp(1.0, std::max(-100, std::min(15, (int)std::floor(15.0 - std::log2(std::max(bound, 1e-30))))));
 }
-// [0, top] -> the next A's largest eigenvalue, max |p| and max |l p| there
-static void poly_bounds(const OrthoParams& p, double top, double* next, double* pmax, double* tmax) {
-    *next = *pmax = *tmax = 0.0;
-    for (int i = 0; i <= 512; ++i) {
-        const double l = top * i / 512.0, q = p.a + l * (p.b + l * p.c);
-        *pmax = std::max(*pmax, std::fabs(q));
-        *tmax = std::max(*tmax, std::fabs(l * q));
-        *next = std::max(*next, l * q * q);
-    }
-    // between the sampled points, and the products' rounding
-    *next *= 1.02;
-    *pmax *= 1.02;
-    *tmax *= 1.02;
-    if (!(*next < 1e30)) *next = 1e30;
-    if (!(*pmax < 1e30)) *pmax = 1e30;
-    if (!(*tmax < 1e30)) *tmax = 1e30;
+// [0, top] -> the next A's largest eigenvalue, max |p| and max |l p| there: at
+// the ends, or where the derivative's quadratic u + v l + w l^2 vanishes
+static void poly_bounds(const OrthoParams& q, double top, double* next, double* pmax, double* tmax) {
+    auto p = [&](double l) { return q.a + l * (q.b + l * q.c); };
+    auto most = [&](double u, double v, double w, auto f) {
+        double m = std::max(std::fabs(f(0.0)), std::fabs(f(top)));
+        auto at = [&](double l) { if (l > 0.0 && l < top) m = std::max(m, std::fabs(f(l))); };
+        if (w == 0.0) {
+            if (v != 0.0) at(-u / v);
+        } else if (v * v - 4 * u * w >= 0.0) {
+            const double d = std::sqrt(v * v - 4 * u * w);
+            at((-v - d) / (2 * w));
+            at((-v + d) / (2 * w));
+        }
+        m *= 1.01;   // the products' rounding
+        return m < 1e30 ? m : 1e30;
+    };
+    *pmax = most(q.b, 2 * q.c, 0.0, p);
+    *tmax = most(q.a, 2 * q.b, 3 * q.c, [&](double l) { return l * p(l); });
+    // (l p^2)' = p (a + 3 b l + 5 c l^2); where p vanishes so does l p^2
+    *next = most(q.a, 3 * q.b, 5 * q.c, [&](double l) { return l * p(l) * p(l); });
 }
 
 struct NsLayout {
@@ -1200,7 +1263,19 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
     // (bf16 pieces have fp32's range)
     t.sx = NP == 2 ? (float)pow2_under(std::sqrt(topx)) : 1.0f;
     t.vec = (t.tall ? t.n : t.m) % 8 == 0 && ((uintptr_t)p.g & 15) == 0;
-    const int seg = NP == 2 ? NS_SEG : 1, segs = (p.steps + seg - 1) / seg;
+    // steps a segment: as many as Q's largest factor stays small for (its
+    // rounding is relative to it), evenly shared
+    constexpr bool WIDE = NPAD == 16 && NP == 2;   // ns_iter64_kernel
+    int seg = WIDE ? NS_SEG64 : NP == 2 ? NS_SEG : 1;
+    double pall = 1.0;
+    top = 1.0;
+    for (int k = 0; k < p.steps; ++k) {
+        poly_bounds(p, top, &next, &pm, &tm);
+        pall = std::max(pall, pm);
+        top = next;
+    }
+    while (seg > 1 && std::pow(pall, seg) > NS_QMAX) --seg;
+    const int segs = (p.steps + seg - 1) / seg;
     const int64_t chunks = L.ldx / S::CW;
     hipError_t e = hipSuccess;
     top = 1.0;
@@ -1221,10 +1296,11 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
         for (int i = 0; i < q.steps; ++i) {
             poly_bounds(p, top, &next, &pm, &tm);
             qmax *= pm;
-            q.sA[i] = NP == 2 ? (float)pow2_under(top) : 1.0f;
-            q.sP[i] = NP == 2 ? (float)pow2_under(pm) : 1.0f;
-            q.sT[i] = NP == 2 ? (float)pow2_under(tm) : 1.0f;
-            q.sQ[i] = NP == 2 ? (float)pow2_under(qmax) : 1.0f;
+            const int at = WIDE ? 0 : i;   // (the 64-bit segment scales its last Q only)
+            q.sA[at] = NP == 2 ? (float)pow2_under(top) : 1.0f;
+            q.sP[at] = NP == 2 ? (float)pow2_under(pm) : 1.0f;
+            q.sT[at] = NP == 2 ? (float)pow2_under(tm) : 1.0f;
+            q.sQ[at] = NP == 2 ? (float)pow2_under(qmax) : 1.0f;
             top = next;
         }
         q.q = (uint16_t*)(W + L.q);
@@ -1242,7 +1318,8 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
             q.exps = (const int*)(W + L.top);
             q.slots = 1;
         }
-        hipLaunchKernelGGL((ns_iter_kernel<NPAD, NP>), dim3(1), dim3(iter_threads(NPAD)), 0, s, q);
+        if constexpr (WIDE) hipLaunchKernelGGL(ns_iter64_kernel, dim3(1), dim3(64), 0, s, q);
+        else hipLaunchKernelGGL((ns_iter_kernel<NPAD, NP>), dim3(1), dim3(iter_threads(NPAD)), 0, s, q);
         if ((e = hipGetLastError()) != hipSuccess) break;
         if (k > 0) {
             t.src = 2;
