@@ -37,6 +37,7 @@ _lib = None
 E4M3 = torch.float8_e4m3fn   # the 8-bit codes (OCP e4m3)
 _CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 _TORCH = {v: k for k, v in _CODE.items()}
+_RAW = (torch.uint8, E4M3)   # dtypes of workspaces and codes
 
 
 class LycError(RuntimeError):
@@ -185,20 +186,21 @@ def resolve_dtypes(dtypes: Sequence[int]) -> Tuple[int, int]:
 
 
 def _ptr(t: Optional[torch.Tensor]):
-    return None if t is None else ctypes.c_void_p(t.data_ptr())
+    # (an int: every pointer parameter is declared c_void_p)
+    return None if t is None else t.data_ptr()
 
 
-def _stream(dev) -> ctypes.c_void_p:
-    return ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)
+def _stream(dev) -> int:
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev.index is None else dev.index)
 
 
 def _shape(t: Optional[torch.Tensor], shape, name: str) -> None:
     """Raise ValueError unless t (if given) has exactly this shape.  The C ABI
     takes bare pointers, so a mis-shaped operand would be read (or an output
     written) out of bounds: every shape is checked here before any call."""
-    if t is None:
+    if t is None or t.shape == shape:
         return
-    if t.shape != tuple(shape) and tuple(t.shape) != tuple(int(s) for s in shape):
+    if tuple(t.shape) != tuple(int(s) for s in shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(int(s) for s in shape)}")
 
 
@@ -231,11 +233,13 @@ def _need_device(*ts):
     for t in ts:
         if t is None:
             continue
+        if t.device == dev and t.is_contiguous() and (t.dtype in _CODE or t.dtype in _RAW):
+            continue
         if not t.is_cuda:
             raise ValueError("lyc operands must be GPU tensors")
         if not t.is_contiguous():
             raise ValueError("lyc operands must be contiguous")
-        if t.dtype not in _CODE and t.dtype != torch.uint8 and t.dtype != E4M3:
+        if t.dtype not in _CODE and t.dtype not in _RAW:
             raise TypeError(f"unsupported dtype {t.dtype}")
         if dev is None:
             dev = t.device

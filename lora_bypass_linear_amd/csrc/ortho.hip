@@ -304,22 +304,24 @@ struct NsSide {
     }
 };
 
-// T x T output tile per workgroup of NW waves (2 x NW / 2), NS stages of one K
+// TI x TJ output tile per workgroup of WVI x WVJ waves, NS stages of one K
 // step (32 k of every piece of both sides).
-template <int NP, bool TR, int T, int NS, int NW>
-__global__ __launch_bounds__(64 * NW, 1) void ns_gemm_kernel(NsParams p, int tiles_i, int tiles_j) {
-    constexpr int WI = T / 2, WJ = T / (NW / 2), FI = WI / 16, FJ = WJ / 16;
-    using Side = NsSide<T, NW, TR>;
-    constexpr int STAGE = 2 * NP * Side::BYTES, Q = 2 * NP * Side::Q;
+template <int NP, bool TR, int TI, int TJ, int WVI, int WVJ, int NS>
+__global__ __launch_bounds__(64 * WVI * WVJ, 1) void ns_gemm_kernel(NsParams p, int tiles_i, int tiles_j) {
+    constexpr int NW = WVI * WVJ, WI = TI / WVI, WJ = TJ / WVJ, FI = WI / 16, FJ = WJ / 16;
+    using SideU = NsSide<TI, NW, TR>;
+    using SideV = NsSide<TJ, NW, TR>;
+    constexpr int STAGE = NP * (SideU::BYTES + SideV::BYTES), Q = NP * (SideU::Q + SideV::Q);
     static_assert(NS * STAGE <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(16))) char smem[NS * STAGE];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int wi = wave & 1, wj = wave >> 1;
+    const int wi = wave % WVI, wj = wave / WVI;
     int ti, tj;
     tile_coords(blockIdx.x, gridDim.x, tiles_i, tiles_j, 4, ti, tj);
-    const int64_t i0 = (int64_t)ti * T, j0 = (int64_t)tj * T;
-    Side su, sv;
+    const int64_t i0 = (int64_t)ti * TI, j0 = (int64_t)tj * TJ;
+    SideU su;
+    SideV sv;
     su.init(p.u, i0, p.I, p.K, wave, lane);
     sv.init(p.v, j0, p.J, p.K, wave, lane);
     const int64_t steps = (p.K + 31) / 32, per = (steps + p.ksplit - 1) / p.ksplit;
@@ -330,8 +332,8 @@ __global__ __launch_bounds__(64 * NW, 1) void ns_gemm_kernel(NsParams p, int til
         char* st = smem + (kt % NS) * STAGE;
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
-            su.issue(st + k * Side::BYTES, k * p.u.stride * 2, s0 + kt, kt < KT, wave, lane);
-            sv.issue(st + (NP + k) * Side::BYTES, k * p.v.stride * 2, s0 + kt, kt < KT, wave, lane);
+            su.issue(st + k * SideU::BYTES, k * p.u.stride * 2, s0 + kt, kt < KT, wave, lane);
+            sv.issue(st + NP * SideU::BYTES + k * SideV::BYTES, k * p.v.stride * 2, s0 + kt, kt < KT, wave, lane);
         }
     };
     f32x4 acc[FI][FJ];
@@ -348,9 +350,9 @@ __global__ __launch_bounds__(64 * NW, 1) void ns_gemm_kernel(NsParams p, int til
 #pragma unroll
         for (int k = 0; k < NP; ++k) {
 #pragma unroll
-            for (int j = 0; j < FJ; ++j) f.b[j][k] = Side::frag(st + (NP + k) * Side::BYTES, wj * WJ + j * 16, lane);
+            for (int j = 0; j < FJ; ++j) f.b[j][k] = SideV::frag(st + NP * SideU::BYTES + k * SideV::BYTES, wj * WJ + j * 16, lane);
 #pragma unroll
-            for (int i = 0; i < FI; ++i) f.a[i][k] = Side::frag(st + k * Side::BYTES, wi * WI + i * 16, lane);
+            for (int i = 0; i < FI; ++i) f.a[i][k] = SideU::frag(st + k * SideU::BYTES, wi * WI + i * 16, lane);
         }
     };
     // step kt's MFMAs, from `f`; step kt+1's fragments into `nx`.  Before them:
@@ -361,8 +363,22 @@ __global__ __launch_bounds__(64 * NW, 1) void ns_gemm_kernel(NsParams p, int til
         wait_vm<(NS - 2) * Q>();
         lds_barrier();
         issue(kt + NS);
+        __builtin_amdgcn_sched_barrier(0);
         read(nx, kt + 1);
         piece_mma<NP>(f.a, f.b, acc);
+        if constexpr (!TR) {
+            // a fragment read, then its share of the MFMAs (left alone, the
+            // compiler sinks the reads below them; the transposing reads' two
+            // halves a fragment made the registers spill so)
+            constexpr int ND = NP * (FI + FJ), NM = FI * FJ * NP * (NP + 1) / 2;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                __builtin_amdgcn_sched_group_barrier(0x008, NM / ND, 0);
+            }
+            __builtin_amdgcn_sched_group_barrier(0x008, NM - NM / ND * ND, 0);
+        }
+        __builtin_amdgcn_sched_barrier(0);
     };
     if (KT > 0) {
         Frags f0, f1;
@@ -1032,19 +1048,31 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
 static int64_t up8(int64_t v) { return (v + 7) & ~(int64_t)7; }
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
-// tile and K split of an I x J product over K: 128 x 128 tiles where they fill
-// half the device, else 64 x 64; a K split while workgroups are fewer than the
-// CUs, at least 4 steps of 32 each
-static void ns_plan(int64_t I, int64_t J, int64_t K, int* tile, int* ksplit) {
-    const int64_t cus = device_rates().cus;
-    const int64_t big = ((I + 127) / 128) * ((J + 127) / 128);
-    *tile = big >= cus / 2 ? 128 : 64;
-    const int64_t t = *tile, tiles = ((I + t - 1) / t) * ((J + t - 1) / t);
+// Tile and K split of an I x J product over K, by modelled time: rounds of
+// workgroups over the CUs times a K step's time as measured (the small tile's
+// workgroups share a CU), plus the partial sums' round trip of a split.  With
+// two pieces: 2048 x 2048 over 4096 100 us in 128 x 128 tiles, 107 us in 256 x
+// 128 tiles with two splits; 4096 x 2048 over 2048, transposed form, 119 and
+// 112 us.  (Three pieces: the large tile's fragments do not fit the registers.)
+enum { NS_256x128, NS_128x128, NS_64x64 };
+static void ns_plan(int64_t I, int64_t J, int64_t K, int np, int* tile, int* ksplit) {
+    struct C { int id, ti, tj, per_cu; double step; };
+    const C cands[] = {{NS_256x128, 256, 128, 1, 1.40}, {NS_128x128, 128, 128, 1, 0.78}, {NS_64x64, 64, 64, 2, 0.9}};
+    const double cus = (double)device_rates().cus;
     const int64_t steps = (K + 31) / 32;
-    int64_t ks = tiles > 0 ? cus / tiles : 1;
-    ks = std::min<int64_t>(ks, steps / 4);
-    ks = std::min<int64_t>(ks, 64);
-    *ksplit = ks > 1 ? (int)ks : 1;
+    double best = 1e300;
+    *tile = NS_64x64;
+    *ksplit = 1;
+    for (const C& c : cands) {
+        if (c.id == NS_256x128 && np != 2) continue;
+        const double tiles = (double)((I + c.ti - 1) / c.ti) * (double)((J + c.tj - 1) / c.tj);
+        for (int ks = 1; ks <= 64; ks *= 2) {
+            if (ks > 1 && ks * 4 > steps) break;
+            double t = std::ceil(tiles * ks / (cus * c.per_cu)) * (double)((steps + ks - 1) / ks + 3) * c.step;
+            if (ks > 1) t += 4.0 + (double)I * (double)J * 4.0 * (ks + 1) / 4e6;
+            if (t < best) { best = t; *tile = c.id; *ksplit = ks; }
+        }
+    }
 }
 
 // powers of two that keep a matrix of the given spectral norm inside fp16
@@ -1094,11 +1122,11 @@ static NsLayout ns_layout(int64_t R, int64_t C, int dt) {
     take(L.P, np * (size_t)(n * L.ldn) * 2);
     size_t part = 0;
     int t, ks;
-    ns_plan(n, n, m, &t, &ks);
+    ns_plan(n, n, m, (int)np, &t, &ks);
     if (ks > 1) part = std::max(part, (size_t)ks * (size_t)(n * ((n + 3) & ~(int64_t)3)) * 4);
-    ns_plan(n, n, n, &t, &ks);
+    ns_plan(n, n, n, (int)np, &t, &ks);
     if (ks > 1) part = std::max(part, (size_t)ks * (size_t)(n * ((n + 3) & ~(int64_t)3)) * 4);
-    ns_plan(C, R, n, &t, &ks);
+    ns_plan(C, R, n, (int)np, &t, &ks);
     if (ks > 1) part = std::max(part, (size_t)ks * (size_t)(R * ((C + 3) & ~(int64_t)3)) * 4);
     take(L.partial, part);
     L.total = off;
@@ -1108,11 +1136,16 @@ static NsLayout ns_layout(int64_t R, int64_t C, int dt) {
 template <int NP, bool TR>
 static hipError_t ns_product(NsParams p, hipStream_t s) {
     int t;
-    ns_plan(p.I, p.J, p.K, &t, &p.ksplit);
-    const int ti = (int)((p.I + t - 1) / t), tj = (int)((p.J + t - 1) / t);
-    const dim3 grid((unsigned)(ti * tj), (unsigned)p.ksplit);
-    if (t == 128) hipLaunchKernelGGL((ns_gemm_kernel<NP, TR, 128, NP == 2 ? 4 : 3, 8>), grid, dim3(512), 0, s, p, ti, tj);
-    else hipLaunchKernelGGL((ns_gemm_kernel<NP, TR, 64, 3, 4>), grid, dim3(256), 0, s, p, ti, tj);
+    ns_plan(p.I, p.J, p.K, NP, &t, &p.ksplit);
+    auto launch = [&](auto kernel, int ti, int tj, int threads) {
+        const int ni = (int)((p.I + ti - 1) / ti), nj = (int)((p.J + tj - 1) / tj);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)(ni * nj), (unsigned)p.ksplit), dim3(threads), 0, s, p, ni, nj);
+    };
+    if constexpr (NP == 2) {
+        if (t == NS_256x128) launch(ns_gemm_kernel<NP, TR, 256, 128, 4, 2, 3>, 256, 128, 512);
+    }
+    if (t == NS_128x128) launch(ns_gemm_kernel<NP, TR, 128, 128, 2, 4, NP == 2 ? 4 : 3>, 128, 128, 512);
+    else if (t == NS_64x64) launch(ns_gemm_kernel<NP, TR, 64, 64, 2, 2, 3>, 64, 64, 256);
     hipError_t e = hipGetLastError();
     if (e == hipSuccess && p.ksplit > 1) {
         const int64_t q = p.J * ((p.mode == NS_OUT ? (p.I + 3) / 4 : p.o.ld / 4));

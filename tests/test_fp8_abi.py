@@ -61,11 +61,9 @@ def test_weight_refusals(kw, st):
     (dict(qx=NULL), INV), (dict(sx=NULL), INV), (dict(qw=NULL), INV), (dict(sw=NULL), INV), (dict(y=NULL), INV),
     (dict(b=P, b_dt=0), INV), (dict(b_dt=2), INV), (dict(y_dt=4), INV), (dict(K=40), UNS), (dict(M=-3), INV),
     (dict(qx=V(8)), UNS), (dict(qw=V(24)), UNS), (dict(sx=V(2)), UNS), (dict(y=V(1)), UNS), (dict(y=P), INV),
-    (dict(y=P3), INV), (dict(y=P2), INV), (dict(M=16, N=64, K=8192, ws=NULL), WSP),
-    (dict(M=16, N=64, K=8192, ws=V(64)), WSP), (dict(M=16, N=64, K=8192, nws=16), WSP)])
+    (dict(y=P3), INV), (dict(y=P2), INV), (dict(M=64, N=64, K=8192, ws=NULL), WSP),
+    (dict(M=64, N=64, K=8192, ws=V(64)), WSP), (dict(M=64, N=64, K=8192, nws=16), WSP)])
 def test_product_refusals(kw, st):
-    if st == WSP and L.fp8_linear_workspace_size(kw["M"], kw["N"], kw["K"]) == 0:
-        pytest.skip("this shape needs no workspace")
     assert _product(**kw) == st
 
 
