@@ -393,6 +393,8 @@ int forward(const Problem& P, const void* x, const void* w, const void* bias, co
         if (cw) { pp.cast_src[nc] = (const float*)w; pp.cast_dst[nc] = W + L.wc; pp.cast_n[nc++] = P.N * P.K; }
         if (timed(LYC_KERNEL_PREP, s, [&] { return lyc::launch_prep(pp, s); }) != hipSuccess) return LYC_ERR_HIP;
     }
+    const lyc::QuantRowsParams qp{x, P.x_dt, W + L.xq, (float*)(W + L.xs), P.M, P.K};   // (P.w8)
+    bool quantized = false;
     if (P.r_pad > 0 && hdot) {
         lyc::HdotParams hq{};
         hq.x = xa;
@@ -404,7 +406,12 @@ int forward(const Problem& P, const void* x, const void* w, const void* bias, co
         hq.vec = ((P.K * (int64_t)esize(P.c_dt)) % 16 == 0 && aligned(xa, 16) && aligned(hq.down, 16)) ? 1 : 0;
         hq.out = W + L.h;
         hq.flagged = (unsigned*)(W + L.flagged);
-        if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_hdot(P.c_dt, hq, s); }) != hipSuccess)
+        // over an 8-bit base, x as stored in the compute dtype: quantized in the same launch
+        quantized = P.w8 && P.c_dt != LYC_F32 && P.x_dt == P.c_dt;
+        if (quantized) {
+            if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_hdot_quant(P.c_dt, hq, qp, s); }) != hipSuccess)
+                return LYC_ERR_HIP;
+        } else if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_hdot(P.c_dt, hq, s); }) != hipSuccess)
             return LYC_ERR_HIP;
         g.af = up_stored ? up : (const void*)(W + L.uc);
         g.bf = W + L.h;
@@ -441,10 +448,7 @@ int forward(const Problem& P, const void* x, const void* w, const void* bias, co
         g.rf = P.r_pad;
     }
     if (P.w8) {
-        if (P.K > 0 && timed(LYC_KERNEL_PREP, s, [&] {
-                return lyc::launch_quant_rows(
-                    lyc::QuantRowsParams{x, P.x_dt, W + L.xq, (float*)(W + L.xs), P.M, P.K}, s);
-            }) != hipSuccess)
+        if (P.K > 0 && !quantized && timed(LYC_KERNEL_PREP, s, [&] { return lyc::launch_quant_rows(qp, s); }) != hipSuccess)
             return LYC_ERR_HIP;
         g.b = W + L.xq;
         const lyc::Fp8GemmParams q{g, (const float*)(W + L.xs), w_s, (P.K + 127) / 128, 1};

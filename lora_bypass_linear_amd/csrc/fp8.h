@@ -20,6 +20,10 @@ struct QuantRowsParams {
     int64_t M, K;
 };
 hipError_t launch_quant_rows(const QuantRowsParams& p, hipStream_t s);
+inline int quant_pairs(int64_t K) { return (int)((K + 2 * FP8_BLOCK - 1) / (2 * FP8_BLOCK)); }
+// the few-row h pass and the quantization of the same x in one launch (x in
+// the 16-bit compute dtype), hpass.hip
+hipError_t launch_hdot_quant(int c_dt, const HdotParams& h, const QuantRowsParams& q, hipStream_t s);
 
 // the same with one scale per 128 x 128 tile, s[n / 128][k / 128]; q and the
 // transposed codes q_t [K][N] (N a multiple of 16) may each be nullptr

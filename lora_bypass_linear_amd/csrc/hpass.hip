@@ -49,8 +49,10 @@
 // the blocks g, g+KS, ...; partial sums meet in LDS at the end).  The b_hi,
 // b_lo and x tiles of KS blocks at a time are staged through LDS straight
 // from global memory, several rounds ahead.
+#include "fp8.h"
 #include "kernels.h"
 #include "lyc_device.h"
+#include "quant_device.h"
 
 #ifndef LYC_R16_KS
 #define LYC_R16_KS 8
@@ -1018,11 +1020,10 @@ __device__ __forceinline__ void two_sum(double a, double b, double& s, double& t
 }
 
 template <class CT>
-__global__ __launch_bounds__(256) void hdot_kernel(HdotParams p) {
+__device__ __forceinline__ void hdot_body(const HdotParams& p, int64_t wg, unsigned* wflag) {
     constexpr int V = CT::dt == DT_F32 ? 4 : 8;   // values per 16-byte chunk
     const int lane = threadIdx.x & 63;
-    const int64_t e = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);   // element m * r_pad + j
-    __shared__ unsigned wflag[4];
+    const int64_t e = wg * 4 + (threadIdx.x >> 6);   // element m * r_pad + j
     unsigned straddled = 0;
     if (e < p.M * p.r_pad) {
         const int64_t m = e / p.r_pad;
@@ -1126,7 +1127,22 @@ __global__ __launch_bounds__(256) void hdot_kernel(HdotParams p) {
     }
     if (lane == 0) wflag[threadIdx.x >> 6] = straddled;
     __syncthreads();
-    if (threadIdx.x == 0) p.flagged[blockIdx.x] = wflag[0] + wflag[1] + wflag[2] + wflag[3];
+    if (threadIdx.x == 0) p.flagged[wg] = wflag[0] + wflag[1] + wflag[2] + wflag[3];
+}
+
+template <class CT>
+__global__ __launch_bounds__(256) void hdot_kernel(HdotParams p) {
+    __shared__ unsigned wflag[4];
+    hdot_body<CT>(p, blockIdx.x, wflag);
+}
+
+// the first nq workgroups quantize x, the others take h: both read the same
+// few rows, and a launch of its own costs the 1-token forward 3 of 13 us
+template <class CT>
+__global__ __launch_bounds__(256) void hdot_quant_kernel(HdotParams p, QuantRowsParams q, int pairs, unsigned nq) {
+    __shared__ unsigned wflag[4];
+    if (blockIdx.x < nq) quant_rows_body<CT::dt>(q, blockIdx.x, pairs);
+    else hdot_body<CT>(p, blockIdx.x - nq, wflag);
 }
 
 int64_t hdot_workgroups(int64_t M, int64_t r_pad) { return (M * r_pad + 3) / 4; }
@@ -1138,6 +1154,17 @@ hipError_t launch_hdot(int c_dt, const HdotParams& p, hipStream_t s) {
     if (c_dt == DT_F16) hipLaunchKernelGGL(hdot_kernel<CF16>, dim3((unsigned)g), dim3(256), 0, s, p);
     else if (c_dt == DT_BF16) hipLaunchKernelGGL(hdot_kernel<CBF16>, dim3((unsigned)g), dim3(256), 0, s, p);
     else hipLaunchKernelGGL(hdot_kernel<CF32>, dim3((unsigned)g), dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
+hipError_t launch_hdot_quant(int c_dt, const HdotParams& h, const QuantRowsParams& q, hipStream_t s) {
+    const int64_t g = hdot_workgroups(h.M, h.r_pad);
+    const int pairs = quant_pairs(q.K);
+    const int64_t nq = (q.M + 15) / 16 * pairs;
+    if (g <= 0 || nq <= 0 || c_dt == DT_F32 || q.x_dt != c_dt || g + nq >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)(g + nq));
+    if (c_dt == DT_F16) hipLaunchKernelGGL(hdot_quant_kernel<CF16>, grid, dim3(256), 0, s, h, q, pairs, (unsigned)nq);
+    else hipLaunchKernelGGL(hdot_quant_kernel<CBF16>, grid, dim3(256), 0, s, h, q, pairs, (unsigned)nq);
     return hipGetLastError();
 }
 

@@ -356,3 +356,25 @@ def test_side_stream_and_graph():
         torch.cuda.synchronize()
         eager = call()
         assert all(torch.equal(a, b) for a, b in zip(outs, eager)), k
+
+
+def test_offsets_past_32_bits():
+    """More than 2^31 elements of x: the last rows come out as they do alone."""
+    M, K, N, tail = 270000, 8192, 144, 40
+    say("fp8 offsets past 32 bits")
+    g = torch.Generator(device="cuda").manual_seed(5)
+    x = torch.empty(M, K, dtype=BF16, device="cuda")
+    for i in range(0, M, 30000):
+        x[i:i + 30000] = torch.randn(min(30000, M - i), K, generator=g, device="cuda")
+    w = _rand(6, N, K, std=K ** -0.5).to(BF16).cuda()
+    wq, wsc, _ = L.fp8_quantize_weight(w)
+    q, s = L.fp8_quantize_rows(x)
+    last = x[M - tail:].clone()
+    del x
+    q1, s1 = L.fp8_quantize_rows(last)
+    assert torch.equal(q[M - tail:].view(torch.uint8), q1.view(torch.uint8))
+    assert torch.equal(s[:, M - tail:], s1)
+    y = L.fp8_linear(q, s, wq, wsc, out_dtype=F32)[M - tail:]
+    xv, wv = R.rows_value(_bits(q1), s1.cpu().numpy()), R.tiles_value(_bits(wq), wsc.cpu().numpy())
+    exact, mass = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    assert np.all(np.abs(R.f64(y) - exact) <= R.product_bound(exact, mass, 128 + K // 128 + 8, F32))
