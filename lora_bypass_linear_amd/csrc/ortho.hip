@@ -1049,15 +1049,18 @@ static int64_t up8(int64_t v) { return (v + 7) & ~(int64_t)7; }
 static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 
 // Tile and K split of an I x J product over K, by modelled time: rounds of
-// workgroups over the CUs times a K step's time as measured (the small tile's
-// workgroups share a CU), plus the partial sums' round trip of a split.  With
-// two pieces: 2048 x 2048 over 4096 100 us in 128 x 128 tiles, 107 us in 256 x
-// 128 tiles with two splits; 4096 x 2048 over 2048, transposed form, 119 and
-// 112 us.  (Three pieces: the large tile's fragments do not fit the registers.)
+// workgroups over the CUs (two of the small tile's share one) times a fixed
+// part and a K step's as measured, plus the partial sums' round trip of a
+// split.  2048 x 2048 over 4096, two pieces: 100 us in 128 x 128 tiles, 107 us
+// in 256 x 128 tiles with two splits; 4096 x 2048 over 2048, transposed form:
+// 119 and 112 us; 400 x 400 over 600, three pieces, four splits: 13.4 us in
+// 128 x 128 tiles, 8.2 us in 64 x 64 tiles.  (Three pieces: the large tile's
+// fragments do not fit the registers.)
 enum { NS_256x128, NS_128x128, NS_64x64 };
 static void ns_plan(int64_t I, int64_t J, int64_t K, int np, int* tile, int* ksplit) {
-    struct C { int id, ti, tj, per_cu; double step; };
-    const C cands[] = {{NS_256x128, 256, 128, 1, 1.40}, {NS_128x128, 128, 128, 1, 0.78}, {NS_64x64, 64, 64, 2, 0.9}};
+    struct C { int id, ti, tj, per_cu; double fixed, step2, step3; };   // us
+    const C cands[] = {{NS_256x128, 256, 128, 1, 9.0, 1.30, 0.0}, {NS_128x128, 128, 128, 1, 6.5, 0.76, 1.25},
+                       {NS_64x64, 64, 64, 2, 3.3, 0.70, 1.0}};
     const double cus = (double)device_rates().cus;
     const int64_t steps = (K + 31) / 32;
     double best = 1e300;
@@ -1068,8 +1071,9 @@ static void ns_plan(int64_t I, int64_t J, int64_t K, int np, int* tile, int* ksp
         const double tiles = (double)((I + c.ti - 1) / c.ti) * (double)((J + c.tj - 1) / c.tj);
         for (int ks = 1; ks <= 64; ks *= 2) {
             if (ks > 1 && ks * 4 > steps) break;
-            double t = std::ceil(tiles * ks / (cus * c.per_cu)) * (double)((steps + ks - 1) / ks + 3) * c.step;
-            if (ks > 1) t += 4.0 + (double)I * (double)J * 4.0 * (ks + 1) / 4e6;
+            double t = std::ceil(tiles * ks / (cus * c.per_cu)) *
+                       (c.fixed + (double)((steps + ks - 1) / ks) * (np == 2 ? c.step2 : c.step3));
+            if (ks > 1) t += 3.5 + (double)I * (double)J * 4.0 * (ks + 1) / 4e6;
             if (t < best) { best = t; *tile = c.id; *ksplit = ks; }
         }
     }
