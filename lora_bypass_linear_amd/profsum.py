@@ -29,7 +29,7 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # the sources each profiled kernel is built from
-SOURCES = {"gemm": ("csrc/gemm.hip", "csrc/kernels.h", "csrc/lyc_device.h"),
+SOURCES = {"gemm": ("csrc/gemm.hip", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h"),
            "hpass": ("csrc/hpass.hip", "csrc/kernels.h", "csrc/lyc_device.h"),
            "merge": ("csrc/merge.hip", "csrc/merge.h", "csrc/lyc_device.h")}
 
