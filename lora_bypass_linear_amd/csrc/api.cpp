@@ -803,11 +803,22 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
     }
 
     // gh_r = round_c(scale * dy_c . up_c): the h pass over dy with b = up_c^T
+    // (over an 8-bit base one launch makes up^T, down^T and dy's codes)
+    bool prepped = false;
     if (L.need_gh && M > 0 && N == 0) {
         // no outputs: gh = 0 (a transpose of an empty source writes only its zero padding)
         if (!transpose(W, P.c_dt, 0, 0, W + L.gh, P.r_pad, M)) return LYC_ERR_HIP;
     } else if (L.need_gh && M > 0) {
-        if (!transpose(up, P.u_dt, N, r, W + L.ut, N, P.r_pad)) return LYC_ERR_HIP;
+        prepped = P.w8 && wdx && K > 0 && esize(P.u_dt) == esize(P.d_dt);
+        if (prepped) {
+            const lyc::TransposeParams tu{up, P.u_dt, N, r, W + L.ut, P.c_dt, N, P.r_pad};
+            const lyc::TransposeParams td{down, P.d_dt, r, K, W + L.dt, P.c_dt, P.r_pad, K};
+            const lyc::QuantRowsParams qd{dy, B.dy_dt, W + L.gq, (float*)(W + L.gs), M, N};
+            if (timed(LYC_KERNEL_PREP, s, [&] { return lyc::launch_bwd_prep(tu, td, qd, s); }) != hipSuccess)
+                return LYC_ERR_HIP;
+        } else if (!transpose(up, P.u_dt, N, r, W + L.ut, N, P.r_pad)) {
+            return LYC_ERR_HIP;
+        }
         if (L.gh_dot) {
             lyc::HdotParams hq{};
             hq.x = ga;
@@ -851,7 +862,7 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
     if (wdx && M > 0 && K > 0) {
         lyc::GemmParams g{};
         if (!wt_given && N > 0 && !transpose(w, P.w_dt, N, K, W + L.wt, N, K)) return LYC_ERR_HIP;
-        if (r > 0 && !transpose(down, P.d_dt, r, K, W + L.dt, P.r_pad, K)) return LYC_ERR_HIP;
+        if (r > 0 && !prepped && !transpose(down, P.d_dt, r, K, W + L.dt, P.r_pad, K)) return LYC_ERR_HIP;
         g.a = wt_given ? w_t : (const void*)(W + L.wt);
         g.af = r > 0 ? (const void*)(W + L.dt) : nullptr;
         g.b = ga;
@@ -868,7 +879,7 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
         g.partial = L.ks_dx > 1 ? (float*)(W + L.partial) : nullptr;
         g.vec_store = (K % 4 == 0) && aligned(dx, P.x_dt == LYC_F32 ? 16 : 8);
         if (P.w8) {
-            if (N > 0 && timed(LYC_KERNEL_PREP, s, [&] {
+            if (N > 0 && !prepped && timed(LYC_KERNEL_PREP, s, [&] {
                     return lyc::launch_quant_rows(
                         lyc::QuantRowsParams{dy, B.dy_dt, W + L.gq, (float*)(W + L.gs), M, N}, s);
                 }) != hipSuccess)

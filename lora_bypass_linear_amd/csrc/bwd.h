@@ -18,5 +18,9 @@ struct TransposeParams {
     int64_t rows_pad, cols_pad;  // dst [cols_pad][rows_pad]; rows_pad >= rows, cols_pad >= cols
 };
 hipError_t launch_transpose(const TransposeParams& p, hipStream_t s);
+// both factors' transposed copies (stored dtypes of one size) and dy's
+// quantization in one launch
+struct QuantRowsParams;
+hipError_t launch_bwd_prep(const TransposeParams& u, const TransposeParams& d, const QuantRowsParams& q, hipStream_t s);
 
 }  // namespace lyc

@@ -6,6 +6,7 @@
 // with zero padding to 8-element rows.
 #include "bwd.h"
 #include "lyc_device.h"
+#include "quant_device.h"
 
 namespace lyc {
 
@@ -19,10 +20,9 @@ __device__ __forceinline__ float widen_t(T v, int dt) {
 // rows and the writes along destination rows (64 consecutive elements per
 // wave instruction on both sides).
 template <class T>
-__global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p, int64_t tiles_r) {
-    __shared__ float t[64][65];
+__device__ __forceinline__ void transpose_body(const TransposeParams& p, int64_t tile, int64_t tiles_r, float (*t)[65]) {
     const int tid = threadIdx.x, l = tid & 63, g = tid >> 6;
-    const int64_t r0 = ((int64_t)blockIdx.x % tiles_r) * 64, c0 = ((int64_t)blockIdx.x / tiles_r) * 64;
+    const int64_t r0 = (tile % tiles_r) * 64, c0 = (tile / tiles_r) * 64;
     const T* src = (const T*)p.src;
     // loads: 16 rows per thread (g, g+4, ...), column l; clamped, then masked
     float v[16];
@@ -46,6 +46,48 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p, int64
         if (p.c_dt == DT_F32) ((float*)p.dst)[at] = x;
         else ((uint16_t*)p.dst)[at] = p.c_dt == DT_F16 ? f32_to_f16(x) : f32_to_bf16(x);
     }
+}
+
+template <class T>
+__global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p, int64_t tiles_r) {
+    __shared__ float t[64][65];
+    transpose_body<T>(p, blockIdx.x, tiles_r, t);
+}
+
+// What the backward over an 8-bit base prepares, in one launch: up^T, down^T
+// (workgroups below na, below nb) and dy quantized (the rest).
+template <class T, int DT>
+__global__ __launch_bounds__(256) void bwd_prep_kernel(TransposeParams u, TransposeParams d, QuantRowsParams q, unsigned na,
+                                                       unsigned nb, int pairs) {
+    __shared__ float t[64][65];
+    if (blockIdx.x < na) transpose_body<T>(u, blockIdx.x, (u.rows_pad + 63) / 64, t);
+    else if (blockIdx.x < nb) transpose_body<T>(d, blockIdx.x - na, (d.rows_pad + 63) / 64, t);
+    else quant_rows_body<DT>(q, blockIdx.x - nb, pairs);
+}
+
+static int64_t transpose_tiles(const TransposeParams& p) {
+    return ((p.rows_pad + 63) / 64) * ((p.cols_pad + 63) / 64);
+}
+
+template <class T>
+static hipError_t run_bwd_prep(const TransposeParams& u, const TransposeParams& d, const QuantRowsParams& q,
+                               hipStream_t s) {
+    const int pairs = quant_pairs(q.K);
+    const int64_t na = transpose_tiles(u), nb = na + transpose_tiles(d), all = nb + (q.M + 15) / 16 * pairs;
+    if (all >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    const dim3 g((unsigned)all);
+    if (q.x_dt == DT_F32)
+        hipLaunchKernelGGL((bwd_prep_kernel<T, DT_F32>), g, dim3(256), 0, s, u, d, q, (unsigned)na, (unsigned)nb, pairs);
+    else if (q.x_dt == DT_F16)
+        hipLaunchKernelGGL((bwd_prep_kernel<T, DT_F16>), g, dim3(256), 0, s, u, d, q, (unsigned)na, (unsigned)nb, pairs);
+    else
+        hipLaunchKernelGGL((bwd_prep_kernel<T, DT_BF16>), g, dim3(256), 0, s, u, d, q, (unsigned)na, (unsigned)nb, pairs);
+    return hipGetLastError();
+}
+
+hipError_t launch_bwd_prep(const TransposeParams& u, const TransposeParams& d, const QuantRowsParams& q, hipStream_t s) {
+    if ((u.src_dt == DT_F32) != (d.src_dt == DT_F32)) return hipErrorInvalidValue;
+    return u.src_dt == DT_F32 ? run_bwd_prep<uint32_t>(u, d, q, s) : run_bwd_prep<uint16_t>(u, d, q, s);
 }
 
 hipError_t launch_transpose(const TransposeParams& p, hipStream_t s) {

@@ -477,6 +477,7 @@ struct ThinParams {
     float sx;           // the power of two that scales X after the first segment
     void* out;          // [R][C]
     int tall;
+    int vec_out;        // out's rows hold whole groups of 4 elements, aligned for one store each
 };
 
 __device__ __forceinline__ int exponent_of(uint32_t abs_bits) { return (int)(abs_bits >> 23) - 127; }
@@ -974,6 +975,20 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
                 for (int c = 0; c < S::CB; ++c) {
                     // wide: row i of the block, 4 consecutive columns; tall: the other way round
                     const int64_t i = ib * 16 + (p.tall ? 4 * g : r), cc = c0 + (cb0 + c) * 16 + (p.tall ? r : 4 * g);
+                    if (p.vec_out) {   // the four are inside the row, or none is
+                        if (i >= p.n || cc >= p.m) continue;
+                        const f32x4 val = acc[c][0] * f;
+                        const int64_t o = p.tall ? cc * p.n + i : i * p.m + cc;
+                        if (p.dt == DT_F32) {
+                            *(f32x4*)((float*)p.out + o) = val;
+                        } else {
+                            const bool h = p.dt == DT_F16;
+                            const uint32_t lo = h ? pack_f16x2(val[0], val[1]) : pack_bf16x2(val[0], val[1]);
+                            const uint32_t hi = h ? pack_f16x2(val[2], val[3]) : pack_bf16x2(val[2], val[3]);
+                            *(i32x2*)((uint16_t*)p.out + o) = i32x2{(int)lo, (int)hi};
+                        }
+                        continue;
+                    }
 #pragma unroll
                     for (int el = 0; el < 4; ++el) {
                         const int64_t ie = p.tall ? i + el : i, ce = p.tall ? cc : cc + el;
@@ -1299,6 +1314,7 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
     }
     // (bf16 pieces have fp32's range)
     t.sx = NP == 2 ? (float)pow2_under(std::sqrt(topx)) : 1.0f;
+    t.vec_out = (t.tall ? t.n : t.m) % 4 == 0 && ((uintptr_t)p.out & (p.dt == DT_F32 ? 15 : 7)) == 0;
     t.vec = (t.tall ? t.n : t.m) % 8 == 0 && ((uintptr_t)p.g & 15) == 0;
     // steps a segment: as many as Q's largest factor stays small for (its
     // rounding is relative to it), evenly shared
