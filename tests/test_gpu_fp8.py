@@ -378,3 +378,31 @@ def test_offsets_past_32_bits():
     xv, wv = R.rows_value(_bits(q1), s1.cpu().numpy()), R.tiles_value(_bits(wq), wsc.cpu().numpy())
     exact, mass = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
     assert np.all(np.abs(R.f64(y) - exact) <= R.product_bound(exact, mass, 128 + K // 128 + 8, F32))
+
+
+@pytest.mark.parametrize("M", [5, 200])
+@pytest.mark.parametrize("c", [F16, BF16])
+def test_fp32_activations_with_16_bit_factors(M, c):
+    """x and dy in fp32 beside 16-bit factors: the codes come from them as
+    stored, the bypass from them rounded to the compute dtype, y and dx are fp32."""
+    N, K, r, scale = 272, 528, 12, 0.5
+    say("fp8 fp32 activations", M, c)
+    t = _layer(61, M, N, K, r, F32, c)
+    wq, wsc, wqt = L.fp8_quantize_weight(t["w"], transposed=True)
+    y = L.fp8_lora_linear(t["x"], wq, wsc, t["down"], t["up"], scale)
+    dx, dd, du = L.fp8_lora_linear_backward(t["x"], wqt, wsc, t["down"], t["up"], scale, t["dy"])
+    assert (y.dtype, dx.dtype, dd.dtype, du.dtype) == (F32, F32, c, c)
+    wv = R.tiles_value(_bits(wq), wsc.cpu().numpy())
+    xv, gv = R.rows_value(*R.quantize_rows(t["x"])), R.rows_value(*R.quantize_rows(t["dy"]))
+    xc, gc = R.f64(t["x"].to(c)), R.f64(t["dy"].to(c))
+    de, ue = R.f64(t["down"]), R.f64(t["up"])
+    h, gh = _round(xc @ de.T, c), _round(scale * (gc @ ue), c)
+    for name, got, exact, mass, terms in (
+            ("y", y, xv @ wv.T + scale * (h @ ue.T), np.abs(xv) @ np.abs(wv).T + scale * (np.abs(h) @ np.abs(ue).T),
+             128 + 5 + r + 8),
+            ("dx", dx, gv @ wv + gh @ de, np.abs(gv) @ np.abs(wv) + np.abs(gh) @ np.abs(de), 128 + 3 + r + 8),
+            ("d_down", dd, gh.T @ xc, np.abs(gh).T @ np.abs(xc), M + 8),
+            ("d_up", du, scale * (gc.T @ h), scale * (np.abs(gc).T @ np.abs(h)), M + 8)):
+        err = np.abs(R.f64(got) - exact)
+        bound = R.product_bound(exact, mass, terms, got.dtype)
+        assert np.all(err <= bound), (name, float((err / bound).max()))
