@@ -195,21 +195,43 @@ struct NsParams {
     int mode;
     void* out;
     int dt;
+    int sym;          // out is symmetric: only tiles that reach i >= j, mirrored by ns_sym_reduce_kernel
     int ksplit;
-    float* partial;   // [ksplit][J][I rounded up to 4] when ksplit > 1
+    float* partial;   // [ksplit][J][I rounded up to 4] when ksplit > 1 or sym
 };
 
+// the finished values of four consecutive i of row j from their sums (i a
+// multiple of 4 inside a row of pieces; zeros past I)
 template <int NP>
-__device__ __forceinline__ float ns_value(const NsParams& p, float sum, int64_t j, int64_t i) {
-    float v = sum * p.alpha;
-    if (p.mode == NS_POLY) {
-        uint16_t w[NP];
+__device__ __forceinline__ void ns_values4(const NsParams& p, f32x4 s, int64_t j, int64_t i, float (&v)[4]) {
 #pragma unroll
-        for (int k = 0; k < NP; ++k) w[k] = p.old.p[k * p.old.stride + j * p.old.ld + i];
-        v = p.c * v + p.b * (Pieces<NP>::join(w) * p.old_inv);
-        if (i == j) v += p.a;
+    for (int e = 0; e < 4; ++e) v[e] = s[e] * p.alpha;
+    if (p.mode == NS_POLY) {
+        i32x2 w[NP];
+#pragma unroll
+        for (int k = 0; k < NP; ++k) w[k] = *(const i32x2*)(p.old.p + k * p.old.stride + j * p.old.ld + i);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            uint16_t u[NP];
+#pragma unroll
+            for (int k = 0; k < NP; ++k) u[k] = (uint16_t)((uint32_t)w[k][e >> 1] >> (e & 1) * 16);
+            v[e] = p.c * v[e] + p.b * (Pieces<NP>::join(u) * p.old_inv);
+            if (i + e == j) v[e] += p.a;
+        }
     }
-    return v;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] = i + e < p.I ? v[e] : 0.f;
+}
+
+template <int NP>
+__device__ __forceinline__ void ns_store4(const NsParams& p, const float (&v)[4], int64_t j, int64_t i) {
+    uint16_t o[4][NP];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) Pieces<NP>::split(v[e] * p.scale, o[e]);
+#pragma unroll
+    for (int k = 0; k < NP; ++k)
+        *(i32x2*)(p.o.p + k * p.o.stride + j * p.o.ld + i) =
+            i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16), (int)((uint32_t)o[2][k] | (uint32_t)o[3][k] << 16)};
 }
 
 // four consecutive i of row j (j < J; i past the row's end masked)
@@ -219,7 +241,7 @@ __device__ __forceinline__ void ns_finish4(const NsParams& p, f32x4 s, int64_t j
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (i + e >= p.I) continue;
-            const float v = ns_value<NP>(p, s[e], j, i + e);
+            const float v = s[e] * p.alpha;
             const int64_t at = j * p.I + i + e;
             if (p.dt == DT_F32) ((float*)p.out)[at] = v;
             else ((uint16_t*)p.out)[at] = p.dt == DT_F16 ? f32_to_f16(v) : f32_to_bf16(v);
@@ -227,16 +249,9 @@ __device__ __forceinline__ void ns_finish4(const NsParams& p, f32x4 s, int64_t j
         return;
     }
     if (i >= p.o.ld) return;   // (ld a multiple of 8: all four or none)
-    uint16_t o[4][NP];
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-        const float v = i + e < p.I ? ns_value<NP>(p, s[e], j, i + e) : 0.f;
-        Pieces<NP>::split(v * p.scale, o[e]);
-    }
-#pragma unroll
-    for (int k = 0; k < NP; ++k)
-        *(i32x2*)(p.o.p + k * p.o.stride + j * p.o.ld + i) =
-            i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16), (int)((uint32_t)o[2][k] | (uint32_t)o[3][k] << 16)};
+    float v[4];
+    ns_values4<NP>(p, s, j, i, v);
+    ns_store4<NP>(p, v, j, i);
 }
 
 // One side's rows of a K step (32 k) in LDS, and its loads.
@@ -304,6 +319,12 @@ struct NsSide {
     }
 };
 
+// tiles of tile row ti that hold an element with i >= j
+__host__ __device__ __forceinline__ int sym_tiles(int ti, int TI, int TJ, int tiles_j) {
+    const int c = (ti * TI + TI - 1) / TJ + 1;
+    return c < tiles_j ? c : tiles_j;
+}
+
 // TI x TJ output tile per workgroup of WVI x WVJ waves, NS stages of one K
 // step (32 k of every piece of both sides).
 template <int NP, bool TR, int TI, int TJ, int WVI, int WVJ, int NS>
@@ -318,7 +339,18 @@ __global__ __launch_bounds__(64 * WVI * WVJ, 1) void ns_gemm_kernel(NsParams p, 
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wi = wave % WVI, wj = wave / WVI;
     int ti, tj;
-    tile_coords(blockIdx.x, gridDim.x, tiles_i, tiles_j, 4, ti, tj);
+    if (p.sym) {
+        // the first tj of row ti are wanted; each XCD takes a run of the list
+        const int n = gridDim.x, per = n >> 3, rem = n & 7, xcd = blockIdx.x & 7;
+        tj = xcd * per + (xcd < rem ? xcd : rem) + ((int)blockIdx.x >> 3);
+        for (ti = 0;; ++ti) {
+            const int c = sym_tiles(ti, TI, TJ, tiles_j);
+            if (tj < c) break;
+            tj -= c;
+        }
+    } else {
+        tile_coords(blockIdx.x, gridDim.x, tiles_i, tiles_j, 4, ti, tj);
+    }
     const int64_t i0 = (int64_t)ti * TI, j0 = (int64_t)tj * TJ;
     SideU su;
     SideV sv;
@@ -401,7 +433,7 @@ __global__ __launch_bounds__(64 * WVI * WVJ, 1) void ns_gemm_kernel(NsParams p, 
         for (int j = 0; j < FJ; ++j) {
             const int64_t oj = j0 + wj * WJ + j * 16 + r;
             if (oj >= p.J) continue;
-            if (p.ksplit > 1) {
+            if (p.ksplit > 1 || p.sym) {
                 const int64_t ldp = (p.I + 3) & ~(int64_t)3;
                 if (oi < ldp) *(f32x4*)(p.partial + ((int64_t)blockIdx.y * p.J + oj) * ldp + oi) = acc[i][j];
             } else {
@@ -424,6 +456,43 @@ __global__ __launch_bounds__(256) void ns_reduce_kernel(NsParams p) {
         if (i < ldp)
             for (int k = 0; k < p.ksplit; ++k) s += *(const f32x4*)(p.partial + ((int64_t)k * p.J + j) * ldp + i);
         ns_finish4<NP>(p, s, j, i);
+    }
+}
+
+// The same for a symmetric output of which the tiles reaching i >= j were
+// computed: a 64 x 64 block with i >= j a workgroup (tiles are multiples of
+// 64, so every such block is whole), written as it is and mirrored through LDS.
+template <int NP>
+__global__ __launch_bounds__(256) void ns_sym_reduce_kernel(NsParams p) {
+    __shared__ float tile[64][65];
+    const int64_t ldp = (p.I + 3) & ~(int64_t)3;
+    int bi = 0, bj = blockIdx.x;
+    while (bj > bi) bj -= ++bi;
+    const int row = threadIdx.x >> 4, quad = (threadIdx.x & 15) * 4;
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int64_t j = (int64_t)bj * 64 + u * 16 + row, i = (int64_t)bi * 64 + quad;
+        float v[4] = {0.f, 0.f, 0.f, 0.f};
+        if (j < p.J && i < p.o.ld) {
+            f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
+            if (i < ldp)
+                for (int k = 0; k < p.ksplit; ++k) s += *(const f32x4*)(p.partial + ((int64_t)k * p.J + j) * ldp + i);
+            ns_values4<NP>(p, s, j, i, v);
+            ns_store4<NP>(p, v, j, i);
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) tile[u * 16 + row][quad + e] = v[e];
+    }
+    if (bi == bj) return;
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+        const int64_t j = (int64_t)bi * 64 + u * 16 + row, i = (int64_t)bj * 64 + quad;
+        if (j >= p.J) continue;   // (i is inside: block bj is before the last)
+        float v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = tile[quad + e][u * 16 + row];
+        ns_store4<NP>(p, v, j, i);
     }
 }
 
@@ -1076,26 +1145,35 @@ static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 // 128 x 128 tiles, 8.2 us in 64 x 64 tiles.  (Three pieces: the large tile's
 // fragments do not fit the registers.)
 enum { NS_256x128, NS_128x128, NS_64x64 };
-static void ns_plan(int64_t I, int64_t J, int64_t K, int np, int* tile, int* ksplit) {
+struct NsPlan {
+    int tile, ksplit, sym, blocks;   // blocks: workgroups of one split
+};
+static NsPlan ns_plan(int64_t I, int64_t J, int64_t K, int np, bool symmetric) {
     struct C { int id, ti, tj, per_cu; double fixed, step2, step3; };   // us
     const C cands[] = {{NS_256x128, 256, 128, 1, 9.0, 1.30, 0.0}, {NS_128x128, 128, 128, 1, 6.5, 0.76, 1.25},
                        {NS_64x64, 64, 64, 2, 3.3, 0.70, 1.0}};
     const double cus = (double)device_rates().cus;
     const int64_t steps = (K + 31) / 32;
     double best = 1e300;
-    *tile = NS_64x64;
-    *ksplit = 1;
+    NsPlan plan{NS_64x64, 1, 0, 0};
     for (const C& c : cands) {
         if (c.id == NS_256x128 && np != 2) continue;
-        const double tiles = (double)((I + c.ti - 1) / c.ti) * (double)((J + c.tj - 1) / c.tj);
-        for (int ks = 1; ks <= 64; ks *= 2) {
-            if (ks > 1 && ks * 4 > steps) break;
-            double t = std::ceil(tiles * ks / (cus * c.per_cu)) *
-                       (c.fixed + (double)((steps + ks - 1) / ks) * (np == 2 ? c.step2 : c.step3));
-            if (ks > 1) t += 3.5 + (double)I * (double)J * 4.0 * (ks + 1) / 4e6;
-            if (t < best) { best = t; *tile = c.id; *ksplit = ks; }
+        const int64_t ni = (I + c.ti - 1) / c.ti, nj = (J + c.tj - 1) / c.tj;
+        for (int sym = 0; sym <= (symmetric ? 1 : 0); ++sym) {
+            int64_t blocks = sym ? 0 : ni * nj;
+            if (sym)
+                for (int64_t i = 0; i < ni; ++i) blocks += sym_tiles((int)i, c.ti, c.tj, (int)nj);
+            for (int u = 0; u < 12; ++u) {
+                const int ks = (u & 1 ? 3 : 2) << (u >> 1) >> 1;   // 1, 1, 2, 3, 4, 6, 8, .. 48
+                if (ks > 1 && ks * 4 > steps) break;
+                double t = std::ceil((double)blocks * ks / (cus * c.per_cu)) *
+                           (c.fixed + (double)((steps + ks - 1) / ks) * (np == 2 ? c.step2 : c.step3));
+                if (ks > 1 || sym) t += 3.5 + (double)I * (double)J * 4.0 * (sym ? 0.5 * ks + 1 : ks + 1) / 4e6;
+                if (t < best) { best = t; plan = NsPlan{c.id, ks, sym, (int)blocks}; }
+            }
         }
     }
+    return plan;
 }
 
 // powers of two that keep a matrix of the given spectral norm inside fp16
@@ -1144,33 +1222,39 @@ static NsLayout ns_layout(int64_t R, int64_t C, int dt) {
     take(L.A, np * (size_t)(n * L.ldn) * 2);
     take(L.P, np * (size_t)(n * L.ldn) * 2);
     size_t part = 0;
-    int t, ks;
-    ns_plan(n, n, m, (int)np, &t, &ks);
-    if (ks > 1) part = std::max(part, (size_t)ks * (size_t)(n * ((n + 3) & ~(int64_t)3)) * 4);
-    ns_plan(n, n, n, (int)np, &t, &ks);
-    if (ks > 1) part = std::max(part, (size_t)ks * (size_t)(n * ((n + 3) & ~(int64_t)3)) * 4);
-    ns_plan(C, R, n, (int)np, &t, &ks);
-    if (ks > 1) part = std::max(part, (size_t)ks * (size_t)(R * ((C + 3) & ~(int64_t)3)) * 4);
+    auto partial = [&](int64_t I, int64_t J, int64_t K, bool symmetric) {
+        const NsPlan q = ns_plan(I, J, K, (int)np, symmetric);
+        if (q.ksplit > 1 || q.sym) part = std::max(part, (size_t)q.ksplit * (size_t)(J * ((I + 3) & ~(int64_t)3)) * 4);
+    };
+    partial(n, n, m, true);
+    partial(n, n, n, true);
+    partial(C, R, n, false);
     take(L.partial, part);
     L.total = off;
     return L;
 }
 
 template <int NP, bool TR>
-static hipError_t ns_product(NsParams p, hipStream_t s) {
-    int t;
-    ns_plan(p.I, p.J, p.K, NP, &t, &p.ksplit);
+static hipError_t ns_product(NsParams p, bool symmetric, hipStream_t s) {
+    const NsPlan plan = ns_plan(p.I, p.J, p.K, NP, symmetric);
+    p.ksplit = plan.ksplit;
+    p.sym = plan.sym;
     auto launch = [&](auto kernel, int ti, int tj, int threads) {
         const int ni = (int)((p.I + ti - 1) / ti), nj = (int)((p.J + tj - 1) / tj);
-        hipLaunchKernelGGL(kernel, dim3((unsigned)(ni * nj), (unsigned)p.ksplit), dim3(threads), 0, s, p, ni, nj);
+        hipLaunchKernelGGL(kernel, dim3((unsigned)plan.blocks, (unsigned)p.ksplit), dim3(threads), 0, s, p, ni, nj);
     };
     if constexpr (NP == 2) {
-        if (t == NS_256x128) launch(ns_gemm_kernel<NP, TR, 256, 128, 4, 2, 3>, 256, 128, 512);
+        if (plan.tile == NS_256x128) launch(ns_gemm_kernel<NP, TR, 256, 128, 4, 2, 3>, 256, 128, 512);
     }
-    if (t == NS_128x128) launch(ns_gemm_kernel<NP, TR, 128, 128, 2, 4, NP == 2 ? 4 : 3>, 128, 128, 512);
-    else if (t == NS_64x64) launch(ns_gemm_kernel<NP, TR, 64, 64, 2, 2, 3>, 64, 64, 256);
+    if (plan.tile == NS_128x128) launch(ns_gemm_kernel<NP, TR, 128, 128, 2, 4, NP == 2 ? 4 : 3>, 128, 128, 512);
+    else if (plan.tile == NS_64x64) launch(ns_gemm_kernel<NP, TR, 64, 64, 2, 2, 3>, 64, 64, 256);
     hipError_t e = hipGetLastError();
-    if (e == hipSuccess && p.ksplit > 1) {
+    if (e != hipSuccess) return e;
+    if (p.sym) {
+        const int64_t nb = (p.I + 63) / 64;
+        hipLaunchKernelGGL(ns_sym_reduce_kernel<NP>, dim3((unsigned)(nb * (nb + 1) / 2)), dim3(256), 0, s, p);
+        e = hipGetLastError();
+    } else if (p.ksplit > 1) {
         const int64_t q = p.J * ((p.mode == NS_OUT ? (p.I + 3) / 4 : p.o.ld / 4));
         hipLaunchKernelGGL(ns_reduce_kernel<NP>, dim3((unsigned)std::min<int64_t>((q + 255) / 256, 4096)), dim3(256), 0, s, p);
         e = hipGetLastError();
@@ -1224,7 +1308,7 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
         q.alpha = (float)(1.0 / (sx * sx));
         q.scale = (float)sa;
         q.mode = NS_SPLIT;
-        e = tall ? ns_product<NP, true>(q, s) : ns_product<NP, false>(q, s);
+        e = tall ? ns_product<NP, true>(q, true, s) : ns_product<NP, false>(q, true, s);
         if (e != hipSuccess) return e;
         // P = a I + b A + c A A
         q.u = q.v = q.old = A;
@@ -1237,7 +1321,7 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
         q.b = (float)p.b;
         q.c = (float)p.c;
         q.mode = NS_POLY;
-        if ((e = ns_product<NP, false>(q, s)) != hipSuccess) return e;
+        if ((e = ns_product<NP, false>(q, true, s)) != hipSuccess) return e;
         // X <- P X (stored [R][C]: i runs over C, j over R)
         q.alpha = (float)(1.0 / (sx * sp));
         q.scale = (float)sx;
@@ -1251,11 +1335,11 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
         if (tall) {
             q.u = P;
             q.v = cur;
-            e = ns_product<NP, false>(q, s);
+            e = ns_product<NP, false>(q, false, s);
         } else {
             q.u = cur;
             q.v = P;
-            e = ns_product<NP, true>(q, s);
+            e = ns_product<NP, true>(q, false, s);
         }
         if (e != hipSuccess) return e;
     }

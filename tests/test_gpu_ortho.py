@@ -70,6 +70,15 @@ def test_large(R, C):
     _check(g, L.orthogonalize(g.cuda()))
 
 
+@pytest.mark.parametrize("dt,R,C", [(F32, 700, 1001), (F16, 1001, 700), (F32, 1501, 1290), (BF16, 1900, 2061)])
+def test_halves_mirrored(dt, R, C):
+    """Sizes whose two symmetric products are computed on and below the
+    diagonal and mirrored, each tile with ragged edges."""
+    say("ortho halves", R, C, dt)
+    g = _update(R + C, R, C, dt)
+    _check(g, L.orthogonalize(g.cuda()))
+
+
 @pytest.mark.parametrize("steps", [1, 2, 3, 4, 6, 7, 9])
 @pytest.mark.parametrize("dt,R,C", [(BF16, 24, 300), (F32, 300, 24), (F16, 150, 200)])
 def test_steps(steps, dt, R, C):
