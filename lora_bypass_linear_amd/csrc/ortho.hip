@@ -182,8 +182,8 @@ __global__ __launch_bounds__(256) void ns_split_kernel(const void* g, int dt, in
 enum { NS_SPLIT = 0, NS_POLY = 1, NS_OUT = 2 };
 
 // out(j, i) = finish( alpha * sum_k U(i, k) V(j, k) ), i < I, j < J, k < K.
-// Rows-as-stored form: u [I][ld], v [J][ld], k consecutive.  Transposed form:
-// u [K][ld], v [K][ld].
+// Each of u and v rows-as-stored ([I or J][ld], k consecutive) or transposed
+// ([K][ld]).
 //   NS_SPLIT: v' = sum                      into pieces, times `scale`
 //   NS_POLY:  v' = a delta_ij + b A + c sum into pieces, times `scale`; A from `old`
 //   NS_OUT:   v' into out [J][I] of dtype dt
@@ -327,11 +327,11 @@ __host__ __device__ __forceinline__ int sym_tiles(int ti, int TI, int TJ, int ti
 
 // TI x TJ output tile per workgroup of WVI x WVJ waves, NS stages of one K
 // step (32 k of every piece of both sides).
-template <int NP, bool TR, int TI, int TJ, int WVI, int WVJ, int NS>
+template <int NP, bool TRU, bool TRV, int TI, int TJ, int WVI, int WVJ, int NS>
 __global__ __launch_bounds__(64 * WVI * WVJ, 1) void ns_gemm_kernel(NsParams p, int tiles_i, int tiles_j) {
     constexpr int NW = WVI * WVJ, WI = TI / WVI, WJ = TJ / WVJ, FI = WI / 16, FJ = WJ / 16;
-    using SideU = NsSide<TI, NW, TR>;
-    using SideV = NsSide<TJ, NW, TR>;
+    using SideU = NsSide<TI, NW, TRU>;
+    using SideV = NsSide<TJ, NW, TRV>;
     constexpr int STAGE = NP * (SideU::BYTES + SideV::BYTES), Q = NP * (SideU::Q + SideV::Q);
     static_assert(NS * STAGE <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(16))) char smem[NS * STAGE];
@@ -398,10 +398,10 @@ __global__ __launch_bounds__(64 * WVI * WVJ, 1) void ns_gemm_kernel(NsParams p, 
         __builtin_amdgcn_sched_barrier(0);
         read(nx, kt + 1);
         piece_mma<NP>(f.a, f.b, acc);
-        if constexpr (!TR) {
+        if constexpr (!TRU && !TRV) {
             // a fragment read, then its share of the MFMAs (left alone, the
-            // compiler sinks the reads below them; the transposing reads' two
-            // halves a fragment made the registers spill so)
+            // compiler sinks the reads below them; with transposing reads, two
+            // halves a fragment, it took 112 us for 107 and registers spilled)
             constexpr int ND = NP * (FI + FJ), NM = FI * FJ * NP * (NP + 1) / 2;
 #pragma unroll
             for (int d = 0; d < ND; ++d) {
@@ -1139,11 +1139,16 @@ static size_t up256(size_t v) { return (v + 255) & ~(size_t)255; }
 // Tile and K split of an I x J product over K, by modelled time: rounds of
 // workgroups over the CUs (two of the small tile's share one) times a fixed
 // part and a K step's as measured, plus the partial sums' round trip of a
-// split.  2048 x 2048 over 4096, two pieces: 100 us in 128 x 128 tiles, 107 us
-// in 256 x 128 tiles with two splits; 4096 x 2048 over 2048, transposed form:
-// 119 and 112 us; 400 x 400 over 600, three pieces, four splits: 13.4 us in
-// 128 x 128 tiles, 8.2 us in 64 x 64 tiles.  (Three pieces: the large tile's
-// fragments do not fit the registers.)
+// split.  A symmetric output (A and P) may take the tiles that reach i >= j
+// alone, about half, with more splits to fill the device, and a reduction that
+// mirrors them.  us:
+//   A of 2048 x 4096, two pieces: 100 in 128 x 128 tiles, 107 in 256 x 128
+//     tiles with two splits; halved, 256 x 128, three splits: 64 + 11
+//   A^2 there: 67 in 128 x 128 tiles; halved as above: 37 + 11
+//   4096 x 2048 over 2048, X transposed: 119 in 128 x 128, 107 in 256 x 128
+//   400 x 400 over 600, three pieces, four splits: 13.4 in 128 x 128 tiles, 8.2
+//     in 64 x 64
+// (Three pieces: the large tile's fragments do not fit the registers.)
 enum { NS_256x128, NS_128x128, NS_64x64 };
 struct NsPlan {
     int tile, ksplit, sym, blocks;   // blocks: workgroups of one split
@@ -1234,7 +1239,7 @@ static NsLayout ns_layout(int64_t R, int64_t C, int dt) {
     return L;
 }
 
-template <int NP, bool TR>
+template <int NP, bool TRU, bool TRV>
 static hipError_t ns_product(NsParams p, bool symmetric, hipStream_t s) {
     const NsPlan plan = ns_plan(p.I, p.J, p.K, NP, symmetric);
     p.ksplit = plan.ksplit;
@@ -1244,10 +1249,10 @@ static hipError_t ns_product(NsParams p, bool symmetric, hipStream_t s) {
         hipLaunchKernelGGL(kernel, dim3((unsigned)plan.blocks, (unsigned)p.ksplit), dim3(threads), 0, s, p, ni, nj);
     };
     if constexpr (NP == 2) {
-        if (plan.tile == NS_256x128) launch(ns_gemm_kernel<NP, TR, 256, 128, 4, 2, 3>, 256, 128, 512);
+        if (plan.tile == NS_256x128) launch(ns_gemm_kernel<NP, TRU, TRV, 256, 128, 4, 2, 3>, 256, 128, 512);
     }
-    if (plan.tile == NS_128x128) launch(ns_gemm_kernel<NP, TR, 128, 128, 2, 4, NP == 2 ? 4 : 3>, 128, 128, 512);
-    else if (plan.tile == NS_64x64) launch(ns_gemm_kernel<NP, TR, 64, 64, 2, 2, 3>, 64, 64, 256);
+    if (plan.tile == NS_128x128) launch(ns_gemm_kernel<NP, TRU, TRV, 128, 128, 2, 4, NP == 2 ? 4 : 3>, 128, 128, 512);
+    else if (plan.tile == NS_64x64) launch(ns_gemm_kernel<NP, TRU, TRV, 64, 64, 2, 2, 3>, 64, 64, 256);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     if (p.sym) {
@@ -1308,7 +1313,7 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
         q.alpha = (float)(1.0 / (sx * sx));
         q.scale = (float)sa;
         q.mode = NS_SPLIT;
-        e = tall ? ns_product<NP, true>(q, true, s) : ns_product<NP, false>(q, true, s);
+        e = tall ? ns_product<NP, true, true>(q, true, s) : ns_product<NP, false, false>(q, true, s);
         if (e != hipSuccess) return e;
         // P = a I + b A + c A A
         q.u = q.v = q.old = A;
@@ -1321,7 +1326,7 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
         q.b = (float)p.b;
         q.c = (float)p.c;
         q.mode = NS_POLY;
-        if ((e = ns_product<NP, false>(q, true, s)) != hipSuccess) return e;
+        if ((e = ns_product<NP, false, false>(q, true, s)) != hipSuccess) return e;
         // X <- P X (stored [R][C]: i runs over C, j over R)
         q.alpha = (float)(1.0 / (sx * sp));
         q.scale = (float)sx;
@@ -1335,11 +1340,11 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
         if (tall) {
             q.u = P;
             q.v = cur;
-            e = ns_product<NP, false>(q, false, s);
+            e = ns_product<NP, false, false>(q, false, s);
         } else {
             q.u = cur;
             q.v = P;
-            e = ns_product<NP, true>(q, false, s);
+            e = ns_product<NP, true, false>(q, false, s);
         }
         if (e != hipSuccess) return e;
     }
