@@ -469,15 +469,27 @@ __global__ __launch_bounds__(256) void ns_sym_reduce_kernel(NsParams p) {
     int bi = 0, bj = blockIdx.x;
     while (bj > bi) bj -= ++bi;
     const int row = threadIdx.x >> 4, quad = (threadIdx.x & 15) * 4;
+    const int64_t i = (int64_t)bi * 64 + quad;
+    f32x4 s[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) s[u] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 3
+    for (int k = 0; k < p.ksplit; ++k) {
+        f32x4 w[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            const int64_t j = (int64_t)bj * 64 + u * 16 + row;
+            w[u] = j < p.J && i < ldp ? *(const f32x4*)(p.partial + ((int64_t)k * p.J + j) * ldp + i) : f32x4{0.f, 0.f, 0.f, 0.f};
+        }
+#pragma unroll
+        for (int u = 0; u < 4; ++u) s[u] += w[u];
+    }
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-        const int64_t j = (int64_t)bj * 64 + u * 16 + row, i = (int64_t)bi * 64 + quad;
+        const int64_t j = (int64_t)bj * 64 + u * 16 + row;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (j < p.J && i < p.o.ld) {
-            f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
-            if (i < ldp)
-                for (int k = 0; k < p.ksplit; ++k) s += *(const f32x4*)(p.partial + ((int64_t)k * p.J + j) * ldp + i);
-            ns_values4<NP>(p, s, j, i, v);
+            ns_values4<NP>(p, s[u], j, i, v);
             ns_store4<NP>(p, v, j, i);
         }
 #pragma unroll
@@ -487,12 +499,12 @@ __global__ __launch_bounds__(256) void ns_sym_reduce_kernel(NsParams p) {
     __syncthreads();
 #pragma unroll
     for (int u = 0; u < 4; ++u) {
-        const int64_t j = (int64_t)bi * 64 + u * 16 + row, i = (int64_t)bj * 64 + quad;
-        if (j >= p.J) continue;   // (i is inside: block bj is before the last)
+        const int64_t j = (int64_t)bi * 64 + u * 16 + row;
+        if (j >= p.J) continue;   // (the columns are inside: block bj is before the last)
         float v[4];
 #pragma unroll
         for (int e = 0; e < 4; ++e) v[e] = tile[quad + e][u * 16 + row];
-        ns_store4<NP>(p, v, j, i);
+        ns_store4<NP>(p, v, j, (int64_t)bj * 64 + quad);
     }
 }
 
