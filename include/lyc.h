@@ -423,9 +423,10 @@ int lyc_dora_linear_fwd(const void* x, int x_dt, const void* w, int w_dt, const 
  * lyc_fp8_linear_fwd: y = round_out( sum_kb s_x[kb][m] s_w[n/128][kb] *
  *   sum_{k in kb} q_x[m][k] q_w[n][k] + b[n] ) over the groups kb of 128, each
  *   group's sum added by one fp32 fused multiply-add; one final rounding.  For
- *   a 16-bit y the group's sum is one 8-bit MFMA, which keeps about 15 bits
- *   below the largest product of every 8 (far inside y's rounding); for an
- *   fp32 y it is 16-bit MFMAs of the widened codes, fp32 throughout.  y_dt is
+ *   a 16-bit y of more than 32 rows the group's sum is one 8-bit MFMA, which
+ *   keeps about 15 bits below the largest product of every 8 (far inside y's
+ *   rounding); for an fp32 y or up to 32 rows it is 16-bit MFMAs of the widened
+ *   codes, fp32 throughout.  y_dt is
  *   the caller's choice, and so is the bias's dtype (8-bit operands enter no
  *   dtype policy).
  */

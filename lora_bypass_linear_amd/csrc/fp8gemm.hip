@@ -16,9 +16,10 @@
 // every 8 consecutive k to the largest of them and keeps about 15 bits below
 // it (a product 2^-16 of its neighbour vanishes; across the groups of 8 it
 // sums in fp32): 1.6e-5 of a result's norm on normal data, a fifteenth of
-// fp16's rounding and a hundredth of bf16's, so 16-bit outputs take it.  fp32
-// outputs take EXACT: the codes widened to fp16, which holds every e4m3 value,
-// and summed by 16-bit MFMAs in fp32 at half the rate.
+// fp16's rounding and a hundredth of bf16's, so the tiles' 16-bit outputs take
+// it.  Their fp32 outputs, and every output of the few-row kernel, take EXACT:
+// the codes widened to fp16, which holds every e4m3 value, and summed by
+// 16-bit MFMAs in fp32 at half the rate.
 //  The LoRA fold runs first in the same pipeline with 16-bit (or fp32)
 // MFMAs, as in gemm.hip.
 #include <algorithm>
@@ -426,8 +427,10 @@ __global__ __launch_bounds__(TL::NT, 1) void fp8_gemm_kernel(Fp8GemmParams pp, i
 // blocks ahead (every weight byte is used once); the waves' sums meet in LDS
 // in wave order, wave 0's with the fold.  Bound by the weight's bytes: x's
 // rows, read by every workgroup from L2, cost as much again per 16 features,
-// so NF = 2 where that still leaves a workgroup per CU.
-template <class CT, int MT, int NF, int D, int NW, bool EXACT>
+// so NF = 2 where that still leaves a workgroup per CU.  The matrix pipe has
+// room, so the codes are widened and the sums are fp32 throughout: 14.5 us at
+// 16 x 8192 x 8192 where 8-bit MFMAs took 14.4, 56.7 for 54.8 at 16 x 28672 x 8192.
+template <class CT, int MT, int NF, int D, int NW>
 __global__ __launch_bounds__(64 * NW) void fp8_skinny_kernel(Fp8GemmParams pp) {
     const GemmParams& p = pp.g;
     __shared__ __attribute__((aligned(16))) f32x4 red[NW][NF][MT][64];
@@ -496,7 +499,7 @@ __global__ __launch_bounds__(64 * NW) void fp8_skinny_kernel(Fp8GemmParams pp) {
     for (int sb = s0; sb < se; sb += D) {
 #pragma unroll
         for (int u = 0; u < D; ++u) {
-            Frag8<EXACT> fx[MT];
+            Frag8<true> fx[MT];
             float sc[MT];
 #pragma unroll
             for (int t = 0; t < MT; ++t) {
@@ -505,11 +508,11 @@ __global__ __launch_bounds__(64 * NW) void fp8_skinny_kernel(Fp8GemmParams pp) {
             }
 #pragma unroll
             for (int f = 0; f < NF; ++f) {
-                Frag8<EXACT> fw;
+                Frag8<true> fw;
                 fw.set(wa[u][f][0], wa[u][f][1]);
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
-                    const f32x4 v = block_sum<EXACT>(fw, fx[t]);
+                    const f32x4 v = block_sum<true>(fw, fx[t]);
 #pragma unroll
                     for (int e = 0; e < 4; ++e) acc[f][t][e] = __builtin_fmaf(v[e], sc[t], acc[f][t][e]);
                 }
@@ -546,19 +549,19 @@ static bool fp8_skinny(int64_t M, int64_t K) {
     return M >= 1 && M <= 32 && K > 0 && 32 * K < ((int64_t)1 << 31);
 }
 
-template <class CT, int MT, int NF, bool EXACT>
+template <class CT, int MT, int NF>
 static hipError_t run_skinny8(const Fp8GemmParams& p, hipStream_t s) {
     // 4 waves, 2 blocks ahead: more waves or loads in flight were slower (16 x
     // 8192 x 8192: 14.6 us; 8 waves 19.4, 4 blocks ahead 15.0, 8 ahead 15.8)
-    hipLaunchKernelGGL((fp8_skinny_kernel<CT, MT, NF, 2, 4, EXACT>), dim3((unsigned)((p.g.N + 16 * NF - 1) / (16 * NF))),
+    hipLaunchKernelGGL((fp8_skinny_kernel<CT, MT, NF, 2, 4>), dim3((unsigned)((p.g.N + 16 * NF - 1) / (16 * NF))),
                        dim3(256), 0, s, p);
     return hipGetLastError();
 }
-template <class CT, bool EXACT>
+template <class CT>
 static hipError_t run_skinny8_ct(const Fp8GemmParams& p, hipStream_t s) {
     const bool wide = p.g.N >= 32 * device_rates().cus;
-    if (p.g.M <= 16) return wide ? run_skinny8<CT, 1, 2, EXACT>(p, s) : run_skinny8<CT, 1, 1, EXACT>(p, s);
-    return wide ? run_skinny8<CT, 2, 2, EXACT>(p, s) : run_skinny8<CT, 2, 1, EXACT>(p, s);
+    if (p.g.M <= 16) return wide ? run_skinny8<CT, 1, 2>(p, s) : run_skinny8<CT, 1, 1>(p, s);
+    return wide ? run_skinny8<CT, 2, 2>(p, s) : run_skinny8<CT, 2, 1>(p, s);
 }
 
 enum { T8_L, T8_M, T8_S };
@@ -631,10 +634,9 @@ static hipError_t run8_ct(const Fp8GemmParams& p, int t, hipStream_t s) {
 hipError_t launch_fp8_gemm(int c_dt, const Fp8GemmParams& p, hipStream_t s) {
     if (p.g.M <= 0 || p.g.N <= 0) return hipSuccess;
     if (p.g.ksplit <= 1 && fp8_skinny(p.g.M, p.g.K)) {
-        const bool exact = p.g.y_dt == DT_F32;
-        if (c_dt == DT_F16) return exact ? run_skinny8_ct<CF16, true>(p, s) : run_skinny8_ct<CF16, false>(p, s);
-        if (c_dt == DT_BF16) return exact ? run_skinny8_ct<CBF16, true>(p, s) : run_skinny8_ct<CBF16, false>(p, s);
-        return exact ? run_skinny8_ct<CF32, true>(p, s) : hipErrorInvalidValue;   // fp32 compute gives fp32 outputs
+        if (c_dt == DT_F16) return run_skinny8_ct<CF16>(p, s);
+        if (c_dt == DT_BF16) return run_skinny8_ct<CBF16>(p, s);
+        return run_skinny8_ct<CF32>(p, s);
     }
     int t, ks;
     fp8_pick(p.g.M, p.g.N, p.g.K, &t, &ks);

@@ -1,0 +1,64 @@
+"""GPU tests of the sums inside the 8-bit product: which bits of small products
+beside large ones are kept."""
+import numpy as np
+import pytest
+import torch
+
+import lora_bypass_linear_amd as L
+from tests import fp8_ref as R
+from tests.gpu_cases import say
+
+pytestmark = pytest.mark.gpu
+F16, BF16, F32 = torch.float16, torch.bfloat16, torch.float32
+
+
+def _spread(seed, rows, K):
+    """e4m3 values whose sizes differ by up to 2^16 from one k to the next, both signs."""
+    g = torch.Generator().manual_seed(seed)
+    e = torch.randint(-8, 9, (rows, K), generator=g).float()
+    m = 1 + torch.randint(0, 8, (rows, K), generator=g).float() / 8
+    s = torch.where(torch.rand(rows, K, generator=g) < 0.5, -1.0, 1.0)
+    # (2^8 * 1.875 is past the largest code)
+    return (s * m * torch.exp2(e)).clamp(-448, 448).to(L.E4M3)
+
+
+def _operands(seed, M, N, K):
+    q, w = _spread(seed, M, K), _spread(seed + 1, N, K)
+    g = torch.Generator().manual_seed(seed + 2)
+    s = torch.exp2(torch.randint(-8, 1, (-(-K // 128), M), generator=g).float() - 12)
+    ws = torch.exp2(torch.randint(-8, 1, (-(-N // 128), -(-K // 128)), generator=g).float())
+    xv, wv = R.rows_value(_bits(q), s.numpy()), R.tiles_value(_bits(w), ws.numpy())
+    return (q.cuda(), s.cuda(), w.cuda(), ws.cuda()), xv, wv
+
+
+def _bits(q):
+    return q.view(torch.uint8).numpy()
+
+
+@pytest.mark.parametrize("M,N,K", [(1, 130, 144), (16, 64, 1040), (17, 300, 528), (32, 8208, 272)])
+@pytest.mark.parametrize("dt", [F16, BF16, F32])
+def test_few_rows_sum_in_fp32(M, N, K, dt):
+    say("fp8 few rows, spread products", M, N, K, dt)
+    ops, xv, wv = _operands(M + N, M, N, K)
+    y = L.fp8_linear(*ops, out_dtype=dt)
+    exact, mass = xv @ wv.T, np.abs(xv) @ np.abs(wv).T
+    # the bound of fp32 sums (2^-23 of the running sum an addition) without
+    # fp8_ref's margin of terms: each 32-wide step adds its products in fp32
+    bound = R.half_step(dt) * np.abs(exact) + 2.0 ** -23 * (K / 32 + 32) * mass + (2.0 ** -25 if dt == F16 else 0.0)
+    err = np.abs(R.f64(y) - exact)
+    assert np.all(err <= bound), float((err / bound).max())
+
+
+@pytest.mark.parametrize("M", [1, 16, 32])
+@pytest.mark.parametrize("j", range(-4, 9))
+def test_few_rows_keep_a_small_product_beside_large_ones(M, j):
+    """2^16 - 2^16 + 2^j in one group of 8 products is 2^j: at most 21
+    of fp32's 24 bits lie between them, whatever the order of the sum."""
+    say("fp8 few rows, 2^16 - 2^16 + 2^j", M, j)
+    N, K = 48, 144
+    x, w = torch.zeros(M, K), torch.zeros(N, K)
+    x[:, 8], x[:, 9], x[:, 10] = 256, -256, 2.0 ** j
+    w[:, 8], w[:, 9], w[:, 10] = 256, 256, 1
+    y = L.fp8_linear(x.to(L.E4M3).cuda(), torch.ones(2, M, device="cuda"), w.to(L.E4M3).cuda(),
+                     torch.ones(1, 2, device="cuda"), out_dtype=F16)
+    assert torch.equal(y.cpu(), torch.full((M, N), 2.0 ** j, dtype=F16))
