@@ -498,6 +498,15 @@ int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const flo
  *  - Workspace: lyc_orthogonalize_workspace_size bytes, 256-byte aligned.
  */
 int lyc_orthogonalize_workspace_size(int64_t R, int64_t C, int dt, size_t* bytes);
+/*
+ * How the dense update's products run (host only): output tile (columns x rows
+ * of the result as stored), K split, and *halved = 1 where a symmetric result's
+ * tiles on and below the diagonal are computed and mirrored.  product 0: A = X
+ * X^T, 1: P = a I + b A + c A A, 2: P X.  A short side of up to 128 (or an
+ * empty update) has no such products: zeros.  Any output may be NULL.
+ */
+int lyc_orthogonalize_plan(int64_t R, int64_t C, int dt, int product, int* tile_n, int* tile_m, int* ksplit,
+                           int* halved);
 int lyc_orthogonalize(const void* g, int dt, void* out, int64_t R, int64_t C, int steps, double a, double b, double c,
                       double eps, void* workspace, size_t workspace_bytes, void* stream);
 

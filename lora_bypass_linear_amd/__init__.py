@@ -21,7 +21,7 @@ __all__ = ["F16", "BF16", "F32", "LycError", "MixedHalfError", "lib", "resolve_d
            "tuning_load", "tuning_clear", "tuning_count", "tuning_key", "tuning_lookup", "tuning_cache_path", "profile_begin", "profile_end",
            "dtype_code", "torch_dtype", "fp8_quantize_rows", "fp8_quantize_weight", "fp8_linear", "fp8_lora_linear",
            "fp8_lora_saved_h", "fp8_lora_linear_backward", "fp8_linear_workspace_size", "fp8_lora_workspace_size",
-           "fp8_lora_bwd_workspace_size", "orthogonalize", "orthogonalize_workspace_size"]
+           "fp8_lora_bwd_workspace_size", "orthogonalize", "orthogonalize_workspace_size", "orthogonalize_plan"]
 
 F16, BF16, F32 = 1, 2, 3
 OK, ERR_MIXED_HALF, ERR_INVALID_ARG, ERR_DTYPE_MISMATCH, ERR_UNSUPPORTED, ERR_HIP, ERR_WORKSPACE, ERR_IO, ERR_SCRATCH = range(9)
@@ -134,6 +134,7 @@ def lib():
                                               c_vp, c_sz, c_vp]
         c_d = ctypes.c_double
         L.lyc_orthogonalize_workspace_size.argtypes = [c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]
+        L.lyc_orthogonalize_plan.argtypes = [c_i64, c_i64, c_int, c_int] + [ctypes.POINTER(c_int)] * 4
         L.lyc_orthogonalize.argtypes = [c_vp, c_int, c_vp, c_i64, c_i64, c_int, c_d, c_d, c_d, c_d, c_vp, c_sz, c_vp]
         L.lyc_gemm_tile.argtypes = [c_i64, c_i64, c_int, ctypes.POINTER(c_int), ctypes.POINTER(c_int)]
         L.lyc_profile_begin.argtypes = [c_int]
@@ -154,7 +155,7 @@ def lib():
                    L.lyc_fp8_quantize_rows, L.lyc_fp8_quantize_weight, L.lyc_fp8_linear_workspace_size,
                    L.lyc_fp8_linear_fwd, L.lyc_fp8_lora_linear_workspace_size, L.lyc_fp8_lora_workspace_layout,
                    L.lyc_fp8_lora_linear_fwd, L.lyc_fp8_lora_linear_bwd_workspace_size, L.lyc_fp8_lora_linear_bwd,
-                   L.lyc_orthogonalize_workspace_size, L.lyc_orthogonalize, L.lyc_gemm_tile, L.lyc_profile_begin, L.lyc_profile_end):
+                   L.lyc_orthogonalize_workspace_size, L.lyc_orthogonalize_plan, L.lyc_orthogonalize, L.lyc_gemm_tile, L.lyc_profile_begin, L.lyc_profile_end):
             fn.restype = c_int
         _lib = L
     return _lib
@@ -870,6 +871,17 @@ def orthogonalize_workspace_size(R: int, C: int, dt: int) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().lyc_orthogonalize_workspace_size(R, C, dt, ctypes.byref(n)))
     return n.value
+
+
+def orthogonalize_plan(R: int, C: int, dt: int):
+    """How the products A, P and P X of a dense update run: [(tile_n, tile_m,
+    ksplit, halved)], empty for a short side of up to 128."""
+    plan = []
+    for product in range(3):
+        v = [ctypes.c_int(0) for _ in range(4)]
+        _check(lib().lyc_orthogonalize_plan(R, C, dt, product, *(ctypes.byref(i) for i in v)))
+        plan.append((v[0].value, v[1].value, v[2].value, bool(v[3].value)))
+    return plan if plan[0][0] else []
 
 
 def orthogonalize(g: torch.Tensor, steps: int = 5, coefficients: Sequence[float] = (3.4445, -4.7750, 2.0315),

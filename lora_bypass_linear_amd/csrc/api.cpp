@@ -1452,6 +1452,19 @@ int lyc_orthogonalize_workspace_size(int64_t R, int64_t C, int dt, size_t* bytes
     return LYC_OK;
 }
 
+int lyc_orthogonalize_plan(int64_t R, int64_t C, int dt, int product, int* tile_n, int* tile_m, int* ksplit,
+                           int* halved) {
+    const int st = check_ortho(R, C, dt);
+    if (st != LYC_OK) return st;
+    if (product < 0 || product > 2) return LYC_ERR_INVALID_ARG;
+    const lyc::OrthoPlan p = lyc::ortho_plan(R, C, dt, product);
+    if (tile_n) *tile_n = p.tile_n;
+    if (tile_m) *tile_m = p.tile_m;
+    if (ksplit) *ksplit = p.ksplit;
+    if (halved) *halved = p.halved;
+    return LYC_OK;
+}
+
 int lyc_orthogonalize(const void* g, int dt, void* out, int64_t R, int64_t C, int steps, double a, double b, double c,
                       double eps, void* workspace, size_t workspace_bytes, void* stream) {
     const int st = check_ortho(R, C, dt);

@@ -20,6 +20,11 @@ struct OrthoParams {
     char* ws;        // ortho_workspace(R, C, dt) bytes, 256-byte aligned
 };
 size_t ortho_workspace(int64_t R, int64_t C, int dt);
+// a dense update's product (0: A, 1: P, 2: P X); tile 0 where there is none
+struct OrthoPlan {
+    int tile_n, tile_m, ksplit, halved;
+};
+OrthoPlan ortho_plan(int64_t R, int64_t C, int dt, int product);
 hipError_t launch_ortho(const OrthoParams& p, hipStream_t s);
 
 }  // namespace lyc

@@ -1502,6 +1502,16 @@ static hipError_t ns_run(const OrthoParams& p, hipStream_t s) {
     return ns_direct<NP>(p, s);
 }
 
+OrthoPlan ortho_plan(int64_t R, int64_t C, int dt, int product) {
+    const int64_t n = std::min(R, C), m = std::max(R, C);
+    if (n <= NS_THIN) return OrthoPlan{0, 0, 0, 0};
+    const int np = dt == DT_F32 ? 3 : 2;
+    const NsPlan q = product == 0 ? ns_plan(n, n, m, np, true)
+                                  : product == 1 ? ns_plan(n, n, n, np, true) : ns_plan(C, R, n, np, false);
+    const int tn = q.tile == NS_256x128 ? 256 : q.tile == NS_128x128 ? 128 : 64;
+    return OrthoPlan{tn, std::min(tn, 128), q.ksplit, q.sym};
+}
+
 size_t ortho_workspace(int64_t R, int64_t C, int dt) {
     if (R <= 0 || C <= 0) return 0;
     return std::min(R, C) <= NS_THIN ? thin_layout(R, C, dt).total : ns_layout(R, C, dt).total;
