@@ -118,7 +118,13 @@ __global__ __launch_bounds__(256) void ns_norm_kernel(const void* g, int dt, int
     if (tid == 0) part[blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
-// 1 / (|G|_F + eps) from the partial sums, the same in every thread
+// 1 / (|G|_F + eps); a zero G with eps = 0 stays zero
+__device__ __forceinline__ double ns_inverse(double norm, double eps) {
+    const double d = norm + eps;
+    return d == 0.0 ? 0.0 : 1.0 / d;
+}
+
+// the same from the partial sums, in every thread
 __device__ __forceinline__ double ns_inverse_norm(const double* part, double eps) {
     const int lane = threadIdx.x & 63;
     double s = 0;
@@ -126,7 +132,7 @@ __device__ __forceinline__ double ns_inverse_norm(const double* part, double eps
     for (int i = 0; i < NORM_WGS / 64; ++i) s += part[i * 64 + lane];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-    return 1.0 / (__builtin_sqrt(s) + eps);
+    return ns_inverse(__builtin_sqrt(s), eps);
 }
 
 // x = pieces of scale * g / (|g| + eps), 8 columns a thread (rows padded to 8
@@ -718,7 +724,7 @@ struct Iter {
 #pragma unroll
             for (int d = 1; d < 64; d <<= 1) tr += __shfl_xor(tr, d);
             const double norm = top == NS_EMPTY ? 0.0 : __builtin_ldexp(__builtin_sqrt(tr), top);
-            inv = 1.0 / (norm + p.eps);
+            inv = ns_inverse(norm, p.eps);
         }
         const double half = top == NS_EMPTY ? 0.0 : __builtin_ldexp(inv, top);
         const float fA = (float)(half * half);
@@ -846,7 +852,7 @@ __global__ __launch_bounds__(64) void ns_iter64_kernel(IterParams p) {
         for (int e = 0; e < 4; ++e) tr += 4 * e + g == r ? A[e] : 0.0;
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) tr += __shfl_xor(tr, d);
-        inv = 1.0 / ((top == NS_EMPTY ? 0.0 : __builtin_ldexp(__builtin_sqrt(tr), top)) + p.eps);
+        inv = ns_inverse(top == NS_EMPTY ? 0.0 : __builtin_ldexp(__builtin_sqrt(tr), top), p.eps);
     }
     const double half = top == NS_EMPTY ? 0.0 : __builtin_ldexp(inv, top);
     A *= half * half;
