@@ -488,20 +488,24 @@ int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const flo
  * c l^2, and keeps the singular vectors (a = 3.4445, b = -4.775, c = 2.0315
  * take 5 steps to bring them near 1).  Products are summed in fp32 from
  * operands split into 16-bit pieces (22 bits for a 16-bit G, 24 for an fp32
- * one); out has G's dtype, rounded once.
+ * one or for coefficients that part X's directions by more than 2^8, whatever
+ * |G| is beside eps); out has G's dtype, rounded once.
  *  - g, out [R][C] row-major, element alignment; out may be g itself, any
  *    other overlap is LYC_ERR_INVALID_ARG.
  *  - R, C <= 2^20, min(R, C) <= 16384, R * C <= 2^31 (LYC_ERR_UNSUPPORTED).
  *    1 <= steps <= 32, |a|, |b|, |c| < 1e6, 0 <= eps < 1e6
  *    (LYC_ERR_INVALID_ARG).  A zero G gives zeros; one that holds a NaN or an
- *    infinity gives NaN.
+ *    infinity gives NaN.  Coefficients may shrink or grow X; with a short side
+ *    of up to 128 its norm has to stay between 2^-100 and 2^60 on the way (X
+ *    and A are held in fp32 there).
  *  - Workspace: lyc_orthogonalize_workspace_size bytes, 256-byte aligned.
  */
 int lyc_orthogonalize_workspace_size(int64_t R, int64_t C, int dt, size_t* bytes);
 /*
  * How the dense update's products run (host only): output tile (columns x rows
  * of the result as stored), K split, and *halved = 1 where a symmetric result's
- * tiles on and below the diagonal are computed and mirrored.  product 0: A = X
+ * tiles on and below the diagonal are computed and mirrored (for coefficients
+ * such as the usual ones).  product 0: A = X
  * X^T, 1: P = a I + b A + c A A, 2: P X.  A short side of up to 128 (or an
  * empty update) has no such products: zeros.  Any output may be NULL.
  */

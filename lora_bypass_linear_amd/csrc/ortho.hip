@@ -11,9 +11,13 @@
 // rounding errors of X with them, so 16-bit operands would leave errors of a
 // percent.  Operands are split into 16-bit pieces and their products summed in
 // fp32 by 16-bit MFMAs:
-//   16-bit G: two fp16 pieces (22 bits), 3 of the 4 products; the matrices are
-//     scaled by powers of two that the coefficients' bounds keep inside fp16;
-//   fp32 G: three bf16 pieces (24 bits), 6 of the 9 products.
+//   16-bit G: two fp16 pieces (22 bits), 3 of the 4 products;
+//   fp32 G: three bf16 pieces (24 bits), 6 of the 9 products.  They have fp32's
+//     range, so a 16-bit G whose coefficients leave X's size unknown by too
+//     much (ns_loose) takes them too.
+// Every matrix is held times a power of two that puts its largest possible
+// element near the top of fp16 (near 1 for bf16), step by step: the bits are
+// there whatever the size of G beside eps and wherever the coefficients take X.
 #include <algorithm>
 #include <cmath>
 
@@ -124,24 +128,104 @@ __device__ __forceinline__ double ns_inverse(double norm, double eps) {
     return d == 0.0 ? 0.0 : 1.0 / d;
 }
 
-// the same from the partial sums, in every thread
-__device__ __forceinline__ double ns_inverse_norm(const double* part, double eps) {
+// |G|_F from the partial sums, the same in every thread
+__device__ __forceinline__ double ns_norm(const double* part) {
     const int lane = threadIdx.x & 63;
     double s = 0;
 #pragma unroll
     for (int i = 0; i < NORM_WGS / 64; ++i) s += part[i * 64 + lane];
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) s += __shfl_xor(s, d);
-    return ns_inverse(__builtin_sqrt(s), eps);
+    return __builtin_sqrt(s);
 }
 
-// x = pieces of scale * g / (|g| + eps), 8 columns a thread (rows padded to 8
-// columns with zeros)
+// The powers of two of a dense update's products, five a step: A = ldexp of
+// the sum of X X^T; P's of c A A, of b A and of a; ldexp of the sum of P X (into
+// the next X, or the result itself after the last step).
+constexpr int NS_EXPS = 5;
+
+// A matrix of spectral norm up to `bound` (its elements are at most that) is
+// held times 2^ns_exponent: below 2^15 in fp16 pieces, below 1 in bf16 ones.
 template <int NP>
-__global__ __launch_bounds__(256) void ns_split_kernel(const void* g, int dt, int64_t rows, int64_t cols, Planes x,
-                                                       const double* part, double eps, float scale) {
+__host__ __device__ inline int ns_exponent(double bound) {
+    if (!(bound > 0.0 && bound < 1e300)) return 0;
+    int e;
+    frexp(bound, &e);   // bound < 2^e
+    return (NP == 2 ? 15 : 0) - e;
+}
+
+// What a step does to eigenvalues of A in [0, top]: the largest |p|, |l p| and
+// next eigenvalue l p^2, at the ends or where the derivative's quadratic
+// u + v l + w l^2 vanishes.
+struct NsBounds {
+    double p, lp, next;
+};
+__host__ __device__ inline NsBounds ns_bounds(double a, double b, double c, double top) {
+    double m[3];
+    for (int i = 0; i < 3; ++i) {
+        const double u = i == 0 ? b : a;
+        const double v = i == 0 ? 2 * c : i == 1 ? 2 * b : 3 * b;
+        const double w = i == 0 ? 0.0 : i == 1 ? 3 * c : 5 * c;
+        auto f = [&](double l) {
+            const double p = a + l * (b + l * c);
+            return fabs(i == 0 ? p : i == 1 ? l * p : l * p * p);   // (where p vanishes so does l p^2)
+        };
+        double t = fmax(f(0.0), f(top));
+        auto at = [&](double l) { if (l > 0.0 && l < top) t = fmax(t, f(l)); };
+        const double d = v * v - 4 * u * w;
+        if (w == 0.0) {
+            if (v != 0.0) at(-u / v);
+        } else if (d >= 0.0) {
+            at((-v - sqrt(d)) / (2 * w));
+            at((-v + sqrt(d)) / (2 * w));
+        }
+        t *= 1.01;   // the products' rounding
+        m[i] = t < 1e290 ? t : 1e290;
+    }
+    return NsBounds{m[0], m[1], m[2]};
+}
+
+// the table, from theta = |X0|_F
+template <int NP>
+__device__ void ns_exponents(int* e, int steps, double a, double b, double c, double theta) {
+    double top = theta * theta;
+    int ex = ns_exponent<NP>(theta);
+    for (int k = 0; k < steps; ++k) {
+        const NsBounds n = ns_bounds(a, b, c, top);
+        const int ea = ns_exponent<NP>(top), ep = ns_exponent<NP>(n.p), en = ns_exponent<NP>(sqrt(n.next));
+        e[0] = ea - 2 * ex;
+        e[1] = ep - 2 * ea;
+        e[2] = ep - ea;
+        e[3] = ep;
+        e[4] = (k + 1 < steps ? en : 0) - ex - ep;
+        e += NS_EXPS;
+        top = n.next;
+        ex = en;
+    }
+}
+
+// x = pieces of g / (|g| + eps), 8 columns a thread (rows padded to 8 columns
+// with zeros), and the table of the powers of two of what follows
+struct SplitParams {
+    const void* g;
+    int dt;
+    int64_t rows, cols;
+    Planes x;
+    const double* part;
+    int* exps;   // [steps][NS_EXPS]
+    int steps;
+    double a, b, c, eps;
+};
+template <int NP>
+__global__ __launch_bounds__(256) void ns_split_kernel(SplitParams p) {
+    const void* g = p.g;
+    const int dt = p.dt;
+    const int64_t rows = p.rows, cols = p.cols;
+    const Planes x = p.x;
     // (the whole factor in 64 bits: a norm near fp32's ends has no fp32 reciprocal)
-    const double f = ns_inverse_norm(part, eps) * (double)scale;
+    const double norm = ns_norm(p.part), inv = ns_inverse(norm, p.eps);
+    const double f = ldexp(inv, ns_exponent<NP>(norm * inv));
+    if (blockIdx.x == 0 && threadIdx.x == 0) ns_exponents<NP>(p.exps, p.steps, p.a, p.b, p.c, norm * inv);
     const int64_t q = x.ld / 8, total = rows * q;
     const bool vec = cols % 8 == 0 && ((uintptr_t)g & 15) == 0;
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
@@ -187,17 +271,17 @@ __global__ __launch_bounds__(256) void ns_split_kernel(const void* g, int dt, in
 
 enum { NS_SPLIT = 0, NS_POLY = 1, NS_OUT = 2 };
 
-// out(j, i) = finish( alpha * sum_k U(i, k) V(j, k) ), i < I, j < J, k < K.
+// out(j, i) = finish( s = sum_k U(i, k) V(j, k) ), i < I, j < J, k < K.
 // Each of u and v rows-as-stored ([I or J][ld], k consecutive) or transposed
-// ([K][ld]).
-//   NS_SPLIT: v' = sum                      into pieces, times `scale`
-//   NS_POLY:  v' = a delta_ij + b A + c sum into pieces, times `scale`; A from `old`
-//   NS_OUT:   v' into out [J][I] of dtype dt
+// ([K][ld]); e: this product's powers of two in the table.
+//   NS_SPLIT: 2^e0 s                                  into pieces
+//   NS_POLY:  2^e2 a delta_ij + 2^e1 b A + 2^e0 c s   into pieces; A from `old`
+//   NS_OUT:   2^e0 s                                  into out [J][I] of dtype dt
 struct NsParams {
     Planes u, v, o, old;
     int64_t I, J, K;
-    float alpha, scale;
-    float a, b, c, old_inv;
+    const int* e;
+    float a, b, c;
     int mode;
     void* out;
     int dt;
@@ -210,9 +294,9 @@ struct NsParams {
 // multiple of 4 inside a row of pieces; zeros past I)
 template <int NP>
 __device__ __forceinline__ void ns_values4(const NsParams& p, f32x4 s, int64_t j, int64_t i, float (&v)[4]) {
-#pragma unroll
-    for (int e = 0; e < 4; ++e) v[e] = s[e] * p.alpha;
+    const int e0 = p.e[0];
     if (p.mode == NS_POLY) {
+        const int e1 = p.e[1], e2 = p.e[2];
         i32x2 w[NP];
 #pragma unroll
         for (int k = 0; k < NP; ++k) w[k] = *(const i32x2*)(p.old.p + k * p.old.stride + j * p.old.ld + i);
@@ -221,9 +305,12 @@ __device__ __forceinline__ void ns_values4(const NsParams& p, f32x4 s, int64_t j
             uint16_t u[NP];
 #pragma unroll
             for (int k = 0; k < NP; ++k) u[k] = (uint16_t)((uint32_t)w[k][e >> 1] >> (e & 1) * 16);
-            v[e] = p.c * v[e] + p.b * (Pieces<NP>::join(u) * p.old_inv);
-            if (i + e == j) v[e] += p.a;
+            v[e] = __builtin_ldexpf(p.c * s[e], e0) + __builtin_ldexpf(p.b * Pieces<NP>::join(u), e1);
+            if (i + e == j) v[e] += __builtin_ldexpf(p.a, e2);
         }
+    } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(s[e], e0);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = i + e < p.I ? v[e] : 0.f;
@@ -233,7 +320,7 @@ template <int NP>
 __device__ __forceinline__ void ns_store4(const NsParams& p, const float (&v)[4], int64_t j, int64_t i) {
     uint16_t o[4][NP];
 #pragma unroll
-    for (int e = 0; e < 4; ++e) Pieces<NP>::split(v[e] * p.scale, o[e]);
+    for (int e = 0; e < 4; ++e) Pieces<NP>::split(v[e], o[e]);
 #pragma unroll
     for (int k = 0; k < NP; ++k)
         *(i32x2*)(p.o.p + k * p.o.stride + j * p.o.ld + i) =
@@ -244,10 +331,11 @@ __device__ __forceinline__ void ns_store4(const NsParams& p, const float (&v)[4]
 template <int NP>
 __device__ __forceinline__ void ns_finish4(const NsParams& p, f32x4 s, int64_t j, int64_t i) {
     if (p.mode == NS_OUT) {
+        const int e0 = p.e[0];
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (i + e >= p.I) continue;
-            const float v = s[e] * p.alpha;
+            const float v = __builtin_ldexpf(s[e], e0);
             const int64_t at = j * p.I + i + e;
             if (p.dt == DT_F32) ((float*)p.out)[at] = v;
             else ((uint16_t*)p.out)[at] = p.dt == DT_F16 ? f32_to_f16(v) : f32_to_bf16(v);
@@ -565,7 +653,6 @@ struct ThinParams {
     const double* fac;  // X' = fac * 2^e * (q . pieces)
     float* part;        // a Gram matrix per workgroup, [NPAD][NPAD]
     int* exps;          // which stands for 2^(2 e) times its values
-    float sx;           // the power of two that scales X after the first segment
     void* out;          // [R][C]
     int tall;
     int vec_out;        // out's rows hold whole groups of 4 elements, aligned for one store each
@@ -594,7 +681,7 @@ struct IterParams {
     int slots, steps, first;
     float a, b, c;
     double eps;
-    float sA[NS_SEG], sP[NS_SEG], sT[NS_SEG], sQ[NS_SEG];   // powers of two that keep each matrix inside fp16
+    int eA[NS_SEG], eP[NS_SEG], eT[NS_SEG], eQ[NS_SEG];   // the powers of two each step's matrices are held times
     uint16_t* q;         // pieces [NP][NPAD][KR]
     double* fac;
 };
@@ -639,14 +726,14 @@ struct Iter {
     __device__ __forceinline__ int col_of(int tj) const { return (wj * TW + tj) * 16 + r; }
     __device__ __forceinline__ uint16_t* at(int b, int k) const { return buf + (b * NP + k) * NPAD * LD; }
 
-    __device__ __forceinline__ void put(int b, const M& m, float scale) const {
+    __device__ __forceinline__ void put(int b, const M& m, int ex) const {
 #pragma unroll
         for (int ti = 0; ti < TW; ++ti)
 #pragma unroll
             for (int tj = 0; tj < TW; ++tj) {
                 uint16_t o[4][NP];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) Pieces<NP>::split(m[ti][tj][e] * scale, o[e]);
+                for (int e = 0; e < 4; ++e) Pieces<NP>::split(__builtin_ldexpf(m[ti][tj][e], ex), o[e]);
 #pragma unroll
                 for (int k = 0; k < NP; ++k) {
                     *(i32x2*)(at(b, k) + col_of(tj) * LD + row_of(ti)) =
@@ -659,7 +746,7 @@ struct Iter {
                 }
             }
     }
-    __device__ __forceinline__ void product(int bu, int bv, float scale, M& out) const {
+    __device__ __forceinline__ void product(int bu, int bv, M& out) const {
 #pragma unroll
         for (int ti = 0; ti < TW; ++ti)
 #pragma unroll
@@ -676,10 +763,15 @@ struct Iter {
                 }
             piece_mma<NP>(u, v, out);
         }
+    }
+    __device__ __forceinline__ void product(int bu, int bv, int ex, M& out) const {
+        product(bu, bv, out);
 #pragma unroll
         for (int ti = 0; ti < TW; ++ti)
 #pragma unroll
-            for (int tj = 0; tj < TW; ++tj) out[ti][tj] *= scale;
+            for (int tj = 0; tj < TW; ++tj)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) out[ti][tj][e] = __builtin_ldexpf(out[ti][tj][e], ex);
     }
 
     // all of the workgroup's WAVES * 64 threads
@@ -735,37 +827,38 @@ struct Iter {
 
         for (int k = 0; k < p.steps; ++k) {
             M P;
-            put(0, A, p.sA[k]);
+            put(0, A, p.eA[k]);
             __syncthreads();
-            product(0, 0, 1.f / (p.sA[k] * p.sA[k]), P);
+            product(0, 0, P);
+            const int e2 = -2 * p.eA[k];
 #pragma unroll
             for (int ti = 0; ti < TW; ++ti)
 #pragma unroll
                 for (int tj = 0; tj < TW; ++tj)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float v = p.c * P[ti][tj][e] + p.b * A[ti][tj][e];
+                        float v = __builtin_ldexpf(p.c * P[ti][tj][e], e2) + p.b * A[ti][tj][e];
                         if (row_of(ti) + e == col_of(tj)) v += p.a;
                         P[ti][tj][e] = v;
                     }
             const bool more = k + 1 < p.steps;
             if constexpr (NP == 2) {
                 if (k > 0 || more) {
-                    put(1, P, p.sP[k]);
+                    put(1, P, p.eP[k]);
                     __syncthreads();
                 }
-                if (more) product(0, 1, 1.f / (p.sA[k] * p.sP[k]), A);   // T = A P
+                if (more) product(0, 1, -p.eA[k] - p.eP[k], A);   // T = A P
                 if (k > 0) {
                     __syncthreads();   // buffer 0 has been read
-                    put(0, Q, p.sQ[k - 1]);
+                    put(0, Q, p.eQ[k - 1]);
                     __syncthreads();
-                    product(0, 1, 1.f / (p.sQ[k - 1] * p.sP[k]), Q);
+                    product(0, 1, -p.eQ[k - 1] - p.eP[k], Q);
                 }
                 if (more) {
                     __syncthreads();
-                    put(0, A, p.sT[k]);
+                    put(0, A, p.eT[k]);
                     __syncthreads();
-                    product(0, 1, 1.f / (p.sT[k] * p.sP[k]), A);   // P A P
+                    product(0, 1, -p.eT[k] - p.eP[k], A);   // P A P
                     __syncthreads();
                 }
             }
@@ -776,14 +869,14 @@ struct Iter {
                     for (int tj = 0; tj < TW; ++tj) Q[ti][tj] = P[ti][tj];
             }
         }
-        const float sq = p.sQ[p.steps - 1];
+        const int eq = p.eQ[p.steps - 1];
 #pragma unroll
         for (int ti = 0; ti < TW; ++ti)
 #pragma unroll
             for (int tj = 0; tj < TW; ++tj) {
                 uint16_t o[4][NP];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) Pieces<NP>::split(Q[ti][tj][e] * sq, o[e]);
+                for (int e = 0; e < 4; ++e) Pieces<NP>::split(__builtin_ldexpf(Q[ti][tj][e], eq), o[e]);
 #pragma unroll
                 for (int k = 0; k < NP; ++k) {
                     uint16_t* q = p.q + (int64_t)k * NPAD * KR;
@@ -800,7 +893,7 @@ struct Iter {
             for (int i = tid; i < NP * NPAD * (KR - NPAD); i += nt)
                 p.q[(i / (KR - NPAD)) * KR + NPAD + i % (KR - NPAD)] = 0;
         }
-        if (tid == 0) *p.fac = inv / (double)sq;
+        if (tid == 0) *p.fac = __builtin_ldexp(inv, -eq);
     }
 };
 
@@ -870,18 +963,18 @@ __global__ __launch_bounds__(64) void ns_iter64_kernel(IterParams p) {
         Q = k == 0 ? P : product(Q, P);
         if (k + 1 < p.steps) A = product(product(A, P), P);
     }
-    const float sq = p.sQ[0];
+    const int eq = p.eQ[0];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         uint16_t o[2];
-        Pieces<2>::split((float)Q[e] * sq, o);
+        Pieces<2>::split((float)__builtin_ldexp(Q[e], eq), o);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             p.q[(k * 16 + r) * KR + 4 * e + g] = o[k];
             p.q[(k * 16 + r) * KR + 16 + 4 * e + g] = 0;
         }
     }
-    if (lane == 0) *p.fac = inv / (double)sq;
+    if (lane == 0) *p.fac = __builtin_ldexp(inv, -eq);
 }
 
 template <int NPAD, int NP>
@@ -910,19 +1003,49 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
             for (int k = 0; k < NP; ++k) xs[k][NPAD * LD + i] = 0;
     }
     i32x4 q[KS][1][NP];
-    double fac = 0;
+    float fac = 0;   // X' = 2^(fexp + e) fac (q . pieces)
+    int fexp = 0;
     if constexpr (MODE != THIN_GRAM) {
 #pragma unroll
         for (int s = 0; s < KS; ++s)
 #pragma unroll
             for (int k = 0; k < NP; ++k)
                 q[s][0][k] = *(const i32x4*)(p.q + ((int64_t)k * NPAD + ib * 16 + r) * S::KR + s * 32 + g * 8);
-        fac = *p.fac;
+        fac = (float)frexp(*p.fac, &fexp);
     }
     f32x4 gacc[1][S::GT];
 #pragma unroll
     for (int t = 0; t < S::GT; ++t) gacc[0][t] = f32x4{0.f, 0.f, 0.f, 0.f};
-    int erun = MODE == THIN_GRAM && p.src != 2 ? NS_EMPTY : -exponent_of(__builtin_bit_cast(uint32_t, p.sx));
+    // Pieces of X are taken from a chunk scaled by 2^-e, its largest magnitude
+    // to [2^11, 2^12) (fp16 pieces' low bits stay normal; subnormal maxima count
+    // as 2^-126).  The chunks of a Gram matrix share the largest e so far, the
+    // sums made with a smaller one are scaled down.
+    int erun = NS_EMPTY;
+    auto wave_max = [](uint32_t v) {
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const uint32_t o = (uint32_t)__shfl_xor((int)v, d);
+            v = o > v ? o : v;
+        }
+        return v;
+    };
+    auto group_max = [&]() {
+        uint32_t v = wmax[0];
+#pragma unroll
+        for (int w = 1; w < S::NW; ++w) v = wmax[w] > v ? wmax[w] : v;
+        return v;
+    };
+    auto chunk_exponent = [](uint32_t top) { return exponent_of(top < 0x00800000u ? 0x00800000u : top) - 11; };
+    auto gram_exponent = [&](int e) {
+        if (erun == NS_EMPTY) erun = e;
+        else if (e > erun) {
+            const float f = __builtin_ldexpf(1.f, 2 * (erun - e) < -126 ? -126 : 2 * (erun - e));
+#pragma unroll
+            for (int t = 0; t < S::GT; ++t) gacc[0][t] *= f;
+            erun = e;
+        }
+        return erun;
+    };
 
     const int64_t chunks = (p.m + CW - 1) / CW;
     for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
@@ -977,75 +1100,54 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
 #pragma unroll
             for (int u = 0; u < S::PT; ++u) v[u] = f32 ? __builtin_bit_cast(float, raw[u]) : widen(raw[u]);
         }
-        uint32_t mx = 0;
+        // (bf16 pieces have fp32's range: X between the segments stays as it is)
+        int e = 0;
+        if (NP == 2 || p.src != 2) {
+            uint32_t mx = 0;
 #pragma unroll
-        for (int u = 0; u < S::PT; ++u) {
-            const uint32_t b = __builtin_bit_cast(uint32_t, v[u]) & 0x7FFFFFFFu;
-            mx = b > mx ? b : mx;
-        }
-        // a raw chunk is scaled by 2^-e, its largest magnitude to [2^11, 2^12)
-        // (fp16 pieces' low bits stay normal); subnormal maxima count as 2^-126
-        int e = -exponent_of(__builtin_bit_cast(uint32_t, p.sx));
-        if (p.src != 2) {
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const uint32_t o = (uint32_t)__shfl_xor((int)mx, d);
-                mx = o > mx ? o : mx;
+            for (int u = 0; u < S::PT; ++u) {
+                const uint32_t b = __builtin_bit_cast(uint32_t, v[u]) & 0x7FFFFFFFu;
+                mx = b > mx ? b : mx;
             }
+            mx = wave_max(mx);
             if (lane == 0) wmax[wave] = mx;
-            __syncthreads();
-#pragma unroll
-            for (int w = 0; w < S::NW; ++w) mx = wmax[w] > mx ? wmax[w] : mx;
-            if (mx == 0) {
-                e = 0;
-            } else {
-                const int top = exponent_of(mx < 0x00800000u ? 0x00800000u : mx);
-                e = top - 11;
-            }
-        }
-        if constexpr (MODE == THIN_GRAM) {
-            if (mx == 0 && p.src != 2) {
-                __syncthreads();   // (wmax is read by all before the next chunk writes it)
-                continue;          // zeros add nothing
-            }
-            if (p.src != 2) {
-                if (erun == NS_EMPTY) erun = e;
-                else if (e > erun) {
-                    const float f = __builtin_ldexpf(1.f, 2 * (erun - e) < -126 ? -126 : 2 * (erun - e));
-#pragma unroll
-                    for (int t = 0; t < S::GT; ++t) gacc[0][t] *= f;
-                    erun = e;
+            __syncthreads();   // (the previous chunk's tile has been read, too)
+            mx = group_max();
+            if (mx != 0) e = chunk_exponent(mx);
+            if constexpr (MODE == THIN_GRAM) {
+                if (mx == 0) {
+                    __syncthreads();   // (wmax is read by all before the next chunk writes it)
+                    continue;          // zeros add nothing
                 }
-                e = erun;
+                e = gram_exponent(e);
             }
+        } else {
+            __syncthreads();   // the previous chunk's tile has been read
         }
-        __syncthreads();   // the previous chunk's tile has been read
-        {
-            // 2^-e in two factors (e reaches past fp32's exponents)
-            const float f1 = __builtin_ldexpf(1.f, -(e / 2)), f2 = __builtin_ldexpf(1.f, -(e - e / 2));
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint16_t o[8][NP];
+        for (int h = 0; h < 2; ++h) {
+            uint16_t o[8][NP];
 #pragma unroll
-                for (int u = 0; u < 8; ++u) Pieces<NP>::split(v[8 * h + u] * f1 * f2, o[u]);
+            for (int u = 0; u < 8; ++u) Pieces<NP>::split(__builtin_ldexpf(v[8 * h + u], -e), o[u]);
 #pragma unroll
-                for (int k = 0; k < NP; ++k) {
-                    if (p.src == 1) {
+            for (int k = 0; k < NP; ++k) {
+                if (p.src == 1) {
 #pragma unroll
-                        for (int u = 0; u < 8; ++u) xs[k][(row0[h] + u) * LD + col0[h]] = o[u][k];
-                    } else {
-                        i32x4 w;
+                    for (int u = 0; u < 8; ++u) xs[k][(row0[h] + u) * LD + col0[h]] = o[u][k];
+                } else {
+                    i32x4 w;
 #pragma unroll
-                        for (int u = 0; u < 4; ++u) w[u] = (int)((uint32_t)o[2 * u][k] | (uint32_t)o[2 * u + 1][k] << 16);
-                        *(i32x4*)&xs[k][row0[h] * LD + col0[h]] = w;
-                    }
+                    for (int u = 0; u < 4; ++u) w[u] = (int)((uint32_t)o[2 * u][k] | (uint32_t)o[2 * u + 1][k] << 16);
+                    *(i32x4*)&xs[k][row0[h] * LD + col0[h]] = w;
                 }
             }
         }
         __syncthreads();
 
         if constexpr (MODE != THIN_GRAM) {
-            const float f = (float)__builtin_ldexp(fac, e);
+            // (a factor and an exponent: the two together may leave fp32's range)
+            const int fe = fexp + e;
+            auto finished = [&](float s) { return __builtin_ldexpf(s * fac, fe); };
             f32x4 acc[S::CB][1];
 #pragma unroll
             for (int c = 0; c < S::CB; ++c) acc[c][0] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -1068,7 +1170,9 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
                     const int64_t i = ib * 16 + (p.tall ? 4 * g : r), cc = c0 + (cb0 + c) * 16 + (p.tall ? r : 4 * g);
                     if (p.vec_out) {   // the four are inside the row, or none is
                         if (i >= p.n || cc >= p.m) continue;
-                        const f32x4 val = acc[c][0] * f;
+                        f32x4 val;
+#pragma unroll
+                        for (int el = 0; el < 4; ++el) val[el] = finished(acc[c][0][el]);
                         const int64_t o = p.tall ? cc * p.n + i : i * p.m + cc;
                         if (p.dt == DT_F32) {
                             *(f32x4*)((float*)p.out + o) = val;
@@ -1085,22 +1189,47 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
                         const int64_t ie = p.tall ? i + el : i, ce = p.tall ? cc : cc + el;
                         if (ie >= p.n || ce >= p.m) continue;
                         const int64_t o = p.tall ? ce * p.n + ie : ie * p.m + ce;
-                        const float val = acc[c][0][el] * f;
+                        const float val = finished(acc[c][0][el]);
                         if (p.dt == DT_F32) ((float*)p.out)[o] = val;
                         else ((uint16_t*)p.out)[o] = p.dt == DT_F16 ? f32_to_f16(val) : f32_to_bf16(val);
                     }
                 }
                 continue;
             } else {
-                __syncthreads();   // the tile has been read: X' takes its place
+                const int i = ib * 16 + r;
+                uint32_t top = 0;
 #pragma unroll
                 for (int c = 0; c < S::CB; ++c) {
-                    const int i = ib * 16 + r, cc = (cb0 + c) * 16 + 4 * g;
-                    acc[c][0] *= f;
-                    if (i < p.n) *(f32x4*)(p.x + i * p.ldx + c0 + cc) = acc[c][0];
+#pragma unroll
+                    for (int el = 0; el < 4; ++el) {
+                        acc[c][0][el] = finished(acc[c][0][el]);
+                        const float val = acc[c][0][el];
+                        const uint32_t b = __builtin_bit_cast(uint32_t, val) & 0x7FFFFFFFu;
+                        top = b > top ? b : top;
+                    }
+                    if (i < p.n) *(f32x4*)(p.x + i * p.ldx + c0 + (cb0 + c) * 16 + 4 * g) = acc[c][0];
+                }
+                int en = 0;
+                if constexpr (NP == 2) {
+                    top = wave_max(top);
+                    if (lane == 0) wmax[wave] = top;
+                    __syncthreads();   // the tile has been read: X' takes its place
+                    top = group_max();
+                    if (top == 0) {
+                        __syncthreads();
+                        continue;
+                    }
+                    en = gram_exponent(chunk_exponent(top));
+                } else {
+                    __syncthreads();   // the tile has been read: X' takes its place
+                    erun = 0;
+                }
+#pragma unroll
+                for (int c = 0; c < S::CB; ++c) {
+                    const int cc = (cb0 + c) * 16 + 4 * g;
                     uint16_t o[4][NP];
 #pragma unroll
-                    for (int el = 0; el < 4; ++el) Pieces<NP>::split(acc[c][0][el] * p.sx, o[el]);
+                    for (int el = 0; el < 4; ++el) Pieces<NP>::split(__builtin_ldexpf(acc[c][0][el], -en), o[el]);
 #pragma unroll
                     for (int k = 0; k < NP; ++k)
                         *(i32x2*)&xs[k][i * LD + cc] = i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16),
@@ -1199,40 +1328,12 @@ static NsPlan ns_plan(int64_t I, int64_t J, int64_t K, int np, bool symmetric) {
     return plan;
 }
 
-// powers of two that keep a matrix of the given spectral norm inside fp16
-// (elements are at most the norm)
-static double pow2_under(double bound) {
-    return std::ldexp(1.0, std::max(-100, std::min(15, (int)std::floor(15.0 - std::log2(std::max(bound, 1e-30))))));
-}
-// [0, top] -> the next A's largest eigenvalue, max |p| and max |l p| there: at
-// the ends, or where the derivative's quadratic u + v l + w l^2 vanishes
-static void poly_bounds(const OrthoParams& q, double top, double* next, double* pmax, double* tmax) {
-    auto p = [&](double l) { return q.a + l * (q.b + l * q.c); };
-    auto most = [&](double u, double v, double w, auto f) {
-        double m = std::max(std::fabs(f(0.0)), std::fabs(f(top)));
-        auto at = [&](double l) { if (l > 0.0 && l < top) m = std::max(m, std::fabs(f(l))); };
-        if (w == 0.0) {
-            if (v != 0.0) at(-u / v);
-        } else if (v * v - 4 * u * w >= 0.0) {
-            const double d = std::sqrt(v * v - 4 * u * w);
-            at((-v - d) / (2 * w));
-            at((-v + d) / (2 * w));
-        }
-        m *= 1.01;   // the products' rounding
-        return m < 1e30 ? m : 1e30;
-    };
-    *pmax = most(q.b, 2 * q.c, 0.0, p);
-    *tmax = most(q.a, 2 * q.b, 3 * q.c, [&](double l) { return l * p(l); });
-    // (l p^2)' = p (a + 3 b l + 5 c l^2); where p vanishes so does l p^2
-    *next = most(q.a, 3 * q.b, 5 * q.c, [&](double l) { return l * p(l) * p(l); });
-}
-
 struct NsLayout {
-    size_t norm, x[2], A, P, partial, total;
+    size_t norm, exps, x[2], A, P, partial, total;
     int64_t ldx, ldn, rows;
 };
 static NsLayout ns_layout(int64_t R, int64_t C, int dt) {
-    const size_t np = dt == DT_F32 ? 3 : 2;
+    const size_t np = 3;   // (a 16-bit G may take three pieces)
     const int64_t n = std::min(R, C), m = std::max(R, C);
     NsLayout L{};
     L.rows = R;
@@ -1241,13 +1342,17 @@ static NsLayout ns_layout(int64_t R, int64_t C, int dt) {
     size_t off = 0;
     auto take = [&](size_t& at, size_t bytes) { at = off; off = up256(off + bytes); };
     take(L.norm, NORM_WGS * sizeof(double));
+    take(L.exps, ORTHO_MAX_STEPS * NS_EXPS * sizeof(int));
     for (int i = 0; i < 2; ++i) take(L.x[i], np * (size_t)(R * L.ldx) * 2);
     take(L.A, np * (size_t)(n * L.ldn) * 2);
     take(L.P, np * (size_t)(n * L.ldn) * 2);
     size_t part = 0;
     auto partial = [&](int64_t I, int64_t J, int64_t K, bool symmetric) {
-        const NsPlan q = ns_plan(I, J, K, (int)np, symmetric);
-        if (q.ksplit > 1 || q.sym) part = std::max(part, (size_t)q.ksplit * (size_t)(J * ((I + 3) & ~(int64_t)3)) * 4);
+        for (int pieces = dt == DT_F32 ? 3 : 2; pieces <= 3; ++pieces) {
+            const NsPlan q = ns_plan(I, J, K, pieces, symmetric);
+            if (q.ksplit > 1 || q.sym)
+                part = std::max(part, (size_t)q.ksplit * (size_t)(J * ((I + 3) & ~(int64_t)3)) * 4);
+        }
     };
     partial(n, n, m, true);
     partial(n, n, n, true);
@@ -1297,27 +1402,14 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
     A = Planes{(uint16_t*)(W + L.A), L.ldn, n * L.ldn};
     P = Planes{(uint16_t*)(W + L.P), L.ldn, n * L.ldn};
 
-    // power-of-two scales that keep every element inside fp16
-    double top = 1.0, topx = 1.0, pmax = 0.0, next, pm, tm, sx = 1.0, sa = 1.0, sp = 1.0;
-    for (int k = 0; k < p.steps; ++k) {
-        poly_bounds(p, top, &next, &pm, &tm);
-        pmax = std::max(pmax, pm);
-        top = next;
-        topx = std::max(topx, top);
-    }
-    if (NP == 2) {
-        sx = pow2_under(std::sqrt(topx));
-        sa = pow2_under(topx);
-        sp = pow2_under(pmax);
-    }
-
     hipLaunchKernelGGL(ns_norm_kernel, dim3(NORM_WGS), dim3(256), 0, s, p.g, p.dt, p.R * p.C,
                        ((uintptr_t)p.g & 15) == 0 ? 1 : 0, part);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int64_t wgs = std::min<int64_t>((p.R * L.ldx / 8 + 255) / 256, 2048);
-    hipLaunchKernelGGL(ns_split_kernel<NP>, dim3((unsigned)wgs), dim3(256), 0, s, p.g, p.dt, p.R, p.C, x[0], part, p.eps,
-                       (float)sx);
+    int* const exps = (int*)(W + L.exps);
+    const SplitParams sp{p.g, p.dt, p.R, p.C, x[0], part, exps, p.steps, p.a, p.b, p.c, p.eps};
+    hipLaunchKernelGGL(ns_split_kernel<NP>, dim3((unsigned)wgs), dim3(256), 0, s, sp);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     for (int k = 0; k < p.steps; ++k) {
         const Planes& cur = x[k & 1];
@@ -1328,8 +1420,7 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
         q.o = A;
         q.I = q.J = n;
         q.K = m;
-        q.alpha = (float)(1.0 / (sx * sx));
-        q.scale = (float)sa;
+        q.e = exps + k * NS_EXPS;
         q.mode = NS_SPLIT;
         e = tall ? ns_product<NP, true, true>(q, true, s) : ns_product<NP, false, false>(q, true, s);
         if (e != hipSuccess) return e;
@@ -1337,17 +1428,14 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
         q.u = q.v = q.old = A;
         q.o = P;
         q.K = n;
-        q.alpha = (float)(1.0 / (sa * sa));
-        q.old_inv = (float)(1.0 / sa);
-        q.scale = (float)sp;
+        q.e = exps + k * NS_EXPS + 1;
         q.a = (float)p.a;
         q.b = (float)p.b;
         q.c = (float)p.c;
         q.mode = NS_POLY;
         if ((e = ns_product<NP, false, false>(q, true, s)) != hipSuccess) return e;
         // X <- P X (stored [R][C]: i runs over C, j over R)
-        q.alpha = (float)(1.0 / (sx * sp));
-        q.scale = (float)sx;
+        q.e = exps + k * NS_EXPS + 4;
         q.o = x[(k + 1) & 1];
         q.I = p.C;
         q.J = p.R;
@@ -1374,8 +1462,7 @@ struct ThinLayout {
     int64_t npad, kr, ldx;
     int wgs;
 };
-static ThinLayout thin_layout(int64_t R, int64_t C, int dt) {
-    const size_t np = dt == DT_F32 ? 3 : 2;
+static ThinLayout thin_layout(int64_t R, int64_t C) {
     const int64_t n = std::min(R, C), m = std::max(R, C);
     ThinLayout L{};
     L.npad = n <= 16 ? 16 : n <= 32 ? 32 : n <= 64 ? 64 : 128;
@@ -1391,7 +1478,7 @@ static ThinLayout thin_layout(int64_t R, int64_t C, int dt) {
     take(L.exps, (size_t)L.wgs * 4);
     take(L.sum, (size_t)(L.npad * L.npad) * 4);
     take(L.top, 4);
-    take(L.q, np * (size_t)(L.npad * L.kr) * 2);
+    take(L.q, 3 * (size_t)(L.npad * L.kr) * 2);
     take(L.fac, 8);
     take(L.x, (size_t)(n * L.ldx) * 4);
     L.total = off;
@@ -1401,7 +1488,7 @@ static ThinLayout thin_layout(int64_t R, int64_t C, int dt) {
 template <int NPAD, int NP>
 static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
     using S = ThinShape<NPAD>;
-    const ThinLayout L = thin_layout(p.R, p.C, p.dt);
+    const ThinLayout L = thin_layout(p.R, p.C);
     char* W = p.ws;
     ThinParams t{};
     t.g = p.g;
@@ -1417,26 +1504,17 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
     t.part = (float*)(W + L.part);
     t.exps = (int*)(W + L.exps);
     t.out = p.out;
-    double topx = 1.0, top = 1.0, next, pm, tm;
-    for (int k = 0; k < p.steps; ++k) {
-        poly_bounds(p, top, &next, &pm, &tm);
-        top = next;
-        topx = std::max(topx, top);
-    }
-    // (bf16 pieces have fp32's range)
-    t.sx = NP == 2 ? (float)pow2_under(std::sqrt(topx)) : 1.0f;
     t.vec_out = (t.tall ? t.n : t.m) % 4 == 0 && ((uintptr_t)p.out & (p.dt == DT_F32 ? 15 : 7)) == 0;
     t.vec = (t.tall ? t.n : t.m) % 8 == 0 && ((uintptr_t)p.g & 15) == 0;
     // steps a segment: as many as Q's largest factor stays small for (its
     // rounding is relative to it), evenly shared
     constexpr bool WIDE = NPAD == 16 && NP == 2;   // ns_iter64_kernel
     int seg = WIDE ? NS_SEG64 : NP == 2 ? NS_SEG : 1;
-    double pall = 1.0;
-    top = 1.0;
+    double pall = 1.0, top = 1.0;
     for (int k = 0; k < p.steps; ++k) {
-        poly_bounds(p, top, &next, &pm, &tm);
-        pall = std::max(pall, pm);
-        top = next;
+        const NsBounds n = ns_bounds(p.a, p.b, p.c, top);
+        pall = std::max(pall, n.p);
+        top = n.next;
     }
     while (seg > 1 && std::pow(pall, seg) > NS_QMAX) --seg;
     const int segs = (p.steps + seg - 1) / seg;
@@ -1458,14 +1536,14 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
         q.eps = p.eps;
         double qmax = 1.0;
         for (int i = 0; i < q.steps; ++i) {
-            poly_bounds(p, top, &next, &pm, &tm);
-            qmax *= pm;
+            const NsBounds n = ns_bounds(p.a, p.b, p.c, top);
+            qmax *= n.p;
             const int at = WIDE ? 0 : i;   // (the 64-bit segment scales its last Q only)
-            q.sA[at] = NP == 2 ? (float)pow2_under(top) : 1.0f;
-            q.sP[at] = NP == 2 ? (float)pow2_under(pm) : 1.0f;
-            q.sT[at] = NP == 2 ? (float)pow2_under(tm) : 1.0f;
-            q.sQ[at] = NP == 2 ? (float)pow2_under(qmax) : 1.0f;
-            top = next;
+            q.eA[at] = ns_exponent<NP>(top);
+            q.eP[at] = ns_exponent<NP>(n.p);
+            q.eT[at] = ns_exponent<NP>(n.lp);
+            q.eQ[at] = ns_exponent<NP>(qmax);
+            top = n.next;
         }
         q.q = (uint16_t*)(W + L.q);
         q.fac = (double*)(W + L.fac);
@@ -1498,6 +1576,20 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
     return e;
 }
 
+// X's exponent follows from what the coefficients can make of |X0|.  Directions
+// of small singular values grow by |a| a step, none by more than max |p|: if
+// those part by more than 2^8 over the steps, X may be so far below its bound
+// that two fp16 pieces lose bits of it (ten are to spare at usual sizes).
+static bool ns_loose(const OrthoParams& p) {
+    double top = 1.0, part = 1.0;
+    for (int k = 0; k < p.steps; ++k) {
+        const NsBounds n = ns_bounds(p.a, p.b, p.c, top);
+        part *= n.p / std::fabs(p.a);
+        top = n.next;
+    }
+    return !(part <= 256.0);
+}
+
 template <int NP>
 static hipError_t ns_run(const OrthoParams& p, hipStream_t s) {
     const int64_t n = std::min(p.R, p.C);
@@ -1520,12 +1612,12 @@ OrthoPlan ortho_plan(int64_t R, int64_t C, int dt, int product) {
 
 size_t ortho_workspace(int64_t R, int64_t C, int dt) {
     if (R <= 0 || C <= 0) return 0;
-    return std::min(R, C) <= NS_THIN ? thin_layout(R, C, dt).total : ns_layout(R, C, dt).total;
+    return std::min(R, C) <= NS_THIN ? thin_layout(R, C).total : ns_layout(R, C, dt).total;
 }
 
 hipError_t launch_ortho(const OrthoParams& p, hipStream_t s) {
     if (p.R <= 0 || p.C <= 0) return hipSuccess;
-    return p.dt == DT_F32 ? ns_run<3>(p, s) : ns_run<2>(p, s);
+    return p.dt == DT_F32 || ns_loose(p) ? ns_run<3>(p, s) : ns_run<2>(p, s);
 }
 
 }  // namespace lyc

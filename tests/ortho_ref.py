@@ -44,7 +44,9 @@ def _rounded(v, bits):
 
 
 def _sum32(u, v):
-    return torch.mm(u.to(F32), v.to(F32).contiguous()).to(F64)
+    # (sizes by powers of two inside fp32's range: the sums' relative errors stay)
+    su, sv = (2.0 ** -torch.frexp(t.abs().max())[1].item() for t in (u, v))
+    return torch.mm((u * su).to(F32), (v * sv).to(F32).contiguous()).to(F64) / su / sv
 
 
 def emulate(g, bits, steps=5, coef=COEF, eps=1e-7):
