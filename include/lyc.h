@@ -436,6 +436,14 @@ int lyc_fp8_quantize_rows(const void* x, int x_dt, void* q, float* s, int64_t M,
 int lyc_fp8_quantize_weight(const void* w, int w_dt, void* q, void* q_t, float* s, int64_t N, int64_t K,
                             void* stream);
 int lyc_fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
+/*
+ * lyc_fp8_linear_plan (host only): output tile (features x rows) and K split of
+ * the product of an M x N y in y_dt over K, here, in lyc_fp8_lora_linear_fwd
+ * and, with N and K exchanged, in dx of its backward.  Up to 32 rows: the
+ * features and rows of one workgroup of the few-row kernel.  Any output may be
+ * NULL.
+ */
+int lyc_fp8_linear_plan(int64_t M, int64_t N, int64_t K, int y_dt, int* tile_n, int* tile_m, int* ksplit);
 int lyc_fp8_linear_fwd(const void* q_x, const float* s_x, const void* q_w, const float* s_w, const void* bias,
                        int bias_dt, void* y, int y_dt, int64_t M, int64_t N, int64_t K, void* workspace,
                        size_t workspace_bytes, void* stream);

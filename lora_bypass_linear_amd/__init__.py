@@ -21,7 +21,8 @@ __all__ = ["F16", "BF16", "F32", "LycError", "MixedHalfError", "lib", "resolve_d
            "tuning_load", "tuning_clear", "tuning_count", "tuning_key", "tuning_lookup", "tuning_cache_path", "profile_begin", "profile_end",
            "dtype_code", "torch_dtype", "fp8_quantize_rows", "fp8_quantize_weight", "fp8_linear", "fp8_lora_linear",
            "fp8_lora_saved_h", "fp8_lora_linear_backward", "fp8_linear_workspace_size", "fp8_lora_workspace_size",
-           "fp8_lora_bwd_workspace_size", "orthogonalize", "orthogonalize_workspace_size", "orthogonalize_plan"]
+           "fp8_lora_bwd_workspace_size", "orthogonalize", "orthogonalize_workspace_size", "orthogonalize_plan",
+           "fp8_linear_plan"]
 
 F16, BF16, F32 = 1, 2, 3
 OK, ERR_MIXED_HALF, ERR_INVALID_ARG, ERR_DTYPE_MISMATCH, ERR_UNSUPPORTED, ERR_HIP, ERR_WORKSPACE, ERR_IO, ERR_SCRATCH = range(9)
@@ -119,6 +120,7 @@ def lib():
         L.lyc_fp8_quantize_rows.argtypes = [c_vp, c_int, c_vp, c_vp, c_i64, c_i64, c_vp]
         L.lyc_fp8_quantize_weight.argtypes = [c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_vp]
         L.lyc_fp8_linear_workspace_size.argtypes = [c_i64, c_i64, c_i64, ctypes.POINTER(c_sz)]
+        L.lyc_fp8_linear_plan.argtypes = [c_i64, c_i64, c_i64, c_int] + [ctypes.POINTER(c_int)] * 3
         L.lyc_fp8_linear_fwd.argtypes = [c_vp, c_vp, c_vp, c_vp, c_vp, c_int, c_vp, c_int, c_i64, c_i64, c_i64, c_vp,
                                          c_sz, c_vp]
         L.lyc_fp8_lora_linear_workspace_size.argtypes = [c_i64, c_i64, c_i64, c_i64, c_int, c_int, c_int, c_int,
@@ -153,7 +155,7 @@ def lib():
                    L.lyc_tuning_load, L.lyc_tuning_clear, L.lyc_tuning_count, L.lyc_dora_norms_workspace_size,
                    L.lyc_dora_norms, L.lyc_dora_linear_workspace_size, L.lyc_dora_linear_fwd,
                    L.lyc_fp8_quantize_rows, L.lyc_fp8_quantize_weight, L.lyc_fp8_linear_workspace_size,
-                   L.lyc_fp8_linear_fwd, L.lyc_fp8_lora_linear_workspace_size, L.lyc_fp8_lora_workspace_layout,
+                   L.lyc_fp8_linear_plan, L.lyc_fp8_linear_fwd, L.lyc_fp8_lora_linear_workspace_size, L.lyc_fp8_lora_workspace_layout,
                    L.lyc_fp8_lora_linear_fwd, L.lyc_fp8_lora_linear_bwd_workspace_size, L.lyc_fp8_lora_linear_bwd,
                    L.lyc_orthogonalize_workspace_size, L.lyc_orthogonalize_plan, L.lyc_orthogonalize, L.lyc_gemm_tile, L.lyc_profile_begin, L.lyc_profile_end):
             fn.restype = c_int
@@ -744,6 +746,14 @@ def fp8_linear_workspace_size(M: int, N: int, K: int) -> int:
     n = ctypes.c_size_t(0)
     _check(lib().lyc_fp8_linear_workspace_size(M, N, K, ctypes.byref(n)))
     return n.value
+
+
+def fp8_linear_plan(M: int, N: int, K: int, y_dt: int) -> Tuple[int, int, int]:
+    """(tile_n, tile_m, ksplit) of the 8-bit product; up to 32 rows the
+    features and rows of one workgroup of the few-row kernel."""
+    v = [ctypes.c_int(0) for _ in range(3)]
+    _check(lib().lyc_fp8_linear_plan(M, N, K, y_dt, *(ctypes.byref(i) for i in v)))
+    return v[0].value, v[1].value, v[2].value
 
 
 def fp8_lora_workspace_size(M, N, K, r, x_dt, b_dt, d_dt, u_dt) -> int:

@@ -164,7 +164,7 @@ Layout layout(const Problem& P) {
         // x's codes and scales, and the partial sums of a K-split product
         L.xq = off; off = align256(off + (size_t)(P.M * P.K));
         L.xs = off; off = align256(off + (size_t)P.M * (size_t)((P.K + 127) / 128) * 4);
-        L.ksplit = lyc::fp8_gemm_ksplit(P.M, P.N, P.K);
+        L.ksplit = lyc::fp8_gemm_plan(P.M, P.N, P.K, P.o_dt).ksplit;
         if (L.ksplit > 1) { L.partial = off; off = align256(off + (size_t)L.ksplit * (size_t)(P.M * P.N) * 4); }
     } else if (P.lora) {
         // fp32 partial sums of a K-split GEMM (few output tiles), sized for
@@ -655,7 +655,7 @@ BwdLayout bwd_layout(const Bwd& B) {
             take(L.gq, M * N);
             take(L.gs, M * ((N + 127) / 128) * 4);
         }
-        L.ks_dx = P.w8 ? lyc::fp8_gemm_ksplit(P.M, P.K, P.N) : lyc::gemm_ksplit(P.M, P.K, P.N, P.c_dt);
+        L.ks_dx = P.w8 ? lyc::fp8_gemm_plan(P.M, P.K, P.N, P.x_dt).ksplit : lyc::gemm_ksplit(P.M, P.K, P.N, P.c_dt);
         if (L.ks_dx > 1) part = std::max(part, (size_t)L.ks_dx * M * K * 4);
     }
     if (dd) {
@@ -1317,8 +1317,20 @@ static int check_fp8_linear(int64_t M, int64_t N, int64_t K) {
 int lyc_fp8_linear_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
     const int st = check_fp8_linear(M, N, K);
     if (st != LYC_OK) return st;
-    const int ks = lyc::fp8_gemm_ksplit(M, N, K);
+    // (enough for every y_dt)
+    const int ks = std::max(lyc::fp8_gemm_plan(M, N, K, LYC_BF16).ksplit, lyc::fp8_gemm_plan(M, N, K, LYC_F32).ksplit);
     if (bytes) *bytes = ks > 1 ? align256((size_t)ks * (size_t)(M * N) * 4) : 0;
+    return LYC_OK;
+}
+
+int lyc_fp8_linear_plan(int64_t M, int64_t N, int64_t K, int y_dt, int* tile_n, int* tile_m, int* ksplit) {
+    const int st = check_fp8_linear(M, N, K);
+    if (st != LYC_OK) return st;
+    if (!valid_dt(y_dt)) return LYC_ERR_INVALID_ARG;
+    const lyc::Fp8Plan p = lyc::fp8_gemm_plan(M, N, K, y_dt);
+    if (tile_n) *tile_n = p.tile_n;
+    if (tile_m) *tile_m = p.tile_m;
+    if (ksplit) *ksplit = p.ksplit;
     return LYC_OK;
 }
 
@@ -1341,7 +1353,7 @@ int lyc_fp8_linear_fwd(const void* q_x, const float* s_x, const void* q_w, const
         overlaps(y, ny, s_w, (size_t)((N + 127) / 128 * ((K + 127) / 128)) * 4) ||
         (bias && overlaps(y, ny, bias, (size_t)N * esize(bias_dt))))
         return LYC_ERR_INVALID_ARG;
-    const int ks = lyc::fp8_gemm_ksplit(M, N, K);
+    const int ks = lyc::fp8_gemm_plan(M, N, K, y_dt).ksplit;
     const size_t need = ks > 1 ? align256((size_t)ks * (size_t)(M * N) * 4) : 0;
     if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
         return LYC_ERR_WORKSPACE;

@@ -49,9 +49,13 @@ struct Fp8GemmParams {
     int64_t sw_n, sw_k;
 };
 hipError_t launch_fp8_gemm(int c_dt, const Fp8GemmParams& p, hipStream_t s);
-// K splits launch_fp8_gemm takes for this shape (its partial sums then need
-// ksplit * M * N * 4 bytes)
-int fp8_gemm_ksplit(int64_t M, int64_t N, int64_t K);
+// Output tile and K split launch_fp8_gemm takes (the partial sums of a split
+// need ksplit * M * N * 4 bytes); up to 32 rows: the features and rows of a
+// workgroup of the few-row kernel
+struct Fp8Plan {
+    int tile_n, tile_m, ksplit;
+};
+Fp8Plan fp8_gemm_plan(int64_t M, int64_t N, int64_t K, int y_dt);
 
 // y = round_out(post * (the K splits' partial sums in split order) + bias), gemm.hip
 hipError_t launch_gemm_reduce(const GemmParams& p, hipStream_t s);

@@ -553,6 +553,9 @@ static bool fp8_skinny(int64_t M, int64_t K) {
     return M >= 1 && M <= 32 && K > 0 && 32 * K < ((int64_t)1 << 31);
 }
 
+// enough features for a workgroup per CU at 32 each
+static bool fp8_wide(int64_t N) { return N >= 32 * device_rates().cus; }
+
 template <class CT, int MT, int NF>
 static hipError_t run_skinny8(const Fp8GemmParams& p, hipStream_t s) {
     // 4 waves, 2 blocks ahead: more waves or loads in flight were slower (16 x
@@ -563,43 +566,62 @@ static hipError_t run_skinny8(const Fp8GemmParams& p, hipStream_t s) {
 }
 template <class CT>
 static hipError_t run_skinny8_ct(const Fp8GemmParams& p, hipStream_t s) {
-    const bool wide = p.g.N >= 32 * device_rates().cus;
+    const bool wide = fp8_wide(p.g.N);
     if (p.g.M <= 16) return wide ? run_skinny8<CT, 1, 2>(p, s) : run_skinny8<CT, 1, 1>(p, s);
     return wide ? run_skinny8<CT, 2, 2>(p, s) : run_skinny8<CT, 2, 1>(p, s);
 }
 
 enum { T8_L, T8_M, T8_S };
 
-// Output tile and K split: the fewest rounds of workgroups over the device's
-// CUs, weighted by the tile's area and a penalty for its operand re-reads,
-// plus the partial sums' round trip of a split.
-static void fp8_pick(int64_t M, int64_t N, int64_t K, int* tile, int* ksplit) {
-    struct C { int id, tn, tm, per_cu; double pen; };
-    const C cands[] = {{T8_L, 256, 256, 1, 1.0}, {T8_M, 128, 128, 1, 1.3}, {T8_S, 64, 64, 2, 2.0}};
+// Output tile and K split by modelled time, us: rounds of workgroups over the
+// CUs (two 64 x 64 ones share one), each a fixed part and its K steps, plus a
+// split's partial sums out and in again.  Measured steps of 128, on a device
+// up to four fifths full (64 x 64: of one a CU) and full:
+//             16-bit y (8-bit MFMAs)      fp32 y (EXACT)
+//   256 x 256    1.3, 1.3  fixed 10.5       3.05, 3.05  fixed 12
+//   128 x 128    0.41, 0.5       7          1.1, 1.1          6
+//   64 x 64      0.42, 0.52      5          0.57, 0.8         5
+// (16-bit rows of y that are not whole 16-byte pieces are stored by element: 15,
+// 4.5 and 1.5 more: 2500 x 2500 x 2560 took 50.0 in 256 x 256, 2560 x 2560 34.3.)
+// Whole calls, the pick and what it is held against: 64 x 4096 x 4096 bf16 64 x
+// 64 tiles in 4 splits 12.0, one 17.6; 1024 x 1024 x 8192 bf16 128 x 128 in 4
+// splits 22.5, 64 x 64 in one 32.0; 256 x 2048 x 4096 fp32 64 x 64 in 4 splits
+// 15.8, in one 23.3.
+static void fp8_pick(int64_t M, int64_t N, int64_t K, bool exact, int* tile, int* ksplit) {
+    struct C { int id, tn, tm, per_cu; double light, fixed, few, full, by_element; };
+    const C cands[2][3] = {
+        {{T8_L, 256, 256, 1, 0.8, 10.5, 1.3, 1.3, 15.0},
+         {T8_M, 128, 128, 1, 0.8, 7.0, 0.41, 0.5, 4.5},
+         {T8_S, 64, 64, 2, 1.0, 5.0, 0.42, 0.52, 1.5}},
+        {{T8_L, 256, 256, 1, 0.8, 12.0, 3.05, 3.05, 0.0},
+         {T8_M, 128, 128, 1, 0.8, 6.0, 1.1, 1.1, 0.0},
+         {T8_S, 64, 64, 2, 1.0, 5.0, 0.57, 0.8, 0.0}}};
     const double cus = (double)device_rates().cus;
     const int64_t ksteps = (K + 127) / 128;
     double best = 1e300;
     *tile = T8_S;
     *ksplit = 1;
-    for (const C& c : cands) {
+    for (const C& c : cands[exact ? 1 : 0]) {
         const double tiles = (double)((N + c.tn - 1) / c.tn) * (double)((M + c.tm - 1) / c.tm);
         for (int ks = 1; ks <= 8; ks *= 2) {
             if (ks > 1 && (ks > ksteps / 2 || (double)M * N * 4.0 * ks > 32.0 * 1024 * 1024)) continue;
             const double steps = (double)((ksteps + ks - 1) / ks);
-            const double rounds = std::ceil(tiles * ks / cus);
-            // a step of 256 x 256 x 128 takes about 1 us
-            double t = rounds * steps * (c.tn * c.tm / 65536.0) * c.pen;
-            if (ks > 1) t += (double)M * N * 4.0 * (ks + 1) / 4e6 + 4.0;
+            const double fixed = c.fixed + (ks == 1 && N % 8 != 0 ? c.by_element : 0.0);
+            const double rounds = std::ceil(tiles * ks / (cus * c.per_cu));
+            double t = rounds * (fixed + steps * (tiles * ks <= c.light * rounds * cus ? c.few : c.full));
+            if (ks > 1) t += 2.5 + (double)M * N * 4.0 * (ks + 1) / 2.5e6;
             if (t < best) { best = t; *tile = c.id; *ksplit = ks; }
         }
     }
 }
 
-int fp8_gemm_ksplit(int64_t M, int64_t N, int64_t K) {
-    if (M <= 0 || N <= 0 || K <= 0 || fp8_skinny(M, K)) return 1;
+Fp8Plan fp8_gemm_plan(int64_t M, int64_t N, int64_t K, int y_dt) {
+    if (M <= 0 || N <= 0) return Fp8Plan{0, 0, 1};
+    if (fp8_skinny(M, K)) return Fp8Plan{fp8_wide(N) ? 32 : 16, M <= 16 ? 16 : 32, 1};
     int t, ks;
-    fp8_pick(M, N, K, &t, &ks);
-    return ks;
+    fp8_pick(M, N, K, y_dt == DT_F32, &t, &ks);
+    const int tn = t == T8_L ? 256 : t == T8_M ? 128 : 64;
+    return Fp8Plan{tn, tn, ks};
 }
 
 template <class CT, class TL>
@@ -643,7 +665,7 @@ hipError_t launch_fp8_gemm(int c_dt, const Fp8GemmParams& p, hipStream_t s) {
         return run_skinny8_ct<CF32>(p, s);
     }
     int t, ks;
-    fp8_pick(p.g.M, p.g.N, p.g.K, &t, &ks);
+    fp8_pick(p.g.M, p.g.N, p.g.K, p.g.y_dt == DT_F32, &t, &ks);
     if (p.g.ksplit > 1 && p.g.partial == nullptr) return hipErrorInvalidValue;
     if (c_dt == DT_F16) return run8_ct<CF16>(p, t, s);
     if (c_dt == DT_BF16) return run8_ct<CBF16>(p, t, s);
