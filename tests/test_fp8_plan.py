@@ -58,3 +58,23 @@ def test_refusals():
         with pytest.raises(L.LycError):
             L.fp8_linear_plan(*bad)
     assert L.lib().lyc_fp8_linear_plan(64, 64, 64, 2, None, None, None) == L.OK
+
+
+def _path(M, N, K, dt):
+    tn, _, ks = L.fp8_linear_plan(M, N, K, dt)
+    blocks = -(-K // 128)
+    return tn, ks > 1, dt == L.F32, ks > 1 and -(-blocks // ks) * (ks - 1) >= blocks
+
+
+def test_gpu_shapes_reach_every_path():
+    """(tile, split, widened sums, last split empty) of 20000 shapes of more
+    than 32 rows: each is taken by the GPU tests, with and without the fold."""
+    from tests.test_gpu_fp8_paths import CASES, F32, RAGGED
+    with_fold = {_path(M, N, K, L.F32 if F32 in (dt, adt) else L.BF16) for M, N, K, _, dt, adt in CASES}
+    by_element = {_path(M, N, K, L.dtype_code(out))[:2] for M, N, K, out in RAGGED}
+    assert by_element == {(256, False), (256, True), (128, False), (128, True), (64, False), (64, True)}
+    rng = random.Random(7)
+    for _ in range(10000):
+        M, N, K = int(33 * 2 ** rng.uniform(0, 8)), 16 * int(2 ** rng.uniform(0, 9)), 16 * int(2 ** rng.uniform(0, 9.2))
+        for dt in (L.BF16, L.F32):
+            assert _path(M, N, K, dt) in with_fold, (M, N, K, dt, _path(M, N, K, dt))
