@@ -38,7 +38,6 @@ _lib = None
 E4M3 = torch.float8_e4m3fn   # the 8-bit codes (OCP e4m3)
 _CODE = {torch.float16: F16, torch.bfloat16: BF16, torch.float32: F32}
 _TORCH = {v: k for k, v in _CODE.items()}
-_RAW = (torch.uint8, E4M3)   # dtypes of workspaces and codes
 
 
 class LycError(RuntimeError):
@@ -231,18 +230,21 @@ def _lora_shapes(x, w, down, up, bias, out):
     return M, N, K, r
 
 
-def _need_device(*ts):
+def _need_device(*ts, codes=()):
+    """The one device of the operands (of a dtype code, or raw bytes) and of the
+    8-bit codes, all contiguous."""
     dev = None
-    for t in ts:
+    for i, t in enumerate((*ts, *codes)):
         if t is None:
             continue
-        if t.device == dev and t.is_contiguous() and (t.dtype in _CODE or t.dtype in _RAW):
+        raw = torch.uint8 if i < len(ts) else E4M3
+        if t.device == dev and t.is_contiguous() and (t.dtype in _CODE or t.dtype == raw):
             continue
         if not t.is_cuda:
             raise ValueError("lyc operands must be GPU tensors")
         if not t.is_contiguous():
             raise ValueError("lyc operands must be contiguous")
-        if t.dtype not in _CODE and t.dtype not in _RAW:
+        if t.dtype not in _CODE and t.dtype != raw:
             raise TypeError(f"unsupported dtype {t.dtype}")
         if dev is None:
             dev = t.device
@@ -701,7 +703,7 @@ def fp8_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     c * s[k // 128, m]."""
     M, K = _dims(x, 2, "x")
     _codes(q, s, (M, K), (_blocks(K), M), "q")
-    dev = _need_device(x, q, s)
+    dev = _need_device(x, s, codes=(q,))
     q = torch.empty((M, K), dtype=E4M3, device=dev) if q is None else q
     s = torch.empty((_blocks(K), M), dtype=torch.float32, device=dev) if s is None else s
     _check(lib().lyc_fp8_quantize_rows(_ptr(x), dtype_code(x), _ptr(q), _ptr(s), M, K, _stream(dev)))
@@ -782,7 +784,7 @@ def fp8_linear(q: torch.Tensor, s: torch.Tensor, w_q: torch.Tensor, w_s: torch.T
     _shape(out, (M, N), "out")
     b_dt = dtype_code(bias) if bias is not None else 0
     o_dt = dtype_code(out if out is not None else out_dtype)
-    dev = _need_device(q, s, w_q, w_s, bias, out, workspace)
+    dev = _need_device(s, w_s, bias, out, workspace, codes=(q, w_q))
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     ws = _workspace(_fp8_linear_plan(dev, M, N, K), dev, workspace)
@@ -812,7 +814,7 @@ def fp8_lora_linear(x: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor, down:
     M, N, K, r = _fp8_lora_shapes(x, w_q, w_s, down, up, bias, out)
     x_dt, d_dt, u_dt = dtype_code(x), dtype_code(down), dtype_code(up)
     b_dt = dtype_code(bias) if bias is not None else 0
-    dev = _need_device(x, w_q, w_s, down, up, bias, out, workspace)
+    dev = _need_device(x, w_s, down, up, bias, out, workspace, codes=(w_q,))
     o_dt, need = _fp8_lora_plan(dev, M, N, K, r, x_dt, b_dt, d_dt, u_dt)
     _out_dtype(out, o_dt)
     if out is None:
@@ -850,7 +852,7 @@ def fp8_lora_linear_backward(x: torch.Tensor, w_qt: torch.Tensor, w_s: torch.Ten
     ``h``: optional h_r the forward left (``fp8_lora_saved_h``)."""
     M, N, K, r = _fp8_lora_shapes(x, w_qt, w_s, down, up, None, None, transposed=True)
     _shape(dy, (M, N), "dy")
-    dev = _need_device(x, w_qt, w_s, down, up, dy, workspace, h)
+    dev = _need_device(x, w_s, down, up, dy, workspace, h, codes=(w_qt,))
     x_dt, d_dt, u_dt, g_dt = (dtype_code(t) for t in (x, down, up, dy))
     b_dt = _CODE[bias_dtype] if bias_dtype is not None else 0
     want = (BWD_DX if want_dx else 0) | (BWD_DDOWN if want_ddown else 0) | (BWD_DUP if want_dup else 0) | \
