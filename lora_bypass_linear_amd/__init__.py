@@ -542,6 +542,13 @@ def lora_merge(w: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale: flo
     return out
 
 
+def _saved_h(workspace: torch.Tensor, offset: int, M: int, ld: int, c_dt: int) -> torch.Tensor:
+    """[M, ld] in the compute dtype at a byte of the workspace, whose own dtype is any."""
+    es = 4 if c_dt == F32 else 2
+    raw = workspace.view(-1).view(torch.uint8)
+    return raw[offset: offset + M * ld * es].view(_TORCH[c_dt]).view(M, ld)
+
+
 def lora_saved_h(workspace: torch.Tensor, x: torch.Tensor, w: torch.Tensor, down: torch.Tensor, up: torch.Tensor,
                  bias: Optional[torch.Tensor] = None) -> torch.Tensor:
     """The h_r [M, r_pad] that lora_linear left in ``workspace`` (returned by
@@ -551,9 +558,7 @@ def lora_saved_h(workspace: torch.Tensor, x: torch.Tensor, w: torch.Tensor, down
     codes = [dtype_code(t) for t in (x, w)] + [dtype_code(bias) if bias is not None else 0] + \
         [dtype_code(down), dtype_code(up)]
     ho, ld, _, _ = lora_workspace_layout(M, N, K, r, *codes)
-    c_dt = resolve_dtypes([c for c in codes if c])[0]
-    es = 4 if c_dt == F32 else 2
-    return workspace[ho: ho + M * ld * es].view(_TORCH[c_dt]).view(M, ld)
+    return _saved_h(workspace, ho, M, ld, resolve_dtypes([c for c in codes if c])[0])
 
 
 def lora_linear_backward(x: torch.Tensor, w: torch.Tensor, down: torch.Tensor, up: torch.Tensor, scale: float,
@@ -775,7 +780,8 @@ def fp8_linear(q: torch.Tensor, s: torch.Tensor, w_q: torch.Tensor, w_s: torch.T
                bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
     """y [M,N] = round_out(x.W^T + b) of quantized x (``fp8_quantize_rows``)
-    and W (``fp8_quantize_weight``), fp32 accumulation; y in ``out_dtype``."""
+    and W (``fp8_quantize_weight``); y in ``out_dtype``, or in ``out``'s own
+    dtype where that is given."""
     M, K = _dims(q, 2, "q")
     N, _ = _dims(w_q, 2, "w_q")
     _codes(q, s, (M, K), (_blocks(K), M), "q")
@@ -836,9 +842,7 @@ def fp8_lora_saved_h(workspace: torch.Tensor, x: torch.Tensor, down: torch.Tenso
     codes = [dtype_code(x), dtype_code(bias) if bias is not None else 0, dtype_code(down), dtype_code(up)]
     ho, ld = ctypes.c_size_t(0), ctypes.c_int64(0)
     _check(lib().lyc_fp8_lora_workspace_layout(M, N, K, r, *codes, ctypes.byref(ho), ctypes.byref(ld)))
-    c_dt = resolve_dtypes([c for c in codes if c])[0]
-    es = 4 if c_dt == F32 else 2
-    return workspace[ho.value: ho.value + M * ld.value * es].view(_TORCH[c_dt]).view(M, ld.value)
+    return _saved_h(workspace, ho.value, M, ld.value, resolve_dtypes([c for c in codes if c])[0])
 
 
 def fp8_lora_linear_backward(x: torch.Tensor, w_qt: torch.Tensor, w_s: torch.Tensor, down: torch.Tensor,
