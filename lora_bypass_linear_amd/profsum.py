@@ -9,7 +9,7 @@
     # HBM traffic of one kernel (from one --pmc FETCH_SIZE run and one --pmc
     # WRITE_SIZE run of a command that also performs a plain copy of a known size)
     python -m lora_bypass_linear_amd.profsum traffic --fetch DIR_F --write DIR_W --kernel SUBSTR \\
-        --sources gemm|hpass|merge --calib-kernel copyBuffer --calib-bytes N --cmd "<commands>" --out profiles/NAME.txt
+        --sources gemm|hpass|merge|fp8|quant|ortho --calib-kernel copyBuffer --calib-bytes N --cmd "<commands>" --out profiles/NAME.txt
 
 FETCH_SIZE and WRITE_SIZE are reported in KiB per dispatch.  Each is scaled by
 the ratio (known bytes of the copy) / (what the same counter reports for the
@@ -29,9 +29,12 @@ import sys
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 # the sources each profiled kernel is built from
-SOURCES = {"gemm": ("csrc/gemm.hip", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h"),
-           "hpass": ("csrc/hpass.hip", "csrc/kernels.h", "csrc/lyc_device.h"),
-           "merge": ("csrc/merge.hip", "csrc/merge.h", "csrc/lyc_device.h")}
+SOURCES = {"gemm": ("csrc/gemm.hip", "csrc/fp8.h", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h"),
+           "hpass": ("csrc/hpass.hip", "csrc/fp8.h", "csrc/quant_device.h", "csrc/kernels.h", "csrc/lyc_device.h"),
+           "merge": ("csrc/merge.hip", "csrc/merge.h", "csrc/lyc_device.h"),
+           "fp8": ("csrc/fp8gemm.hip", "csrc/fp8.h", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h"),
+           "quant": ("csrc/quant.hip", "csrc/quant_device.h", "csrc/fp8.h", "csrc/kernels.h", "csrc/lyc_device.h"),
+           "ortho": ("csrc/ortho.hip", "csrc/ortho.h", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h")}
 
 
 def source_hash(kind: str) -> str:
@@ -102,22 +105,22 @@ def traffic(args) -> str:
 
 def mfma(args) -> str:
     """MFMA activity of one kernel from a --pmc run of SQ_VALU_MFMA_BUSY_CYCLES,
-    SQ_INSTS_VALU_MFMA_MOPS_F16, SQ_INSTS_VALU_MFMA_MOPS_BF16 and GRBM_GUI_ACTIVE:
+    GRBM_GUI_ACTIVE and SQ_INSTS_VALU_MFMA_MOPS_ of F16, BF16 and F8 (those collected):
     the fraction of SIMD cycles in which the matrix pipe was busy while the
     GPU was active, and the MFMA flops the counters saw (MOPS count units of
     512 flops).  GRBM_GUI_ACTIVE is counted once per XCD (the value is the
     sum over the XCDs' instances), SQ_VALU_MFMA_BUSY_CYCLES once per SIMD."""
     path = _find(args.dir, "counter_collection.csv")
     vals = {}
-    for c in ("SQ_VALU_MFMA_BUSY_CYCLES", "SQ_INSTS_VALU_MFMA_MOPS_F16", "SQ_INSTS_VALU_MFMA_MOPS_BF16",
-              "GRBM_GUI_ACTIVE"):
+    mops = tuple(f"SQ_INSTS_VALU_MFMA_MOPS_{t}" for t in ("F16", "BF16", "F8"))
+    for c in ("SQ_VALU_MFMA_BUSY_CYCLES", "GRBM_GUI_ACTIVE") + mops:
         per = _per_dispatch(path, c)
         ker = [v for n, v in per.values() if args.kernel in n]
-        if not ker:
+        if not ker and not (c in mops and not per):
             raise SystemExit(f"{c}: kernel not found in {args.dir}")
-        vals[c] = statistics.median(ker)
+        vals[c] = statistics.median(ker) if ker else 0.0
     busy, active = vals["SQ_VALU_MFMA_BUSY_CYCLES"], vals["GRBM_GUI_ACTIVE"] / args.xcds
-    flops = (vals["SQ_INSTS_VALU_MFMA_MOPS_F16"] + vals["SQ_INSTS_VALU_MFMA_MOPS_BF16"]) * 512.0
+    flops = sum(vals[c] for c in mops) * 512.0
     lines = ["# MFMA activity per launch (rocprofv3 --pmc, median over dispatches)",
              f"command: {args.cmd}",
              f"kernel: {args.kernel}",
