@@ -68,6 +68,18 @@ __device__ __forceinline__ void piece_mma(const i32x4 (&a)[I][NP], const i32x4 (
                 for (int j = 0; j < J; ++j) c[i][j] = Pieces<NP>::CT::step(a[i][k], b[j][o - k], c[i][j]);
 }
 
+// 2^e as two factors, for an e past fp32's exponents (an ldexp takes as long as
+// four products)
+struct Pow2 {
+    float a, b;
+    static __device__ __forceinline__ float one(int e) {
+        e = e < -126 ? -126 : e > 126 ? 126 : e;
+        return __builtin_bit_cast(float, (uint32_t)(e + 127) << 23);
+    }
+    explicit __device__ __forceinline__ Pow2(int e) : a(one(e / 2)), b(one(e - e / 2)) {}
+    __device__ __forceinline__ float operator()(float v) const { return v * a * b; }
+};
+
 // A matrix as pieces: [rows][ld] per piece, ld a multiple of 8, zero past cols
 struct Planes {
     uint16_t* p;
@@ -185,19 +197,19 @@ __host__ __device__ inline NsBounds ns_bounds(double a, double b, double c, doub
     return NsBounds{m[0], m[1], m[2]};
 }
 
-// the table, from theta = |X0|_F
-template <int NP>
-__device__ void ns_exponents(int* e, int steps, double a, double b, double c, double theta) {
+// the table, from a bound of |X0|_F
+template <int NP, class T>
+__host__ __device__ void ns_exponents(T* e, int steps, double a, double b, double c, double theta) {
     double top = theta * theta;
     int ex = ns_exponent<NP>(theta);
     for (int k = 0; k < steps; ++k) {
         const NsBounds n = ns_bounds(a, b, c, top);
         const int ea = ns_exponent<NP>(top), ep = ns_exponent<NP>(n.p), en = ns_exponent<NP>(sqrt(n.next));
-        e[0] = ea - 2 * ex;
-        e[1] = ep - 2 * ea;
-        e[2] = ep - ea;
-        e[3] = ep;
-        e[4] = (k + 1 < steps ? en : 0) - ex - ep;
+        e[0] = (T)(ea - 2 * ex);
+        e[1] = (T)(ep - 2 * ea);
+        e[2] = (T)(ep - ea);
+        e[3] = (T)ep;
+        e[4] = (T)((k + 1 < steps ? en : 0) - ex - ep);
         e += NS_EXPS;
         top = n.next;
         ex = en;
@@ -205,7 +217,9 @@ __device__ void ns_exponents(int* e, int steps, double a, double b, double c, do
 }
 
 // x = pieces of g / (|g| + eps), 8 columns a thread (rows padded to 8 columns
-// with zeros), and the table of the powers of two of what follows
+// with zeros), and the table of the powers of two of what follows: the host's
+// where |X0| > 1/2, which is where |G| > eps; one lane makes another from |X0|
+// itself (8 us for five steps).
 struct SplitParams {
     const void* g;
     int dt;
@@ -215,6 +229,7 @@ struct SplitParams {
     int* exps;   // [steps][NS_EXPS]
     int steps;
     double a, b, c, eps;
+    short usual[ORTHO_MAX_STEPS * NS_EXPS];   // the table for |X0| = 1
 };
 template <int NP>
 __global__ __launch_bounds__(256) void ns_split_kernel(SplitParams p) {
@@ -224,8 +239,16 @@ __global__ __launch_bounds__(256) void ns_split_kernel(SplitParams p) {
     const Planes x = p.x;
     // (the whole factor in 64 bits: a norm near fp32's ends has no fp32 reciprocal)
     const double norm = ns_norm(p.part), inv = ns_inverse(norm, p.eps);
-    const double f = ldexp(inv, ns_exponent<NP>(norm * inv));
-    if (blockIdx.x == 0 && threadIdx.x == 0) ns_exponents<NP>(p.exps, p.steps, p.a, p.b, p.c, norm * inv);
+    const double theta = norm * inv;
+    const bool usual = theta > 0.5;
+    const double f = ldexp(inv, ns_exponent<NP>(usual ? 1.0 : theta));
+    if (blockIdx.x == 0) {
+        if (usual) {
+            if ((int)threadIdx.x < p.steps * NS_EXPS) p.exps[threadIdx.x] = p.usual[threadIdx.x];
+        } else if (threadIdx.x == 0) {
+            ns_exponents<NP>(p.exps, p.steps, p.a, p.b, p.c, theta);
+        }
+    }
     const int64_t q = x.ld / 8, total = rows * q;
     const bool vec = cols % 8 == 0 && ((uintptr_t)g & 15) == 0;
     for (int64_t t = (int64_t)blockIdx.x * 256 + threadIdx.x; t < total; t += (int64_t)gridDim.x * 256) {
@@ -290,13 +313,24 @@ struct NsParams {
     float* partial;   // [ksplit][J][I rounded up to 4] when ksplit > 1 or sym
 };
 
+// a product's entries of the table, read at the kernel's start (at its end the
+// load would be waited for; left to the compiler, bf16 256 x 4096 took 199.5 us,
+// not 197.5)
+struct NsExps {
+    int e0, e1, e2;
+    explicit __device__ __forceinline__ NsExps(const NsParams& p)
+        : e0(__builtin_amdgcn_readfirstlane(p.e[0])), e1(__builtin_amdgcn_readfirstlane(p.e[1])),
+          e2(__builtin_amdgcn_readfirstlane(p.e[2])) {}
+};
+
 // the finished values of four consecutive i of row j from their sums (i a
 // multiple of 4 inside a row of pieces; zeros past I)
 template <int NP>
-__device__ __forceinline__ void ns_values4(const NsParams& p, f32x4 s, int64_t j, int64_t i, float (&v)[4]) {
-    const int e0 = p.e[0];
+__device__ __forceinline__ void ns_values4(const NsParams& p, const NsExps& x, f32x4 s, int64_t j, int64_t i,
+                                           float (&v)[4]) {
+    const Pow2 f0(x.e0);
     if (p.mode == NS_POLY) {
-        const int e1 = p.e[1], e2 = p.e[2];
+        const Pow2 f1(x.e1), f2(x.e2);
         i32x2 w[NP];
 #pragma unroll
         for (int k = 0; k < NP; ++k) w[k] = *(const i32x2*)(p.old.p + k * p.old.stride + j * p.old.ld + i);
@@ -305,12 +339,12 @@ __device__ __forceinline__ void ns_values4(const NsParams& p, f32x4 s, int64_t j
             uint16_t u[NP];
 #pragma unroll
             for (int k = 0; k < NP; ++k) u[k] = (uint16_t)((uint32_t)w[k][e >> 1] >> (e & 1) * 16);
-            v[e] = __builtin_ldexpf(p.c * s[e], e0) + __builtin_ldexpf(p.b * Pieces<NP>::join(u), e1);
-            if (i + e == j) v[e] += __builtin_ldexpf(p.a, e2);
+            v[e] = f0(p.c * s[e]) + f1(p.b * Pieces<NP>::join(u));
+            if (i + e == j) v[e] += f2(p.a);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) v[e] = __builtin_ldexpf(s[e], e0);
+        for (int e = 0; e < 4; ++e) v[e] = f0(s[e]);
     }
 #pragma unroll
     for (int e = 0; e < 4; ++e) v[e] = i + e < p.I ? v[e] : 0.f;
@@ -329,13 +363,13 @@ __device__ __forceinline__ void ns_store4(const NsParams& p, const float (&v)[4]
 
 // four consecutive i of row j (j < J; i past the row's end masked)
 template <int NP>
-__device__ __forceinline__ void ns_finish4(const NsParams& p, f32x4 s, int64_t j, int64_t i) {
+__device__ __forceinline__ void ns_finish4(const NsParams& p, const NsExps& x, f32x4 s, int64_t j, int64_t i) {
     if (p.mode == NS_OUT) {
-        const int e0 = p.e[0];
+        const Pow2 f0(x.e0);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
             if (i + e >= p.I) continue;
-            const float v = __builtin_ldexpf(s[e], e0);
+            const float v = f0(s[e]);
             const int64_t at = j * p.I + i + e;
             if (p.dt == DT_F32) ((float*)p.out)[at] = v;
             else ((uint16_t*)p.out)[at] = p.dt == DT_F16 ? f32_to_f16(v) : f32_to_bf16(v);
@@ -344,7 +378,7 @@ __device__ __forceinline__ void ns_finish4(const NsParams& p, f32x4 s, int64_t j
     }
     if (i >= p.o.ld) return;   // (ld a multiple of 8: all four or none)
     float v[4];
-    ns_values4<NP>(p, s, j, i, v);
+    ns_values4<NP>(p, x, s, j, i, v);
     ns_store4<NP>(p, v, j, i);
 }
 
@@ -429,6 +463,7 @@ __global__ __launch_bounds__(64 * WVI * WVJ, 1) void ns_gemm_kernel(NsParams p, 
     constexpr int STAGE = NP * (SideU::BYTES + SideV::BYTES), Q = NP * (SideU::Q + SideV::Q);
     static_assert(NS * STAGE <= 160 * 1024, "LDS");
     __shared__ __attribute__((aligned(16))) char smem[NS * STAGE];
+    const NsExps exps(p);
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int wi = wave % WVI, wj = wave / WVI;
@@ -531,7 +566,7 @@ __global__ __launch_bounds__(64 * WVI * WVJ, 1) void ns_gemm_kernel(NsParams p, 
                 const int64_t ldp = (p.I + 3) & ~(int64_t)3;
                 if (oi < ldp) *(f32x4*)(p.partial + ((int64_t)blockIdx.y * p.J + oj) * ldp + oi) = acc[i][j];
             } else {
-                ns_finish4<NP>(p, acc[i][j], oj, oi);
+                ns_finish4<NP>(p, exps, acc[i][j], oj, oi);
             }
         }
     }
@@ -540,6 +575,7 @@ __global__ __launch_bounds__(64 * WVI * WVJ, 1) void ns_gemm_kernel(NsParams p, 
 // sums of the K splits in split order, then the same finish
 template <int NP>
 __global__ __launch_bounds__(256) void ns_reduce_kernel(NsParams p) {
+    const NsExps exps(p);
     const int64_t ldp = (p.I + 3) & ~(int64_t)3;
     // (pieces: up to the padded row end, whose last four are zeros)
     const int64_t q = (p.mode == NS_OUT ? ldp : p.o.ld) / 4;
@@ -549,7 +585,7 @@ __global__ __launch_bounds__(256) void ns_reduce_kernel(NsParams p) {
         f32x4 s = f32x4{0.f, 0.f, 0.f, 0.f};
         if (i < ldp)
             for (int k = 0; k < p.ksplit; ++k) s += *(const f32x4*)(p.partial + ((int64_t)k * p.J + j) * ldp + i);
-        ns_finish4<NP>(p, s, j, i);
+        ns_finish4<NP>(p, exps, s, j, i);
     }
 }
 
@@ -558,6 +594,7 @@ __global__ __launch_bounds__(256) void ns_reduce_kernel(NsParams p) {
 // 64, so every such block is whole), written as it is and mirrored through LDS.
 template <int NP>
 __global__ __launch_bounds__(256) void ns_sym_reduce_kernel(NsParams p) {
+    const NsExps exps(p);
     __shared__ float tile[64][65];
     const int64_t ldp = (p.I + 3) & ~(int64_t)3;
     int bi = 0, bj = blockIdx.x;
@@ -583,7 +620,7 @@ __global__ __launch_bounds__(256) void ns_sym_reduce_kernel(NsParams p) {
         const int64_t j = (int64_t)bj * 64 + u * 16 + row;
         float v[4] = {0.f, 0.f, 0.f, 0.f};
         if (j < p.J && i < p.o.ld) {
-            ns_values4<NP>(p, s[u], j, i, v);
+            ns_values4<NP>(p, exps, s[u], j, i, v);
             ns_store4<NP>(p, v, j, i);
         }
 #pragma unroll
@@ -653,10 +690,23 @@ struct ThinParams {
     const double* fac;  // X' = fac * 2^e * (q . pieces)
     float* part;        // a Gram matrix per workgroup, [NPAD][NPAD]
     int* exps;          // which stands for 2^(2 e) times its values
+    int* chunk_e;       // x's chunks' exponents (two pieces)
     void* out;          // [R][C]
     int tall;
     int vec_out;        // out's rows hold whole groups of 4 elements, aligned for one store each
 };
+
+// the largest of a wave's values, in every lane
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+    auto step = [&](uint32_t o) { v = o > v ? o : v; };
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x111, 0xF, 0xF, false));   // row_shr 1, 2, 4, 8
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x112, 0xF, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x114, 0xF, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x118, 0xF, 0xF, false));
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x142, 0xF, 0xF, false));   // row_bcast 15, 31
+    step((uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, 0x143, 0xF, 0xF, false));
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
 
 __device__ __forceinline__ int exponent_of(uint32_t abs_bits) { return (int)(abs_bits >> 23) - 127; }
 
@@ -681,7 +731,7 @@ struct IterParams {
     int slots, steps, first;
     float a, b, c;
     double eps;
-    int eA[NS_SEG], eP[NS_SEG], eT[NS_SEG], eQ[NS_SEG];   // the powers of two each step's matrices are held times
+    float sA[NS_SEG], sP[NS_SEG], sT[NS_SEG], sQ[NS_SEG];   // the powers of two fp16 pieces are held times, step by step
     uint16_t* q;         // pieces [NP][NPAD][KR]
     double* fac;
 };
@@ -726,14 +776,17 @@ struct Iter {
     __device__ __forceinline__ int col_of(int tj) const { return (wj * TW + tj) * 16 + r; }
     __device__ __forceinline__ uint16_t* at(int b, int k) const { return buf + (b * NP + k) * NPAD * LD; }
 
-    __device__ __forceinline__ void put(int b, const M& m, int ex) const {
+    // 2^ex v (bf16 pieces have fp32's range and are taken as they are)
+    static __device__ __forceinline__ float held(float v, float scale) { return NP == 2 ? v * scale : v; }
+
+    __device__ __forceinline__ void put(int b, const M& m, float scale) const {
 #pragma unroll
         for (int ti = 0; ti < TW; ++ti)
 #pragma unroll
             for (int tj = 0; tj < TW; ++tj) {
                 uint16_t o[4][NP];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) Pieces<NP>::split(__builtin_ldexpf(m[ti][tj][e], ex), o[e]);
+                for (int e = 0; e < 4; ++e) Pieces<NP>::split(held(m[ti][tj][e], scale), o[e]);
 #pragma unroll
                 for (int k = 0; k < NP; ++k) {
                     *(i32x2*)(at(b, k) + col_of(tj) * LD + row_of(ti)) =
@@ -746,7 +799,7 @@ struct Iter {
                 }
             }
     }
-    __device__ __forceinline__ void product(int bu, int bv, M& out) const {
+    __device__ __forceinline__ void product(int bu, int bv, float scale, M& out) const {
 #pragma unroll
         for (int ti = 0; ti < TW; ++ti)
 #pragma unroll
@@ -763,15 +816,12 @@ struct Iter {
                 }
             piece_mma<NP>(u, v, out);
         }
-    }
-    __device__ __forceinline__ void product(int bu, int bv, int ex, M& out) const {
-        product(bu, bv, out);
+        if constexpr (NP == 2) {
 #pragma unroll
-        for (int ti = 0; ti < TW; ++ti)
+            for (int ti = 0; ti < TW; ++ti)
 #pragma unroll
-            for (int tj = 0; tj < TW; ++tj)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) out[ti][tj][e] = __builtin_ldexpf(out[ti][tj][e], ex);
+                for (int tj = 0; tj < TW; ++tj) out[ti][tj] *= scale;
+        }
     }
 
     // all of the workgroup's WAVES * 64 threads
@@ -827,38 +877,38 @@ struct Iter {
 
         for (int k = 0; k < p.steps; ++k) {
             M P;
-            put(0, A, p.eA[k]);
+            put(0, A, p.sA[k]);
             __syncthreads();
-            product(0, 0, P);
-            const int e2 = -2 * p.eA[k];
+            product(0, 0, 1.f / (p.sA[k] * p.sA[k]), P);
 #pragma unroll
             for (int ti = 0; ti < TW; ++ti)
 #pragma unroll
                 for (int tj = 0; tj < TW; ++tj)
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
-                        float v = __builtin_ldexpf(p.c * P[ti][tj][e], e2) + p.b * A[ti][tj][e];
+                        // (A^2 may leave fp32's range where nothing takes it)
+                        float v = (p.c != 0.f ? p.c * P[ti][tj][e] : 0.f) + p.b * A[ti][tj][e];
                         if (row_of(ti) + e == col_of(tj)) v += p.a;
                         P[ti][tj][e] = v;
                     }
             const bool more = k + 1 < p.steps;
             if constexpr (NP == 2) {
                 if (k > 0 || more) {
-                    put(1, P, p.eP[k]);
+                    put(1, P, p.sP[k]);
                     __syncthreads();
                 }
-                if (more) product(0, 1, -p.eA[k] - p.eP[k], A);   // T = A P
+                if (more) product(0, 1, 1.f / (p.sA[k] * p.sP[k]), A);   // T = A P
                 if (k > 0) {
                     __syncthreads();   // buffer 0 has been read
-                    put(0, Q, p.eQ[k - 1]);
+                    put(0, Q, p.sQ[k - 1]);
                     __syncthreads();
-                    product(0, 1, -p.eQ[k - 1] - p.eP[k], Q);
+                    product(0, 1, 1.f / (p.sQ[k - 1] * p.sP[k]), Q);
                 }
                 if (more) {
                     __syncthreads();
-                    put(0, A, p.eT[k]);
+                    put(0, A, p.sT[k]);
                     __syncthreads();
-                    product(0, 1, -p.eT[k] - p.eP[k], A);   // P A P
+                    product(0, 1, 1.f / (p.sT[k] * p.sP[k]), A);   // P A P
                     __syncthreads();
                 }
             }
@@ -869,14 +919,14 @@ struct Iter {
                     for (int tj = 0; tj < TW; ++tj) Q[ti][tj] = P[ti][tj];
             }
         }
-        const int eq = p.eQ[p.steps - 1];
+        const float sq = NP == 2 ? p.sQ[p.steps - 1] : 1.f;
 #pragma unroll
         for (int ti = 0; ti < TW; ++ti)
 #pragma unroll
             for (int tj = 0; tj < TW; ++tj) {
                 uint16_t o[4][NP];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) Pieces<NP>::split(__builtin_ldexpf(Q[ti][tj][e], eq), o[e]);
+                for (int e = 0; e < 4; ++e) Pieces<NP>::split(held(Q[ti][tj][e], sq), o[e]);
 #pragma unroll
                 for (int k = 0; k < NP; ++k) {
                     uint16_t* q = p.q + (int64_t)k * NPAD * KR;
@@ -893,7 +943,7 @@ struct Iter {
             for (int i = tid; i < NP * NPAD * (KR - NPAD); i += nt)
                 p.q[(i / (KR - NPAD)) * KR + NPAD + i % (KR - NPAD)] = 0;
         }
-        if (tid == 0) *p.fac = __builtin_ldexp(inv, -eq);
+        if (tid == 0) *p.fac = inv / (double)sq;
     }
 };
 
@@ -963,18 +1013,18 @@ __global__ __launch_bounds__(64) void ns_iter64_kernel(IterParams p) {
         Q = k == 0 ? P : product(Q, P);
         if (k + 1 < p.steps) A = product(product(A, P), P);
     }
-    const int eq = p.eQ[0];
+    const float sq = p.sQ[0];
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
         uint16_t o[2];
-        Pieces<2>::split((float)__builtin_ldexp(Q[e], eq), o);
+        Pieces<2>::split((float)(Q[e] * (double)sq), o);
 #pragma unroll
         for (int k = 0; k < 2; ++k) {
             p.q[(k * 16 + r) * KR + 4 * e + g] = o[k];
             p.q[(k * 16 + r) * KR + 16 + 4 * e + g] = 0;
         }
     }
-    if (lane == 0) *p.fac = __builtin_ldexp(inv, -eq);
+    if (lane == 0) *p.fac = inv / (double)sq;
 }
 
 template <int NPAD, int NP>
@@ -1021,14 +1071,6 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
     // as 2^-126).  The chunks of a Gram matrix share the largest e so far, the
     // sums made with a smaller one are scaled down.
     int erun = NS_EMPTY;
-    auto wave_max = [](uint32_t v) {
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const uint32_t o = (uint32_t)__shfl_xor((int)v, d);
-            v = o > v ? o : v;
-        }
-        return v;
-    };
     auto group_max = [&]() {
         uint32_t v = wmax[0];
 #pragma unroll
@@ -1050,6 +1092,10 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
     const int64_t chunks = (p.m + CW - 1) / CW;
     for (int64_t ch = blockIdx.x; ch < chunks; ch += gridDim.x) {
         const int64_t c0 = ch * CW;
+        int x_exponent = 0;
+        if constexpr (NP == 2 && MODE != THIN_GRAM) {
+            if (p.src == 2) x_exponent = p.chunk_e[ch];
+        }
         // the chunk, 16 elements a thread: two runs of 8 along the stored rows
         // where those are whole 16-byte pieces (vec), else single elements
         float v[S::PT];
@@ -1100,9 +1146,10 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
 #pragma unroll
             for (int u = 0; u < S::PT; ++u) v[u] = f32 ? __builtin_bit_cast(float, raw[u]) : widen(raw[u]);
         }
-        // (bf16 pieces have fp32's range: X between the segments stays as it is)
+        // (X between the segments: the pass that stored it knows; bf16 pieces have
+        // fp32's range and take it as it is)
         int e = 0;
-        if (NP == 2 || p.src != 2) {
+        if (p.src != 2) {
             uint32_t mx = 0;
 #pragma unroll
             for (int u = 0; u < S::PT; ++u) {
@@ -1122,13 +1169,15 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
                 e = gram_exponent(e);
             }
         } else {
+            if constexpr (NP == 2 && MODE != THIN_GRAM) e = x_exponent;
             __syncthreads();   // the previous chunk's tile has been read
         }
+        const Pow2 scaled(-e);
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             uint16_t o[8][NP];
 #pragma unroll
-            for (int u = 0; u < 8; ++u) Pieces<NP>::split(__builtin_ldexpf(v[8 * h + u], -e), o[u]);
+            for (int u = 0; u < 8; ++u) Pieces<NP>::split(scaled(v[8 * h + u]), o[u]);
 #pragma unroll
             for (int k = 0; k < NP; ++k) {
                 if (p.src == 1) {
@@ -1146,8 +1195,9 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
 
         if constexpr (MODE != THIN_GRAM) {
             // (a factor and an exponent: the two together may leave fp32's range)
-            const int fe = fexp + e;
-            auto finished = [&](float s) { return __builtin_ldexpf(s * fac, fe); };
+            const Pow2 fe(fexp + e);
+            const float fa = fac * fe.a;
+            auto finished = [&](float s) { return s * fa * fe.b; };
             f32x4 acc[S::CB][1];
 #pragma unroll
             for (int c = 0; c < S::CB; ++c) acc[c][0] = f32x4{0.f, 0.f, 0.f, 0.f};
@@ -1215,21 +1265,24 @@ __global__ __launch_bounds__(ThinShape<NPAD>::NT) void ns_chunk_kernel(ThinParam
                     if (lane == 0) wmax[wave] = top;
                     __syncthreads();   // the tile has been read: X' takes its place
                     top = group_max();
+                    en = top == 0 ? 0 : chunk_exponent(top);
+                    if (tid == 0) p.chunk_e[ch] = en;
                     if (top == 0) {
                         __syncthreads();
                         continue;
                     }
-                    en = gram_exponent(chunk_exponent(top));
+                    en = gram_exponent(en);
                 } else {
                     __syncthreads();   // the tile has been read: X' takes its place
                     erun = 0;
                 }
+                const Pow2 scaled_next(-en);
 #pragma unroll
                 for (int c = 0; c < S::CB; ++c) {
                     const int cc = (cb0 + c) * 16 + 4 * g;
                     uint16_t o[4][NP];
 #pragma unroll
-                    for (int el = 0; el < 4; ++el) Pieces<NP>::split(__builtin_ldexpf(acc[c][0][el], -en), o[el]);
+                    for (int el = 0; el < 4; ++el) Pieces<NP>::split(scaled_next(acc[c][0][el]), o[el]);
 #pragma unroll
                     for (int k = 0; k < NP; ++k)
                         *(i32x2*)&xs[k][i * LD + cc] = i32x2{(int)((uint32_t)o[0][k] | (uint32_t)o[1][k] << 16),
@@ -1342,7 +1395,7 @@ static NsLayout ns_layout(int64_t R, int64_t C, int dt) {
     size_t off = 0;
     auto take = [&](size_t& at, size_t bytes) { at = off; off = up256(off + bytes); };
     take(L.norm, NORM_WGS * sizeof(double));
-    take(L.exps, ORTHO_MAX_STEPS * NS_EXPS * sizeof(int));
+    take(L.exps, (ORTHO_MAX_STEPS * NS_EXPS + 2) * sizeof(int));   // (NsExps reads three from any entry)
     for (int i = 0; i < 2; ++i) take(L.x[i], np * (size_t)(R * L.ldx) * 2);
     take(L.A, np * (size_t)(n * L.ldn) * 2);
     take(L.P, np * (size_t)(n * L.ldn) * 2);
@@ -1408,7 +1461,9 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
     if (e != hipSuccess) return e;
     const int64_t wgs = std::min<int64_t>((p.R * L.ldx / 8 + 255) / 256, 2048);
     int* const exps = (int*)(W + L.exps);
-    const SplitParams sp{p.g, p.dt, p.R, p.C, x[0], part, exps, p.steps, p.a, p.b, p.c, p.eps};
+    SplitParams sp{p.g, p.dt, p.R, p.C, x[0], part, exps, p.steps, p.a, p.b, p.c, p.eps, {}};
+    static_assert(ORTHO_MAX_STEPS * NS_EXPS <= 256, "a thread for each of the table");
+    ns_exponents<NP>(sp.usual, p.steps, p.a, p.b, p.c, 1.0);
     hipLaunchKernelGGL(ns_split_kernel<NP>, dim3((unsigned)wgs), dim3(256), 0, s, sp);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     for (int k = 0; k < p.steps; ++k) {
@@ -1458,7 +1513,7 @@ static hipError_t ns_direct(const OrthoParams& p, hipStream_t s) {
 }
 
 struct ThinLayout {
-    size_t part, exps, sum, top, q, fac, x, total;
+    size_t part, exps, sum, top, q, fac, chunk_e, x, total;
     int64_t npad, kr, ldx;
     int wgs;
 };
@@ -1480,6 +1535,7 @@ static ThinLayout thin_layout(int64_t R, int64_t C) {
     take(L.top, 4);
     take(L.q, 3 * (size_t)(L.npad * L.kr) * 2);
     take(L.fac, 8);
+    take(L.chunk_e, (size_t)chunks * 4);
     take(L.x, (size_t)(n * L.ldx) * 4);
     L.total = off;
     return L;
@@ -1503,6 +1559,7 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
     t.fac = (const double*)(W + L.fac);
     t.part = (float*)(W + L.part);
     t.exps = (int*)(W + L.exps);
+    t.chunk_e = (int*)(W + L.chunk_e);
     t.out = p.out;
     t.vec_out = (t.tall ? t.n : t.m) % 4 == 0 && ((uintptr_t)p.out & (p.dt == DT_F32 ? 15 : 7)) == 0;
     t.vec = (t.tall ? t.n : t.m) % 8 == 0 && ((uintptr_t)p.g & 15) == 0;
@@ -1518,6 +1575,9 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
     }
     while (seg > 1 && std::pow(pall, seg) > NS_QMAX) --seg;
     const int segs = (p.steps + seg - 1) / seg;
+    // (ns_loose keeps the bounds below 2^45 and P's above 2^-9; an A or T below
+    // 2^-45 loses bits that no P sees)
+    auto pow2 = [](double bound) { return std::ldexp(1.f, std::max(-60, std::min(60, ns_exponent<NP>(bound)))); };
     const int64_t chunks = L.ldx / S::CW;
     hipError_t e = hipSuccess;
     top = 1.0;
@@ -1539,10 +1599,10 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
             const NsBounds n = ns_bounds(p.a, p.b, p.c, top);
             qmax *= n.p;
             const int at = WIDE ? 0 : i;   // (the 64-bit segment scales its last Q only)
-            q.eA[at] = ns_exponent<NP>(top);
-            q.eP[at] = ns_exponent<NP>(n.p);
-            q.eT[at] = ns_exponent<NP>(n.lp);
-            q.eQ[at] = ns_exponent<NP>(qmax);
+            q.sA[at] = pow2(top);
+            q.sP[at] = pow2(n.p);
+            q.sT[at] = pow2(n.lp);
+            q.sQ[at] = pow2(qmax);
             top = n.next;
         }
         q.q = (uint16_t*)(W + L.q);
@@ -1579,11 +1639,14 @@ static hipError_t ns_thin(const OrthoParams& p, hipStream_t s) {
 // X's exponent follows from what the coefficients can make of |X0|.  Directions
 // of small singular values grow by |a| a step, none by more than max |p|: if
 // those part by more than 2^8 over the steps, X may be so far below its bound
-// that two fp16 pieces lose bits of it (ten are to spare at usual sizes).
+// that two fp16 pieces lose bits of it (ten are to spare at usual sizes).  So
+// are steps that shrink or grow X by 2^9, or A past 2^45: the thin iteration's
+// scales and their products stay fp32 numbers.
 static bool ns_loose(const OrthoParams& p) {
     double top = 1.0, part = 1.0;
     for (int k = 0; k < p.steps; ++k) {
         const NsBounds n = ns_bounds(p.a, p.b, p.c, top);
+        if (n.p < 0x1p-9 || n.p > 0x1p9 || std::max(n.lp, n.next) > 0x1p45) return true;
         part *= n.p / std::fabs(p.a);
         top = n.next;
     }
