@@ -694,7 +694,7 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
     const bool use_w = wdx && M > 0 && N > 0 && K > 0;
     const bool use_f = r > 0 && M > 0;
     if ((use_x && x == nullptr) || (use_dy && dy == nullptr) || (use_w && (wt_given ? w_t : w) == nullptr) ||
-        (use_f && (down == nullptr || up == nullptr)))
+        (use_f && ((K > 0 && down == nullptr) || (N > 0 && up == nullptr))))
         return LYC_ERR_INVALID_ARG;
     // a caller-kept W_c^T [K][N] is read in place by the dx GEMM: 16-byte rows
     if (wt_given && use_w && !aligned(w_t, 16)) return LYC_ERR_UNSUPPORTED;
