@@ -428,9 +428,10 @@ int lyc_dora_linear_fwd(const void* x, int x_dt, const void* w, int w_dt, const 
  *   product's exponent: y is off by up to 7 * 2^-13 of the largest product of
  *   each 8 beside its own rounding (1.5e-5 of y's norm on normal data).  For an
  *   fp32 y, or up to 32 rows, it is 16-bit MFMAs of the widened codes, fp32
- *   throughout.  y_dt is
- *   the caller's choice, and so is the bias's dtype (8-bit operands enter no
- *   dtype policy).
+ *   throughout.  y_dt is the caller's choice, and so is the bias's dtype (8-bit
+ *   operands enter no dtype policy).  s_x s_w is formed in fp32: scales whose
+ *   product leaves its range (largest magnitudes of x and W that multiply to
+ *   more than 6e43, or less than 3e-33) give infinities or NaN, or lose bits.
  */
 int lyc_fp8_quantize_rows(const void* x, int x_dt, void* q, float* s, int64_t M, int64_t K, void* stream);
 int lyc_fp8_quantize_weight(const void* w, int w_dt, void* q, void* q_t, float* s, int64_t N, int64_t K,

@@ -653,14 +653,14 @@ __global__ __launch_bounds__(256) void ns_sym_reduce_kernel(NsParams p) {
 // one segment measured 1e-4 and more), and one step with three.
 // Times at bf16 8192 x 128 / bf16 16 x 4096 / fp32 64 x 4096, us a launch:
 //   ns_chunk_kernel  Gram matrix of X / X <- Q X with it / the last X <- Q X:
-//                    10, 15, 8 / 5, -, 5 / 5, 7, 6 (launch, one round of loads,
-//                    LDS and the Gram matrices' writes; no bandwidth near its limit)
+//                    10.5, 14.8, 8.3 / 4.1, -, 5.4 / 5.3, 7.4, 6.1 (launch, one round of
+//                    loads, LDS and the Gram matrices' writes; no bandwidth near its limit)
 //   Iter             a segment of steps; the first one scales by 1 / (|G| + eps),
 //                    |G|^2 being the trace: 29 and 19 (9 and 5 dependent 128^3
-//                    products) / 7 (in 64 bits) / 4.3
+//                    products) / 7.3 (in 64 bits) / 3.9
 //                    (a kernel of its own: run by the last workgroup of the one
 //                    before, behind a device-wide fence, it took 2 us more)
-//   ns_sum_kernel    the workgroups' Gram matrices added up (n > 32): 4.6 / - / 3.2
+//   ns_sum_kernel    the workgroups' Gram matrices added up (n > 32): 4.5 / - / 3.3
 
 constexpr int NS_SEG = 3, NS_SEG64 = 5;
 constexpr double NS_QMAX = 1024.0;   // bound on Q's largest factor within a segment
@@ -1525,7 +1525,9 @@ static ThinLayout thin_layout(int64_t R, int64_t C) {
     const int64_t cw = L.npad == 16 ? 256 : L.npad == 32 ? 128 : 64;
     const int64_t chunks = (m + cw - 1) / cw;
     L.ldx = chunks * cw;
-    // (few enough Gram matrices that adding them up stays short)
+    // few enough Gram matrices that adding them up stays short; a long side past
+    // 8192 (4096 for 17 .. 32) leaves each workgroup several chunks in turn
+    // (bf16 16 x 4096 16 us, 16 x 32768 22, 16 x 131072 40)
     L.wgs = (int)std::min<int64_t>(chunks, L.npad <= 32 ? 32 : 128);
     size_t off = 0;
     auto take = [&](size_t& at, size_t bytes) { at = off; off = up256(off + bytes); };
