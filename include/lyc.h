@@ -488,6 +488,110 @@ int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const flo
                             int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
 
 /*
+ * Gated feed-forward block: two LoRA-bypass projections of the same x, an
+ * activation and their product, in one kernel behind the h pass:
+ *   g = x_c.W_gate_c^T  + scale * round_c(x_c.down_gate_c^T).up_gate_c^T   + b_gate
+ *   v = x_c.W_value_c^T + scale * round_c(x_c.down_value_c^T).up_value_c^T + b_value
+ *   y = round_out( act(g) * v )
+ * Each projection is lyc_lora_linear_fwd's before its rounding: g and v stay in
+ * the fp32 accumulators, are never rounded on the way to y and reach memory
+ * only where the caller keeps them.  act: LYC_ACT_SILU g / (1 + exp(-g)),
+ * LYC_ACT_GELU g Phi(g), LYC_ACT_GELU_TANH g (1 + tanh(sqrt(2/pi) (g + 0.044715
+ * g^3))) / 2, in fp32 (a few units of 2^-23 of the result; the tanh form's
+ * tail of negative g, where it falls to 0 as exp(u), also 2^-22 |u| of it).
+ *  - Shapes as lyc_lora_linear_fwd for each projection; both have the same
+ *    sizes, dtypes and rank.  The dtype policy runs over (x, W, b, down, up);
+ *    both biases or neither.  rank == 0: no bypass (factors may be NULL).
+ *  - gate, value: NULL (both), or [M][N] in the compute dtype: round_c(g) and
+ *    round_c(v), which the backward reads.  h: NULL, or [M][2 r_pad] in the
+ *    compute dtype, 16-byte aligned (r_pad as lyc_lora_linear_workspace_size has
+ *    it): h_r of gate in columns 0 .., of value in columns r_pad .., zeros from
+ *    the rank on.  Nothing is written there for rank == 0.
+ *  - No output may overlap an input, the workspace or another output
+ *    (LYC_ERR_INVALID_ARG).  M * N <= 2^40 (LYC_ERR_UNSUPPORTED); everything
+ *    else, the workspace (lyc_lora_gated_workspace_size) and errors as
+ *    lyc_lora_linear_fwd.
+ * lyc_lora_gated_plan (host only): output tile (features x rows) and K split of
+ * the block's product, or with backward = 1 of dx's (N and K as the forward's);
+ * up to 32 rows the features and rows of one workgroup of the few-row kernel.
+ * Any output may be NULL.
+ */
+enum { LYC_ACT_SILU = 0, LYC_ACT_GELU = 1, LYC_ACT_GELU_TANH = 2 };
+int lyc_lora_gated_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int w_dt, int bias_dt,
+                                  int down_dt, int up_dt, size_t* bytes);
+int lyc_lora_gated_plan(int64_t M, int64_t N, int64_t K, int compute_dt, int backward, int* tile_n, int* tile_m,
+                        int* ksplit);
+int lyc_lora_gated_fwd(const void* x, int x_dt, const void* w_gate, const void* w_value, int w_dt,
+                       const void* bias_gate, const void* bias_value, int bias_dt, const void* down_gate,
+                       const void* down_value, int down_dt, const void* up_gate, const void* up_value, int up_dt,
+                       int64_t rank, double scale, int act, void* y, int y_dt, void* gate, void* value, void* h,
+                       int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+/*
+ * Its backward (W and the biases frozen), from dy and the kept projections (the
+ * values as stored, in the compute dtype c of the policy over (x, W, b, down,
+ * up, dy)):
+ *   dg    = round_c( dy * value * act'(gate) )       dv = round_c( dy * act(gate) )
+ *   gh_p  = round_c( scale * d_p . up_p_c )           p = gate (d = dg), value (d = dv); rounded
+ *                                                     once from its exact value
+ *   dx    = round_x( sum_p d_p . W_p_c + gh_p . down_p_c )
+ *   d_down_p = round_down( gh_p^T . x_c ),  d_up_p = round_up( scale * d_p^T . h_p )
+ * fp32 accumulation; dx's two products run in one kernel.
+ *  - w_gate, w_value or the caller-kept transposes w_gate_t, w_value_t [K][N] in
+ *    c (16-byte aligned): exactly one pair, read only when dx is wanted.
+ *  - h: the forward's [M][2 r_pad], or NULL (recomputed); read for d_up.
+ *  - dx, d_down_*, d_up_*: NULL where not wanted (the factors' in pairs).
+ *  - gate, value, dy and h 16-byte aligned; x too where it is in c.  K and N
+ *    multiples of 8, M, N, K <= 2^20, rank <= 256.  Workspace:
+ *    lyc_lora_gated_bwd_workspace_size with `want` as for lyc_lora_linear_bwd (1
+ *    dx, 2 d_down, 4 d_up, 8 transposes given, 16 h given).  Everything else as
+ *    lyc_lora_linear_bwd.
+ */
+int lyc_lora_gated_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int w_dt, int bias_dt,
+                                      int down_dt, int up_dt, int dy_dt, int want, size_t* bytes);
+int lyc_lora_gated_bwd(const void* x, int x_dt, const void* w_gate, const void* w_value, const void* w_gate_t,
+                       const void* w_value_t, int w_dt, int bias_dt, const void* down_gate, const void* down_value,
+                       int down_dt, const void* up_gate, const void* up_value, int up_dt, const void* gate,
+                       const void* value, const void* h, int64_t rank, double scale, int act, const void* dy,
+                       int dy_dt, void* dx, void* d_down_gate, void* d_down_value, void* d_up_gate, void* d_up_value,
+                       int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * 8-bit integers: the form in which merged weights are served.  A token's row of
+ * x and an output channel's row of W each have one fp32 scale:
+ *   s = max(amax, 2^-100) / 127          amax = max |x| over the row; fp32 division
+ *   q = rint(x / s)                      of the exact quotient, ties to even
+ * A row that holds an infinity or a NaN gets an infinite or NaN scale and codes
+ * 0 (its products are NaN).  lyc_int8_quantize_rows: x [M][K] -> q [M][K], s [M],
+ * for activations and for weights [N][K] alike.
+ *
+ * lyc_int8_linear_fwd: y = round_out( (sum_k q_x[m][k] q_w[n][k]) * s_w[n] * s_x[m]
+ *   + b[n] ): the sum is exact (32-bit integers; any code from -128 to 127), made
+ *   fp32 once, times s_w, then one fused multiply-add with s_x and b.
+ * lyc_int8_gated_fwd: the gated block over such weights, y = round_out( act(g) *
+ *   v ) with g and v as above before their rounding, in one kernel.
+ *  - K a multiple of 16, at most 131056; M, N <= 2^30, M * N <= 2^40
+ *    (LYC_ERR_UNSUPPORTED).  x and codes 16-byte aligned.  y_dt and the bias's
+ *    dtype are the caller's choice (8-bit operands enter no dtype policy).
+ *    Outputs and workspace must not overlap inputs or each other
+ *    (LYC_ERR_INVALID_ARG).  Scales are read, and written by the quantization,
+ *    for K == 0 too.
+ *  - *_plan (host only): output tile (features x rows) and K split; up to 32 rows
+ *    the features and rows of one workgroup of the few-row kernel.
+ */
+int lyc_int8_quantize_rows(const void* x, int x_dt, void* q, float* s, int64_t M, int64_t K, void* stream);
+int lyc_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int lyc_int8_linear_plan(int64_t M, int64_t N, int64_t K, int* tile_n, int* tile_m, int* ksplit);
+int lyc_int8_linear_fwd(const void* q_x, const float* s_x, const void* q_w, const float* s_w, const void* bias,
+                        int bias_dt, void* y, int y_dt, int64_t M, int64_t N, int64_t K, void* workspace,
+                        size_t workspace_bytes, void* stream);
+int lyc_int8_gated_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
+int lyc_int8_gated_plan(int64_t M, int64_t N, int64_t K, int* tile_n, int* tile_m, int* ksplit);
+int lyc_int8_gated_fwd(const void* q_x, const float* s_x, const void* q_gate, const float* s_gate, const void* q_value,
+                       const float* s_value, const void* bias_gate, const void* bias_value, int bias_dt, int act,
+                       void* y, int y_dt, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                       void* stream);
+
+/*
  * Orthogonalized update (the step an optimizer takes with a factor's or a
  * dense weight's gradient or momentum in place of the gradient itself): the
  * Newton-Schulz iteration

@@ -22,7 +22,9 @@ __all__ = ["F16", "BF16", "F32", "LycError", "MixedHalfError", "lib", "resolve_d
            "dtype_code", "torch_dtype", "fp8_quantize_rows", "fp8_quantize_weight", "fp8_linear", "fp8_lora_linear",
            "fp8_lora_saved_h", "fp8_lora_linear_backward", "fp8_linear_workspace_size", "fp8_lora_workspace_size",
            "fp8_lora_bwd_workspace_size", "orthogonalize", "orthogonalize_workspace_size", "orthogonalize_plan",
-           "fp8_linear_plan"]
+           "fp8_linear_plan", "lora_gated_linear", "lora_gated_linear_backward", "lora_gated_workspace_size",
+           "lora_gated_bwd_workspace_size", "lora_gated_plan", "int8_quantize_rows", "int8_linear", "int8_gated_linear",
+           "int8_linear_workspace_size", "int8_gated_workspace_size", "int8_linear_plan", "int8_gated_plan"]
 
 F16, BF16, F32 = 1, 2, 3
 OK, ERR_MIXED_HALF, ERR_INVALID_ARG, ERR_DTYPE_MISMATCH, ERR_UNSUPPORTED, ERR_HIP, ERR_WORKSPACE, ERR_IO, ERR_SCRATCH = range(9)
@@ -137,6 +139,21 @@ def lib():
         L.lyc_orthogonalize_workspace_size.argtypes = [c_i64, c_i64, c_int, ctypes.POINTER(c_sz)]
         L.lyc_orthogonalize_plan.argtypes = [c_i64, c_i64, c_int, c_int] + [ctypes.POINTER(c_int)] * 4
         L.lyc_orthogonalize.argtypes = [c_vp, c_int, c_vp, c_i64, c_i64, c_int, c_d, c_d, c_d, c_d, c_vp, c_sz, c_vp]
+        psz, pin = ctypes.POINTER(c_sz), ctypes.POINTER(c_int)
+        L.lyc_lora_gated_workspace_size.argtypes = [c_i64] * 4 + [c_int] * 5 + [psz]
+        L.lyc_lora_gated_plan.argtypes = [c_i64] * 3 + [c_int] * 2 + [pin] * 3
+        L.lyc_lora_gated_fwd.argtypes = [c_vp, c_int] + [c_vp, c_vp, c_int] * 4 + \
+            [c_i64, c_d, c_int, c_vp, c_int, c_vp, c_vp, c_vp, c_i64, c_i64, c_i64, c_vp, c_sz, c_vp]
+        L.lyc_lora_gated_bwd_workspace_size.argtypes = [c_i64] * 4 + [c_int] * 7 + [psz]
+        L.lyc_lora_gated_bwd.argtypes = [c_vp, c_int] + [c_vp] * 4 + [c_int, c_int] + [c_vp, c_vp, c_int] * 2 + \
+            [c_vp] * 3 + [c_i64, c_d, c_int, c_vp, c_int] + [c_vp] * 5 + [c_i64] * 3 + [c_vp, c_sz, c_vp]
+        L.lyc_int8_quantize_rows.argtypes = [c_vp, c_int, c_vp, c_vp, c_i64, c_i64, c_vp]
+        L.lyc_int8_linear_workspace_size.argtypes = [c_i64] * 3 + [psz]
+        L.lyc_int8_linear_plan.argtypes = [c_i64] * 3 + [pin] * 3
+        L.lyc_int8_linear_fwd.argtypes = [c_vp] * 5 + [c_int, c_vp, c_int] + [c_i64] * 3 + [c_vp, c_sz, c_vp]
+        L.lyc_int8_gated_workspace_size.argtypes = [c_i64] * 3 + [psz]
+        L.lyc_int8_gated_plan.argtypes = [c_i64] * 3 + [pin] * 3
+        L.lyc_int8_gated_fwd.argtypes = [c_vp] * 8 + [c_int, c_int, c_vp, c_int] + [c_i64] * 3 + [c_vp, c_sz, c_vp]
         L.lyc_gemm_tile.argtypes = [c_i64, c_i64, c_int, ctypes.POINTER(c_int), ctypes.POINTER(c_int)]
         L.lyc_profile_begin.argtypes = [c_int]
         L.lyc_profile_end.argtypes = [ctypes.POINTER(ctypes.c_double), ctypes.POINTER(c_int)]
@@ -156,7 +173,11 @@ def lib():
                    L.lyc_fp8_quantize_rows, L.lyc_fp8_quantize_weight, L.lyc_fp8_linear_workspace_size,
                    L.lyc_fp8_linear_plan, L.lyc_fp8_linear_fwd, L.lyc_fp8_lora_linear_workspace_size, L.lyc_fp8_lora_workspace_layout,
                    L.lyc_fp8_lora_linear_fwd, L.lyc_fp8_lora_linear_bwd_workspace_size, L.lyc_fp8_lora_linear_bwd,
-                   L.lyc_orthogonalize_workspace_size, L.lyc_orthogonalize_plan, L.lyc_orthogonalize, L.lyc_gemm_tile, L.lyc_profile_begin, L.lyc_profile_end):
+                   L.lyc_orthogonalize_workspace_size, L.lyc_orthogonalize_plan, L.lyc_orthogonalize,
+                   L.lyc_lora_gated_workspace_size, L.lyc_lora_gated_plan, L.lyc_lora_gated_fwd,
+                   L.lyc_lora_gated_bwd_workspace_size, L.lyc_lora_gated_bwd, L.lyc_int8_quantize_rows,
+                   L.lyc_int8_linear_workspace_size, L.lyc_int8_linear_plan, L.lyc_int8_linear_fwd,
+                   L.lyc_int8_gated_workspace_size, L.lyc_int8_gated_plan, L.lyc_int8_gated_fwd, L.lyc_gemm_tile, L.lyc_profile_begin, L.lyc_profile_end):
             fn.restype = c_int
         _lib = L
     return _lib
@@ -230,14 +251,14 @@ def _lora_shapes(x, w, down, up, bias, out):
     return M, N, K, r
 
 
-def _need_device(*ts, codes=()):
+def _need_device(*ts, codes=(), code_dtype=None):
     """The one device of the operands (of a dtype code, or raw bytes) and of the
-    8-bit codes, all contiguous."""
+    8-bit codes (e4m3 unless another dtype is named), all contiguous."""
     dev = None
     for i, t in enumerate((*ts, *codes)):
         if t is None:
             continue
-        raw = torch.uint8 if i < len(ts) else E4M3
+        raw = torch.uint8 if i < len(ts) else (code_dtype or E4M3)
         if t.device == dev and t.is_contiguous() and (t.dtype in _CODE or t.dtype == raw):
             continue
         if not t.is_cuda:
@@ -876,6 +897,275 @@ def fp8_lora_linear_backward(x: torch.Tensor, w_qt: torch.Tensor, w_s: torch.Ten
                                          _ptr(h), r, float(scale), _ptr(dy), g_dt, p(dx), p(dd), p(du), M, N, K,
                                          _ptr(ws), nbytes, _stream(dev)))
     return dx, dd, du
+
+
+# ---- gated feed-forward block ---------------------------------------------------
+
+ACTIVATIONS = {"silu": 0, "gelu": 1, "gelu_tanh": 2}
+
+
+def _activation(name: str) -> int:
+    if name not in ACTIVATIONS:
+        raise ValueError(f"activation {name!r} is none of {sorted(ACTIVATIONS)}")
+    return ACTIVATIONS[name]
+
+
+def lora_gated_workspace_size(M, N, K, r, x_dt, w_dt, b_dt, d_dt, u_dt) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().lyc_lora_gated_workspace_size(M, N, K, r, x_dt, w_dt, b_dt, d_dt, u_dt, ctypes.byref(n)))
+    return n.value
+
+
+def lora_gated_bwd_workspace_size(M, N, K, r, x_dt, w_dt, b_dt, d_dt, u_dt, dy_dt, want=7) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().lyc_lora_gated_bwd_workspace_size(M, N, K, r, x_dt, w_dt, b_dt, d_dt, u_dt, dy_dt, want,
+                                                   ctypes.byref(n)))
+    return n.value
+
+
+def lora_gated_plan(M: int, N: int, K: int, compute_dt: int, backward: bool = False) -> Tuple[int, int, int]:
+    """(tile_n, tile_m, ksplit) of the gated block's product, or of its dx; up
+    to 32 rows the features and rows of one workgroup of the few-row kernel."""
+    v = [ctypes.c_int(0) for _ in range(3)]
+    _check(lib().lyc_lora_gated_plan(M, N, K, compute_dt, int(backward), *(ctypes.byref(i) for i in v)))
+    return v[0].value, v[1].value, v[2].value
+
+
+@functools.lru_cache(maxsize=4096)
+def _gated_plan(dev, M, N, K, r, x_dt, w_dt, b_dt, d_dt, u_dt) -> Tuple[int, int, int, int]:
+    """(compute dtype, output dtype, r_pad, workspace bytes) of a forward."""
+    c_dt, o_dt = resolve_dtypes([x_dt, w_dt] + ([b_dt] if b_dt else []) + [d_dt, u_dt])
+    return c_dt, o_dt, _r_pad(r, c_dt), lora_gated_workspace_size(M, N, K, r, x_dt, w_dt, b_dt, d_dt, u_dt)
+
+
+@functools.lru_cache(maxsize=4096)
+def _gated_bwd_plan(dev, M, N, K, r, x_dt, w_dt, b_dt, d_dt, u_dt, g_dt, want) -> Tuple[int, int, int]:
+    c_dt, _ = resolve_dtypes([x_dt, w_dt] + ([b_dt] if b_dt else []) + [d_dt, u_dt, g_dt])
+    return c_dt, _r_pad(r, c_dt), lora_gated_bwd_workspace_size(M, N, K, r, x_dt, w_dt, b_dt, d_dt, u_dt, g_dt, want)
+
+
+def _r_pad(r: int, c_dt: int) -> int:
+    """The rank as the library pads it."""
+    if r == 0:
+        return 0
+    return next((p for p in ((32, 64, 128, 256) if c_dt == F32 else (16, 32, 64, 128, 256)) if r <= p), r)
+
+
+def _same_dtype(a: Optional[torch.Tensor], b: Optional[torch.Tensor], names: str) -> int:
+    """The dtype code that both tensors of a pair have (0: both absent)."""
+    if (a is None) != (b is None):
+        raise ValueError(f"{names}: both or neither")
+    if a is None:
+        return 0
+    if a.dtype != b.dtype:
+        raise ValueError(f"{names} have dtypes {a.dtype} and {b.dtype}, expected one")
+    return dtype_code(a)
+
+
+def _gated_shapes(x, w_gate, w_value, down_gate, up_gate, down_value, up_value, bias_gate, bias_value):
+    M, N, K, r = _lora_shapes(x, w_gate, down_gate, up_gate, bias_gate, None)
+    _shape(w_value, (N, K), "w_value")
+    _shape(down_value, (r, K), "down_value")
+    _shape(up_value, (N, r), "up_value")
+    _shape(bias_value, (N,), "bias_value")
+    dts = (dtype_code(x), _same_dtype(w_gate, w_value, "w_gate and w_value"),
+           _same_dtype(bias_gate, bias_value, "bias_gate and bias_value"),
+           _same_dtype(down_gate, down_value, "down_gate and down_value"),
+           _same_dtype(up_gate, up_value, "up_gate and up_value"))
+    return (M, N, K, r), dts
+
+
+def lora_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_value: torch.Tensor, down_gate: torch.Tensor,
+                      up_gate: torch.Tensor, down_value: torch.Tensor, up_value: torch.Tensor, scale: float,
+                      bias_gate: Optional[torch.Tensor] = None, bias_value: Optional[torch.Tensor] = None,
+                      activation: str = "silu", out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None, keep: bool = False):
+    """The gated feed-forward block y [M,N] = round_out(act(g) * v), g and v the
+    LoRA-bypass projections of x [M,K] (each as ``lora_linear``, both of the same
+    sizes, rank and dtypes) before their rounding; ``activation`` "silu", "gelu"
+    or "gelu_tanh".  With ``keep`` returns (y, gate, value, h): what
+    ``lora_gated_linear_backward`` reads, g and v [M,N] rounded to the compute
+    dtype and h_r of both [M, 2 r_pad] (None without a rank)."""
+    act = _activation(activation)
+    (M, N, K, r), dts = _gated_shapes(x, w_gate, w_value, down_gate, up_gate, down_value, up_value, bias_gate,
+                                      bias_value)
+    _shape(out, (M, N), "out")
+    dev = _need_device(x, w_gate, w_value, down_gate, up_gate, down_value, up_value, bias_gate, bias_value, out,
+                       workspace)
+    c_dt, o_dt, r_pad, need = _gated_plan(dev, M, N, K, r, *dts)
+    _out_dtype(out, o_dt)
+    if out is None:
+        out = torch.empty((M, N), dtype=_TORCH[o_dt], device=dev)
+    gate = torch.empty((M, N), dtype=_TORCH[c_dt], device=dev) if keep else None
+    value = torch.empty_like(gate) if keep else None
+    h = torch.empty((M, 2 * r_pad), dtype=_TORCH[c_dt], device=dev) if keep and r else None
+    ws = _workspace(need, dev, workspace)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    x_dt, w_dt, b_dt, d_dt, u_dt = dts
+    _check(lib().lyc_lora_gated_fwd(_ptr(x), x_dt, _ptr(w_gate), _ptr(w_value), w_dt, _ptr(bias_gate),
+                                    _ptr(bias_value), b_dt, _ptr(down_gate), _ptr(down_value), d_dt, _ptr(up_gate),
+                                    _ptr(up_value), u_dt, r, float(scale), act, _ptr(out), o_dt, _ptr(gate),
+                                    _ptr(value), _ptr(h), M, N, K, _ptr(ws), nbytes, _stream(dev)))
+    return (out, gate, value, h) if keep else out
+
+
+def lora_gated_linear_backward(x: torch.Tensor, w_gate: torch.Tensor, w_value: torch.Tensor, down_gate: torch.Tensor,
+                               up_gate: torch.Tensor, down_value: torch.Tensor, up_value: torch.Tensor, scale: float,
+                               dy: torch.Tensor, gate: torch.Tensor, value: torch.Tensor, activation: str = "silu",
+                               bias_dtype: Optional[torch.dtype] = None, want_dx: bool = True,
+                               want_ddown: bool = True, want_dup: bool = True,
+                               workspace: Optional[torch.Tensor] = None, w_gate_t: Optional[torch.Tensor] = None,
+                               w_value_t: Optional[torch.Tensor] = None, h: Optional[torch.Tensor] = None):
+    """Gradients (dx, d_down_gate, d_up_gate, d_down_value, d_up_value) of
+    ``lora_gated_linear`` for dy, each in its leaf's dtype (None where not
+    wanted), from the kept ``gate`` and ``value``.  ``w_gate_t``, ``w_value_t``:
+    optional caller-kept transposes [K,N] in the compute dtype (both or
+    neither).  ``h``: optional kept h (else recomputed for the ups' gradients)."""
+    act = _activation(activation)
+    (M, N, K, r), dts = _gated_shapes(x, w_gate, w_value, down_gate, up_gate, down_value, up_value, None, None)
+    x_dt, w_dt, _, d_dt, u_dt = dts
+    g_dt = dtype_code(dy)
+    b_dt = _CODE[bias_dtype] if bias_dtype is not None else 0
+    for t, shape, name in ((dy, (M, N), "dy"), (gate, (M, N), "gate"), (value, (M, N), "value"),
+                           (w_gate_t, (K, N), "w_gate_t"), (w_value_t, (K, N), "w_value_t")):
+        _shape(t, shape, name)
+    if (w_gate_t is None) != (w_value_t is None):
+        raise ValueError("w_gate_t and w_value_t: both or neither")
+    dev = _need_device(x, w_gate, w_value, down_gate, up_gate, down_value, up_value, dy, gate, value, workspace,
+                       w_gate_t, w_value_t, h)
+    given = w_gate_t is not None
+    want = (BWD_DX if want_dx else 0) | (BWD_DDOWN if want_ddown else 0) | (BWD_DUP if want_dup else 0) | \
+        (BWD_WT if given else 0) | (BWD_H if h is not None else 0)
+    c_dt, r_pad, need = _gated_bwd_plan(dev, M, N, K, r, x_dt, w_dt, b_dt, d_dt, u_dt, g_dt, want)
+    _shape(h, (M, 2 * r_pad), "h")
+    for t, name in ((gate, "gate"), (value, "value"), (w_gate_t, "w_gate_t"), (w_value_t, "w_value_t"), (h, "h")):
+        _typed(t, _TORCH[c_dt], name)
+    dx = torch.empty((M, K), dtype=x.dtype, device=dev) if want_dx else None
+    dd = torch.empty((2, r, K), dtype=down_gate.dtype, device=dev) if want_ddown else (None, None)
+    du = torch.empty((2, N, r), dtype=up_gate.dtype, device=dev) if want_dup else (None, None)
+    ws = _workspace(need, dev, workspace)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    # an empty output still has to be passed (non-NULL) to be "wanted", an empty
+    # h to count as given
+    p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr() if t.numel() else 256)
+    wg, wv = (None, None) if given else (_ptr(w_gate), _ptr(w_value))
+    gt, vt = (p(w_gate_t), p(w_value_t)) if given else (None, None)
+    _check(lib().lyc_lora_gated_bwd(_ptr(x), x_dt, wg, wv, gt, vt, w_dt, b_dt, _ptr(down_gate), _ptr(down_value), d_dt,
+                                    _ptr(up_gate), _ptr(up_value), u_dt, _ptr(gate), _ptr(value), p(h), r,
+                                    float(scale), act, _ptr(dy), g_dt, p(dx), p(dd[0]), p(dd[1]), p(du[0]), p(du[1]),
+                                    M, N, K, _ptr(ws), nbytes, _stream(dev)))
+    return dx, dd[0], du[0], dd[1], du[1]
+
+
+# ---- 8-bit integers -------------------------------------------------------------
+
+def _int8_codes(q: Optional[torch.Tensor], s: Optional[torch.Tensor], rows: int, K: int, name: str) -> None:
+    """Check int8 codes [rows, K] and their row scales: shapes and dtypes."""
+    _shape(q, (rows, K), name)
+    _typed(q, torch.int8, name)
+    _shape(s, (rows,), f"{name}'s scales")
+    _typed(s, torch.float32, f"{name}'s scales")
+
+
+def int8_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
+                       s: Optional[torch.Tensor] = None) -> Tuple[torch.Tensor, torch.Tensor]:
+    """int8 codes [M,K] of x [M,K] (tokens of activations, output channels of a
+    weight) with one scale per row [M]: a code c of row m stands for c * s[m]."""
+    M, K = _dims(x, 2, "x")
+    _int8_codes(q, s, M, K, "q")
+    dev = _need_device(x, s, codes=(q,), code_dtype=torch.int8)
+    q = torch.empty((M, K), dtype=torch.int8, device=dev) if q is None else q
+    s = torch.empty((M,), dtype=torch.float32, device=dev) if s is None else s
+    _check(lib().lyc_int8_quantize_rows(_ptr(x), dtype_code(x), _ptr(q), _ptr(s), M, K, _stream(dev)))
+    return q, s
+
+
+def int8_linear_workspace_size(M: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().lyc_int8_linear_workspace_size(M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def int8_gated_workspace_size(M: int, N: int, K: int) -> int:
+    n = ctypes.c_size_t(0)
+    _check(lib().lyc_int8_gated_workspace_size(M, N, K, ctypes.byref(n)))
+    return n.value
+
+
+def _int8_plan(fn, M, N, K) -> Tuple[int, int, int]:
+    v = [ctypes.c_int(0) for _ in range(3)]
+    _check(fn(M, N, K, *(ctypes.byref(i) for i in v)))
+    return v[0].value, v[1].value, v[2].value
+
+
+def int8_linear_plan(M: int, N: int, K: int) -> Tuple[int, int, int]:
+    """(tile_n, tile_m, ksplit) of the int8 product; up to 32 rows the features
+    and rows of one workgroup of the few-row kernel."""
+    return _int8_plan(lib().lyc_int8_linear_plan, M, N, K)
+
+
+def int8_gated_plan(M: int, N: int, K: int) -> Tuple[int, int, int]:
+    """The same of the gated block over int8 weights."""
+    return _int8_plan(lib().lyc_int8_gated_plan, M, N, K)
+
+
+@functools.lru_cache(maxsize=4096)
+def _int8_need(dev, gated, M, N, K) -> int:
+    return (int8_gated_workspace_size if gated else int8_linear_workspace_size)(M, N, K)
+
+
+def int8_linear(q: torch.Tensor, s: torch.Tensor, w_q: torch.Tensor, w_s: torch.Tensor,
+                bias: Optional[torch.Tensor] = None, out_dtype: torch.dtype = torch.bfloat16,
+                out: Optional[torch.Tensor] = None, workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """y [M,N] = round_out(x.W^T + b) of x and W quantized by
+    ``int8_quantize_rows``; y in ``out_dtype``, or in ``out``'s own dtype where
+    that is given."""
+    M, K = _dims(q, 2, "q")
+    N, _ = _dims(w_q, 2, "w_q")
+    _int8_codes(q, s, M, K, "q")
+    _int8_codes(w_q, w_s, N, K, "w_q")
+    _shape(bias, (N,), "bias")
+    _shape(out, (M, N), "out")
+    b_dt = dtype_code(bias) if bias is not None else 0
+    o_dt = dtype_code(out if out is not None else out_dtype)
+    dev = _need_device(s, w_s, bias, out, workspace, codes=(q, w_q), code_dtype=torch.int8)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    ws = _workspace(_int8_need(dev, False, M, N, K), dev, workspace)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().lyc_int8_linear_fwd(_ptr(q), _ptr(s), _ptr(w_q), _ptr(w_s), _ptr(bias), b_dt, _ptr(out), o_dt, M, N,
+                                     K, _ptr(ws), nbytes, _stream(dev)))
+    return out
+
+
+def int8_gated_linear(q: torch.Tensor, s: torch.Tensor, gate_q: torch.Tensor, gate_s: torch.Tensor,
+                      value_q: torch.Tensor, value_s: torch.Tensor, bias_gate: Optional[torch.Tensor] = None,
+                      bias_value: Optional[torch.Tensor] = None, activation: str = "silu",
+                      out_dtype: torch.dtype = torch.bfloat16, out: Optional[torch.Tensor] = None,
+                      workspace: Optional[torch.Tensor] = None) -> torch.Tensor:
+    """The gated feed-forward block y [M,N] = round_out(act(g) * v) over int8
+    weights, g and v each as ``int8_linear`` before its rounding."""
+    act = _activation(activation)
+    M, K = _dims(q, 2, "q")
+    N, _ = _dims(gate_q, 2, "gate_q")
+    _int8_codes(q, s, M, K, "q")
+    _int8_codes(gate_q, gate_s, N, K, "gate_q")
+    _int8_codes(value_q, value_s, N, K, "value_q")
+    _shape(bias_gate, (N,), "bias_gate")
+    _shape(bias_value, (N,), "bias_value")
+    _shape(out, (M, N), "out")
+    b_dt = _same_dtype(bias_gate, bias_value, "bias_gate and bias_value")
+    o_dt = dtype_code(out if out is not None else out_dtype)
+    dev = _need_device(s, gate_s, value_s, bias_gate, bias_value, out, workspace, codes=(q, gate_q, value_q),
+                       code_dtype=torch.int8)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=dev)
+    ws = _workspace(_int8_need(dev, True, M, N, K), dev, workspace)
+    nbytes = 0 if ws is None else ws.numel() * ws.element_size()
+    _check(lib().lyc_int8_gated_fwd(_ptr(q), _ptr(s), _ptr(gate_q), _ptr(gate_s), _ptr(value_q), _ptr(value_s),
+                                    _ptr(bias_gate), _ptr(bias_value), b_dt, act, _ptr(out), o_dt, M, N, K, _ptr(ws),
+                                    nbytes, _stream(dev)))
+    return out
 
 
 @functools.lru_cache(maxsize=4096)

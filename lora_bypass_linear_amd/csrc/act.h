@@ -1,0 +1,84 @@
+// act.h -- the gated block's activations and their derivatives in fp32, free of
+// branches: a tile's end evaluates them on up to 64 outputs a lane.
+#pragma once
+
+#include "lyc_device.h"
+#include "pair.h"
+
+namespace lyc {
+
+// exp(t), t below 88, to about two ulps: the product t log2(e) in two pieces, so
+// that the exponent's own rounding (2^-24 of up to 128) does not reach the result
+__device__ __forceinline__ float exp_f32(float t) {
+    constexpr float L = 1.44269502f, LL = 1.92596303e-8f;   // log2(e) = L + LL
+    const float hi = t * L;
+    const float lo = __builtin_fmaf(t, LL, __builtin_fmaf(t, L, -hi));
+    const float e = __builtin_amdgcn_exp2f(hi);
+    return __builtin_fmaf(e, lo * 0.693147182f, e);
+}
+
+// 1 / d to an ulp, d finite and normal
+__device__ __forceinline__ float rcp_f32(float d) {
+    const float r = __builtin_amdgcn_rcpf(d);
+    return __builtin_fmaf(__builtin_fmaf(-d, r, 1.f), r, r);
+}
+
+//   silu       g p(g)                                           slope p + g p (1 - p)
+//   gelu_tanh  g p(u), u = 2 sqrt(2/pi) (g + 0.044715 g^3)      slope p + g p (1 - p) u'
+// with p(u) = 1 / (1 + exp(-u)) (1/2 (1 + tanh z) is p(2 z)): u = g (b g^2 + a).
+// exp(-u) leaves the fp32 range below u = -87: there p is 0 (it is under 2e-38)
+// and 1 - p is 1.  u is taken of g within +-1e6, where p has long been 0 or 1, so
+// that no infinity meets another; a NaN passes through the factor g.
+template <bool GRAD>
+__device__ __forceinline__ float act_logistic(float a, float b, float g, float* slope) {
+    const float c = __builtin_amdgcn_fmed3f(g, -1e6f, 1e6f), c2 = c * c;
+    const float u = c * __builtin_fmaf(b, c2, a);
+    const float e = exp_f32(-u);
+    const float r = rcp_f32(1.f + e);
+    const float p = u < -87.f ? 0.f : r;
+    if constexpr (GRAD) {
+        const float q = u < -87.f ? 1.f : e * r;
+        *slope = __builtin_fmaf(g * p * q, __builtin_fmaf(3.f * b, c2, a), p);
+    }
+    return g * p;
+}
+
+//   gelu   g Phi(g)      slope Phi(g) + g exp(-g^2 / 2) / sqrt(2 pi)
+// Phi(-|g|) = 1/2 exp(-z^2) erfcx(z), z = |g| / sqrt(2), keeps its relative
+// accuracy where 1 + erf cancels.  (1 + 2 z) erfcx(z) is smooth in s = (z - 5/2) /
+// (z + 5/2): a polynomial of degree 9 fitted at Chebyshev nodes of z up to 13.5
+// (beyond, exp(-z^2) is 0) is within 3e-8 of it, 4e-7 with fp32's roundings.
+// exp(-z^2) takes z^2 = g^2 / 2 in two pieces.
+template <bool GRAD>
+__device__ __forceinline__ float act_gelu(float g, float* slope) {
+    const float c = __builtin_amdgcn_fmed3f(g, -1e6f, 1e6f), h = 0.5f * c;
+    const float hi = h * c, lo = __builtin_fmaf(h, c, -hi);
+    float e = exp_f32(-hi);
+    e = __builtin_fmaf(-e, lo, e);
+    const float z = __builtin_fabsf(c) * 0.707106769f;
+    const float d = __builtin_fmaf(2.f, z, 1.f), k = z + 2.5f;
+    const float r = rcp_f32(k * d);
+    const float s = (z - 2.5f) * d * r;
+    float y = 0.000472367508f;
+    y = __builtin_fmaf(y, s, 0.000361906888f);
+    y = __builtin_fmaf(y, s, -0.00428514602f);
+    y = __builtin_fmaf(y, s, 0.00100247574f);
+    y = __builtin_fmaf(y, s, 0.0327323899f);
+    y = __builtin_fmaf(y, s, -0.102982864f);
+    y = __builtin_fmaf(y, s, 0.157633707f);
+    y = __builtin_fmaf(y, s, -0.0990233123f);
+    y = __builtin_fmaf(y, s, -0.122356921f);
+    y = __builtin_fmaf(y, s, 1.26483822f);
+    const float tail = 0.5f * e * (y * k * r);
+    const float cdf = g < 0.f ? tail : 1.f - tail;
+    if constexpr (GRAD) *slope = __builtin_fmaf(g * 0.398942292f, e, cdf);
+    return g * cdf;
+}
+
+// the logistic form's coefficients
+__device__ __forceinline__ void act_coeffs(int act, float& a, float& b) {
+    a = act == ACT_GELU_TANH ? 1.59576917f : 1.f;
+    b = act == ACT_GELU_TANH ? 0.0713548139f : 0.f;
+}
+
+}  // namespace lyc

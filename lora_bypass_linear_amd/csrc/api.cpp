@@ -18,6 +18,7 @@
 #include "kernels.h"
 #include "merge.h"
 #include "ortho.h"
+#include "pair.h"
 #include "tune.h"
 
 namespace {
@@ -965,6 +966,551 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
     return LYC_OK;
 }
 
+// ---- gated feed-forward block ----------------------------------------------------
+// Two LoRA problems that share x, every size and every dtype.  h of both is one
+// [M][2 r_pad] array (gate's columns first), from one pass over x.
+struct GatedLayout {
+    size_t xc = 0, wc[2] = {0, 0}, dc = 0, dh = 0, dl = 0, uc[2] = {0, 0}, h = 0, dnorm = 0, flagged = 0, partial = 0,
+           total = 0;
+    int64_t flag_slots = 0;
+    bool cast_x = false, cast_w = false, hdot = false;
+    int ksplit = 1;
+};
+
+// y and the kept projections are addressed by tiles: their count fits a grid
+bool grid_fits(int64_t M, int64_t N) { return (double)M * (double)N <= 1099511627776.0; }   // 2^40
+
+GatedLayout gated_layout(const Problem& P, bool h_given) {
+    GatedLayout L;
+    size_t off = 0;
+    auto take = [&](size_t& at, size_t bytes) { at = off; off = align256(off + bytes); };
+    const size_t ce = esize(P.c_dt), M = (size_t)P.M, N = (size_t)P.N, K = (size_t)P.K, R = (size_t)P.r_pad;
+    const bool split = P.c_dt != LYC_F32;
+    L.cast_x = P.x_dt == LYC_F32 && split;
+    L.cast_w = P.w_dt == LYC_F32 && split;
+    if (L.cast_x) take(L.xc, M * K * 2);
+    if (L.cast_w)
+        for (size_t& w : L.wc) take(w, N * K * 2);
+    if (R > 0) {
+        L.hdot = P.K > 0 && P.M <= 128 && (double)P.M * 2.0 * (double)R * (double)P.K <= 33554432.0;
+        take(L.dc, 2 * R * K * ce);
+        if (split && !L.hdot) {
+            take(L.dh, 2 * R * K * ce);
+            take(L.dl, 2 * R * K * ce);
+        }
+        for (size_t& u : L.uc) take(u, N * R * ce);
+        take(L.dnorm, 2 * R * 2 * sizeof(double));
+        L.flag_slots = L.hdot ? lyc::hdot_workgroups(P.M, 2 * P.r_pad) : 1;
+        take(L.flagged, (size_t)L.flag_slots * sizeof(unsigned));
+        if (!h_given) take(L.h, M * 2 * R * ce);
+    }
+    L.ksplit = lyc::pair_plan(lyc::PAIR_PAIR, P.c_dt, P.M, P.N, P.K).ksplit;
+    if (L.ksplit > 1) take(L.partial, (size_t)L.ksplit * 2 * M * N * 4);
+    L.total = off;
+    return L;
+}
+
+// The factors of both projections prepared, and h of both into h [M][2 r_pad]
+// (dc, dh, dl, dnorm, flagged: workspace regions of 2 r_pad rows; uc: the
+// copies of up, nullptr: none wanted; cast_*: fp32 operands narrowed meanwhile)
+struct PairH {
+    const void* down[2];
+    const void* up[2];
+    void* uc[2];
+    char *dc, *dh, *dl;
+    double2* dnorm;
+    unsigned* flagged;
+    int64_t flag_slots;
+    bool hdot;
+    const void* x;   // compute dtype
+    void* h;
+};
+int pair_h(const Problem& P, const PairH& H, const float* const (&cast_src)[3], void* const (&cast_dst)[3],
+           const int64_t (&cast_n)[3], hipStream_t s) {
+    const size_t half = (size_t)P.r_pad * (size_t)P.K * esize(P.c_dt);
+    const bool split = P.c_dt != LYC_F32 && !H.hdot;
+    for (int i = 0; i < 2; ++i) {
+        lyc::PrepParams pp{};
+        if (P.r_pad > 0) {
+            pp.down = H.down[i];
+            pp.down_dt = P.d_dt;
+            pp.up = H.up[i];
+            pp.up_dt = P.u_dt;
+            pp.dc = H.dc + i * half;
+            pp.dh = split ? H.dh + i * half : nullptr;
+            pp.dl = split ? H.dl + i * half : nullptr;
+            pp.uc = H.uc[i];
+            pp.dnorm = H.dnorm + i * P.r_pad;
+            pp.flagged = i == 0 ? H.flagged : nullptr;
+            pp.flag_slots = H.flag_slots;
+            pp.vec = aligned(H.down[i], 16) ? 1 : 0;
+        }
+        pp.N = P.N;
+        pp.K = P.K;
+        pp.rank = P.rank;
+        pp.r_pad = P.r_pad;
+        pp.c_dt = P.c_dt;
+        int nc = 0;
+        for (int c = i == 0 ? 0 : 2; c < (i == 0 ? 2 : 3); ++c)
+            if (cast_n[c] > 0) {
+                pp.cast_src[nc] = cast_src[c];
+                pp.cast_dst[nc] = cast_dst[c];
+                pp.cast_n[nc++] = cast_n[c];
+            }
+        if (P.r_pad == 0 && nc == 0) continue;
+        if (timed(LYC_KERNEL_PREP, s, [&] { return lyc::launch_prep(pp, s); }) != hipSuccess) return LYC_ERR_HIP;
+    }
+    if (P.r_pad == 0 || P.M == 0) return LYC_OK;
+    if (H.hdot) {
+        lyc::HdotParams hq{};
+        hq.x = H.x;
+        hq.down = H.dc;   // (rows from the rank on are zeros)
+        hq.M = P.M;
+        hq.K = P.K;
+        hq.rank = 2 * P.r_pad;
+        hq.r_pad = 2 * P.r_pad;
+        hq.vec = aligned(H.x, 16) ? 1 : 0;   // (K is a multiple of 8)
+        hq.out = H.h;
+        hq.flagged = H.flagged;
+        return timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_hdot(P.c_dt, hq, s); }) == hipSuccess ? LYC_OK
+                                                                                                         : LYC_ERR_HIP;
+    }
+    // one pass over x for both while their columns fit it
+    const int passes = 2 * P.r_pad <= MAX_RANK ? 1 : 2;
+    for (int i = 0; i < passes; ++i) {
+        lyc::XrParams hp{};
+        hp.x = H.x;
+        hp.b = (split ? H.dh : H.dc) + i * half;
+        hp.b_lo = split ? (const void*)(H.dl + i * half) : nullptr;
+        hp.b_full = H.dc + i * half;
+        hp.bnorm = H.dnorm + i * P.r_pad;
+        hp.M = P.M;
+        hp.Nc = passes == 1 ? 2 * P.r_pad : P.r_pad;
+        hp.K = P.K;
+        hp.guard = P.c_dt != LYC_F32 ? 1 : 0;
+        hp.flagged = H.flagged;
+        hp.mode = lyc::XR_H;
+        hp.out = (char*)H.h + (size_t)(i * P.r_pad) * esize(P.c_dt);
+        hp.ld_out = 2 * P.r_pad;
+        hp.scale = 1.0;
+        if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_xr(P.c_dt, hp, s); }) != hipSuccess) return LYC_ERR_HIP;
+    }
+    return LYC_OK;
+}
+
+bool bad_scale(double scale) { return !(scale == scale) || scale > 3.4e38 || scale < -3.4e38; }
+
+// no output overlaps an input or another output
+template <int NI, int NO>
+bool any_overlap(const void* const (&in)[NI], const size_t (&nin)[NI], const void* const (&out)[NO],
+                 const size_t (&nout)[NO]) {
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (overlaps(out[i], nout[i], in[j], nin[j])) return true;
+        for (int j = i + 1; j < NO; ++j)
+            if (overlaps(out[i], nout[i], out[j], nout[j])) return true;
+    }
+    return false;
+}
+
+int check_gated(Problem& P, int act) {
+    const int st = check_problem(P);
+    if (st != LYC_OK) return st;
+    if (act < 0 || act >= lyc::ACT_COUNT) return LYC_ERR_INVALID_ARG;
+    return grid_fits(P.M, P.N) ? LYC_OK : LYC_ERR_UNSUPPORTED;
+}
+
+int gated_forward(const Problem& P, const void* x, const void* const (&w)[2], const void* const (&bias)[2],
+                  const void* const (&down)[2], const void* const (&up)[2], double scale, int act, void* y, int y_dt,
+                  void* const (&keep)[2], void* h, void* ws, size_t ws_bytes, void* stream) {
+    if (y_dt != P.o_dt) return LYC_ERR_DTYPE_MISMATCH;
+    if (bad_scale(scale)) return LYC_ERR_INVALID_ARG;
+    for (int i = 0; i < 2; ++i)
+        if ((bias[i] == nullptr) != (P.b_dt == 0)) return LYC_ERR_INVALID_ARG;
+    if ((keep[0] == nullptr) != (keep[1] == nullptr)) return LYC_ERR_INVALID_ARG;
+    if (P.M == 0 || P.N == 0) return LYC_OK;
+    if (y == nullptr) return LYC_ERR_INVALID_ARG;
+    const bool lora = P.rank > 0;
+    if (!lora) h = nullptr;
+    if (P.K > 0 && x == nullptr) return LYC_ERR_INVALID_ARG;
+    if (P.K > 0 && !aligned(x, 16)) return LYC_ERR_UNSUPPORTED;
+    for (int i = 0; i < 2; ++i) {
+        if (P.K > 0 && w[i] == nullptr) return LYC_ERR_INVALID_ARG;
+        if (lora && (up[i] == nullptr || (P.K > 0 && down[i] == nullptr))) return LYC_ERR_INVALID_ARG;
+        if (P.K > 0 && !aligned(w[i], 16)) return LYC_ERR_UNSUPPORTED;
+        if (lora && (!aligned(up[i], esize(P.u_dt)) || !aligned(down[i], esize(P.d_dt)))) return LYC_ERR_UNSUPPORTED;
+        if (bias[i] && !aligned(bias[i], esize(P.b_dt))) return LYC_ERR_UNSUPPORTED;
+        if (!aligned(keep[i], esize(P.c_dt))) return LYC_ERR_UNSUPPORTED;
+    }
+    if (!aligned(y, esize(y_dt)) || !aligned(h, 16)) return LYC_ERR_UNSUPPORTED;
+    const size_t ce = esize(P.c_dt), M = (size_t)P.M, N = (size_t)P.N, K = (size_t)P.K, r = (size_t)P.rank;
+    const size_t nw = N * K * esize(P.w_dt), nb = N * (P.b_dt ? esize(P.b_dt) : 0), nd = r * K * esize(P.d_dt),
+                 nu = N * r * esize(P.u_dt), nk = M * N * ce;
+    const GatedLayout L = gated_layout(P, h != nullptr);
+    const size_t need = L.total;
+    const void* ins[9] = {x, w[0], w[1], bias[0], bias[1], lora ? down[0] : nullptr, lora ? down[1] : nullptr,
+                          lora ? up[0] : nullptr, lora ? up[1] : nullptr};
+    const size_t nin[9] = {M * K * esize(P.x_dt), nw, nw, nb, nb, nd, nd, nu, nu};
+    const void* outs[5] = {y, keep[0], keep[1], h, ws};
+    const size_t nout[5] = {M * N * esize(y_dt), nk, nk, M * 2 * (size_t)P.r_pad * ce, need};
+    if (need > 0 && (ws == nullptr || ws_bytes < need || !aligned(ws, 256))) return LYC_ERR_WORKSPACE;
+    if (any_overlap(ins, nin, outs, nout)) return LYC_ERR_INVALID_ARG;
+    hipStream_t s = (hipStream_t)stream;
+    char* W = (char*)ws;
+    (void)hipGetLastError();
+
+    const bool cx = L.cast_x && K > 0, cw = L.cast_w && K > 0;
+    const float* cs[3] = {(const float*)x, (const float*)w[0], (const float*)w[1]};
+    void* cd[3] = {W + L.xc, W + L.wc[0], W + L.wc[1]};
+    const int64_t cn[3] = {cx ? P.M * P.K : 0, cw ? P.N * P.K : 0, cw ? P.N * P.K : 0};
+    lyc::PairParams g{};
+    PairH H{};
+    H.x = cx ? (const void*)(W + L.xc) : x;
+    for (int i = 0; i < 2; ++i) {
+        // up already in the compute dtype, unpadded and 16-byte aligned: read as stored
+        const bool stored = P.u_dt == P.c_dt && P.rank == P.r_pad && aligned(up[i], 16);
+        H.down[i] = down[i];
+        H.up[i] = up[i];
+        H.uc[i] = stored ? nullptr : W + L.uc[i];
+        g.a[i] = cw ? (const void*)(W + L.wc[i]) : w[i];
+        g.af[i] = stored ? up[i] : (const void*)(W + L.uc[i]);
+        g.bias[i] = bias[i];
+        g.keep[i] = keep[i];
+    }
+    H.dc = W + L.dc;
+    H.dh = W + L.dh;
+    H.dl = W + L.dl;
+    H.dnorm = (double2*)(W + L.dnorm);
+    H.flagged = (unsigned*)(W + L.flagged);
+    H.flag_slots = L.flag_slots;
+    H.hdot = L.hdot;
+    H.h = h != nullptr ? h : (void*)(W + L.h);
+    const int st = pair_h(P, H, cs, cd, cn, s);
+    if (st != LYC_OK) return st;
+    g.b[0] = H.x;
+    g.bf[0] = H.h;
+    g.bf[1] = (const char*)H.h + (size_t)P.r_pad * ce;
+    g.ldf = 2 * P.r_pad;
+    g.rf = P.r_pad;
+    g.M = P.M;
+    g.N = P.N;
+    g.K = P.K;
+    g.scale = (float)scale;
+    g.bias_dt = P.b_dt;
+    g.act = act;
+    g.y = y;
+    g.y_dt = y_dt;
+    g.ksplit = L.ksplit;
+    g.partial = L.ksplit > 1 ? (void*)(W + L.partial) : nullptr;
+    return timed(LYC_KERNEL_GEMM, s, [&] { return lyc::launch_pair(lyc::PAIR_PAIR, P.c_dt, g, s); }) == hipSuccess
+               ? LYC_OK
+               : LYC_ERR_HIP;
+}
+
+// the gated backward's workspace (Bwd's want bits, each for both projections)
+struct GatedBwdLayout {
+    size_t xc = 0, d[2] = {0, 0}, dc = 0, dh = 0, dl = 0, dnorm = 0, flag_h = 0, h = 0, hv = 0, ut = 0, uth = 0, utl = 0,
+           unorm = 0, flag_g = 0, gh[2] = {0, 0}, wt[2] = {0, 0}, dt[2] = {0, 0}, xt = 0, rt = 0, dyt = 0, partial = 0,
+           total = 0;
+    bool cast_x = false, need_h = false, need_gh = false, gh_dot = false, tr_tok = false;
+    bool h_dot = false;
+    int ks_dx = 1, ks_dd = 1, ks_du = 1;
+    int tile_dd = lyc::GEMM_TILE_AUTO, tile_du = lyc::GEMM_TILE_AUTO;
+};
+
+GatedBwdLayout gated_bwd_layout(const Bwd& B) {
+    const Problem& P = B.P;
+    GatedBwdLayout L;
+    size_t off = 0;
+    auto take = [&](size_t& at, size_t bytes) { at = off; off = align256(off + bytes); };
+    const size_t ce = esize(P.c_dt), M = (size_t)P.M, N = (size_t)P.N, K = (size_t)P.K, R = (size_t)P.r_pad,
+                 M8 = (size_t)B.M8, G1 = (size_t)1 << 30;
+    const bool split = P.c_dt != LYC_F32;
+    const bool dx = B.want & BWD_DX, dd = (B.want & BWD_DDOWN) && P.rank > 0, du = (B.want & BWD_DUP) && P.rank > 0;
+    L.need_h = du && !(B.want & BWD_H);
+    L.need_gh = P.rank > 0 && (dx || dd);
+    L.tr_tok = split && M * K * 2 < G1 && M * N * 2 < G1;
+    L.cast_x = P.x_dt == LYC_F32 && split && (L.need_h || (L.tr_tok && dd));
+    if (L.cast_x) take(L.xc, M * K * 2);
+    for (size_t& d : L.d) take(d, M * N * ce);
+    if (L.need_h) {
+        L.h_dot = P.K > 0 && P.M <= 128 && (double)P.M * 2.0 * (double)R * (double)P.K <= 33554432.0;
+        take(L.dc, 2 * R * K * ce);
+        if (split && !L.h_dot) {
+            take(L.dh, 2 * R * K * ce);
+            take(L.dl, 2 * R * K * ce);
+        }
+        take(L.dnorm, 2 * R * 2 * sizeof(double));
+        take(L.flag_h, (L.h_dot ? (size_t)lyc::hdot_workgroups(P.M, 2 * P.r_pad) : 1) * sizeof(unsigned));
+        take(L.h, M * 2 * R * ce);
+    }
+    if (du) take(L.hv, M * R * ce);
+    if (L.need_gh) {
+        L.gh_dot = P.N > 0 && hdot_few(P.M, P.r_pad, P.N);
+        take(L.ut, 2 * R * N * ce);
+        if (split && !L.gh_dot) {
+            take(L.uth, 2 * R * N * ce);
+            take(L.utl, 2 * R * N * ce);
+        }
+        take(L.unorm, 2 * R * 2 * sizeof(double));
+        take(L.flag_g, (L.gh_dot ? (size_t)lyc::hdot_workgroups(P.M, P.r_pad) : 1) * sizeof(unsigned));
+        for (size_t& g : L.gh) take(g, M * R * ce);
+    }
+    size_t part = 0;
+    const int64_t Kt = L.tr_tok ? P.M : B.M8;
+    if (dx) {
+        if (!(B.want & BWD_WT))
+            for (size_t& w : L.wt) take(w, K * N * ce);
+        if (P.rank > 0)
+            for (size_t& d : L.dt) take(d, K * R * ce);
+        L.ks_dx = lyc::pair_plan(lyc::PAIR_SEQ, P.c_dt, P.M, P.K, P.N).ksplit;
+        if (L.ks_dx > 1) part = std::max(part, (size_t)L.ks_dx * M * K * 4);
+    }
+    if (dd) {
+        if (!L.tr_tok) take(L.xt, K * M8 * ce);
+        L.ks_dd = L.tr_tok ? lyc::gemm_tok_plan(P.rank, P.K, Kt, &L.tile_dd) : lyc::gemm_ksplit(P.rank, P.K, Kt, P.c_dt);
+        if (L.ks_dd > 1) part = std::max(part, (size_t)L.ks_dd * (size_t)P.rank * K * 4);
+    }
+    if (du) {
+        if (!L.tr_tok) take(L.dyt, N * M8 * ce);
+        L.ks_du = L.tr_tok ? lyc::gemm_tok_plan(P.N, P.rank, Kt, &L.tile_du) : lyc::gemm_ksplit(P.N, P.rank, Kt, P.c_dt);
+        if (L.ks_du > 1) part = std::max(part, (size_t)L.ks_du * N * (size_t)P.rank * 4);
+    }
+    if (!L.tr_tok && (dd || du)) take(L.rt, R * M8 * ce);   // the rank side's transposed copy
+    if (part > 0) take(L.partial, part);
+    L.total = off;
+    return L;
+}
+
+int gated_backward(const Bwd& B, const void* x, const void* const (&w)[2], const void* const (&w_t)[2],
+                   const void* const (&down)[2], const void* const (&up)[2], const void* const (&kept)[2],
+                   const void* h_r, double scale, int act, const void* dy, void* dx, void* const (&d_down)[2],
+                   void* const (&d_up)[2], void* ws, size_t ws_bytes, void* stream) {
+    const Problem& P = B.P;
+    if (bad_scale(scale)) return LYC_ERR_INVALID_ARG;
+    const bool wdx = B.want & BWD_DX, wdd = B.want & BWD_DDOWN, wdu = B.want & BWD_DUP;
+    const bool wt_given = B.want & BWD_WT, h_given = B.want & BWD_H;
+    const int64_t M = P.M, N = P.N, K = P.K, r = P.rank;
+    const size_t ce = esize(P.c_dt);
+    const bool use_x = (wdd || (wdu && !h_given)) && r > 0 && M > 0 && K > 0;
+    const bool use_dy = M > 0 && N > 0 && (wdx || (r > 0 && (wdd || wdu)));
+    const bool use_w = wdx && M > 0 && N > 0 && K > 0;
+    const bool use_up = r > 0 && M > 0 && N > 0 && (wdx || wdd);
+    const bool use_down = r > 0 && M > 0 && K > 0 && (wdx || (wdu && !h_given));
+    const bool use_h = h_given && wdu && r > 0 && M > 0 && N > 0;
+    if ((use_x && x == nullptr) || (use_dy && dy == nullptr) || (use_h && h_r == nullptr)) return LYC_ERR_INVALID_ARG;
+    const size_t ndx = (size_t)(M * K) * esize(P.x_dt), ndd = (size_t)(r * K) * esize(P.d_dt),
+                 ndu = (size_t)(N * r) * esize(P.u_dt), nmn = (size_t)(M * N) * ce,
+                 nw = (size_t)(N * K) * (wt_given ? ce : esize(P.w_dt));
+    if (wdx && ndx > 0 && dx == nullptr) return LYC_ERR_INVALID_ARG;
+    const void* wq[2];
+    for (int i = 0; i < 2; ++i) {
+        wq[i] = use_w ? (wt_given ? w_t[i] : w[i]) : nullptr;
+        if ((use_w && wq[i] == nullptr) || (use_dy && kept[i] == nullptr) || (use_up && up[i] == nullptr) ||
+            (use_down && down[i] == nullptr) || (wdd && ndd > 0 && d_down[i] == nullptr) ||
+            (wdu && ndu > 0 && d_up[i] == nullptr))
+            return LYC_ERR_INVALID_ARG;
+        if (use_w && !aligned(wq[i], wt_given ? 16 : esize(P.w_dt))) return LYC_ERR_UNSUPPORTED;
+        if ((use_dy && !aligned(kept[i], 16)) || (use_up && !aligned(up[i], esize(P.u_dt))) ||
+            (use_down && !aligned(down[i], esize(P.d_dt))) || (wdd && !aligned(d_down[i], esize(P.d_dt))) ||
+            (wdu && !aligned(d_up[i], esize(P.u_dt))))
+            return LYC_ERR_UNSUPPORTED;
+    }
+    if ((use_x && !aligned(x, P.x_dt == P.c_dt ? 16 : esize(P.x_dt))) || (use_dy && !aligned(dy, 16)) ||
+        (use_h && !aligned(h_r, 16)) || (wdx && !aligned(dx, esize(P.x_dt))))
+        return LYC_ERR_UNSUPPORTED;
+    const GatedBwdLayout L = gated_bwd_layout(B);
+    if (L.total > 0 && (ws == nullptr || ws_bytes < L.total || !aligned(ws, 256))) return LYC_ERR_WORKSPACE;
+    {
+        const size_t nd = (size_t)(r * K) * esize(P.d_dt), nu = (size_t)(N * r) * esize(P.u_dt);
+        const void* ins[11] = {use_x ? x : nullptr, wq[0], wq[1], use_down ? down[0] : nullptr, use_down ? down[1] : nullptr,
+                               use_up ? up[0] : nullptr, use_up ? up[1] : nullptr, use_dy ? dy : nullptr,
+                               use_dy ? kept[0] : nullptr, use_dy ? kept[1] : nullptr, use_h ? h_r : nullptr};
+        const size_t nin[11] = {(size_t)(M * K) * esize(P.x_dt), nw, nw, nd, nd, nu, nu, (size_t)(M * N) * esize(B.dy_dt),
+                                nmn, nmn, (size_t)(M * 2 * P.r_pad) * ce};
+        const void* outs[6] = {wdx ? dx : nullptr, wdd ? d_down[0] : nullptr, wdd ? d_down[1] : nullptr,
+                               wdu ? d_up[0] : nullptr, wdu ? d_up[1] : nullptr, ws};
+        const size_t nout[6] = {ndx, ndd, ndd, ndu, ndu, L.total};
+        if (any_overlap(ins, nin, outs, nout)) return LYC_ERR_INVALID_ARG;
+    }
+    hipStream_t s = (hipStream_t)stream;
+    char* W = (char*)ws;
+    (void)hipGetLastError();
+    const bool split = P.c_dt != LYC_F32;
+    auto transpose = [&](const void* src, int src_dt, int64_t rows, int64_t cols, void* dst, int64_t rows_pad,
+                         int64_t cols_pad) {
+        lyc::TransposeParams tp{src, src_dt, rows, cols, dst, P.c_dt, rows_pad, cols_pad};
+        return timed(LYC_KERNEL_CAST, s, [&] { return lyc::launch_transpose(tp, s); }) == hipSuccess;
+    };
+
+    // h_r of both projections, recomputed as the forward computes it
+    const void* xa = x;
+    const void* hs = use_h ? h_r : nullptr;
+    if (L.need_h && M > 0) {
+        const bool cx = L.cast_x && K > 0;
+        if (cx) xa = W + L.xc;
+        PairH H{};
+        H.x = xa;
+        for (int i = 0; i < 2; ++i) {
+            H.down[i] = down[i];
+            H.up[i] = up[i];
+        }
+        H.dc = W + L.dc;
+        H.dh = W + L.dh;
+        H.dl = W + L.dl;
+        H.dnorm = (double2*)(W + L.dnorm);
+        H.flagged = (unsigned*)(W + L.flag_h);
+        H.flag_slots = L.h_dot ? lyc::hdot_workgroups(M, 2 * P.r_pad) : 1;
+        H.hdot = L.h_dot;
+        H.h = W + L.h;
+        const float* cs[3] = {(const float*)x, nullptr, nullptr};
+        void* cd[3] = {W + L.xc, nullptr, nullptr};
+        const int64_t cn[3] = {cx ? M * K : 0, 0, 0};
+        const int st = pair_h(P, H, cs, cd, cn, s);
+        if (st != LYC_OK) return st;
+        hs = W + L.h;
+    } else if (L.cast_x && M * K > 0) {
+        if (timed(LYC_KERNEL_CAST, s, [&] { return lyc::launch_cast((const float*)x, W + L.xc, M * K, P.c_dt, s); }) !=
+            hipSuccess)
+            return LYC_ERR_HIP;
+        xa = W + L.xc;
+    }
+
+    // dg, dv, and h's second half as rows of its own
+    if (use_dy) {
+        const lyc::GateGradParams gp{dy, B.dy_dt, kept[0], kept[1], W + L.d[0], W + L.d[1], M * N, act,
+                                     wdu && r > 0 ? hs : nullptr, W + L.hv, M, P.r_pad};
+        if (timed(LYC_KERNEL_PREP, s, [&] { return lyc::launch_gate_grad(P.c_dt, gp, s); }) != hipSuccess)
+            return LYC_ERR_HIP;
+    }
+
+    // gh = round_c(scale * d . up) of both
+    if (L.need_gh && M > 0 && N == 0) {
+        for (size_t g : L.gh)
+            if (!transpose(W, P.c_dt, 0, 0, W + g, P.r_pad, M)) return LYC_ERR_HIP;
+    } else if (L.need_gh && M > 0) {
+        const size_t half = (size_t)P.r_pad * (size_t)N * ce;
+        for (int i = 0; i < 2; ++i) {
+            char* ut = W + L.ut + i * half;
+            if (!transpose(up[i], P.u_dt, N, r, ut, N, P.r_pad)) return LYC_ERR_HIP;
+            if (L.gh_dot) {
+                lyc::HdotParams hq{};
+                hq.x = W + L.d[i];
+                hq.down = ut;
+                hq.M = M;
+                hq.K = N;
+                hq.rank = r;
+                hq.r_pad = P.r_pad;
+                hq.vec = 1;   // (N is a multiple of 8)
+                hq.out = W + L.gh[i];
+                hq.flagged = (unsigned*)(W + L.flag_g);
+                hq.scale = scale;
+                if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_hdot(P.c_dt, hq, s); }) != hipSuccess)
+                    return LYC_ERR_HIP;
+                continue;
+            }
+            char *uth = W + L.uth + i * half, *utl = W + L.utl + i * half;
+            double2* un = (double2*)(W + L.unorm) + i * P.r_pad;
+            if (split && timed(LYC_KERNEL_PREP, s, [&] {
+                    return lyc::launch_rownorm(ut, P.c_dt, P.r_pad, N, uth, utl, un, (unsigned*)(W + L.flag_g), s);
+                }) != hipSuccess)
+                return LYC_ERR_HIP;
+            lyc::XrParams gp{};
+            gp.x = W + L.d[i];
+            gp.b = split ? uth : ut;
+            gp.b_lo = split ? utl : nullptr;
+            gp.b_full = ut;
+            gp.bnorm = un;
+            gp.M = M;
+            gp.Nc = P.r_pad;
+            gp.K = N;
+            gp.guard = split ? 1 : 0;
+            gp.flagged = (unsigned*)(W + L.flag_g);
+            gp.mode = lyc::XR_H;
+            gp.out = W + L.gh[i];
+            gp.ld_out = P.r_pad;
+            gp.scale = scale;
+            if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_xr(P.c_dt, gp, s); }) != hipSuccess) return LYC_ERR_HIP;
+        }
+    }
+
+    // dx over both weights and both factors in one product
+    if (wdx && M > 0 && K > 0) {
+        lyc::PairParams g{};
+        for (int i = 0; i < 2; ++i) {
+            if (!wt_given && N > 0 && !transpose(w[i], P.w_dt, N, K, W + L.wt[i], N, K)) return LYC_ERR_HIP;
+            if (r > 0 && !transpose(down[i], P.d_dt, r, K, W + L.dt[i], P.r_pad, K)) return LYC_ERR_HIP;
+            g.a[i] = wt_given ? w_t[i] : (const void*)(W + L.wt[i]);
+            g.b[i] = W + L.d[i];
+            g.af[i] = W + L.dt[i];
+            g.bf[i] = W + L.gh[i];
+        }
+        g.ldf = P.r_pad;
+        g.rf = r > 0 ? P.r_pad : 0;
+        g.M = M;
+        g.N = K;
+        g.K = N;
+        g.scale = 1.0f;
+        g.y = dx;
+        g.y_dt = P.x_dt;
+        g.ksplit = L.ks_dx;
+        g.partial = L.ks_dx > 1 ? (void*)(W + L.partial) : nullptr;
+        if (timed(LYC_KERNEL_GEMM, s, [&] { return lyc::launch_pair(lyc::PAIR_SEQ, P.c_dt, g, s); }) != hipSuccess)
+            return LYC_ERR_HIP;
+    }
+
+    // the factors' gradients, over the tokens
+    auto tokens = [&](const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t cols, void* out,
+                      int out_dt, int tile, int ks, float post) {
+        lyc::GemmParams g{};
+        g.a = a;
+        g.b = b;
+        if (L.tr_tok) {
+            g.ta = g.tb = 1;
+            g.lda_t = lda;
+            g.ldb_t = ldb;
+        }
+        g.K = L.tr_tok ? M : B.M8;
+        g.M = rows;
+        g.N = cols;
+        g.scale = 1.0f;
+        g.post = post;
+        g.y = out;
+        g.y_dt = out_dt;
+        g.tile = tile;
+        g.ksplit = ks;
+        g.partial = ks > 1 ? (float*)(W + L.partial) : nullptr;
+        g.vec_store = (cols % 4 == 0) && aligned(out, out_dt == LYC_F32 ? 16 : 8);
+        return timed(LYC_KERNEL_GEMM, s, [&] { return lyc::launch_gemm(P.c_dt, g, s); }) == hipSuccess;
+    };
+    if (wdd && r > 0 && K > 0) {
+        if (!L.tr_tok && M > 0 && !transpose(x, P.x_dt, M, K, W + L.xt, B.M8, K)) return LYC_ERR_HIP;
+        for (int i = 0; i < 2; ++i) {
+            if (!L.tr_tok && M > 0 && !transpose(W + L.gh[i], P.c_dt, M, P.r_pad, W + L.rt, B.M8, P.r_pad))
+                return LYC_ERR_HIP;
+            if (!tokens(L.tr_tok ? (M > 0 ? xa : W) : W + L.xt, K, L.tr_tok ? W + L.gh[i] : W + L.rt, P.r_pad, r, K,
+                        d_down[i], P.d_dt, L.tile_dd, L.ks_dd, 1.0f))
+                return LYC_ERR_HIP;
+        }
+    }
+    if (wdu && r > 0 && N > 0) {
+        for (int i = 0; i < 2; ++i) {
+            // gate's half of h in place, value's from its own rows
+            const void* h = i == 0 ? hs : (const void*)(W + L.hv);
+            const int64_t ld = i == 0 ? 2 * P.r_pad : P.r_pad;
+            if (M == 0) h = W;
+            if (!L.tr_tok && M > 0) {
+                if (!transpose(W + L.d[i], P.c_dt, M, N, W + L.dyt, B.M8, N)) return LYC_ERR_HIP;
+                if (!transpose(h, P.c_dt, M, ld, W + L.rt, B.M8, P.r_pad)) return LYC_ERR_HIP;
+            }
+            if (!tokens(L.tr_tok ? h : W + L.rt, ld, L.tr_tok ? W + L.d[i] : W + L.dyt, N, N, r, d_up[i], P.u_dt,
+                        L.tile_du, L.ks_du, (float)scale))
+                return LYC_ERR_HIP;
+        }
+    }
+    return LYC_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -1446,6 +1992,226 @@ int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const flo
     if (st != LYC_OK) return st;
     return backward(B, x, nullptr, down, up, scale, dy, dx, d_down, d_up, workspace, workspace_bytes, stream, q_wt,
                     h_r, s_w);
+}
+
+// ---- 8-bit integers -------------------------------------------------------------------
+
+// 16-byte rows of codes, exact 32-bit sums of products of up to 128 * 128
+static int check_int8(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0) return LYC_ERR_INVALID_ARG;
+    if (M > MAX_DIM || N > MAX_DIM || K > 131056 || K % 16 != 0) return LYC_ERR_UNSUPPORTED;
+    return grid_fits(M, N) ? LYC_OK : LYC_ERR_UNSUPPORTED;
+}
+
+int lyc_int8_quantize_rows(const void* x, int x_dt, void* q, float* s, int64_t M, int64_t K, void* stream) {
+    if (!valid_dt(x_dt)) return LYC_ERR_INVALID_ARG;
+    const int st = check_int8(M, 0, K);
+    if (st != LYC_OK) return st;
+    if (M == 0) return LYC_OK;
+    if (s == nullptr || (K > 0 && (x == nullptr || q == nullptr))) return LYC_ERR_INVALID_ARG;
+    if (!aligned(x, 16) || !aligned(q, 16) || !aligned(s, 4)) return LYC_ERR_UNSUPPORTED;
+    const size_t nx = (size_t)(M * K) * esize(x_dt), nq = (size_t)(M * K), ns = (size_t)M * 4;
+    if (overlaps(q, nq, x, nx) || overlaps(s, ns, x, nx) || overlaps(s, ns, q, nq)) return LYC_ERR_INVALID_ARG;
+    (void)hipGetLastError();
+    hipStream_t h = (hipStream_t)stream;
+    return timed(LYC_KERNEL_PREP, h, [&] {
+               return lyc::launch_quant_int8(lyc::QuantInt8Params{x, x_dt, q, s, M, K}, h);
+           }) == hipSuccess
+               ? LYC_OK
+               : LYC_ERR_HIP;
+}
+
+static size_t int8_workspace(int mode, int64_t M, int64_t N, int64_t K) {
+    const int ks = lyc::pair_plan(mode, lyc::DT_I8, M, N, K).ksplit;
+    return ks > 1 ? align256((size_t)ks * (mode == lyc::PAIR_PAIR ? 2 : 1) * (size_t)(M * N) * 4) : 0;
+}
+
+static int int8_plan(int mode, int64_t M, int64_t N, int64_t K, int* tile_n, int* tile_m, int* ksplit) {
+    const int st = check_int8(M, N, K);
+    if (st != LYC_OK) return st;
+    const lyc::PairPlan p = lyc::pair_plan(mode, lyc::DT_I8, M, N, K);
+    if (tile_n) *tile_n = p.tile_n;
+    if (tile_m) *tile_m = p.tile_m;
+    if (ksplit) *ksplit = p.ksplit;
+    return LYC_OK;
+}
+
+// the product (w[1] unused) and the gated block over quantized operands
+static int int8_forward(int mode, const void* q_x, const float* s_x, const void* const (&q_w)[2],
+                        const float* const (&s_w)[2], const void* const (&bias)[2], int bias_dt, int act, void* y,
+                        int y_dt, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                        void* stream) {
+    const int st = check_int8(M, N, K);
+    if (st != LYC_OK) return st;
+    const int H = mode == lyc::PAIR_PAIR ? 2 : 1;
+    if (!valid_dt(y_dt) || (bias_dt != 0 && !valid_dt(bias_dt))) return LYC_ERR_INVALID_ARG;
+    if (act < 0 || act >= lyc::ACT_COUNT) return LYC_ERR_INVALID_ARG;
+    for (int i = 0; i < H; ++i)
+        if ((bias[i] == nullptr) != (bias_dt == 0)) return LYC_ERR_INVALID_ARG;
+    if (M == 0 || N == 0) return LYC_OK;
+    if (y == nullptr || s_x == nullptr || (K > 0 && q_x == nullptr)) return LYC_ERR_INVALID_ARG;
+    if (!aligned(q_x, 16) || !aligned(s_x, 4) || !aligned(y, esize(y_dt))) return LYC_ERR_UNSUPPORTED;
+    for (int i = 0; i < H; ++i) {
+        if (s_w[i] == nullptr || (K > 0 && q_w[i] == nullptr)) return LYC_ERR_INVALID_ARG;
+        if (!aligned(q_w[i], 16) || !aligned(s_w[i], 4) || (bias[i] && !aligned(bias[i], esize(bias_dt))))
+            return LYC_ERR_UNSUPPORTED;
+    }
+    const size_t need = int8_workspace(mode, M, N, K), nb = (size_t)N * (bias_dt ? esize(bias_dt) : 0);
+    if (need > 0 && (workspace == nullptr || workspace_bytes < need || !aligned(workspace, 256)))
+        return LYC_ERR_WORKSPACE;
+    const void* w1 = H == 2 ? q_w[1] : nullptr;
+    const void* ins[8] = {q_x, s_x, q_w[0], w1, s_w[0], H == 2 ? s_w[1] : nullptr, bias[0], H == 2 ? bias[1] : nullptr};
+    const size_t nin[8] = {(size_t)(M * K), (size_t)M * 4, (size_t)(N * K), (size_t)(N * K), (size_t)N * 4, (size_t)N * 4,
+                           nb, nb};
+    const void* outs[2] = {y, workspace};
+    const size_t nout[2] = {(size_t)(M * N) * esize(y_dt), need};
+    if (any_overlap(ins, nin, outs, nout)) return LYC_ERR_INVALID_ARG;
+    (void)hipGetLastError();
+    hipStream_t s = (hipStream_t)stream;
+    lyc::PairParams g{};
+    g.b[0] = q_x;
+    g.sx = s_x;
+    for (int i = 0; i < H; ++i) {
+        g.a[i] = q_w[i];
+        g.sw[i] = s_w[i];
+        g.bias[i] = bias[i];
+    }
+    g.M = M;
+    g.N = N;
+    g.K = K;
+    g.scale = 1.0f;
+    g.bias_dt = bias_dt;
+    g.act = act;
+    g.y = y;
+    g.y_dt = y_dt;
+    g.ksplit = lyc::pair_plan(mode, lyc::DT_I8, M, N, K).ksplit;
+    g.partial = workspace;
+    return timed(LYC_KERNEL_GEMM, s, [&] { return lyc::launch_pair(mode, lyc::DT_I8, g, s); }) == hipSuccess ? LYC_OK
+                                                                                                             : LYC_ERR_HIP;
+}
+
+int lyc_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+    const int st = check_int8(M, N, K);
+    if (st != LYC_OK) return st;
+    if (bytes) *bytes = int8_workspace(lyc::PAIR_ONE, M, N, K);
+    return LYC_OK;
+}
+
+int lyc_int8_linear_plan(int64_t M, int64_t N, int64_t K, int* tile_n, int* tile_m, int* ksplit) {
+    return int8_plan(lyc::PAIR_ONE, M, N, K, tile_n, tile_m, ksplit);
+}
+
+int lyc_int8_linear_fwd(const void* q_x, const float* s_x, const void* q_w, const float* s_w, const void* bias,
+                        int bias_dt, void* y, int y_dt, int64_t M, int64_t N, int64_t K, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+    const void* q[2] = {q_w, nullptr};
+    const float* sw[2] = {s_w, nullptr};
+    const void* b[2] = {bias, nullptr};
+    return int8_forward(lyc::PAIR_ONE, q_x, s_x, q, sw, b, bias_dt, 0, y, y_dt, M, N, K, workspace, workspace_bytes,
+                        stream);
+}
+
+int lyc_int8_gated_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+    const int st = check_int8(M, N, K);
+    if (st != LYC_OK) return st;
+    if (bytes) *bytes = int8_workspace(lyc::PAIR_PAIR, M, N, K);
+    return LYC_OK;
+}
+
+int lyc_int8_gated_plan(int64_t M, int64_t N, int64_t K, int* tile_n, int* tile_m, int* ksplit) {
+    return int8_plan(lyc::PAIR_PAIR, M, N, K, tile_n, tile_m, ksplit);
+}
+
+int lyc_int8_gated_fwd(const void* q_x, const float* s_x, const void* q_gate, const float* s_gate, const void* q_value,
+                       const float* s_value, const void* bias_gate, const void* bias_value, int bias_dt, int act,
+                       void* y, int y_dt, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
+                       void* stream) {
+    const void* q[2] = {q_gate, q_value};
+    const float* sw[2] = {s_gate, s_value};
+    const void* b[2] = {bias_gate, bias_value};
+    return int8_forward(lyc::PAIR_PAIR, q_x, s_x, q, sw, b, bias_dt, act, y, y_dt, M, N, K, workspace, workspace_bytes,
+                        stream);
+}
+
+// ---- gated feed-forward block -----------------------------------------------------------
+
+int lyc_lora_gated_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int w_dt, int bias_dt,
+                                  int down_dt, int up_dt, size_t* bytes) {
+    Problem P{true, M, N, K, rank, x_dt, w_dt, bias_dt, down_dt, up_dt, 0, 0, 0};
+    const int st = check_gated(P, 0);
+    if (st != LYC_OK) return st;
+    if (bytes) *bytes = gated_layout(P, false).total;
+    return LYC_OK;
+}
+
+int lyc_lora_gated_plan(int64_t M, int64_t N, int64_t K, int compute_dt, int backward, int* tile_n, int* tile_m,
+                        int* ksplit) {
+    if (M < 0 || N < 0 || K < 0 || !valid_dt(compute_dt) || (backward != 0 && backward != 1)) return LYC_ERR_INVALID_ARG;
+    if (M > MAX_DIM || N > MAX_DIM || K > MAX_K || K % 8 != 0 || !grid_fits(M, N)) return LYC_ERR_UNSUPPORTED;
+    const lyc::PairPlan p = backward ? lyc::pair_plan(lyc::PAIR_SEQ, compute_dt, M, K, N)
+                                     : lyc::pair_plan(lyc::PAIR_PAIR, compute_dt, M, N, K);
+    if (tile_n) *tile_n = p.tile_n;
+    if (tile_m) *tile_m = p.tile_m;
+    if (ksplit) *ksplit = p.ksplit;
+    return LYC_OK;
+}
+
+int lyc_lora_gated_fwd(const void* x, int x_dt, const void* w_gate, const void* w_value, int w_dt,
+                       const void* bias_gate, const void* bias_value, int bias_dt, const void* down_gate,
+                       const void* down_value, int down_dt, const void* up_gate, const void* up_value, int up_dt,
+                       int64_t rank, double scale, int act, void* y, int y_dt, void* gate, void* value, void* h,
+                       int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+    Problem P{true, M, N, K, rank, x_dt, w_dt, bias_dt, down_dt, up_dt, 0, 0, 0};
+    const int st = check_gated(P, act);
+    if (st != LYC_OK) return st;
+    if (!valid_dt(y_dt)) return LYC_ERR_INVALID_ARG;
+    const void* w[2] = {w_gate, w_value};
+    const void* b[2] = {bias_gate, bias_value};
+    const void* d[2] = {down_gate, down_value};
+    const void* u[2] = {up_gate, up_value};
+    void* keep[2] = {gate, value};
+    return gated_forward(P, x, w, b, d, u, scale, act, y, y_dt, keep, h, workspace, workspace_bytes, stream);
+}
+
+static Bwd gated_bwd(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int w_dt, int bias_dt, int down_dt,
+                     int up_dt, int dy_dt, int want) {
+    return Bwd{Problem{true, M, N, K, rank, x_dt, w_dt, bias_dt, down_dt, up_dt, 0, 0, 0}, dy_dt, want, 0};
+}
+
+int lyc_lora_gated_bwd_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank, int x_dt, int w_dt, int bias_dt,
+                                      int down_dt, int up_dt, int dy_dt, int want, size_t* bytes) {
+    Bwd B = gated_bwd(M, N, K, rank, x_dt, w_dt, bias_dt, down_dt, up_dt, dy_dt, want);
+    const int st = check_bwd(B);
+    if (st != LYC_OK) return st;
+    if (bytes) *bytes = gated_bwd_layout(B).total;
+    return LYC_OK;
+}
+
+int lyc_lora_gated_bwd(const void* x, int x_dt, const void* w_gate, const void* w_value, const void* w_gate_t,
+                       const void* w_value_t, int w_dt, int bias_dt, const void* down_gate, const void* down_value,
+                       int down_dt, const void* up_gate, const void* up_value, int up_dt, const void* gate,
+                       const void* value, const void* h, int64_t rank, double scale, int act, const void* dy,
+                       int dy_dt, void* dx, void* d_down_gate, void* d_down_value, void* d_up_gate, void* d_up_value,
+                       int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes, void* stream) {
+    const bool wt = w_gate_t != nullptr || w_value_t != nullptr;
+    if ((w_gate_t == nullptr) != (w_value_t == nullptr) || (wt && (w_gate != nullptr || w_value != nullptr)))
+        return LYC_ERR_INVALID_ARG;
+    if ((d_down_gate == nullptr) != (d_down_value == nullptr) || (d_up_gate == nullptr) != (d_up_value == nullptr))
+        return LYC_ERR_INVALID_ARG;
+    if (act < 0 || act >= lyc::ACT_COUNT) return LYC_ERR_INVALID_ARG;
+    const int want = (dx ? BWD_DX : 0) | (d_down_gate ? BWD_DDOWN : 0) | (d_up_gate ? BWD_DUP : 0) | (wt ? BWD_WT : 0) |
+                     (h ? BWD_H : 0);
+    Bwd B = gated_bwd(M, N, K, rank, x_dt, w_dt, bias_dt, down_dt, up_dt, dy_dt, want);
+    const int st = check_bwd(B);
+    if (st != LYC_OK) return st;
+    const void* w[2] = {w_gate, w_value};
+    const void* w_t[2] = {w_gate_t, w_value_t};
+    const void* d[2] = {down_gate, down_value};
+    const void* u[2] = {up_gate, up_value};
+    const void* kept[2] = {gate, value};
+    void* dd[2] = {d_down_gate, d_down_value};
+    void* du[2] = {d_up_gate, d_up_value};
+    return gated_backward(B, x, w, w_t, d, u, kept, h, scale, act, dy, dx, dd, du, workspace, workspace_bytes, stream);
 }
 
 // ---- orthogonalized update ------------------------------------------------------------
