@@ -43,6 +43,16 @@ __device__ __forceinline__ float act_logistic(float a, float b, float g, float* 
     return g * p;
 }
 
+// The same for 16-bit results: exp2 and the reciprocal as the hardware gives them
+// (an ulp each), the exponent rounded once.  Off by 2^-23 |u| of the result
+// where that is near 0 (negative u) and by a few 2^-24 elsewhere, a 2^-12th of
+// bf16's and a 2^-9th of fp16's rounding at |u| = 8.  No input needs a clamp: exp2 overflows to
+// infinity, whose reciprocal is 0.
+__device__ __forceinline__ float act_logistic16(float a, float b, float g) {
+    const float u = g * __builtin_fmaf(b, g * g, a);
+    return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(u * -1.44269502f));
+}
+
 //   gelu   g Phi(g)      slope Phi(g) + g exp(-g^2 / 2) / sqrt(2 pi)
 // Phi(-|g|) = 1/2 exp(-z^2) erfcx(z), z = |g| / sqrt(2), keeps its relative
 // accuracy where 1 + erf cancels.  (1 + 2 z) erfcx(z) is smooth in s = (z - 5/2) /

@@ -43,15 +43,16 @@ __device__ __forceinline__ f32x4 to_f32(f32x4 v) { return v; }
 __device__ __forceinline__ f32x4 to_f32(i32x4 v) { return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]}; }
 
 // body(act): one copy of the caller's loop for each form of the activation, the
-// choice (uniform) outside it
-template <class F>
+// choice (uniform) outside it; WIDE: for fp32 results
+template <bool WIDE, class F>
 __device__ __forceinline__ void with_activation(int act, F body) {
     if (act == ACT_GELU) {
         body([](float g) { return act_gelu<false>(g, nullptr); });
     } else {
         float a, b;
         act_coeffs(act, a, b);
-        body([=](float g) { return act_logistic<false>(a, b, g, nullptr); });
+        if constexpr (WIDE) body([=](float g) { return act_logistic<false>(a, b, g, nullptr); });
+        else body([=](float g) { return act_logistic16(a, b, g); });
     }
 }
 
@@ -198,6 +199,7 @@ __device__ __forceinline__ void store_tile(char* smem, F val, void* y, int y_dt,
 #pragma unroll
             for (int i = 0; i < SH::FI; ++i) {
                 const int cb = (wn * SH::WF + i * 16 + 4 * (lane >> 4)) * ES;
+                __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
                 for (int j = 0; j < TL::FM; ++j) {
                     const int r = wm * TL::WM + j * 16 + (lane & 15) - ps * TMP;
@@ -409,7 +411,10 @@ __global__ __launch_bounds__(TL::NT, 1) void pair_kernel(PairParams p, int tiles
         return;
     }
 
-    // the projections in fp32
+    // The tile's end works from the accumulators: every output is formed, rounded
+    // and written to LDS block by block, so that no second copy of the tile is
+    // ever in registers (with one, 77 of them spilled: 8192 x 8192 x 4096 took
+    // 910 us, PLACEHOLDER_US without).
     __syncthreads();
     if (tid < TL::TN) aux[tid] = bv;
     if (I8) {
@@ -417,47 +422,57 @@ __global__ __launch_bounds__(TL::NT, 1) void pair_kernel(PairParams p, int tiles
         if (tid < TL::TM) aux[2 * TL::TN + tid] = sx;
     }
     __syncthreads();
-    f32x4 pr[FN][FM];
+    f32x4 bias4[FN], sw4[I8 ? FN : 1];
+    float sxj[I8 ? FM : 1];
 #pragma unroll
     for (int i = 0; i < FN; ++i) {
-        const int half = SH::TWO ? i / SH::FI : 0;
-        const int at = half * SH::TF + wn * SH::WF + (i - half * SH::FI) * 16 + 4 * g4;
-        const f32x4 b4 = *(const f32x4*)(aux + at);
-        f32x4 s4 = f32x4{1.f, 1.f, 1.f, 1.f};
-        if (I8) s4 = *(const f32x4*)(aux + TL::TN + at);
-#pragma unroll
-        for (int j = 0; j < FM; ++j) {
-            f32x4 v = to_f32(acc[i][j]);
-            if constexpr (I8) {
-                const float s = aux[2 * TL::TN + wm * TL::WM + j * 16 + r];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(v[e] * s4[e], s, b4[e]);
-            } else {
-                v += b4;
-            }
-            pr[i][j] = v;
-        }
+        const int at = (i / SH::FI) * SH::TF + wn * SH::WF + (i % SH::FI) * 16 + 4 * g4;
+        bias4[i] = *(const f32x4*)(aux + at);
+        if constexpr (I8) sw4[i] = *(const f32x4*)(aux + TL::TN + at);
     }
-    auto store = [&](auto val, void* y, int y_dt) {
-        if (y_dt == DT_F32) store_tile<TL, MODE, 4>(smem, val, y, y_dt, p.M, p.N, n0, m0, wave, lane, wn, wm);
-        else store_tile<TL, MODE, 2>(smem, val, y, y_dt, p.M, p.N, n0, m0, wave, lane, wn, wm);
+    if constexpr (I8) {
+#pragma unroll
+        for (int j = 0; j < FM; ++j) sxj[j] = aux[2 * TL::TN + wm * TL::WM + j * 16 + r];
+    }
+    // projection `half` of the wave's block (i, j) in fp32
+    auto proj = [&](int half, int i, int j) {
+        const int ii = half * SH::FI + i;
+        f32x4 v = to_f32(acc[ii][j]);
+        if constexpr (I8) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) v[e] = __builtin_fmaf(v[e] * sw4[ii][e], sxj[j], bias4[ii][e]);
+        } else {
+            v += bias4[ii];
+        }
+        return v;
     };
-    if constexpr (SH::TWO) {
-        if (!I8 && p.keep[0] != nullptr) {
-            store([&](int i, int j) { return pr[i][j]; }, p.keep[0], CT::dt);
-            store([&](int i, int j) { return pr[i + SH::FI][j]; }, p.keep[1], CT::dt);
+    auto store = [&](auto es, auto val, void* y, int y_dt) {
+        store_tile<TL, MODE, decltype(es)::value>(smem, val, y, y_dt, p.M, p.N, n0, m0, wave, lane, wn, wm);
+    };
+    auto finish = [&](auto es) {
+        if constexpr (SH::TWO) {
+            with_activation<decltype(es)::value == 4>(p.act, [&](auto act) {
+                store(es, [&](int i, int j) {
+                    const f32x4 g = proj(0, i, j), v = proj(1, i, j);
+                    f32x4 o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) o[e] = act(g[e]) * v[e];
+                    return o;
+                }, p.y, p.y_dt);
+            });
+        } else {
+            store(es, [&](int i, int j) { return proj(0, i, j); }, p.y, p.y_dt);
         }
-        auto gate = [&](auto act) {
-#pragma unroll
-            for (int i = 0; i < SH::FI; ++i)
-#pragma unroll
-                for (int j = 0; j < FM; ++j)
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) pr[i][j][e] = act(pr[i][j][e]) * pr[i + SH::FI][j][e];
-        };
-        with_activation(p.act, gate);
+    };
+    if constexpr (SH::TWO && !I8) {
+        if (p.keep[0] != nullptr) {
+            using KES = std::integral_constant<int, CT::es>;
+            store(KES{}, [&](int i, int j) { return proj(0, i, j); }, p.keep[0], CT::dt);
+            store(KES{}, [&](int i, int j) { return proj(1, i, j); }, p.keep[1], CT::dt);
+        }
     }
-    store([&](int i, int j) { return pr[i][j]; }, p.y, p.y_dt);
+    if (CT::dt == DT_F32 || p.y_dt == DT_F32) finish(std::integral_constant<int, 4>{});
+    else if constexpr (CT::dt != DT_F32) finish(std::integral_constant<int, 2>{});
 }
 
 // The K splits' sums joined in split order, then everything the tile's own end
@@ -506,7 +521,7 @@ __global__ __launch_bounds__(256) void pair_join_kernel(PairParams p) {
             put(p.keep[0], CT::dt, pr[0]);
             put(p.keep[1], CT::dt, pr[1]);
         }
-        with_activation(p.act, [&](auto act) {
+        with_activation<true>(p.act, [&](auto act) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) pr[0][e] = act(pr[0][e]) * pr[1][e];
         });
@@ -635,7 +650,7 @@ __global__ __launch_bounds__(64 * NW) void pair_skinny_kernel(PairParams p) {
             put(p.keep[0], CT::dt, pr[0]);
             put(p.keep[1], CT::dt, pr[1]);
         }
-        with_activation(p.act, [&](auto act) {
+        with_activation<true>(p.act, [&](auto act) {
 #pragma unroll
             for (int e = 0; e < 4; ++e) pr[0][e] = act(pr[0][e]) * pr[1][e];
         });
