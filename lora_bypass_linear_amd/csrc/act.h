@@ -53,6 +53,26 @@ __device__ __forceinline__ float act_logistic16(float a, float b, float g) {
     return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(u * -1.44269502f));
 }
 
+// Value and slope for 16-bit gradients, with the error of each in units of 2^-24
+// relative (fp32 ulps at most), n_slope relative to mass = |t| + p, slope = t + p:
+// the exponent's rounding 1.2 |u| (the tanh form's u 3 |u| more), which counts
+// q-fold in p and p-fold in q = 1 - p; exp2 2, the sum 1, the reciprocal 2, so p 5
+// and q 6; g p one more, t 16 with its products and u'.  e is kept finite, so
+// that q = e r is 1, not a product of infinity and 0, where p is 0.
+__device__ __forceinline__ float act_logistic16_grad(float a, float b, float g, float* slope, float* mass,
+                                                     float* n_act, float* n_slope) {
+    const float g2 = g * g, u = g * __builtin_fmaf(b, g2, a);
+    const float e = __builtin_fminf(__builtin_amdgcn_exp2f(u * -1.44269502f), 3e38f);
+    const float p = __builtin_amdgcn_rcpf(1.f + e), v = g * p;
+    const float t = v * (e * p) * __builtin_fmaf(3.f * b, g2, a);
+    const float nu = (b != 0.f ? 4.25f : 1.25f) * __builtin_fabsf(u);
+    *slope = t + p;
+    *mass = __builtin_fabsf(t) + p;
+    *n_act = nu + 6.f;
+    *n_slope = nu + 16.f;
+    return v;
+}
+
 //   gelu   g Phi(g)      slope Phi(g) + g exp(-g^2 / 2) / sqrt(2 pi)
 // Phi(-|g|) = 1/2 exp(-z^2) erfcx(z), z = |g| / sqrt(2), keeps its relative
 // accuracy where 1 + erf cancels.  (1 + 2 z) erfcx(z) is smooth in s = (z - 5/2) /
@@ -60,7 +80,7 @@ __device__ __forceinline__ float act_logistic16(float a, float b, float g) {
 // (beyond, exp(-z^2) is 0) is within 3e-8 of it, 4e-7 with fp32's roundings.
 // exp(-z^2) takes z^2 = g^2 / 2 in two pieces.
 template <bool GRAD>
-__device__ __forceinline__ float act_gelu(float g, float* slope) {
+__device__ __forceinline__ float act_gelu(float g, float* slope, float* mass) {
     const float c = __builtin_amdgcn_fmed3f(g, -1e6f, 1e6f), h = 0.5f * c;
     const float hi = h * c, lo = __builtin_fmaf(h, c, -hi);
     float e = exp_f32(-hi);
@@ -81,8 +101,29 @@ __device__ __forceinline__ float act_gelu(float g, float* slope) {
     y = __builtin_fmaf(y, s, 1.26483822f);
     const float tail = 0.5f * e * (y * k * r);
     const float cdf = g < 0.f ? tail : 1.f - tail;
-    if constexpr (GRAD) *slope = __builtin_fmaf(g * 0.398942292f, e, cdf);
+    if constexpr (GRAD) {
+        const float t = g * 0.398942292f * e;
+        *slope = t + cdf;
+        *mass = __builtin_fabsf(t) + cdf;   // (both off by less than 16 units of 2^-24)
+    }
     return g * cdf;
+}
+
+// The same in 64 bits, for the few values that an fp32 one cannot round.  (A NaN
+// stays one; at an infinity the value's product with p = 0 is one.)
+__device__ __forceinline__ double act_f64(int act, double g, double* slope) {
+    if (act == ACT_GELU) {
+        const double cdf = 0.5 * erfc(g * -0.70710678118654752);
+        *slope = cdf + g * exp(-0.5 * g * g) * 0.39894228040143268;
+        return g * cdf;
+    }
+    const double a = act == ACT_GELU_TANH ? 1.5957691216057308 : 1.0;
+    const double b = act == ACT_GELU_TANH ? 0.071354816272600243 : 0.0;
+    const double u = g * (a + b * g * g);
+    const double e = exp(-__builtin_fabs(u)), r = 1.0 / (1.0 + e), er = e * r;
+    const double p = u < 0.0 ? er : r, q = u < 0.0 ? r : er;
+    *slope = p + g * p * q * (a + 3.0 * b * g * g);
+    return g * p;
 }
 
 // the logistic form's coefficients

@@ -1209,7 +1209,7 @@ int gated_forward(const Problem& P, const void* x, const void* const (&w)[2], co
 
 // the gated backward's workspace (Bwd's want bits, each for both projections)
 struct GatedBwdLayout {
-    size_t xc = 0, d[2] = {0, 0}, dc = 0, dh = 0, dl = 0, dnorm = 0, flag_h = 0, h = 0, hv = 0, ut = 0, uth = 0, utl = 0,
+    size_t xc = 0, d[2] = {0, 0}, open = 0, dc = 0, dh = 0, dl = 0, dnorm = 0, flag_h = 0, h = 0, hv = 0, ut = 0, uth = 0, utl = 0,
            unorm = 0, flag_g = 0, gh[2] = {0, 0}, wt[2] = {0, 0}, dt[2] = {0, 0}, xt = 0, rt = 0, dyt = 0, partial = 0,
            total = 0;
     bool cast_x = false, need_h = false, need_gh = false, gh_dot = false, tr_tok = false;
@@ -1233,6 +1233,7 @@ GatedBwdLayout gated_bwd_layout(const Bwd& B) {
     L.cast_x = P.x_dt == LYC_F32 && split && (L.need_h || (L.tr_tok && dd));
     if (L.cast_x) take(L.xc, M * K * 2);
     for (size_t& d : L.d) take(d, M * N * ce);
+    if (split) take(L.open, M * N / 8);
     if (L.need_h) {
         L.h_dot = P.K > 0 && P.M <= 128 && (double)P.M * 2.0 * (double)R * (double)P.K <= 33554432.0;
         take(L.dc, 2 * R * K * ce);
@@ -1379,7 +1380,7 @@ int gated_backward(const Bwd& B, const void* x, const void* const (&w)[2], const
     // dg, dv, and h's second half as rows of its own
     if (use_dy) {
         const lyc::GateGradParams gp{dy, B.dy_dt, kept[0], kept[1], W + L.d[0], W + L.d[1], M * N, act,
-                                     wdu && r > 0 ? hs : nullptr, W + L.hv, M, P.r_pad};
+                                     wdu && r > 0 ? hs : nullptr, W + L.hv, M, P.r_pad, (uint8_t*)(W + L.open)};
         if (timed(LYC_KERNEL_PREP, s, [&] { return lyc::launch_gate_grad(P.c_dt, gp, s); }) != hipSuccess)
             return LYC_ERR_HIP;
     }

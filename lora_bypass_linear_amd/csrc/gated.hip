@@ -17,6 +17,20 @@ hipError_t launch_gated(int c_dt, const PairParams& p, hipStream_t s) {
     return run_pair_ct<CF32, PAIR_PAIR>(p, s);
 }
 
+// Tile and K split by modelled time, us: rounds of workgroups over the CUs (two
+// 64 x 64 ones share one), each a fixed part and its K steps of 128 bytes a row,
+// whose time grows with the share of the device that is busy; plus a split's
+// sums out and in again.  Measured steps, on an empty and on a full device
+// (rows x A rows of a tile; the byte widths of the operands do not matter):
+//             8 and 16 bits          fp32
+//   256 x 256    0.8, 1.42  fixed 12.5     --
+//   128 x 128    0.37, 0.53       5      2.0, 2.2
+//   64 x 64      0.22, 0.37       5      0.5, 1.06
+// Whole calls, the pick and what it is held against: int8 product 777 x 4104 x
+// 4112 128 x 128 25.9, 64 x 64 39.5, 256 x 256 in two splits 45.5; 512 x 512 x 8192
+// 64 x 64 in 4 splits 13.7, in one 21.5; bf16 block 777 x 4096 x 4096 128 x 128
+// 67.2, 256 x 256 80.3; 256 x 4096 x 4096 64 x 64 28.7, 128 x 128 33.0; fp32 block 200 x
+// 512 x 4096 64 x 64 in 4 splits 32.2, in one 83.7.
 PairPlan pair_plan(int mode, int c_dt, int64_t M, int64_t N, int64_t K) {
     const int es = c_dt == DT_F32 ? 4 : c_dt == DT_I8 ? 1 : 2;
     const int two = mode == PAIR_PAIR ? 2 : 1;
@@ -24,25 +38,27 @@ PairPlan pair_plan(int mode, int c_dt, int64_t M, int64_t N, int64_t K) {
     if (pair_skinny(M, K, es)) return PairPlan{16, M <= 16 ? 16 : 32, 1};
     struct C {
         int t, per_cu;
-        double fixed, step;
+        double fixed, empty, full;
     };
-    const C cands[3] = {{256, 1, 8.0, 1.15}, {128, 1, 6.0, 0.42}, {64, 2, 5.0, 0.45}};
+    const C cands[2][3] = {{{256, 1, 12.5, 0.8, 1.42}, {128, 1, 5.0, 0.37, 0.53}, {64, 2, 5.0, 0.22, 0.37}},
+                           {{0, 1, 0, 0, 0}, {128, 1, 5.0, 2.0, 2.2}, {64, 2, 5.0, 0.5, 1.06}}};
     const double cus = (double)device_rates().cus;
     const int64_t steps1 = (K * es + 127) / 128;
-    const double seg = mode == PAIR_SEQ ? 2.0 : 1.0;
+    const double segs = mode == PAIR_SEQ ? 2.0 : 1.0;
     PairPlan best{64 / two, 64, 1};
     double best_t = 1e300;
-    for (const C& c : cands) {
-        if (c_dt == DT_F32 && c.t == 256) continue;
-        const double f32 = c_dt == DT_F32 ? 8.0 : 1.0;
+    for (const C& c : cands[c_dt == DT_F32 ? 1 : 0]) {
+        if (c.t == 0) continue;
         const int tf = c.t / two;
         const double tiles = (double)((N + tf - 1) / tf) * (double)((M + c.t - 1) / c.t);
         for (int ks = 1; ks <= 8; ks *= 2) {
-            const double part = (double)M * N * 4.0 * two * ks;
+            const double part = (double)M * (double)N * 4.0 * two * ks;
             if (ks > 1 && (ks > steps1 / 2 || part > 64.0 * 1024 * 1024)) continue;
-            const double st = (double)((steps1 + ks - 1) / ks) * seg;
-            double t = std::ceil(tiles * ks / (cus * c.per_cu)) * (c.fixed + st * c.step * f32);
-            if (ks > 1) t += 3.0 + part * (1.0 + 1.0 / ks) / 2.5e6;
+            const double steps = (double)((steps1 + ks - 1) / ks) * segs;
+            const double slots = cus * c.per_cu, rounds = std::ceil(tiles * ks / slots);
+            const double busy = tiles * ks / (rounds * slots);
+            double t = rounds * (c.fixed + steps * (c.empty + (c.full - c.empty) * busy));
+            if (ks > 1) t += 2.5 + 2.0 * part / 3.0e6;
             if (t < best_t) {
                 best_t = t;
                 best = PairPlan{tf, c.t, ks};

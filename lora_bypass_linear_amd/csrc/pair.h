@@ -75,6 +75,7 @@ struct GateGradParams {
     void* hv;                   // [M][r_pad]
     int64_t M;
     int r_pad;
+    uint8_t* open;              // 16-bit compute: [n / 8] marks of the elements left to 64 bits
 };
 hipError_t launch_gate_grad(int c_dt, const GateGradParams& p, hipStream_t s);
 

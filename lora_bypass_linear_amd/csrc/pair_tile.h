@@ -47,7 +47,7 @@ __device__ __forceinline__ f32x4 to_f32(i32x4 v) { return f32x4{(float)v[0], (fl
 template <bool WIDE, class F>
 __device__ __forceinline__ void with_activation(int act, F body) {
     if (act == ACT_GELU) {
-        body([](float g) { return act_gelu<false>(g, nullptr); });
+        body([](float g) { return act_gelu<false>(g, nullptr, nullptr); });
     } else {
         float a, b;
         act_coeffs(act, a, b);
@@ -321,7 +321,7 @@ __global__ __launch_bounds__(TL::NT, 1) void pair_kernel(PairParams p, int tiles
         // in registers on entry; substep 1's are read under its MFMAs.  The
         // first MFMAs of substep 1 are issued before the wait for step kt+1 and
         // the barrier; after it the loads of step kt+NS into the stage just
-        // consumed and the next fragments go between the other groups.
+        // consumed and the next fragments go between the others.
         auto k_step = [&](int kt) {
             constexpr int ND = FN + FM;
             constexpr int G = FN % 4 == 0 ? 4 : 2, FNG = FN / G;
@@ -353,21 +353,22 @@ __global__ __launch_bounds__(TL::NT, 1) void pair_kernel(PairParams p, int tiles
             lds_barrier();
             const bool ok = fd.ok(lane);
             const char* nx = smem + ((kt + 1) % NS) * TL::STAGE;
+            // Q slots of a load, a share of the fragment reads (done three quarters
+            // through) and of the MFMAs.  A load occupies the CU's address path for
+            // 16 cycles: issued two or three at a time they stalled the waves
+            // (bf16 8192 x 8192 x 4096: 858 us, 830 one at a time)
+            constexpr int NM = FN * FM - FNG * FM, RS = Q - Q / 4, RP = (ND + RS - 1) / RS;
 #pragma unroll
-            for (int g = 1; g < G; ++g) {
+            for (int z = 0; z < Q; ++z) {
+                fd.load(z, st, ok, wave);
 #pragma unroll
-                for (int q = 0; q < Q; ++q)
-                    if (1 + (q * (G - 1)) / Q == g) fd.load(q, st, ok, wave);
+                for (int w = z * RP; w < (z + 1) * RP; ++w) {
+                    if (w < FM) f0b[w] = frag_b(nx, 0, w);
+                    else if (w < ND) f0a[w - FM] = frag_a(nx, 0, w - FM);
+                }
 #pragma unroll
-                for (int i = 0; i < FN; ++i)
-                    if (i * (G - 1) / FN + 1 == g) f0a[i] = frag_a(nx, 0, i);
-#pragma unroll
-                for (int j = 0; j < FM; ++j)
-                    if (j * (G - 1) / FM + 1 == g) f0b[j] = frag_b(nx, 0, j);
-#pragma unroll
-                for (int i = g * FNG; i < (g + 1) * FNG; ++i)
-#pragma unroll
-                    for (int j = 0; j < FM; ++j) acc[i][j] = CT::step(f1a[i], f1b[j], acc[i][j]);
+                for (int m = FNG * FM + z * NM / Q; m < FNG * FM + (z + 1) * NM / Q; ++m)
+                    acc[m / FM][m % FM] = CT::step(f1a[m / FM], f1b[m % FM], acc[m / FM][m % FM]);
                 __builtin_amdgcn_sched_barrier(0);
             }
             advance();
@@ -414,7 +415,7 @@ __global__ __launch_bounds__(TL::NT, 1) void pair_kernel(PairParams p, int tiles
     // The tile's end works from the accumulators: every output is formed, rounded
     // and written to LDS block by block, so that no second copy of the tile is
     // ever in registers (with one, 77 of them spilled: 8192 x 8192 x 4096 took
-    // 910 us, PLACEHOLDER_US without).
+    // 910 us, 845 us without).
     __syncthreads();
     if (tid < TL::TN) aux[tid] = bv;
     if (I8) {
@@ -661,7 +662,7 @@ __global__ __launch_bounds__(64 * NW) void pair_skinny_kernel(PairParams p) {
 // ---- launchers shared by the instances' files -------------------------------------
 
 using PairL = Tile<256, 256, 128, 64, 2, 128>;   // 8 waves, 128 KiB of stages
-using PairM = Tile<128, 128, 64, 64, 4, 128>;    // 4 waves, 128 KiB
+using PairM = Tile<128, 128, 64, 32, 4, 128>;    // 8 waves, 128 KiB
 using PairS = Tile<64, 64, 32, 32, 4, 128>;      // 4 waves, 64 KiB
 
 template <class CT, class TL, int MODE>
