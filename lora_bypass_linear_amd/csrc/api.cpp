@@ -1000,7 +1000,7 @@ GatedLayout gated_layout(const Problem& P, bool h_given) {
         }
         for (size_t& u : L.uc) take(u, N * R * ce);
         take(L.dnorm, 2 * R * 2 * sizeof(double));
-        L.flag_slots = L.hdot ? lyc::hdot_workgroups(P.M, 2 * P.r_pad) : 1;
+        L.flag_slots = L.hdot ? 2 * lyc::hdot_workgroups(P.M, P.r_pad) : 1;
         take(L.flagged, (size_t)L.flag_slots * sizeof(unsigned));
         if (!h_given) take(L.h, M * 2 * R * ce);
     }
@@ -1029,51 +1029,61 @@ int pair_h(const Problem& P, const PairH& H, const float* const (&cast_src)[3], 
            const int64_t (&cast_n)[3], hipStream_t s) {
     const size_t half = (size_t)P.r_pad * (size_t)P.K * esize(P.c_dt);
     const bool split = P.c_dt != LYC_F32 && !H.hdot;
+    // few token rows: the dots read down as stored where it is in the compute dtype
+    const bool down_stored = H.hdot && P.d_dt == P.c_dt;
+    lyc::PrepParams pp[2];
+    bool any = false;
     for (int i = 0; i < 2; ++i) {
-        lyc::PrepParams pp{};
-        if (P.r_pad > 0) {
-            pp.down = H.down[i];
-            pp.down_dt = P.d_dt;
-            pp.up = H.up[i];
-            pp.up_dt = P.u_dt;
-            pp.dc = H.dc + i * half;
-            pp.dh = split ? H.dh + i * half : nullptr;
-            pp.dl = split ? H.dl + i * half : nullptr;
-            pp.uc = H.uc[i];
-            pp.dnorm = H.dnorm + i * P.r_pad;
-            pp.flagged = i == 0 ? H.flagged : nullptr;
-            pp.flag_slots = H.flag_slots;
-            pp.vec = aligned(H.down[i], 16) ? 1 : 0;
+        if (P.r_pad > 0 && !(down_stored && H.uc[i] == nullptr)) {
+            pp[i].down = H.down[i];
+            pp[i].down_dt = P.d_dt;
+            pp[i].up = H.up[i];
+            pp[i].up_dt = P.u_dt;
+            pp[i].dc = H.dc + i * half;
+            pp[i].dh = split ? H.dh + i * half : nullptr;
+            pp[i].dl = split ? H.dl + i * half : nullptr;
+            pp[i].uc = H.uc[i];
+            pp[i].dnorm = H.dnorm + i * P.r_pad;
+            pp[i].flagged = i == 0 && !H.hdot ? H.flagged : nullptr;
+            pp[i].flag_slots = H.flag_slots;
+            pp[i].vec = aligned(H.down[i], 16) ? 1 : 0;
+            pp[i].r_pad = P.r_pad;
+            any = true;
         }
-        pp.N = P.N;
-        pp.K = P.K;
-        pp.rank = P.rank;
-        pp.r_pad = P.r_pad;
-        pp.c_dt = P.c_dt;
+        pp[i].N = P.N;
+        pp[i].K = P.K;
+        pp[i].rank = P.rank;
+        pp[i].c_dt = P.c_dt;
         int nc = 0;
         for (int c = i == 0 ? 0 : 2; c < (i == 0 ? 2 : 3); ++c)
             if (cast_n[c] > 0) {
-                pp.cast_src[nc] = cast_src[c];
-                pp.cast_dst[nc] = cast_dst[c];
-                pp.cast_n[nc++] = cast_n[c];
+                pp[i].cast_src[nc] = cast_src[c];
+                pp[i].cast_dst[nc] = cast_dst[c];
+                pp[i].cast_n[nc++] = cast_n[c];
+                any = true;
             }
-        if (P.r_pad == 0 && nc == 0) continue;
-        if (timed(LYC_KERNEL_PREP, s, [&] { return lyc::launch_prep(pp, s); }) != hipSuccess) return LYC_ERR_HIP;
     }
+    if (any && timed(LYC_KERNEL_PREP, s, [&] { return lyc::launch_prep2(pp[0], pp[1], s); }) != hipSuccess)
+        return LYC_ERR_HIP;
     if (P.r_pad == 0 || P.M == 0) return LYC_OK;
     if (H.hdot) {
-        lyc::HdotParams hq{};
-        hq.x = H.x;
-        hq.down = H.dc;   // (rows from the rank on are zeros)
-        hq.M = P.M;
-        hq.K = P.K;
-        hq.rank = 2 * P.r_pad;
-        hq.r_pad = 2 * P.r_pad;
-        hq.vec = aligned(H.x, 16) ? 1 : 0;   // (K is a multiple of 8)
-        hq.out = H.h;
-        hq.flagged = H.flagged;
-        return timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_hdot(P.c_dt, hq, s); }) == hipSuccess ? LYC_OK
-                                                                                                         : LYC_ERR_HIP;
+        lyc::HdotParams hq[2];
+        for (int i = 0; i < 2; ++i) {
+            hq[i] = lyc::HdotParams{};
+            hq[i].x = H.x;
+            hq[i].down = down_stored ? H.down[i] : (const void*)(H.dc + i * half);
+            hq[i].M = P.M;
+            hq[i].K = P.K;
+            hq[i].rank = P.rank;
+            hq[i].r_pad = P.r_pad;
+            hq[i].vec = aligned(H.x, 16) && aligned(hq[i].down, 16) ? 1 : 0;   // (K is a multiple of 8)
+            hq[i].out = (char*)H.h + (size_t)(i * P.r_pad) * esize(P.c_dt);
+            hq[i].flagged = H.flagged + i * (H.flag_slots / 2);
+        }
+        return timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_hdot2(P.c_dt, hq[0], hq[1], 2 * P.r_pad, s); }) ==
+                       hipSuccess
+                   ? LYC_OK
+                   : LYC_ERR_HIP;
     }
     // one pass over x for both while their columns fit it
     const int passes = 2 * P.r_pad <= MAX_RANK ? 1 : 2;
@@ -1242,7 +1252,7 @@ GatedBwdLayout gated_bwd_layout(const Bwd& B) {
             take(L.dl, 2 * R * K * ce);
         }
         take(L.dnorm, 2 * R * 2 * sizeof(double));
-        take(L.flag_h, (L.h_dot ? (size_t)lyc::hdot_workgroups(P.M, 2 * P.r_pad) : 1) * sizeof(unsigned));
+        take(L.flag_h, (L.h_dot ? 2 * (size_t)lyc::hdot_workgroups(P.M, P.r_pad) : 1) * sizeof(unsigned));
         take(L.h, M * 2 * R * ce);
     }
     if (du) take(L.hv, M * R * ce);
@@ -1254,7 +1264,7 @@ GatedBwdLayout gated_bwd_layout(const Bwd& B) {
             take(L.utl, 2 * R * N * ce);
         }
         take(L.unorm, 2 * R * 2 * sizeof(double));
-        take(L.flag_g, (L.gh_dot ? (size_t)lyc::hdot_workgroups(P.M, P.r_pad) : 1) * sizeof(unsigned));
+        take(L.flag_g, (L.gh_dot ? 2 * (size_t)lyc::hdot_workgroups(P.M, P.r_pad) : 1) * sizeof(unsigned));
         for (size_t& g : L.gh) take(g, M * R * ce);
     }
     size_t part = 0;
@@ -1361,7 +1371,7 @@ int gated_backward(const Bwd& B, const void* x, const void* const (&w)[2], const
         H.dl = W + L.dl;
         H.dnorm = (double2*)(W + L.dnorm);
         H.flagged = (unsigned*)(W + L.flag_h);
-        H.flag_slots = L.h_dot ? lyc::hdot_workgroups(M, 2 * P.r_pad) : 1;
+        H.flag_slots = L.h_dot ? 2 * lyc::hdot_workgroups(M, P.r_pad) : 1;
         H.hdot = L.h_dot;
         H.h = W + L.h;
         const float* cs[3] = {(const float*)x, nullptr, nullptr};
@@ -1386,52 +1396,66 @@ int gated_backward(const Bwd& B, const void* x, const void* const (&w)[2], const
     }
 
     // gh = round_c(scale * d . up) of both
+    bool downs = false;   // down^T made with up^T
     if (L.need_gh && M > 0 && N == 0) {
         for (size_t g : L.gh)
             if (!transpose(W, P.c_dt, 0, 0, W + g, P.r_pad, M)) return LYC_ERR_HIP;
     } else if (L.need_gh && M > 0) {
         const size_t half = (size_t)P.r_pad * (size_t)N * ce;
-        for (int i = 0; i < 2; ++i) {
-            char* ut = W + L.ut + i * half;
-            if (!transpose(up[i], P.u_dt, N, r, ut, N, P.r_pad)) return LYC_ERR_HIP;
-            if (L.gh_dot) {
-                lyc::HdotParams hq{};
-                hq.x = W + L.d[i];
-                hq.down = ut;
-                hq.M = M;
-                hq.K = N;
-                hq.rank = r;
-                hq.r_pad = P.r_pad;
-                hq.vec = 1;   // (N is a multiple of 8)
-                hq.out = W + L.gh[i];
-                hq.flagged = (unsigned*)(W + L.flag_g);
-                hq.scale = scale;
-                if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_hdot(P.c_dt, hq, s); }) != hipSuccess)
-                    return LYC_ERR_HIP;
-                continue;
+        // up^T of both, and down^T for dx, in one launch where the stored sizes agree
+        lyc::TransposeParams tp[4];
+        int nt = 0;
+        for (int i = 0; i < 2; ++i)
+            tp[nt++] = lyc::TransposeParams{up[i], P.u_dt, N, r, W + L.ut + i * half, P.c_dt, N, P.r_pad};
+        downs = wdx && K > 0 && esize(P.u_dt) == esize(P.d_dt);
+        if (downs)
+            for (int i = 0; i < 2; ++i)
+                tp[nt++] = lyc::TransposeParams{down[i], P.d_dt, r, K, W + L.dt[i], P.c_dt, P.r_pad, K};
+        if (timed(LYC_KERNEL_CAST, s, [&] { return lyc::launch_transposes(tp, nt, s); }) != hipSuccess) return LYC_ERR_HIP;
+        if (L.gh_dot) {
+            lyc::HdotParams hq[2];
+            for (int i = 0; i < 2; ++i) {
+                hq[i] = lyc::HdotParams{};
+                hq[i].x = W + L.d[i];
+                hq[i].down = W + L.ut + i * half;
+                hq[i].M = M;
+                hq[i].K = N;
+                hq[i].rank = r;
+                hq[i].r_pad = P.r_pad;
+                hq[i].vec = 1;   // (N is a multiple of 8)
+                hq[i].out = W + L.gh[i];
+                hq[i].flagged = (unsigned*)(W + L.flag_g) + i * lyc::hdot_workgroups(M, P.r_pad);
+                hq[i].scale = scale;
             }
-            char *uth = W + L.uth + i * half, *utl = W + L.utl + i * half;
-            double2* un = (double2*)(W + L.unorm) + i * P.r_pad;
+            if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_hdot2(P.c_dt, hq[0], hq[1], P.r_pad, s); }) != hipSuccess)
+                return LYC_ERR_HIP;
+        } else {
+            // (both halves of ut, its split and norms are one array of 2 r_pad rows)
             if (split && timed(LYC_KERNEL_PREP, s, [&] {
-                    return lyc::launch_rownorm(ut, P.c_dt, P.r_pad, N, uth, utl, un, (unsigned*)(W + L.flag_g), s);
+                    return lyc::launch_rownorm(W + L.ut, P.c_dt, 2 * P.r_pad, N, W + L.uth, W + L.utl,
+                                               (double2*)(W + L.unorm), (unsigned*)(W + L.flag_g), s);
                 }) != hipSuccess)
                 return LYC_ERR_HIP;
-            lyc::XrParams gp{};
-            gp.x = W + L.d[i];
-            gp.b = split ? uth : ut;
-            gp.b_lo = split ? utl : nullptr;
-            gp.b_full = ut;
-            gp.bnorm = un;
-            gp.M = M;
-            gp.Nc = P.r_pad;
-            gp.K = N;
-            gp.guard = split ? 1 : 0;
-            gp.flagged = (unsigned*)(W + L.flag_g);
-            gp.mode = lyc::XR_H;
-            gp.out = W + L.gh[i];
-            gp.ld_out = P.r_pad;
-            gp.scale = scale;
-            if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_xr(P.c_dt, gp, s); }) != hipSuccess) return LYC_ERR_HIP;
+            lyc::XrParams gp[2];
+            for (int i = 0; i < 2; ++i) {
+                gp[i] = lyc::XrParams{};
+                gp[i].x = W + L.d[i];
+                gp[i].b = W + (split ? L.uth : L.ut) + i * half;
+                gp[i].b_lo = split ? W + L.utl + i * half : nullptr;
+                gp[i].b_full = W + L.ut + i * half;
+                gp[i].bnorm = (double2*)(W + L.unorm) + i * P.r_pad;
+                gp[i].M = M;
+                gp[i].Nc = P.r_pad;
+                gp[i].K = N;
+                gp[i].guard = split ? 1 : 0;
+                gp[i].flagged = (unsigned*)(W + L.flag_g);
+                gp[i].mode = lyc::XR_H;
+                gp[i].out = W + L.gh[i];
+                gp[i].ld_out = P.r_pad;
+                gp[i].scale = scale;
+            }
+            if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_xr2(P.c_dt, gp[0], gp[1], s); }) != hipSuccess)
+                return LYC_ERR_HIP;
         }
     }
 
@@ -1440,7 +1464,7 @@ int gated_backward(const Bwd& B, const void* x, const void* const (&w)[2], const
         lyc::PairParams g{};
         for (int i = 0; i < 2; ++i) {
             if (!wt_given && N > 0 && !transpose(w[i], P.w_dt, N, K, W + L.wt[i], N, K)) return LYC_ERR_HIP;
-            if (r > 0 && !transpose(down[i], P.d_dt, r, K, W + L.dt[i], P.r_pad, K)) return LYC_ERR_HIP;
+            if (r > 0 && !downs && !transpose(down[i], P.d_dt, r, K, W + L.dt[i], P.r_pad, K)) return LYC_ERR_HIP;
             g.a[i] = wt_given ? w_t[i] : (const void*)(W + L.wt[i]);
             g.b[i] = W + L.d[i];
             g.af[i] = W + L.dt[i];

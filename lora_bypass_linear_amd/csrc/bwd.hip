@@ -91,6 +91,39 @@ hipError_t launch_bwd_prep(const TransposeParams& u, const TransposeParams& d, c
     return u.src_dt == DT_F32 ? run_bwd_prep<uint32_t>(u, d, q, s) : run_bwd_prep<uint16_t>(u, d, q, s);
 }
 
+// up to four transposed copies (stored dtypes of one size) in one launch
+struct Transposes {
+    TransposeParams p[4];
+    int64_t end[4];   // tiles up to and with each
+};
+template <class T>
+__global__ __launch_bounds__(256) void transposes_kernel(Transposes t) {
+    __shared__ float lds[64][65];
+    const int64_t b = blockIdx.x;
+    int k = 0;
+    while (b >= t.end[k]) ++k;
+    transpose_body<T>(t.p[k], b - (k > 0 ? t.end[k - 1] : 0), (t.p[k].rows_pad + 63) / 64, lds);
+}
+
+hipError_t launch_transposes(const TransposeParams* p, int n, hipStream_t s) {
+    Transposes t{};
+    int64_t all = 0;
+    if (n < 1 || n > 4) return hipErrorInvalidValue;
+    for (int i = 0; i < 4; ++i) {
+        t.p[i] = p[i < n ? i : n - 1];
+        if (i < n) {
+            if ((p[i].src_dt == DT_F32) != (p[0].src_dt == DT_F32)) return hipErrorInvalidValue;
+            if (p[i].rows_pad > 0 && p[i].cols_pad > 0) all += transpose_tiles(p[i]);
+        }
+        t.end[i] = all;
+    }
+    if (all == 0) return hipSuccess;
+    if (all >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (p[0].src_dt == DT_F32) hipLaunchKernelGGL(transposes_kernel<uint32_t>, dim3((unsigned)all), dim3(256), 0, s, t);
+    else hipLaunchKernelGGL(transposes_kernel<uint16_t>, dim3((unsigned)all), dim3(256), 0, s, t);
+    return hipGetLastError();
+}
+
 hipError_t launch_transpose(const TransposeParams& p, hipStream_t s) {
     if (p.rows_pad <= 0 || p.cols_pad <= 0) return hipSuccess;
     const int64_t tr = (p.rows_pad + 63) / 64, tc = (p.cols_pad + 63) / 64;

@@ -421,9 +421,8 @@ struct XrStage {
 // diagonals of MFMA Gram matrices; no preparation pass.  The guard's count is
 // then written per workgroup (p.flagged[workgroup], a plain store), so that
 // nothing needs clearing beforehand.
-template <class CT, int JB, int KS, int CG, int RW_, bool SB = false>
-__global__ __launch_bounds__(64 * RW_ * KS * CG) __attribute__((amdgpu_num_vgpr(256)))
-void xr_kernel(XrParams p) {
+template <class CT, int JB, int KS, int CG, int RW_, bool SB>
+__device__ __forceinline__ void xr_body(const XrParams& p) {
     constexpr bool SPLIT = CT::dt != DT_F32;     // 16-bit compute: hi/lo split and guard
     static_assert(!SB || (SPLIT && JB <= 4), "in-kernel split of b: 16-bit compute, at most 4 column blocks");
     using ST = XrStage<JB, KS, CG, RW_, SPLIT, SB>;
@@ -879,13 +878,34 @@ void xr_kernel(XrParams p) {
     }
 }
 
+template <class CT, int JB, int KS, int CG, int RW_, bool SB = false>
+__global__ __launch_bounds__(64 * RW_ * KS * CG) __attribute__((amdgpu_num_vgpr(256)))
+void xr_kernel(XrParams p) {
+    xr_body<CT, JB, KS, CG, RW_, SB>(p);
+}
+
+// two contractions of the same sizes in one launch (blockIdx.z)
+template <class CT, int JB, int KS, int CG, int RW_>
+__global__ __launch_bounds__(64 * RW_ * KS * CG) __attribute__((amdgpu_num_vgpr(256)))
+void xr2_kernel(XrParams a, XrParams b) {
+    if (blockIdx.z == 0) xr_body<CT, JB, KS, CG, RW_, false>(a);
+    else xr_body<CT, JB, KS, CG, RW_, false>(b);
+}
+
 template <class CT, int JB, int KS, int CG, int RW = xr_row_groups(KS), bool SB = false>
-static hipError_t run_xr(const XrParams& p, hipStream_t s) {
+static hipError_t run_xr(const XrParams& p, hipStream_t s, const XrParams* second = nullptr) {
     constexpr int RP = JB * 16 * CG;
     const dim3 grid((unsigned)((p.M + RW * 16 - 1) / (RW * 16)), (unsigned)((p.Nc + RP - 1) / RP));
     // per-workgroup guard counts: the caller's slots must cover the grid
     if ((SB || p.flag_per_wg) && (int64_t)grid.x * grid.y > p.flag_slots) return hipErrorInvalidValue;
-    hipLaunchKernelGGL((xr_kernel<CT, JB, KS, CG, RW, SB>), grid, dim3(64 * RW * KS * CG), 0, s, p);
+    if (second != nullptr) {
+        if constexpr (!SB)
+            hipLaunchKernelGGL((xr2_kernel<CT, JB, KS, CG, RW>), dim3(grid.x, grid.y, 2), dim3(64 * RW * KS * CG), 0, s,
+                               p, *second);
+        else return hipErrorInvalidValue;
+    } else {
+        hipLaunchKernelGGL((xr_kernel<CT, JB, KS, CG, RW, SB>), grid, dim3(64 * RW * KS * CG), 0, s, p);
+    }
     return hipGetLastError();
 }
 
@@ -899,17 +919,17 @@ static int pick_ks(int64_t M, int64_t col_tiles) {
 // KSMAX 8: where 16 rows per workgroup are needed, 8 k groups (two waves per
 // SIMD) instead of 4
 template <class CT, int JB, int CG, int KSMAX, bool SB = false>
-static hipError_t run_xr_jb(const XrParams& p, hipStream_t s) {
+static hipError_t run_xr_jb(const XrParams& p, hipStream_t s, const XrParams* second = nullptr) {
     const int64_t col_tiles = (p.Nc + JB * 16 * CG - 1) / (JB * 16 * CG);
     const int ks = pick_ks(p.M, col_tiles);
     constexpr int K2 = KSMAX >= 2 ? 2 : 1, K4 = KSMAX >= 4 ? KSMAX : 1;
     // (with b split in the kernel, one b tile per stage: a single k group's
     // loads would not divide among its waves, so it takes two)
     if constexpr (!SB) {
-        if (ks == 1 || KSMAX == 1) return run_xr<CT, JB, 1, CG, xr_row_groups(1), SB>(p, s);
+        if (ks == 1 || KSMAX == 1) return run_xr<CT, JB, 1, CG, xr_row_groups(1), SB>(p, s, second);
     }
-    if (ks <= 2 || KSMAX == 2) return run_xr<CT, JB, K2, CG, xr_row_groups(K2), SB>(p, s);
-    return run_xr<CT, JB, K4, CG, xr_row_groups(K4), SB>(p, s);
+    if (ks <= 2 || KSMAX == 2) return run_xr<CT, JB, K2, CG, xr_row_groups(K2), SB>(p, s, second);
+    return run_xr<CT, JB, K4, CG, xr_row_groups(K4), SB>(p, s, second);
 }
 
 // The plain affine form under 16-bit compute: 64 x 64 tiles (8 waves, two k
@@ -945,7 +965,7 @@ int64_t xr_h_split_b_workgroups(int64_t M, int64_t Nc) { return Nc == 16 ? xr_sp
 // eight waves (two per SIMD) for the wider ranks, and one wave over all
 // columns of its rows where that fits, so that each x fragment is split once.
 template <class CT>
-static hipError_t run_xr_ct(const XrParams& p, hipStream_t s) {
+static hipError_t run_xr_ct(const XrParams& p, hipStream_t s, const XrParams* second = nullptr) {
     if (p.mode == XR_AFFINE) {
         // 16-bit compute: the launches xr_affine_workgroups describes; fp32
         // compute keeps the 4-wave 64-column split
@@ -964,18 +984,18 @@ static hipError_t run_xr_ct(const XrParams& p, hipStream_t s) {
     switch (p.Nc) {
     case 16:   // 16-bit compute only (fp32 compute pads the rank to 32)
         if (CT::dt == DT_F32) return hipErrorInvalidValue;
-        return run_xr_jb<CT, (CT::dt == DT_F32 ? 2 : 1), 1, LYC_R16_KS>(p, s);
-    case 32: return run_xr_jb<CT, 2, 1, 4>(p, s);
+        return run_xr_jb<CT, (CT::dt == DT_F32 ? 2 : 1), 1, LYC_R16_KS>(p, s, second);
+    case 32: return run_xr_jb<CT, 2, 1, 4>(p, s, second);
     case 64:
         // one wave per 16 rows x all 64 columns where M fills the GPU with
         // 32- or 64-row workgroups (the x split is done once per row)
-        if (p.M >= 256 * 64) return run_xr<CT, 4, 2, 1, 4>(p, s);
-        if (p.M >= 256 * 32) return run_xr<CT, 4, 4, 1, 2>(p, s);
-        return run_xr_jb<CT, 2, 2, 4>(p, s);
+        if (p.M >= 256 * 64) return run_xr<CT, 4, 2, 1, 4>(p, s, second);
+        if (p.M >= 256 * 32) return run_xr<CT, 4, 4, 1, 2>(p, s, second);
+        return run_xr_jb<CT, 2, 2, 4>(p, s, second);
     case 128:
-        if (p.M >= 256 * 64) return run_xr<CT, 8, 2, 1, 4>(p, s);
-        return run_xr_jb<CT, 4, 2, 2>(p, s);
-    case 256: return run_xr<CT, 8, 1, 2>(p, s);
+        if (p.M >= 256 * 64) return run_xr<CT, 8, 2, 1, 4>(p, s, second);
+        return run_xr_jb<CT, 4, 2, 2>(p, s, second);
+    case 256: return run_xr<CT, 8, 1, 2>(p, s, second);
     default: return hipErrorInvalidValue;
     }
 }
@@ -1020,7 +1040,7 @@ __device__ __forceinline__ void two_sum(double a, double b, double& s, double& t
 }
 
 template <class CT>
-__device__ __forceinline__ void hdot_body(const HdotParams& p, int64_t wg, unsigned* wflag) {
+__device__ __forceinline__ void hdot_body(const HdotParams& p, int64_t wg, unsigned* wflag, int64_t ld) {
     constexpr int V = CT::dt == DT_F32 ? 4 : 8;   // values per 16-byte chunk
     const int lane = threadIdx.x & 63;
     const int64_t e = wg * 4 + (threadIdx.x >> 6);   // element m * r_pad + j
@@ -1120,7 +1140,7 @@ __device__ __forceinline__ void hdot_body(const HdotParams& p, int64_t wg, unsig
             }
         }
         if (lane == 0) {
-            const int64_t at = m * p.r_pad + j;
+            const int64_t at = m * ld + j;
             if constexpr (CT::dt == DT_F32) ((float*)p.out)[at] = (float)v;
             else ((uint16_t*)p.out)[at] = round16<CT>(v);
         }
@@ -1133,7 +1153,7 @@ __device__ __forceinline__ void hdot_body(const HdotParams& p, int64_t wg, unsig
 template <class CT>
 __global__ __launch_bounds__(256) void hdot_kernel(HdotParams p) {
     __shared__ unsigned wflag[4];
-    hdot_body<CT>(p, blockIdx.x, wflag);
+    hdot_body<CT>(p, blockIdx.x, wflag, p.r_pad);
 }
 
 // the first nq workgroups quantize x, the others take h: both read the same
@@ -1142,7 +1162,15 @@ template <class CT>
 __global__ __launch_bounds__(256) void hdot_quant_kernel(HdotParams p, QuantRowsParams q, int pairs, unsigned nq) {
     __shared__ unsigned wflag[4];
     if (blockIdx.x < nq) quant_rows_body<CT::dt>(q, blockIdx.x, pairs);
-    else hdot_body<CT>(p, blockIdx.x - nq, wflag);
+    else hdot_body<CT>(p, blockIdx.x - nq, wflag, p.r_pad);
+}
+
+// two of the same sizes in one launch, rows of the outputs ld apart
+template <class CT>
+__global__ __launch_bounds__(256) void hdot2_kernel(HdotParams a, HdotParams b, int64_t ld) {
+    __shared__ unsigned wflag[4];
+    if (blockIdx.y == 0) hdot_body<CT>(a, blockIdx.x, wflag, ld);
+    else hdot_body<CT>(b, blockIdx.x, wflag, ld);
 }
 
 int64_t hdot_workgroups(int64_t M, int64_t r_pad) { return (M * r_pad + 3) / 4; }
@@ -1166,6 +1194,29 @@ hipError_t launch_hdot_quant(int c_dt, const HdotParams& h, const QuantRowsParam
     if (c_dt == DT_F16) hipLaunchKernelGGL(hdot_quant_kernel<CF16>, grid, dim3(256), 0, s, h, q, pairs, (unsigned)nq);
     else hipLaunchKernelGGL(hdot_quant_kernel<CBF16>, grid, dim3(256), 0, s, h, q, pairs, (unsigned)nq);
     return hipGetLastError();
+}
+
+// two h dots of the same M and r_pad in one launch, their rows ld apart; each
+// with flagged slots of its own
+hipError_t launch_hdot2(int c_dt, const HdotParams& a, const HdotParams& b, int64_t ld, hipStream_t s) {
+    const int64_t g = hdot_workgroups(a.M, a.r_pad);
+    if (g <= 0) return hipSuccess;
+    if (g > 65535 || a.M != b.M || a.r_pad != b.r_pad) return hipErrorInvalidValue;
+    const dim3 grid((unsigned)g, 2);
+    if (c_dt == DT_F16) hipLaunchKernelGGL(hdot2_kernel<CF16>, grid, dim3(256), 0, s, a, b, ld);
+    else if (c_dt == DT_BF16) hipLaunchKernelGGL(hdot2_kernel<CBF16>, grid, dim3(256), 0, s, a, b, ld);
+    else hipLaunchKernelGGL(hdot2_kernel<CF32>, grid, dim3(256), 0, s, a, b, ld);
+    return hipGetLastError();
+}
+
+// two h passes of the same sizes and mode in one launch
+hipError_t launch_xr2(int c_dt, const XrParams& a, const XrParams& b, hipStream_t s) {
+    if (a.mode != XR_H || b.mode != XR_H || a.split_b || b.split_b || a.flag_per_wg || b.flag_per_wg || a.M != b.M ||
+        a.Nc != b.Nc || a.K != b.K)
+        return hipErrorInvalidValue;
+    if (c_dt == DT_F16) return run_xr_ct<CF16>(a, s, &b);
+    if (c_dt == DT_BF16) return run_xr_ct<CBF16>(a, s, &b);
+    return run_xr_ct<CF32>(a, s, &b);
 }
 
 hipError_t launch_xr(int c_dt, const XrParams& p, hipStream_t s) {

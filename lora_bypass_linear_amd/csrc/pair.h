@@ -8,6 +8,14 @@
 
 namespace lyc {
 
+// both projections' launches at once (hpass.hip, prep.hip)
+struct HdotParams;
+struct XrParams;
+struct PrepParams;
+hipError_t launch_hdot2(int c_dt, const HdotParams& a, const HdotParams& b, int64_t ld, hipStream_t s);
+hipError_t launch_xr2(int c_dt, const XrParams& a, const XrParams& b, hipStream_t s);
+hipError_t launch_prep2(const PrepParams& a, const PrepParams& b, hipStream_t s);
+
 // activations of the gated block: x sigmoid(x); x Phi(x); its tanh form
 enum { ACT_SILU = 0, ACT_GELU = 1, ACT_GELU_TANH = 2, ACT_COUNT = 3 };
 

@@ -220,7 +220,7 @@ __device__ __forceinline__ void cast_range(const float* __restrict__ src, uint16
 // in fp32 under a 16-bit policy), grid-stride over the remaining blocks.  The
 // row passes are latency-bound and the casts stream through HBM, so one
 // launch runs both at once.
-__global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
+__device__ __forceinline__ void prep_body(const PrepParams& p) {
     const int b = blockIdx.x, tid = threadIdx.x;
     if (b == 0 && p.flagged != nullptr)
         for (int64_t i = tid; i < p.flag_slots; i += 256) p.flagged[i] = 0u;
@@ -248,6 +248,15 @@ __global__ __launch_bounds__(256) void prep_kernel(PrepParams p) {
     }
 }
 
+__global__ __launch_bounds__(256) void prep_kernel(PrepParams p) { prep_body(p); }
+
+// two preparations in one launch (blockIdx.y): the shorter one's blocks past its
+// own are cast blocks like the rest
+__global__ __launch_bounds__(256) void prep2_kernel(PrepParams a, PrepParams b) {
+    if (blockIdx.y == 0) prep_body(a);
+    else prep_body(b);
+}
+
 // split and norms of the rows of an operand already in the 16-bit compute
 // dtype; clears *flagged
 __global__ __launch_bounds__(256) void rownorm_kernel(const void* b, int c_dt, int64_t K, void* b_hi, void* b_lo,
@@ -262,8 +271,8 @@ hipError_t launch_rownorm(const void* b, int c_dt, int64_t rows, int64_t K, void
     return hipGetLastError();
 }
 
-hipError_t launch_prep(const PrepParams& p_in, hipStream_t s) {
-    PrepParams p = p_in;
+// the blocks of a launch, p.up_blocks set
+static int64_t prep_blocks(PrepParams& p) {
     // uc == nullptr: no up copy is wanted (the caller reads up as stored, or
     // not at all), so only the down rows are prepared
     const int64_t total = p.uc != nullptr ? p.N * (int64_t)p.r_pad : 0;
@@ -275,7 +284,20 @@ hipError_t launch_prep(const PrepParams& p_in, hipStream_t s) {
     const int64_t cast8 = (p.cast_n[0] + p.cast_n[1]) / 8 + 1;
     int64_t cast_blocks = (p.cast_n[0] + p.cast_n[1]) > 0 ? (cast8 + 255) / 256 : 0;
     if (cast_blocks > 8192) cast_blocks = 8192;
-    const int64_t blocks = p.r_pad + up_blocks + cast_blocks;
+    return p.r_pad + up_blocks + cast_blocks;
+}
+
+hipError_t launch_prep2(const PrepParams& a_in, const PrepParams& b_in, hipStream_t s) {
+    PrepParams a = a_in, b = b_in;
+    const int64_t na = prep_blocks(a), nb = prep_blocks(b), blocks = na > nb ? na : nb;
+    if (blocks == 0) return hipSuccess;
+    hipLaunchKernelGGL(prep2_kernel, dim3((unsigned)blocks, 2), dim3(256), 0, s, a, b);
+    return hipGetLastError();
+}
+
+hipError_t launch_prep(const PrepParams& p_in, hipStream_t s) {
+    PrepParams p = p_in;
+    const int64_t blocks = prep_blocks(p);
     if (blocks == 0) return hipSuccess;
     hipLaunchKernelGGL(prep_kernel, dim3((unsigned)blocks), dim3(256), 0, s, p);
     return hipGetLastError();
