@@ -17,6 +17,8 @@ hipError_t launch_gated(int c_dt, const PairParams& p, hipStream_t s) {
     return run_pair_ct<CF32, PAIR_PAIR>(p, s);
 }
 
+bool pair_wide(int64_t N) { return N >= 32 * device_rates().cus; }
+
 // Tile and K split by modelled time, us: rounds of workgroups over the CUs (two
 // 64 x 64 ones share one), each a fixed part and its K steps of 128 bytes a row,
 // whose time grows with the share of the device that is busy; plus a split's
@@ -35,7 +37,7 @@ PairPlan pair_plan(int mode, int c_dt, int64_t M, int64_t N, int64_t K) {
     const int es = c_dt == DT_F32 ? 4 : c_dt == DT_I8 ? 1 : 2;
     const int two = mode == PAIR_PAIR ? 2 : 1;
     if (M <= 0 || N <= 0) return PairPlan{0, 0, 1};
-    if (pair_skinny(M, K, es)) return PairPlan{16, M <= 16 ? 16 : 32, 1};
+    if (pair_skinny(M, K, es)) return PairPlan{two == 1 && pair_wide(N) ? 32 : 16, M <= 16 ? 16 : 32, 1};
     struct C {
         int t, per_cu;
         double fixed, empty, full;

@@ -530,22 +530,23 @@ __global__ __launch_bounds__(256) void pair_join_kernel(PairParams p) {
     put(p.y, p.y_dt, pr[0]);
 }
 
-// ---- few token rows: one workgroup per 16 features ------------------------------
+// ---- few token rows: one workgroup per 16 FB features ----------------------------
 // M <= 32 with all of K in one workgroup: wave w of the NW takes the w-th share
 // of the 64-byte K steps, its fragments read straight from global memory D
 // steps ahead (every weight byte is used once, so nothing is staged); wave 0
 // takes the folds first.  The waves' sums meet in LDS in wave order.  Bound by
 // the weights' bytes.
-template <class CT, int MODE, int MT, int D, int NW>
+template <class CT, int MODE, int MT, int FB, int D, int NW>
 __global__ __launch_bounds__(64 * NW) void pair_skinny_kernel(PairParams p) {
     constexpr bool TWO = MODE == PAIR_PAIR, I8 = CT::dt == DT_I8;
-    constexpr int H = TWO ? 2 : 1, SEGS = MODE == PAIR_SEQ ? 2 : 1;
+    static_assert(!TWO || FB == 1, "16 features of both matrices");
+    constexpr int H = TWO ? 2 : FB, SEGS = MODE == PAIR_SEQ ? 2 : 1;   // 16-row blocks of weights; products
     __shared__ __attribute__((aligned(16))) Acc<CT> red[NW][H][MT][64];
     const int tid = threadIdx.x, lane = tid & 63, g4 = lane >> 4, r = lane & 15;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int64_t n0 = (int64_t)blockIdx.x * 16;
+    const int64_t n0 = (int64_t)blockIdx.x * (16 * FB);
     const uint32_t kb = (uint32_t)(p.K * CT::es), lo = (uint32_t)g4 * 16;
-    const uint32_t nrows = (uint32_t)(p.N - n0 < 16 ? p.N - n0 : 16);
+    const uint32_t nrows = (uint32_t)(p.N - n0 < 16 * FB ? p.N - n0 : 16 * FB);   // (of each matrix)
     Acc<CT> acc[H][MT];
 #pragma unroll
     for (int h = 0; h < H; ++h)
@@ -557,17 +558,22 @@ __global__ __launch_bounds__(64 * NW) void pair_skinny_kernel(PairParams p) {
             const uint32_t fb = (uint32_t)(p.rf * CT::es), ld = (uint32_t)(p.ldf * CT::es);
 #pragma unroll
             for (int f = 0; f < 2; ++f) {
-                const int h = TWO ? f : 0;
                 const auto ru = make_rsrc_uniform((const char*)p.af[f] + n0 * fb, nrows * fb);
                 const auto rh = make_rsrc_uniform(p.bf[f], (uint32_t)(p.M - 1) * ld + fb);
                 for (uint32_t k = 0; k < fb; k += 64) {
                     const bool in = k + lo < fb;
-                    const i32x4 ua = buf_load16(ru, in ? (uint32_t)r * fb + k + lo : OOB);
+                    i32x4 hb[MT];
 #pragma unroll
                     for (int t = 0; t < MT; ++t) {
                         const bool on = in && 16 * t + r < p.M;
-                        const i32x4 hb = buf_load16(rh, on ? (uint32_t)(16 * t + r) * ld + k + lo : OOB);
-                        acc[h][t] = CT::step(ua, hb, acc[h][t]);
+                        hb[t] = buf_load16(rh, on ? (uint32_t)(16 * t + r) * ld + k + lo : OOB);
+                    }
+#pragma unroll
+                    for (int h = TWO ? f : 0; h < (TWO ? f + 1 : H); ++h) {
+                        const uint32_t row = (uint32_t)(TWO ? r : 16 * h + r);
+                        const i32x4 ua = buf_load16(ru, in ? row * fb + k + lo : OOB);
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) acc[h][t] = CT::step(ua, hb[t], acc[h][t]);
                     }
                 }
             }
@@ -593,8 +599,9 @@ __global__ __launch_bounds__(64 * NW) void pair_skinny_kernel(PairParams p) {
         auto load = [&](int u, int s) {
             const uint32_t k = (uint32_t)s * 64 + lo;
             const bool in = s < s1 && k < kb;
-            wa[u][0] = buf_load16(rw0, in ? (uint32_t)r * kb + k : OOB);
-            if constexpr (TWO) wa[u][1] = buf_load16(rw1, in ? (uint32_t)r * kb + k : OOB);
+#pragma unroll
+            for (int h = 0; h < H; ++h)
+                wa[u][h] = buf_load16(TWO && h ? rw1 : rw0, in ? (uint32_t)(TWO ? r : 16 * h + r) * kb + k : OOB);
 #pragma unroll
             for (int t = 0; t < MT; ++t) xa[u][t] = buf_load16(rx, in ? (uint32_t)(16 * t + r) * kb + k : OOB);
         };
@@ -616,17 +623,19 @@ __global__ __launch_bounds__(64 * NW) void pair_skinny_kernel(PairParams p) {
 #pragma unroll
         for (int t = 0; t < MT; ++t) red[wave][h][t][lane] = acc[h][t];
     __syncthreads();
-    static_assert(MT <= NW, "a wave per 16 rows");
-    if (wave >= MT) return;
-    // wave t ends rows m = 16 t + r, features n0 + 4 g4 .. + 3
-    const int64_t m = 16 * wave + r, nb = n0 + 4 * g4;
+    static_assert(MT * (TWO ? 1 : H) <= NW, "a wave per output block");
+    if (wave >= MT * (TWO ? 1 : H)) return;
+    // wave t (ONE, SEQ: + MT times the block of features) ends rows m = 16 t + r,
+    // features nb .. nb + 3
+    const int mt = wave % MT, fb0 = TWO ? 0 : wave / MT;
+    const int64_t m = 16 * mt + r, nb = n0 + 16 * fb0 + 4 * g4;
     if (m >= p.M) return;
-    f32x4 pr[H];
+    f32x4 pr[TWO ? 2 : 1];
 #pragma unroll
-    for (int h = 0; h < H; ++h) {
-        Acc<CT> sum = red[0][h][wave][lane];
+    for (int h = 0; h < (TWO ? 2 : 1); ++h) {
+        Acc<CT> sum = red[0][fb0 + h][mt][lane];
 #pragma unroll
-        for (int w = 1; w < NW; ++w) sum += red[w][h][wave][lane];
+        for (int w = 1; w < NW; ++w) sum += red[w][fb0 + h][mt][lane];
         f32x4 v = to_f32(sum);
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -680,18 +689,32 @@ hipError_t run_pair(const PairParams& p, hipStream_t s) {
     return hipGetLastError();
 }
 
+// The few-row kernel's x rows are read by every workgroup, from L2: 32 features
+// a workgroup halve that where they still leave one per CU
+bool pair_wide(int64_t N);
 // 32-bit offsets of the few-row kernel
 inline bool pair_skinny(int64_t M, int64_t K, int es) {
     return M >= 1 && M <= 32 && K > 0 && 32 * K * es < ((int64_t)1 << 31);
 }
 
+template <class CT, int MODE, int FB>
+hipError_t run_pair_skinny(const PairParams& p, hipStream_t s) {
+    const dim3 g((unsigned)((p.N + 16 * FB - 1) / (16 * FB)));
+    // 4 waves, 4 steps ahead, 2 where two blocks of rows double the registers: int8
+    // 16 x 8192 x 8192 16.4 us (8 ahead 18.2, 12 19.6, 2 17.6; 8 waves 20.8), 32 x 8192 x
+    // 8192 19.6 (4 ahead 21.1, 6 22.7)
+    if (p.M <= 16) hipLaunchKernelGGL((pair_skinny_kernel<CT, MODE, 1, FB, 4, 4>), g, dim3(256), 0, s, p);
+    else hipLaunchKernelGGL((pair_skinny_kernel<CT, MODE, 2, FB, 2, 4>), g, dim3(256), 0, s, p);
+    return hipGetLastError();
+}
+
 template <class CT, int MODE>
 hipError_t run_pair_ct(const PairParams& p, hipStream_t s) {
     if (p.ksplit <= 1 && pair_skinny(p.M, p.K, CT::es)) {
-        const dim3 g((unsigned)((p.N + 15) / 16));
-        if (p.M <= 16) hipLaunchKernelGGL((pair_skinny_kernel<CT, MODE, 1, 8, 4>), g, dim3(256), 0, s, p);
-        else hipLaunchKernelGGL((pair_skinny_kernel<CT, MODE, 2, 6, 4>), g, dim3(256), 0, s, p);
-        return hipGetLastError();
+        if constexpr (MODE != PAIR_PAIR) {
+            if (pair_wide(p.N)) return run_pair_skinny<CT, MODE, 2>(p, s);
+        }
+        return run_pair_skinny<CT, MODE, 1>(p, s);
     }
     const PairPlan pl = pair_plan(MODE, CT::dt, p.M, p.N, p.K);
     if (p.ksplit > 1 && p.partial == nullptr) return hipErrorInvalidValue;
