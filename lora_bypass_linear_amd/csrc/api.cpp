@@ -19,6 +19,7 @@
 #include "merge.h"
 #include "ortho.h"
 #include "pair.h"
+#include "tokens.h"
 #include "tune.h"
 
 namespace {
@@ -1225,7 +1226,6 @@ struct GatedBwdLayout {
     bool cast_x = false, need_h = false, need_gh = false, gh_dot = false, tr_tok = false;
     bool h_dot = false;
     int ks_dx = 1, ks_dd = 1, ks_du = 1;
-    int tile_dd = lyc::GEMM_TILE_AUTO, tile_du = lyc::GEMM_TILE_AUTO;
 };
 
 GatedBwdLayout gated_bwd_layout(const Bwd& B) {
@@ -1268,7 +1268,6 @@ GatedBwdLayout gated_bwd_layout(const Bwd& B) {
         for (size_t& g : L.gh) take(g, M * R * ce);
     }
     size_t part = 0;
-    const int64_t Kt = L.tr_tok ? P.M : B.M8;
     if (dx) {
         if (!(B.want & BWD_WT))
             for (size_t& w : L.wt) take(w, K * N * ce);
@@ -1277,14 +1276,15 @@ GatedBwdLayout gated_bwd_layout(const Bwd& B) {
         L.ks_dx = lyc::pair_plan(lyc::PAIR_SEQ, P.c_dt, P.M, P.K, P.N).ksplit;
         if (L.ks_dx > 1) part = std::max(part, (size_t)L.ks_dx * M * K * 4);
     }
-    if (dd) {
-        if (!L.tr_tok) take(L.xt, K * M8 * ce);
-        L.ks_dd = L.tr_tok ? lyc::gemm_tok_plan(P.rank, P.K, Kt, &L.tile_dd) : lyc::gemm_ksplit(P.rank, P.K, Kt, P.c_dt);
+    if (L.tr_tok && (dd || du)) part = std::max(part, lyc::tokens_partial(P.M, P.K, P.N, P.rank, dd, du));
+    if (dd && !L.tr_tok) {
+        take(L.xt, K * M8 * ce);
+        L.ks_dd = lyc::gemm_ksplit(P.rank, P.K, B.M8, P.c_dt);
         if (L.ks_dd > 1) part = std::max(part, (size_t)L.ks_dd * (size_t)P.rank * K * 4);
     }
-    if (du) {
-        if (!L.tr_tok) take(L.dyt, N * M8 * ce);
-        L.ks_du = L.tr_tok ? lyc::gemm_tok_plan(P.N, P.rank, Kt, &L.tile_du) : lyc::gemm_ksplit(P.N, P.rank, Kt, P.c_dt);
+    if (du && !L.tr_tok) {
+        take(L.dyt, N * M8 * ce);
+        L.ks_du = lyc::gemm_ksplit(P.N, P.rank, B.M8, P.c_dt);
         if (L.ks_du > 1) part = std::max(part, (size_t)L.ks_du * N * (size_t)P.rank * 4);
     }
     if (!L.tr_tok && (dd || du)) take(L.rt, R * M8 * ce);   // the rank side's transposed copy
@@ -1485,52 +1485,53 @@ int gated_backward(const Bwd& B, const void* x, const void* const (&w)[2], const
     }
 
     // the factors' gradients, over the tokens
-    auto tokens = [&](const void* a, int64_t lda, const void* b, int64_t ldb, int64_t rows, int64_t cols, void* out,
-                      int out_dt, int tile, int ks, float post) {
+    const bool mdd = wdd && r > 0 && K > 0, mdu = wdu && r > 0 && N > 0;
+    if (L.tr_tok && (mdd || mdu)) {
+        lyc::TokenJob jobs[4];
+        int n = 0;
+        for (int i = 0; i < 2 && mdd; ++i)
+            jobs[n++] = lyc::TokenJob{M > 0 ? xa : W, K, W + L.gh[i], P.r_pad, r, d_down[i], P.d_dt, 1, 1.0f};
+        // gate's half of h in place, value's from its own rows
+        for (int i = 0; i < 2 && mdu; ++i)
+            jobs[n++] = lyc::TokenJob{W + L.d[i], N, M == 0 || i == 1 ? (const void*)(W + L.hv) : hs,
+                                      i == 0 ? 2 * P.r_pad : P.r_pad, r, d_up[i], P.u_dt, 0, (float)scale};
+        return timed(LYC_KERNEL_GEMM, s, [&] {
+                   return lyc::launch_tokens(P.c_dt, jobs, n, M, (float*)(W + L.partial), s);
+               }) == hipSuccess
+                   ? LYC_OK
+                   : LYC_ERR_HIP;
+    }
+    auto tokens = [&](const void* a, const void* b, int64_t rows, int64_t cols, void* out, int out_dt, int ks, float post) {
         lyc::GemmParams g{};
         g.a = a;
         g.b = b;
-        if (L.tr_tok) {
-            g.ta = g.tb = 1;
-            g.lda_t = lda;
-            g.ldb_t = ldb;
-        }
-        g.K = L.tr_tok ? M : B.M8;
+        g.K = B.M8;
         g.M = rows;
         g.N = cols;
         g.scale = 1.0f;
         g.post = post;
         g.y = out;
         g.y_dt = out_dt;
-        g.tile = tile;
         g.ksplit = ks;
         g.partial = ks > 1 ? (float*)(W + L.partial) : nullptr;
         g.vec_store = (cols % 4 == 0) && aligned(out, out_dt == LYC_F32 ? 16 : 8);
         return timed(LYC_KERNEL_GEMM, s, [&] { return lyc::launch_gemm(P.c_dt, g, s); }) == hipSuccess;
     };
-    if (wdd && r > 0 && K > 0) {
-        if (!L.tr_tok && M > 0 && !transpose(x, P.x_dt, M, K, W + L.xt, B.M8, K)) return LYC_ERR_HIP;
+    if (mdd) {
+        if (M > 0 && !transpose(x, P.x_dt, M, K, W + L.xt, B.M8, K)) return LYC_ERR_HIP;
         for (int i = 0; i < 2; ++i) {
-            if (!L.tr_tok && M > 0 && !transpose(W + L.gh[i], P.c_dt, M, P.r_pad, W + L.rt, B.M8, P.r_pad))
-                return LYC_ERR_HIP;
-            if (!tokens(L.tr_tok ? (M > 0 ? xa : W) : W + L.xt, K, L.tr_tok ? W + L.gh[i] : W + L.rt, P.r_pad, r, K,
-                        d_down[i], P.d_dt, L.tile_dd, L.ks_dd, 1.0f))
-                return LYC_ERR_HIP;
+            if (M > 0 && !transpose(W + L.gh[i], P.c_dt, M, P.r_pad, W + L.rt, B.M8, P.r_pad)) return LYC_ERR_HIP;
+            if (!tokens(W + L.xt, W + L.rt, r, K, d_down[i], P.d_dt, L.ks_dd, 1.0f)) return LYC_ERR_HIP;
         }
     }
-    if (wdu && r > 0 && N > 0) {
+    if (mdu) {
         for (int i = 0; i < 2; ++i) {
-            // gate's half of h in place, value's from its own rows
             const void* h = i == 0 ? hs : (const void*)(W + L.hv);
-            const int64_t ld = i == 0 ? 2 * P.r_pad : P.r_pad;
-            if (M == 0) h = W;
-            if (!L.tr_tok && M > 0) {
+            if (M > 0) {
                 if (!transpose(W + L.d[i], P.c_dt, M, N, W + L.dyt, B.M8, N)) return LYC_ERR_HIP;
-                if (!transpose(h, P.c_dt, M, ld, W + L.rt, B.M8, P.r_pad)) return LYC_ERR_HIP;
+                if (!transpose(h, P.c_dt, M, i == 0 ? 2 * P.r_pad : P.r_pad, W + L.rt, B.M8, P.r_pad)) return LYC_ERR_HIP;
             }
-            if (!tokens(L.tr_tok ? h : W + L.rt, ld, L.tr_tok ? W + L.d[i] : W + L.dyt, N, N, r, d_up[i], P.u_dt,
-                        L.tile_du, L.ks_du, (float)scale))
-                return LYC_ERR_HIP;
+            if (!tokens(W + L.rt, W + L.dyt, N, r, d_up[i], P.u_dt, L.ks_du, (float)scale)) return LYC_ERR_HIP;
         }
     }
     return LYC_OK;
