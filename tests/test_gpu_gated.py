@@ -51,7 +51,7 @@ FORWARD = [
     (1, 64, 72, 3, F32, F32, F32, None, "gelu"), (31, 100, 520, 32, F32, F32, F32, F32, "silu"),
     (200, 333, 264, 40, F32, F32, F32, F32, "gelu_tanh"), (517, 2056, 136, 5, F32, F32, F32, None, "silu"),
     (40, 64, 4096, 16, F32, F32, F32, None, "silu"), (50, 72, 0, 4, BF16, BF16, BF16, BF16, "silu"),
-    (3, 72, 0, 0, F16, F16, F16, F16, "silu"),
+    (3, 72, 0, 0, F16, F16, F16, F16, "silu"), (1100, 1101, 264, 7, F16, F16, F16, None, "silu"),
 ]
 
 
@@ -154,7 +154,9 @@ BACKWARD = [
     (300, 264, 136, 0, BF16, BF16, BF16, BF16, "silu", "w"),
     (1, 72, 64, 3, F32, F32, F32, F32, "gelu", "wh"), (31, 136, 520, 32, F32, F32, F32, F32, "silu", ""),
     (200, 328, 264, 40, F32, F32, F32, F32, "gelu_tanh", "wh"), (517, 136, 1032, 200, F32, F32, F32, F32, "silu", ""),
-    (64, 2048, 72, 16, BF16, BF16, BF16, BF16, "silu", "wh"),
+    (64, 2048, 72, 16, BF16, BF16, BF16, BF16, "silu", "wh"), (1500, 264, 1544, 20, BF16, BF16, BF16, BF16, "silu", "wh"),
+    (1030, 72, 2056, 40, F32, F32, F32, F32, "gelu", "w"), (5, 72, 8200, 8, F16, F16, F16, F16, "silu", "wh"),
+    (20, 72, 8200, 40, BF16, BF16, F32, F32, "gelu_tanh", ""),
 ]
 
 

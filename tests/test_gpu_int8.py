@@ -73,7 +73,8 @@ def test_rows_that_are_not_finite():
 SHAPES = [(1, 1, 16), (1, 8192, 4096), (2, 33, 64), (7, 130, 1040), (16, 257, 144), (17, 100, 80), (31, 515, 2064),
           (32, 64, 16), (33, 48, 4096), (64, 512, 8192), (65, 67, 272), (129, 1000, 528), (200, 3001, 208),
           (300, 2056, 1040), (777, 1025, 1040), (1030, 2500, 144), (2100, 2057, 528), (4100, 4097, 272), (40, 24, 0),
-          (3, 24, 0), (600, 700, 16)]
+          (3, 24, 0), (600, 700, 16), (5, 8200, 80), (20, 8193, 64),
+          (500, 1500, 528), (900, 1800, 2064)]
 
 
 def _operands(M, N, K, seed):
