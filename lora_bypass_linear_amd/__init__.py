@@ -1072,7 +1072,8 @@ def int8_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     """int8 codes [M,K] of x [M,K] (tokens of activations, output channels of a
     weight) with one scale per row [M]: a code c of row m stands for c * s[m]."""
     M, K = _dims(x, 2, "x")
-    _int8_codes(q, s, M, K, "q")
+    if q is not None or s is not None:
+        _int8_codes(q, s, M, K, "q")
     dev = _need_device(x, s, codes=(q,), code_dtype=torch.int8)
     q = torch.empty((M, K), dtype=torch.int8, device=dev) if q is None else q
     s = torch.empty((M,), dtype=torch.float32, device=dev) if s is None else s

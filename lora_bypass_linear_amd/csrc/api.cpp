@@ -1387,31 +1387,36 @@ int gated_backward(const Bwd& B, const void* x, const void* const (&w)[2], const
         xa = W + L.xc;
     }
 
-    // dg, dv, and h's second half as rows of its own
+    // dg, dv, h's second half as rows of its own, and up^T of both (gh) and down^T
+    // (dx), where the stored sizes agree in the same launch
+    lyc::TransposeParams tp[4];
+    int nt = 0;
+    if (L.need_gh && M > 0 && N > 0)
+        for (int i = 0; i < 2; ++i)
+            tp[nt++] = lyc::TransposeParams{up[i], P.u_dt, N, r, W + L.ut + i * (size_t)P.r_pad * (size_t)N * ce, P.c_dt, N,
+                                            P.r_pad};
+    const int nup = nt;
+    if (wdx && r > 0 && M > 0 && K > 0)
+        for (int i = 0; i < 2; ++i)
+            tp[nt++] = lyc::TransposeParams{down[i], P.d_dt, r, K, W + L.dt[i], P.c_dt, P.r_pad, K};
+    // (the rest of them alone: other stored sizes, or no dg and dv to make)
+    const int joined = !use_dy ? 0 : nup > 0 && esize(P.u_dt) != esize(P.d_dt) ? nup : nt;
     if (use_dy) {
-        const lyc::GateGradParams gp{dy, B.dy_dt, kept[0], kept[1], W + L.d[0], W + L.d[1], M * N, act,
-                                     wdu && r > 0 ? hs : nullptr, W + L.hv, M, P.r_pad, (uint8_t*)(W + L.open)};
+        lyc::GateGradParams gp{dy, B.dy_dt, kept[0], kept[1], W + L.d[0], W + L.d[1], M * N, act,
+                               wdu && r > 0 ? hs : nullptr, W + L.hv, M, P.r_pad, (uint8_t*)(W + L.open), {}, joined};
+        for (int i = 0; i < joined; ++i) gp.tr[i] = tp[i];
         if (timed(LYC_KERNEL_PREP, s, [&] { return lyc::launch_gate_grad(P.c_dt, gp, s); }) != hipSuccess)
             return LYC_ERR_HIP;
     }
+    for (int i = joined; i < nt; ++i)
+        if (timed(LYC_KERNEL_CAST, s, [&] { return lyc::launch_transpose(tp[i], s); }) != hipSuccess) return LYC_ERR_HIP;
 
     // gh = round_c(scale * d . up) of both
-    bool downs = false;   // down^T made with up^T
     if (L.need_gh && M > 0 && N == 0) {
         for (size_t g : L.gh)
             if (!transpose(W, P.c_dt, 0, 0, W + g, P.r_pad, M)) return LYC_ERR_HIP;
     } else if (L.need_gh && M > 0) {
         const size_t half = (size_t)P.r_pad * (size_t)N * ce;
-        // up^T of both, and down^T for dx, in one launch where the stored sizes agree
-        lyc::TransposeParams tp[4];
-        int nt = 0;
-        for (int i = 0; i < 2; ++i)
-            tp[nt++] = lyc::TransposeParams{up[i], P.u_dt, N, r, W + L.ut + i * half, P.c_dt, N, P.r_pad};
-        downs = wdx && K > 0 && esize(P.u_dt) == esize(P.d_dt);
-        if (downs)
-            for (int i = 0; i < 2; ++i)
-                tp[nt++] = lyc::TransposeParams{down[i], P.d_dt, r, K, W + L.dt[i], P.c_dt, P.r_pad, K};
-        if (timed(LYC_KERNEL_CAST, s, [&] { return lyc::launch_transposes(tp, nt, s); }) != hipSuccess) return LYC_ERR_HIP;
         if (L.gh_dot) {
             lyc::HdotParams hq[2];
             for (int i = 0; i < 2; ++i) {
@@ -1464,7 +1469,6 @@ int gated_backward(const Bwd& B, const void* x, const void* const (&w)[2], const
         lyc::PairParams g{};
         for (int i = 0; i < 2; ++i) {
             if (!wt_given && N > 0 && !transpose(w[i], P.w_dt, N, K, W + L.wt[i], N, K)) return LYC_ERR_HIP;
-            if (r > 0 && !downs && !transpose(down[i], P.d_dt, r, K, W + L.dt[i], P.r_pad, K)) return LYC_ERR_HIP;
             g.a[i] = wt_given ? w_t[i] : (const void*)(W + L.wt[i]);
             g.b[i] = W + L.d[i];
             g.af[i] = W + L.dt[i];

@@ -18,8 +18,6 @@ struct TransposeParams {
     int64_t rows_pad, cols_pad;  // dst [cols_pad][rows_pad]; rows_pad >= rows, cols_pad >= cols
 };
 hipError_t launch_transpose(const TransposeParams& p, hipStream_t s);
-// up to four of them in one launch (sources all of 16 or all of 32 bits)
-hipError_t launch_transposes(const TransposeParams* p, int n, hipStream_t s);
 // both factors' transposed copies (stored dtypes of one size) and dy's
 // quantization in one launch
 struct QuantRowsParams;

@@ -6,6 +6,7 @@
 //   dx = round_x( gh_g.down_g + gh_v.down_v + dg.W_g + dv.W_v )
 #include "act.h"
 #include "pair_tile.h"
+#include "transpose_device.h"
 
 namespace lyc {
 
@@ -74,8 +75,10 @@ __device__ __forceinline__ uint32_t grads_f64(int act, float dy, float g, float 
 }
 
 // 8 elements per thread, the rows' shapes do not matter; bound by memory (five
-// passes over M x N).  The last workgroups copy the second half of a saved h to
-// rows of its own, which the product over the tokens reads.
+// passes over M x N).  Workgroups past those copy the second half of a saved h to
+// rows of its own, which the product over the tokens reads, and the factors
+// transposed, which gh and dx read (a launch of their own for those cost a short
+// batch 5 of 52 us).
 //
 // dg and dv round to 16 bits as their exact values do: what is built on them
 // (gh, itself rounded, then dx and the factors' gradients) would carry a step
@@ -84,8 +87,16 @@ __device__ __forceinline__ uint32_t grads_f64(int act, float dy, float g, float 
 // error of a border; those are marked, a bit an element, and a second kernel
 // evaluates them in 64 bits.  (In this one that code's registers halved the
 // waves in flight: bf16 8192 x 8192 177 us with it, 113 and 32 apart.)
-template <int C, int G>
-__global__ __launch_bounds__(256) void gate_grad_kernel(GateGradParams p, unsigned nb) {
+template <int C, int G, class T>
+__global__ __launch_bounds__(256) void gate_grad_kernel(GateGradParams p, unsigned nb, unsigned nh) {
+    if (blockIdx.x >= nb + nh) {
+        __shared__ float lds[64][65];
+        int64_t b = blockIdx.x - nb - nh;
+        int k = 0;
+        while (b >= transpose_tiles(p.tr[k])) b -= transpose_tiles(p.tr[k++]);
+        transpose_body<T>(p.tr[k], b, (p.tr[k].rows_pad + 63) / 64, lds);
+        return;
+    }
     if (blockIdx.x >= nb) {
         const int64_t per = p.r_pad * (C == DT_F32 ? 4 : 2) / 16;   // 16-byte chunks of a half row
         const int64_t i = (int64_t)(blockIdx.x - nb) * 256 + threadIdx.x;
@@ -144,15 +155,16 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateGradParams p, unsign
     if constexpr (C != DT_F32) p.open[i] = (uint8_t)open;
 }
 
-// The marked elements.  A workgroup's (16384 elements) meet in LDS and are
-// evaluated one a thread.  bf16 8192 x 8192: 32 us, about 0.4% of the elements,
-// whose scattered reads and writes bound it.
-constexpr int FIX_CAP = 2048;
+// The marked elements.  A workgroup's meet in LDS and are evaluated one a
+// thread.  bf16 8192 x 8192, about 0.4% of the elements: 32 us, bound by their
+// scattered reads and writes and the evaluation (a quarter of the elements a
+// workgroup, whose one wave with work is then a quarter full: 44).
+constexpr int FIX_N = 16384, FIX_CAP = 2048;   // elements of a workgroup, 64 a thread
 template <int C, int G>
 __global__ __launch_bounds__(256) void gate_fix_kernel(GateGradParams p) {
     __shared__ uint16_t queue[FIX_CAP];
     __shared__ unsigned queued;
-    const int64_t first = (int64_t)blockIdx.x * 16384, bytes = p.n / 8, at = first / 8 + threadIdx.x * 8;
+    const int64_t first = (int64_t)blockIdx.x * FIX_N, bytes = p.n / 8, at = first / 8 + threadIdx.x * 8;
     uint64_t m = 0;
     if (at + 8 <= bytes) {
         m = *(const uint64_t*)(p.open + at);
@@ -183,12 +195,16 @@ __global__ __launch_bounds__(256) void gate_fix_kernel(GateGradParams p) {
 }
 
 template <int C, int G>
-static hipError_t run_gate_grad(const GateGradParams& p, int64_t nb, int64_t nh, hipStream_t s) {
-    hipLaunchKernelGGL((gate_grad_kernel<C, G>), dim3((unsigned)(nb + nh)), dim3(256), 0, s, p, (unsigned)nb);
+static hipError_t run_gate_grad(const GateGradParams& p, int64_t nb, int64_t nh, int64_t nt, hipStream_t s) {
+    const dim3 g((unsigned)(nb + nh + nt));
+    if (p.ntr > 0 && p.tr[0].src_dt == DT_F32)
+        hipLaunchKernelGGL((gate_grad_kernel<C, G, uint32_t>), g, dim3(256), 0, s, p, (unsigned)nb, (unsigned)nh);
+    else
+        hipLaunchKernelGGL((gate_grad_kernel<C, G, uint16_t>), g, dim3(256), 0, s, p, (unsigned)nb, (unsigned)nh);
     hipError_t e = hipGetLastError();
     if constexpr (C != DT_F32) {
         if (e == hipSuccess && nb > 0) {
-            hipLaunchKernelGGL((gate_fix_kernel<C, G>), dim3((unsigned)((p.n + 16383) / 16384)), dim3(256), 0, s, p);
+            hipLaunchKernelGGL((gate_fix_kernel<C, G>), dim3((unsigned)((p.n + FIX_N - 1) / FIX_N)), dim3(256), 0, s, p);
             e = hipGetLastError();
         }
     }
@@ -199,13 +215,20 @@ hipError_t launch_gate_grad(int c_dt, const GateGradParams& p, hipStream_t s) {
     const int64_t nb = (p.n / 8 + 255) / 256;
     const int64_t per = p.r_pad * (c_dt == DT_F32 ? 4 : 2) / 16;
     const int64_t nh = p.h != nullptr ? (p.M * per + 255) / 256 : 0;
-    if (p.n % 8 != 0 || nb + nh >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
-    if (nb + nh == 0) return hipSuccess;
+    int64_t nt = 0;
+    if (p.ntr < 0 || p.ntr > 4) return hipErrorInvalidValue;
+    for (int i = 0; i < p.ntr; ++i) {
+        if ((p.tr[i].src_dt == DT_F32) != (p.tr[0].src_dt == DT_F32)) return hipErrorInvalidValue;
+        nt += transpose_tiles(p.tr[i]);
+    }
+    if (p.n % 8 != 0 || nb + nh + nt >= ((int64_t)1 << 31)) return hipErrorInvalidValue;
+    if (nb + nh + nt == 0) return hipSuccess;
     const bool f32 = p.dy_dt == DT_F32;
-    if (c_dt == DT_F32) return run_gate_grad<DT_F32, DT_F32>(p, nb, nh, s);
+    if (c_dt == DT_F32) return run_gate_grad<DT_F32, DT_F32>(p, nb, nh, nt, s);
     if (p.open == nullptr) return hipErrorInvalidValue;
-    if (c_dt == DT_F16) return f32 ? run_gate_grad<DT_F16, DT_F32>(p, nb, nh, s) : run_gate_grad<DT_F16, DT_F16>(p, nb, nh, s);
-    return f32 ? run_gate_grad<DT_BF16, DT_F32>(p, nb, nh, s) : run_gate_grad<DT_BF16, DT_BF16>(p, nb, nh, s);
+    if (c_dt == DT_F16)
+        return f32 ? run_gate_grad<DT_F16, DT_F32>(p, nb, nh, nt, s) : run_gate_grad<DT_F16, DT_F16>(p, nb, nh, nt, s);
+    return f32 ? run_gate_grad<DT_BF16, DT_F32>(p, nb, nh, nt, s) : run_gate_grad<DT_BF16, DT_BF16>(p, nb, nh, nt, s);
 }
 
 }  // namespace lyc

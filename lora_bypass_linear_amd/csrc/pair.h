@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "bwd.h"
+
 namespace lyc {
 
 // both projections' launches at once (hpass.hip, prep.hip)
@@ -84,6 +86,10 @@ struct GateGradParams {
     int64_t M;
     int r_pad;
     uint8_t* open;              // 16-bit compute: [n / 8] marks of the elements left to 64 bits
+    // up to four transposed copies made by workgroups of the same launch (sources
+    // all of 16 or all of 32 bits)
+    TransposeParams tr[4];
+    int ntr;
 };
 hipError_t launch_gate_grad(int c_dt, const GateGradParams& p, hipStream_t s);
 
