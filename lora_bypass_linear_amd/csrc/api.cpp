@@ -969,7 +969,7 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
 
 // ---- gated feed-forward block ----------------------------------------------------
 // Two LoRA problems that share x, every size and every dtype.  h of both is one
-// [M][2 r_pad] array (gate's columns first), from one pass over x.
+// [M][2 r_pad] array (gate's columns first), from one launch.
 struct GatedLayout {
     size_t xc = 0, wc[2] = {0, 0}, dc = 0, dh = 0, dl = 0, uc[2] = {0, 0}, h = 0, dnorm = 0, flagged = 0, partial = 0,
            total = 0;
@@ -1086,27 +1086,34 @@ int pair_h(const Problem& P, const PairH& H, const float* const (&cast_src)[3], 
                    ? LYC_OK
                    : LYC_ERR_HIP;
     }
-    // one pass over x for both while their columns fit it
-    const int passes = 2 * P.r_pad <= MAX_RANK ? 1 : 2;
-    for (int i = 0; i < passes; ++i) {
-        lyc::XrParams hp{};
-        hp.x = H.x;
-        hp.b = (split ? H.dh : H.dc) + i * half;
-        hp.b_lo = split ? (const void*)(H.dl + i * half) : nullptr;
-        hp.b_full = H.dc + i * half;
-        hp.bnorm = H.dnorm + i * P.r_pad;
-        hp.M = P.M;
-        hp.Nc = passes == 1 ? 2 * P.r_pad : P.r_pad;
-        hp.K = P.K;
-        hp.guard = P.c_dt != LYC_F32 ? 1 : 0;
-        hp.flagged = H.flagged;
-        hp.mode = lyc::XR_H;
-        hp.out = (char*)H.h + (size_t)(i * P.r_pad) * esize(P.c_dt);
-        hp.ld_out = 2 * P.r_pad;
-        hp.scale = 1.0;
-        if (timed(LYC_KERNEL_HPASS, s, [&] { return lyc::launch_xr(P.c_dt, hp, s); }) != hipSuccess) return LYC_ERR_HIP;
+    lyc::XrParams hp[2];
+    // One pass of twice the columns reads x once; two in one launch have twice the
+    // workgroups.  Measured (us, bf16, one | two): M 8192, K 4096: rank 16 33 | 38, 32 38 |
+    // 64, 64 62 | 59, 128 149 | 87; M 16384, K 8192: rank 64 172 | 222, 128 331 | 340; M 2048,
+    // K 4096: rank 16 21 | 16, 64 55 | 29; M 517: rank 16 21 | 15.
+    const bool one = 2 * P.r_pad <= MAX_RANK && P.M >= (P.r_pad <= 32 ? 4096 : 16384);
+    for (int i = 0; i < 2; ++i) {
+        hp[i] = lyc::XrParams{};
+        hp[i].x = H.x;
+        hp[i].b = (split ? H.dh : H.dc) + i * half;
+        hp[i].b_lo = split ? (const void*)(H.dl + i * half) : nullptr;
+        hp[i].b_full = H.dc + i * half;
+        hp[i].bnorm = H.dnorm + i * P.r_pad;
+        hp[i].M = P.M;
+        hp[i].Nc = one ? 2 * P.r_pad : P.r_pad;
+        hp[i].K = P.K;
+        hp[i].guard = P.c_dt != LYC_F32 ? 1 : 0;
+        hp[i].flagged = H.flagged;
+        hp[i].mode = lyc::XR_H;
+        hp[i].out = (char*)H.h + (size_t)(i * P.r_pad) * esize(P.c_dt);
+        hp[i].ld_out = 2 * P.r_pad;
+        hp[i].scale = 1.0;
     }
-    return LYC_OK;
+    return timed(LYC_KERNEL_HPASS, s, [&] {
+               return one ? lyc::launch_xr(P.c_dt, hp[0], s) : lyc::launch_xr2(P.c_dt, hp[0], hp[1], s);
+           }) == hipSuccess
+               ? LYC_OK
+               : LYC_ERR_HIP;
 }
 
 bool bad_scale(double scale) { return !(scale == scale) || scale > 3.4e38 || scale < -3.4e38; }

@@ -981,6 +981,7 @@ static hipError_t run_xr_ct(const XrParams& p, hipStream_t s, const XrParams* se
         }
         return hipErrorInvalidValue;
     }
+    const int64_t rows = second != nullptr ? 2 * p.M : p.M;   // of the launch
     switch (p.Nc) {
     case 16:   // 16-bit compute only (fp32 compute pads the rank to 32)
         if (CT::dt == DT_F32) return hipErrorInvalidValue;
@@ -989,11 +990,11 @@ static hipError_t run_xr_ct(const XrParams& p, hipStream_t s, const XrParams* se
     case 64:
         // one wave per 16 rows x all 64 columns where M fills the GPU with
         // 32- or 64-row workgroups (the x split is done once per row)
-        if (p.M >= 256 * 64) return run_xr<CT, 4, 2, 1, 4>(p, s, second);
-        if (p.M >= 256 * 32) return run_xr<CT, 4, 4, 1, 2>(p, s, second);
+        if (rows >= 256 * 64) return run_xr<CT, 4, 2, 1, 4>(p, s, second);
+        if (rows >= 256 * 32) return run_xr<CT, 4, 4, 1, 2>(p, s, second);
         return run_xr_jb<CT, 2, 2, 4>(p, s, second);
     case 128:
-        if (p.M >= 256 * 64) return run_xr<CT, 8, 2, 1, 4>(p, s, second);
+        if (rows >= 256 * 64) return run_xr<CT, 8, 2, 1, 4>(p, s, second);
         return run_xr_jb<CT, 4, 2, 2>(p, s, second);
     case 256: return run_xr<CT, 8, 1, 2>(p, s, second);
     default: return hipErrorInvalidValue;
