@@ -46,10 +46,10 @@ __device__ __forceinline__ float act_logistic(float a, float b, float g, float* 
 // The same for 16-bit results: exp2 and the reciprocal as the hardware gives them
 // (an ulp each), the exponent rounded once.  Off by 2^-23 |u| of the result
 // where that is near 0 (negative u) and by a few 2^-24 elsewhere, a 2^-12th of
-// bf16's and a 2^-9th of fp16's rounding at |u| = 8.  No input needs a clamp: exp2 overflows to
-// infinity, whose reciprocal is 0.
+// bf16's and a 2^-9th of fp16's rounding at |u| = 8.  exp2 overflows to infinity,
+// whose reciprocal is 0; only g^2 is kept finite, for b = 0.
 __device__ __forceinline__ float act_logistic16(float a, float b, float g) {
-    const float u = g * __builtin_fmaf(b, g * g, a);
+    const float u = g * __builtin_fmaf(b, __builtin_fminf(g * g, 1e30f), a);
     return g * __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(u * -1.44269502f));
 }
 
@@ -61,7 +61,7 @@ __device__ __forceinline__ float act_logistic16(float a, float b, float g) {
 // that q = e r is 1, not a product of infinity and 0, where p is 0.
 __device__ __forceinline__ float act_logistic16_grad(float a, float b, float g, float* slope, float* mass,
                                                      float* n_act, float* n_slope) {
-    const float g2 = g * g, u = g * __builtin_fmaf(b, g2, a);
+    const float g2 = __builtin_fminf(g * g, 1e30f), u = g * __builtin_fmaf(b, g2, a);
     const float e = __builtin_fminf(__builtin_amdgcn_exp2f(u * -1.44269502f), 3e38f);
     const float p = __builtin_amdgcn_rcpf(1.f + e), v = g * p;
     const float t = v * (e * p) * __builtin_fmaf(3.f * b, g2, a);

@@ -27,31 +27,32 @@ bool pair_wide(int64_t N) { return N >= 32 * device_rates().cus; }
 //             8 and 16 bits          fp32
 //   256 x 256    0.8, 1.42  fixed 12.5     --
 //   128 x 128    0.37, 0.53       5      2.0, 2.2
+//   128 x 96         --                  1.5, 1.8     5
 //   64 x 64      0.22, 0.37       5      0.5, 1.06
 // Whole calls, the pick and what it is held against: int8 product 777 x 4104 x
 // 4112 128 x 128 25.9, 64 x 64 39.5, 256 x 256 in two splits 45.5; 512 x 512 x 8192
 // 64 x 64 in 4 splits 13.7, in one 21.5; bf16 block 777 x 4096 x 4096 128 x 128
 // 67.2, 256 x 256 80.3; 256 x 4096 x 4096 64 x 64 28.7, 128 x 128 33.0; fp32 block 200 x
-// 512 x 4096 64 x 64 in 4 splits 32.2, in one 83.7.
+// 512 x 4096 64 x 64 in 4 splits 32.2, in one 83.7; 517 x 2056 x 1032 128 x 96 75.9, 64 x
+// 64 79.4.
 PairPlan pair_plan(int mode, int c_dt, int64_t M, int64_t N, int64_t K) {
     const int es = c_dt == DT_F32 ? 4 : c_dt == DT_I8 ? 1 : 2;
     const int two = mode == PAIR_PAIR ? 2 : 1;
     if (M <= 0 || N <= 0) return PairPlan{0, 0, 1};
     if (pair_skinny(M, K, es)) return PairPlan{two == 1 && pair_wide(N) ? 32 : 16, M <= 16 ? 16 : 32, 1};
     struct C {
-        int t, per_cu;
+        int a, t, per_cu;   // rows of A and of B, workgroups a CU holds
         double fixed, empty, full;
     };
-    const C cands[2][3] = {{{256, 1, 12.5, 0.8, 1.42}, {128, 1, 5.0, 0.37, 0.53}, {64, 2, 5.0, 0.22, 0.37}},
-                           {{0, 1, 0, 0, 0}, {128, 1, 5.0, 2.0, 2.2}, {64, 2, 5.0, 0.5, 1.06}}};
+    const C cands[2][3] = {{{256, 256, 1, 12.5, 0.8, 1.42}, {128, 128, 1, 5.0, 0.37, 0.53}, {64, 64, 2, 5.0, 0.22, 0.37}},
+                           {{128, 128, 1, 5.0, 2.0, 2.2}, {96, 128, 1, 5.0, 1.5, 1.8}, {64, 64, 2, 5.0, 0.5, 1.06}}};
     const double cus = (double)device_rates().cus;
     const int64_t steps1 = (K * es + 127) / 128;
     const double segs = mode == PAIR_SEQ ? 2.0 : 1.0;
     PairPlan best{64 / two, 64, 1};
     double best_t = 1e300;
     for (const C& c : cands[c_dt == DT_F32 ? 1 : 0]) {
-        if (c.t == 0) continue;
-        const int tf = c.t / two;
+        const int tf = c.a / two;
         const double tiles = (double)((N + tf - 1) / tf) * (double)((M + c.t - 1) / c.t);
         for (int ks = 1; ks <= 8; ks *= 2) {
             const double part = (double)M * (double)N * 4.0 * two * ks;

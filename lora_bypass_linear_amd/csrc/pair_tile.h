@@ -186,7 +186,9 @@ template <class TL, int MODE, int ES, class F>
 __device__ __forceinline__ void store_tile(char* smem, F val, void* y, int y_dt, int64_t M, int64_t N, int64_t n0,
                                            int64_t m0, int wave, int lane, int wn, int wm) {
     using SH = PairShape<TL, MODE>;
-    constexpr int RB = SH::TF * ES, CHR = RB / 16, SW = CHR < 8 ? CHR - 1 : 7;
+    // (chunks are permuted within a row by its low bits, 8 or 4 of them)
+    constexpr int RB = SH::TF * ES, CHR = RB / 16, SW = CHR % 8 == 0 ? 7 : 3;
+    static_assert(CHR % 4 == 0, "permuted chunks");
     constexpr int CAP = TL::NS * TL::STAGE;
     constexpr int TMP = TL::TM * RB <= CAP ? TL::TM : TL::TM / 2;   // rows per pass
     constexpr int PASSES = TL::TM / TMP, IT = TMP * CHR / TL::NT;
@@ -672,6 +674,7 @@ __global__ __launch_bounds__(64 * NW) void pair_skinny_kernel(PairParams p) {
 
 using PairL = Tile<256, 256, 128, 64, 2, 128>;   // 8 waves, 128 KiB of stages
 using PairM = Tile<128, 128, 64, 32, 4, 128>;    // 8 waves, 128 KiB
+using PairF = Tile<96, 128, 96, 32, 4, 128>;     // 4 waves, 112 KiB: fp32 only
 using PairS = Tile<64, 64, 32, 32, 4, 128>;      // 4 waves, 64 KiB
 
 template <class CT, class TL, int MODE>
@@ -720,6 +723,9 @@ hipError_t run_pair_ct(const PairParams& p, hipStream_t s) {
     if (p.ksplit > 1 && p.partial == nullptr) return hipErrorInvalidValue;
     if constexpr (CT::dt != DT_F32) {
         if (pl.tile_m == 256) return run_pair<CT, PairL, MODE>(p, s);
+    }
+    if constexpr (CT::dt == DT_F32) {
+        if (pl.tile_m == 128 && pl.tile_n == PairShape<PairF, MODE>::TF) return run_pair<CT, PairF, MODE>(p, s);
     }
     if (pl.tile_m == 128) return run_pair<CT, PairM, MODE>(p, s);
     return run_pair<CT, PairS, MODE>(p, s);

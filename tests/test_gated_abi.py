@@ -107,17 +107,20 @@ def test_binding_checks():
 
 
 def test_cases_reach_every_path():
-    """(tile rows, whether K is split, whether compute is fp32) of the GPU tests' sizes"""
+    """(tile features, tile rows, whether K is split, whether compute is fp32) of the GPU tests' sizes"""
     def seen(cases, backward):
         out = set()
         for M, N, K, r, *dts in cases:
             c, _ = L.resolve_dtypes([L._CODE[t] for t in dts if isinstance(t, torch.dtype)])
-            _, tm, ks = L.lora_gated_plan(M, N, K, c, backward)
-            out.add((tm, ks > 1, c == L.F32))
+            tn, tm, ks = L.lora_gated_plan(M, N, K, c, backward)
+            out.add((tn, tm, ks > 1, c == L.F32))
         return out
-    every = {(16, False, False), (32, False, False), (64, False, False), (64, True, False), (128, False, False),
-             (256, False, False), (16, False, True), (32, False, True), (64, False, True), (64, True, True),
-             (128, False, True)}
     f, b = seen(FORWARD, False), seen(BACKWARD, True)
-    assert every <= f, every - f
-    assert every <= b, every - b
+    for w in (1, 2):   # features of a forward tile are half its weight rows
+        every = {(64 // w, 64, False, False), (64 // w, 64, True, False), (128 // w, 128, False, False),
+                 (256 // w, 256, False, False), (64 // w, 64, False, True), (64 // w, 64, True, True),
+                 (96 // w, 128, False, True), (128 // w, 128, False, True), (16, 16, False, False), (16, 32, False, False),
+                 (16, 16, False, True), (16, 32, False, True)}
+        have = f if w == 2 else b
+        assert every <= have, (w, every - have)
+    assert {(32, 16, False, False), (32, 32, False, False)} <= b

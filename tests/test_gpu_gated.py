@@ -52,6 +52,7 @@ FORWARD = [
     (200, 333, 264, 40, F32, F32, F32, F32, "gelu_tanh"), (517, 2056, 136, 5, F32, F32, F32, None, "silu"),
     (40, 64, 4096, 16, F32, F32, F32, None, "silu"), (50, 72, 0, 4, BF16, BF16, BF16, BF16, "silu"),
     (3, 72, 0, 0, F16, F16, F16, F16, "silu"), (1100, 1101, 264, 7, F16, F16, F16, None, "silu"),
+    (1024, 2048, 264, 3, F32, F32, F32, None, "silu"),
 ]
 
 
@@ -142,6 +143,20 @@ def test_values_that_are_not_finite():
         assert torch.equal(y[keep], clean[keep])
 
 
+@pytest.mark.parametrize("act", ["silu", "gelu", "gelu_tanh"])
+@pytest.mark.parametrize("dt", [BF16, F32])
+def test_an_infinite_gate(act, dt):
+    """act(inf) is inf; -inf times 0 is a NaN, as in the formulas."""
+    say("infinite gate", act, dt)
+    for M in (3, 70):
+        t = _inputs(M, 64, 64, 2, dt, dt, dt, dt)
+        t["bias_gate"][5], t["bias_gate"][6] = float("inf"), -float("inf")
+        y = L.lora_gated_linear(*_args(t), 1.0, t["bias_gate"], t["bias_value"], activation=act)
+        v = R.project(t["x"], t["w_value"], t["down_value"], t["up_value"], 1.0, t["bias_value"], dt)[0]
+        assert torch.equal(y[:, 5].double(), float("inf") * torch.sign(v[:, 5])) and torch.isnan(y[:, 6]).all()
+        assert torch.isfinite(y[:, :5]).all() and torch.isfinite(y[:, 7:]).all()
+
+
 # rows, features, K, rank, x, W, factors' and dy's dtypes, activation, what is given
 BACKWARD = [
     (1, 8, 8, 1, F16, F16, F16, F16, "silu", "wh"), (1, 1032, 520, 16, BF16, BF16, BF16, BF16, "silu", "wh"),
@@ -156,7 +171,7 @@ BACKWARD = [
     (200, 328, 264, 40, F32, F32, F32, F32, "gelu_tanh", "wh"), (517, 136, 1032, 200, F32, F32, F32, F32, "silu", ""),
     (64, 2048, 72, 16, BF16, BF16, BF16, BF16, "silu", "wh"), (1500, 264, 1544, 20, BF16, BF16, BF16, BF16, "silu", "wh"),
     (1030, 72, 2056, 40, F32, F32, F32, F32, "gelu", "w"), (5, 72, 8200, 8, F16, F16, F16, F16, "silu", "wh"),
-    (20, 72, 8200, 40, BF16, BF16, F32, F32, "gelu_tanh", ""),
+    (20, 72, 8200, 40, BF16, BF16, F32, F32, "gelu_tanh", ""), (1024, 136, 4096, 16, F32, F32, F32, F32, "silu", "w"),
 ]
 
 
