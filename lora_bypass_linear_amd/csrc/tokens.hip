@@ -11,7 +11,7 @@
 // per product; the rank side, re-read by every workgroup, comes from L2.  Few
 // columns leave CUs idle, so the tokens are split too; the splits' fp32 sums are
 // added in split order by a second kernel.  Bound by the wide sides' bytes: bf16
-// 8192 tokens, 4096 and 8192 columns, rank 64: 95 us for all four (4.2 TB/s) and 10
+// 8192 tokens, 4096 and 8192 columns, rank 64: 92 us for all four (4.4 TB/s) and 10
 // for the join; as four GEMM launches with their reductions 135 us.
 #include "kernels.h"
 #include "lyc_device.h"
@@ -192,7 +192,7 @@ hipError_t launch_tokens(int c_dt, const TokenJob* jobs, int n, int64_t M, float
     for (int i = 0; i < n; ++i) {
         const TokenJob& j = jobs[i];
         if (j.C % 8 != 0 || j.r < 1 || j.r > 256 || j.r != jobs[0].r || j.ldr % 8 != 0 ||
-            M * j.C * 2 >= ((int64_t)1 << 30) || M * j.ldr * 2 >= ((int64_t)1 << 30))
+            M * j.C * 2 >= ((int64_t)1 << 30) || M * j.ldr * 2 > ((int64_t)1 << 30))   // (the longest batch: h's rows at 1 GiB)
             return hipErrorInvalidValue;
         p.job[i] = j;
         p.at[i] = p.total;

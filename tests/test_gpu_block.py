@@ -204,3 +204,23 @@ def test_backward_past_one_gibibyte():
         part = d @ t["w_" + n].double() + gh @ t["down_" + n].double()
         dx = part if i == 0 else dx + part
     assert torch.linalg.norm(got[0].double() - dx) <= 1.5 * R.U[BF16] * torch.linalg.norm(dx)
+
+
+def test_factor_gradients_of_the_longest_batch():
+    """2^20 tokens at the largest rank: the kept h is then 1 GiB, its rows the farthest apart."""
+    M, N, K, r, scale = 1 << 20, 16, 8, 255, 1.5
+    say("longest batch", M, N, K, r)
+    t = _inputs(M, N, K, r, BF16, BF16, BF16)
+    _, gate, value, h = L.lora_gated_linear(*_args(t), scale, keep=True)
+    assert h.numel() * 2 == 1 << 30
+    dy = _rand(9, M, N).to(BF16)
+    got = L.lora_gated_linear_backward(*_args(t), scale, dy, gate, value, h=h, want_dx=False)
+    rp = R.r_pad(r, BF16)
+    for i, n in enumerate(("gate", "value")):
+        a, slope = R.act("silu", gate.double())
+        d = R.nearest(dy.double() * (value.double() * slope if i == 0 else a), BF16)
+        ref = scale * (d.t() @ h[:, i * rp:i * rp + r].double())
+        assert torch.linalg.norm(got[2 + 2 * i].double() - ref) <= 1.5 * R.U[BF16] * torch.linalg.norm(ref)
+        gh = R.nearest(scale * (d @ t["up_" + n].double()), BF16)
+        ref = gh.t() @ t["x"].double()
+        assert torch.linalg.norm(got[1 + 2 * i].double() - ref) <= 1.5 * R.U[BF16] * torch.linalg.norm(ref)
