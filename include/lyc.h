@@ -508,8 +508,9 @@ int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const flo
  *    it): h_r of gate in columns 0 .., of value in columns r_pad .., zeros from
  *    the rank on.  Nothing is written there for rank == 0.
  *  - No output may overlap an input, the workspace or another output
- *    (LYC_ERR_INVALID_ARG).  M * N <= 2^40 (LYC_ERR_UNSUPPORTED); everything
- *    else, the workspace (lyc_lora_gated_workspace_size) and errors as
+ *    (LYC_ERR_INVALID_ARG).  One launch covers y: sizes whose tiles need 2^32
+ *    threads or more (N = 2^28 for few rows; far past the memory otherwise) are
+ *    LYC_ERR_UNSUPPORTED, with a rank M > 2^26 too.  Everything else, the workspace (lyc_lora_gated_workspace_size) and errors as
  *    lyc_lora_linear_fwd.
  * lyc_lora_gated_plan (host only): output tile (features x rows) and K split of
  * the block's product, or with backward = 1 of dx's (N and K as the forward's);
@@ -569,8 +570,8 @@ int lyc_lora_gated_bwd(const void* x, int x_dt, const void* w_gate, const void* 
  *   fp32 once, times s_w, then one fused multiply-add with s_x and b.
  * lyc_int8_gated_fwd: the gated block over such weights, y = round_out( act(g) *
  *   v ) with g and v as above before their rounding, in one kernel.
- *  - K a multiple of 16, at most 131056; M, N <= 2^30, M * N <= 2^40
- *    (LYC_ERR_UNSUPPORTED).  x and codes 16-byte aligned.  y_dt and the bias's
+ *  - K a multiple of 16, at most 131056; M, N <= 2^30 and, of the products, sizes
+ *    that one launch covers, as lyc_lora_gated_fwd (else LYC_ERR_UNSUPPORTED).  x and codes 16-byte aligned.  y_dt and the bias's
  *    dtype are the caller's choice (8-bit operands enter no dtype policy).
  *    Outputs and workspace must not overlap inputs or each other
  *    (LYC_ERR_INVALID_ARG).  Scales are read, and written by the quantization,

@@ -978,9 +978,6 @@ struct GatedLayout {
     int ksplit = 1;
 };
 
-// y and the kept projections are addressed by tiles: their count fits a grid
-bool grid_fits(int64_t M, int64_t N) { return (double)M * (double)N <= 1099511627776.0; }   // 2^40
-
 GatedLayout gated_layout(const Problem& P, bool h_given) {
     GatedLayout L;
     size_t off = 0;
@@ -1135,7 +1132,9 @@ int check_gated(Problem& P, int act) {
     const int st = check_problem(P);
     if (st != LYC_OK) return st;
     if (act < 0 || act >= lyc::ACT_COUNT) return LYC_ERR_INVALID_ARG;
-    return grid_fits(P.M, P.N) ? LYC_OK : LYC_ERR_UNSUPPORTED;
+    // the h pass has up to 32 threads a token, and a launch fewer than 2^32
+    if (P.rank > 0 && P.M > ((int64_t)1 << 26)) return LYC_ERR_UNSUPPORTED;
+    return lyc::pair_fits(lyc::PAIR_PAIR, P.c_dt, P.M, P.N, P.K) ? LYC_OK : LYC_ERR_UNSUPPORTED;
 }
 
 int gated_forward(const Problem& P, const void* x, const void* const (&w)[2], const void* const (&bias)[2],
@@ -2034,15 +2033,15 @@ int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const flo
 // ---- 8-bit integers -------------------------------------------------------------------
 
 // 16-byte rows of codes, exact 32-bit sums of products of up to 128 * 128
-static int check_int8(int64_t M, int64_t N, int64_t K) {
+static int check_int8(int mode, int64_t M, int64_t N, int64_t K) {
     if (M < 0 || N < 0 || K < 0) return LYC_ERR_INVALID_ARG;
     if (M > MAX_DIM || N > MAX_DIM || K > 131056 || K % 16 != 0) return LYC_ERR_UNSUPPORTED;
-    return grid_fits(M, N) ? LYC_OK : LYC_ERR_UNSUPPORTED;
+    return lyc::pair_fits(mode, lyc::DT_I8, M, N, K) ? LYC_OK : LYC_ERR_UNSUPPORTED;
 }
 
 int lyc_int8_quantize_rows(const void* x, int x_dt, void* q, float* s, int64_t M, int64_t K, void* stream) {
     if (!valid_dt(x_dt)) return LYC_ERR_INVALID_ARG;
-    const int st = check_int8(M, 0, K);
+    const int st = check_int8(lyc::PAIR_ONE, M, 0, K);
     if (st != LYC_OK) return st;
     if (M == 0) return LYC_OK;
     if (s == nullptr || (K > 0 && (x == nullptr || q == nullptr))) return LYC_ERR_INVALID_ARG;
@@ -2064,7 +2063,7 @@ static size_t int8_workspace(int mode, int64_t M, int64_t N, int64_t K) {
 }
 
 static int int8_plan(int mode, int64_t M, int64_t N, int64_t K, int* tile_n, int* tile_m, int* ksplit) {
-    const int st = check_int8(M, N, K);
+    const int st = check_int8(mode, M, N, K);
     if (st != LYC_OK) return st;
     const lyc::PairPlan p = lyc::pair_plan(mode, lyc::DT_I8, M, N, K);
     if (tile_n) *tile_n = p.tile_n;
@@ -2078,7 +2077,7 @@ static int int8_forward(int mode, const void* q_x, const float* s_x, const void*
                         const float* const (&s_w)[2], const void* const (&bias)[2], int bias_dt, int act, void* y,
                         int y_dt, int64_t M, int64_t N, int64_t K, void* workspace, size_t workspace_bytes,
                         void* stream) {
-    const int st = check_int8(M, N, K);
+    const int st = check_int8(mode, M, N, K);
     if (st != LYC_OK) return st;
     const int H = mode == lyc::PAIR_PAIR ? 2 : 1;
     if (!valid_dt(y_dt) || (bias_dt != 0 && !valid_dt(bias_dt))) return LYC_ERR_INVALID_ARG;
@@ -2128,7 +2127,7 @@ static int int8_forward(int mode, const void* q_x, const float* s_x, const void*
 }
 
 int lyc_int8_linear_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
-    const int st = check_int8(M, N, K);
+    const int st = check_int8(lyc::PAIR_ONE, M, N, K);
     if (st != LYC_OK) return st;
     if (bytes) *bytes = int8_workspace(lyc::PAIR_ONE, M, N, K);
     return LYC_OK;
@@ -2149,7 +2148,7 @@ int lyc_int8_linear_fwd(const void* q_x, const float* s_x, const void* q_w, cons
 }
 
 int lyc_int8_gated_workspace_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
-    const int st = check_int8(M, N, K);
+    const int st = check_int8(lyc::PAIR_PAIR, M, N, K);
     if (st != LYC_OK) return st;
     if (bytes) *bytes = int8_workspace(lyc::PAIR_PAIR, M, N, K);
     return LYC_OK;
@@ -2184,7 +2183,8 @@ int lyc_lora_gated_workspace_size(int64_t M, int64_t N, int64_t K, int64_t rank,
 int lyc_lora_gated_plan(int64_t M, int64_t N, int64_t K, int compute_dt, int backward, int* tile_n, int* tile_m,
                         int* ksplit) {
     if (M < 0 || N < 0 || K < 0 || !valid_dt(compute_dt) || (backward != 0 && backward != 1)) return LYC_ERR_INVALID_ARG;
-    if (M > MAX_DIM || N > MAX_DIM || K > MAX_K || K % 8 != 0 || !grid_fits(M, N)) return LYC_ERR_UNSUPPORTED;
+    if (M > MAX_DIM || N > MAX_DIM || K > MAX_K || K % 8 != 0) return LYC_ERR_UNSUPPORTED;
+    if (backward ? M > MAX_K || N > MAX_K : !lyc::pair_fits(lyc::PAIR_PAIR, compute_dt, M, N, K)) return LYC_ERR_UNSUPPORTED;
     const lyc::PairPlan p = backward ? lyc::pair_plan(lyc::PAIR_SEQ, compute_dt, M, K, N)
                                      : lyc::pair_plan(lyc::PAIR_PAIR, compute_dt, M, N, K);
     if (tile_n) *tile_n = p.tile_n;

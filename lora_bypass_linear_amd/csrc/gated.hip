@@ -30,7 +30,7 @@ bool pair_wide(int64_t N) { return N >= 32 * device_rates().cus; }
 //   128 x 96         --                  1.5, 1.8     5
 //   64 x 64      0.22, 0.37       5      0.5, 1.06
 // Whole calls, the pick and what it is held against: int8 product 777 x 4104 x
-// 4112 128 x 128 25.9, 64 x 64 39.5, 256 x 256 in two splits 45.5; 512 x 512 x 8192
+// 4112 128 x 128 24.4, 64 x 64 39.5, 256 x 256 in two splits 45.5; 512 x 512 x 8192
 // 64 x 64 in 4 splits 13.7, in one 21.5; bf16 block 777 x 4096 x 4096 128 x 128
 // 67.2, 256 x 256 80.3; 256 x 4096 x 4096 64 x 64 28.7, 128 x 128 33.0; fp32 block 200 x
 // 512 x 4096 64 x 64 in 4 splits 32.2, in one 83.7; 517 x 2056 x 1032 128 x 96 75.9, 64 x
@@ -69,6 +69,13 @@ PairPlan pair_plan(int mode, int c_dt, int64_t M, int64_t N, int64_t K) {
         }
     }
     return best;
+}
+
+bool pair_fits(int mode, int c_dt, int64_t M, int64_t N, int64_t K) {
+    if (M <= 0 || N <= 0) return true;
+    const PairPlan p = pair_plan(mode, c_dt, M, N, K);
+    const int64_t wgs = ((N + p.tile_n - 1) / p.tile_n) * ((M + p.tile_m - 1) / p.tile_m);
+    return wgs * (p.tile_m >= 128 ? 512 : 256) < ((int64_t)1 << 32);
 }
 
 hipError_t launch_gated(int c_dt, const PairParams& p, hipStream_t s);

@@ -57,6 +57,8 @@ struct PairPlan {
     int tile_n, tile_m, ksplit;   // features x rows
 };
 PairPlan pair_plan(int mode, int c_dt, int64_t M, int64_t N, int64_t K);
+// a launch holds fewer than 2^32 threads a grid dimension
+bool pair_fits(int mode, int c_dt, int64_t M, int64_t N, int64_t K);
 
 // c_dt: DT_F16, DT_BF16, DT_F32 (PAIR, SEQ) or DT_I8 (ONE, PAIR)
 hipError_t launch_pair(int mode, int c_dt, const PairParams& p, hipStream_t s);

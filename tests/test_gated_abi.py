@@ -124,3 +124,13 @@ def test_cases_reach_every_path():
         have = f if w == 2 else b
         assert every <= have, (w, every - have)
     assert {(32, 16, False, False), (32, 32, False, False)} <= b
+
+
+def test_sizes_that_one_launch_covers():
+    assert L.lora_gated_workspace_size(1 << 26, 8, 8, 4, 2, 2, 0, 2, 2) > 0
+    assert L.lora_gated_workspace_size((1 << 26) + 1, 8, 8, 0, 2, 2, 0, 2, 2) == 0
+    for args in (((1 << 26) + 1, 8, 8, 4), (1, 1 << 29, 8, 0), (1 << 30, 1 << 20, 8, 0)):
+        with pytest.raises(L.LycError):
+            L.lora_gated_workspace_size(*args, 2, 2, 0, 2, 2)
+    with pytest.raises(L.LycError):
+        L.lora_gated_plan(1, 1 << 29, 8, 2)

@@ -143,3 +143,32 @@ def test_empty():
     z = lambda *s, dt=torch.int8: torch.zeros(*s, dtype=dt, device="cuda")
     assert L.int8_linear(z(0, 32), z(0, dt=F32), z(8, 32), z(8, dt=F32)).shape == (0, 8)
     assert L.int8_gated_linear(z(4, 32), z(4, dt=F32), z(0, 32), z(0, dt=F32), z(0, 32), z(0, dt=F32)).shape == (4, 0)
+
+
+@pytest.mark.parametrize("M", [1, 3, 4, 6, 1001])
+@pytest.mark.parametrize("K", [16, 112, 1008, 1024, 1040])
+@pytest.mark.parametrize("dt", [F16, BF16, F32])
+def test_short_rows(M, K, dt):
+    """One wave a row, and the first length past it: also rows that are not finite."""
+    say("int8 short rows", M, K, dt)
+    x = (_rand(M + K, M, K) * torch.exp(_rand(1, M, 1))).to(dt)
+    q, s = L.int8_quantize_rows(x)
+    qr, sr = R.int8_rows(x)
+    assert torch.equal(s, sr) and torch.equal(q, qr)
+    if M > 2:
+        x[0, K - 1], x[2, 0] = float("nan"), float("-inf")
+        q2, s2 = L.int8_quantize_rows(x)
+        assert bool(torch.isnan(s2[0])) and bool(torch.isinf(s2[2])) and not q2[0].any() and not q2[2].any()
+        assert torch.equal(q2[1], qr[1]) and torch.equal(q2[3:], qr[3:]) and torch.equal(s2[3:], sr[3:])
+
+
+@pytest.mark.parametrize("M,K", [((1 << 24) + 5, 16), ((1 << 26) + 3, 16), ((1 << 22) + 1, 1040)])
+def test_many_rows(M, K):
+    """More rows than one grid dimension has workgroups for, on both kernels."""
+    say("int8 many rows", M, K)
+    x = torch.randint(-100, 101, (M, K), device="cuda", dtype=torch.int8).to(BF16)
+    q, s = L.int8_quantize_rows(x)
+    for rows in (slice(0, 9), slice((1 << 22) - 5, (1 << 22) + 9), slice(M - 9, M)):
+        qr, sr = R.int8_rows(x[rows])
+        assert torch.equal(s[rows], sr) and torch.equal(q[rows], qr)
+    assert bool((q.abs().amax(1)[:: 1 << 10] == 127).all())

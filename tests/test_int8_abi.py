@@ -93,3 +93,13 @@ def test_shapes_reach_every_path():
         seen = {(plan(*s)[1], plan(*s)[2] > 1) for s in SHAPES if s[0] and s[1]}
         assert {(16, False), (32, False), (64, False), (64, True), (128, False), (256, False)} <= seen, seen
     assert {L.int8_linear_plan(*s)[0] for s in SHAPES if 0 < s[0] <= 32 and s[2]} == {16, 32}
+
+
+def test_sizes_that_one_launch_covers():
+    assert L.int8_linear_workspace_size(1, (1 << 28) - 64, 16) == 0
+    for size, plan in ((L.int8_linear_workspace_size, L.int8_linear_plan), (L.int8_gated_workspace_size, L.int8_gated_plan)):
+        for f in (size, plan):
+            with pytest.raises(L.LycError):
+                f(1, 1 << 29, 16)
+            with pytest.raises(L.LycError):
+                f(1 << 30, 1 << 20, 16)
