@@ -34,6 +34,9 @@ SOURCES = {"gemm": ("csrc/gemm.hip", "csrc/fp8.h", "csrc/gemm_tile.h", "csrc/ker
            "merge": ("csrc/merge.hip", "csrc/merge.h", "csrc/lyc_device.h"),
            "fp8": ("csrc/fp8gemm.hip", "csrc/fp8.h", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h"),
            "quant": ("csrc/quant.hip", "csrc/quant_device.h", "csrc/fp8.h", "csrc/kernels.h", "csrc/lyc_device.h"),
+           "gated": ("csrc/gated.hip", "csrc/pair_tile.h", "csrc/act.h", "csrc/pair.h", "csrc/bwd.h", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h"),
+           "gated_bwd": ("csrc/gated_bwd.hip", "csrc/pair_tile.h", "csrc/act.h", "csrc/pair.h", "csrc/bwd.h", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h", "csrc/transpose_device.h"),
+           "int8": ("csrc/int8.hip", "csrc/pair_tile.h", "csrc/act.h", "csrc/pair.h", "csrc/bwd.h", "csrc/gemm_tile.h", "csrc/quant_device.h", "csrc/fp8.h", "csrc/kernels.h", "csrc/lyc_device.h"),
            "ortho": ("csrc/ortho.hip", "csrc/ortho.h", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h")}
 
 
@@ -105,14 +108,14 @@ def traffic(args) -> str:
 
 def mfma(args) -> str:
     """MFMA activity of one kernel from a --pmc run of SQ_VALU_MFMA_BUSY_CYCLES,
-    GRBM_GUI_ACTIVE and SQ_INSTS_VALU_MFMA_MOPS_ of F16, BF16 and F8 (those collected):
+    GRBM_GUI_ACTIVE and SQ_INSTS_VALU_MFMA_MOPS_ of F16, BF16, F8 and I8 (those collected):
     the fraction of SIMD cycles in which the matrix pipe was busy while the
     GPU was active, and the MFMA flops the counters saw (MOPS count units of
     512 flops).  GRBM_GUI_ACTIVE is counted once per XCD (the value is the
     sum over the XCDs' instances), SQ_VALU_MFMA_BUSY_CYCLES once per SIMD."""
     path = _find(args.dir, "counter_collection.csv")
     vals = {}
-    mops = tuple(f"SQ_INSTS_VALU_MFMA_MOPS_{t}" for t in ("F16", "BF16", "F8"))
+    mops = tuple(f"SQ_INSTS_VALU_MFMA_MOPS_{t}" for t in ("F16", "BF16", "F8", "I8"))
     for c in ("SQ_VALU_MFMA_BUSY_CYCLES", "GRBM_GUI_ACTIVE") + mops:
         per = _per_dispatch(path, c)
         ker = [v for n, v in per.values() if args.kernel in n]
