@@ -217,6 +217,16 @@ def _stream(dev) -> int:
     return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device() if dev.index is None else dev.index)
 
 
+def _launch(dev, fn, *args) -> None:
+    """fn(*args, stream) on dev's current stream, with dev the current device
+    meanwhile: a default stream has no device of its own."""
+    if dev.index is None or dev.index == torch.cuda.current_device():
+        _check(fn(*args, _stream(dev)))
+        return
+    with torch.cuda.device(dev):
+        _check(fn(*args, _stream(dev)))
+
+
 def _shape(t: Optional[torch.Tensor], shape, name: str) -> None:
     """Raise ValueError unless t (if given) has exactly this shape.  The C ABI
     takes bare pointers, so a mis-shaped operand would be read (or an output
@@ -1002,10 +1012,10 @@ def lora_gated_linear(x: torch.Tensor, w_gate: torch.Tensor, w_value: torch.Tens
     ws = _workspace(need, dev, workspace)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
     x_dt, w_dt, b_dt, d_dt, u_dt = dts
-    _check(lib().lyc_lora_gated_fwd(_ptr(x), x_dt, _ptr(w_gate), _ptr(w_value), w_dt, _ptr(bias_gate),
-                                    _ptr(bias_value), b_dt, _ptr(down_gate), _ptr(down_value), d_dt, _ptr(up_gate),
-                                    _ptr(up_value), u_dt, r, float(scale), act, _ptr(out), o_dt, _ptr(gate),
-                                    _ptr(value), _ptr(h), M, N, K, _ptr(ws), nbytes, _stream(dev)))
+    _launch(dev, lib().lyc_lora_gated_fwd, _ptr(x), x_dt, _ptr(w_gate), _ptr(w_value), w_dt, _ptr(bias_gate),
+            _ptr(bias_value), b_dt, _ptr(down_gate), _ptr(down_value), d_dt, _ptr(up_gate),
+            _ptr(up_value), u_dt, r, float(scale), act, _ptr(out), o_dt, _ptr(gate),
+            _ptr(value), _ptr(h), M, N, K, _ptr(ws), nbytes)
     return (out, gate, value, h) if keep else out
 
 
@@ -1050,10 +1060,10 @@ def lora_gated_linear_backward(x: torch.Tensor, w_gate: torch.Tensor, w_value: t
     p = lambda t: None if t is None else ctypes.c_void_p(t.data_ptr() if t.numel() else 256)
     wg, wv = (None, None) if given else (_ptr(w_gate), _ptr(w_value))
     gt, vt = (p(w_gate_t), p(w_value_t)) if given else (None, None)
-    _check(lib().lyc_lora_gated_bwd(_ptr(x), x_dt, wg, wv, gt, vt, w_dt, b_dt, _ptr(down_gate), _ptr(down_value), d_dt,
-                                    _ptr(up_gate), _ptr(up_value), u_dt, _ptr(gate), _ptr(value), p(h), r,
-                                    float(scale), act, _ptr(dy), g_dt, p(dx), p(dd[0]), p(dd[1]), p(du[0]), p(du[1]),
-                                    M, N, K, _ptr(ws), nbytes, _stream(dev)))
+    _launch(dev, lib().lyc_lora_gated_bwd, _ptr(x), x_dt, wg, wv, gt, vt, w_dt, b_dt, _ptr(down_gate), _ptr(down_value), d_dt,
+            _ptr(up_gate), _ptr(up_value), u_dt, _ptr(gate), _ptr(value), p(h), r,
+            float(scale), act, _ptr(dy), g_dt, p(dx), p(dd[0]), p(dd[1]), p(du[0]), p(du[1]),
+            M, N, K, _ptr(ws), nbytes)
     return dx, dd[0], du[0], dd[1], du[1]
 
 
@@ -1077,7 +1087,7 @@ def int8_quantize_rows(x: torch.Tensor, q: Optional[torch.Tensor] = None,
     dev = _need_device(x, s, codes=(q,), code_dtype=torch.int8)
     q = torch.empty((M, K), dtype=torch.int8, device=dev) if q is None else q
     s = torch.empty((M,), dtype=torch.float32, device=dev) if s is None else s
-    _check(lib().lyc_int8_quantize_rows(_ptr(x), dtype_code(x), _ptr(q), _ptr(s), M, K, _stream(dev)))
+    _launch(dev, lib().lyc_int8_quantize_rows, _ptr(x), dtype_code(x), _ptr(q), _ptr(s), M, K)
     return q, s
 
 
@@ -1134,8 +1144,8 @@ def int8_linear(q: torch.Tensor, s: torch.Tensor, w_q: torch.Tensor, w_s: torch.
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     ws = _workspace(_int8_need(dev, False, M, N, K), dev, workspace)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(lib().lyc_int8_linear_fwd(_ptr(q), _ptr(s), _ptr(w_q), _ptr(w_s), _ptr(bias), b_dt, _ptr(out), o_dt, M, N,
-                                     K, _ptr(ws), nbytes, _stream(dev)))
+    _launch(dev, lib().lyc_int8_linear_fwd, _ptr(q), _ptr(s), _ptr(w_q), _ptr(w_s), _ptr(bias), b_dt, _ptr(out), o_dt, M, N,
+            K, _ptr(ws), nbytes)
     return out
 
 
@@ -1163,9 +1173,9 @@ def int8_gated_linear(q: torch.Tensor, s: torch.Tensor, gate_q: torch.Tensor, ga
         out = torch.empty((M, N), dtype=out_dtype, device=dev)
     ws = _workspace(_int8_need(dev, True, M, N, K), dev, workspace)
     nbytes = 0 if ws is None else ws.numel() * ws.element_size()
-    _check(lib().lyc_int8_gated_fwd(_ptr(q), _ptr(s), _ptr(gate_q), _ptr(gate_s), _ptr(value_q), _ptr(value_s),
-                                    _ptr(bias_gate), _ptr(bias_value), b_dt, act, _ptr(out), o_dt, M, N, K, _ptr(ws),
-                                    nbytes, _stream(dev)))
+    _launch(dev, lib().lyc_int8_gated_fwd, _ptr(q), _ptr(s), _ptr(gate_q), _ptr(gate_s), _ptr(value_q), _ptr(value_s),
+            _ptr(bias_gate), _ptr(bias_value), b_dt, act, _ptr(out), o_dt, M, N, K, _ptr(ws),
+            nbytes)
     return out
 
 

@@ -134,3 +134,30 @@ def test_sizes_that_one_launch_covers():
             L.lora_gated_workspace_size(*args, 2, 2, 0, 2, 2)
     with pytest.raises(L.LycError):
         L.lora_gated_plan(1, 1 << 29, 8, 2)
+
+
+def test_calls_run_with_the_operands_device_current(monkeypatch):
+    """A default stream (0) belongs to the current device, so another device's operands make theirs current."""
+    import contextlib
+    import inspect
+    import torch
+    entered = []
+
+    @contextlib.contextmanager
+    def device(d):
+        entered.append(d.index)
+        yield
+        entered.append("left")
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(L, "_stream", lambda d: 70 + d.index)
+    got = []
+    fn = lambda *a: got.append((a, list(entered))) or 0
+    L._launch(torch.device("cuda", 0), fn, 5)
+    L._launch(torch.device("cuda", 1), fn, 6)
+    assert got == [((5, 70), []), ((6, 71), [1])] and entered == [1, "left"]
+    with pytest.raises(L.LycError):
+        L._launch(torch.device("cuda", 0), lambda *a: 1)
+    for f in (L.lora_gated_linear, L.lora_gated_linear_backward, L.int8_quantize_rows, L.int8_linear, L.int8_gated_linear):
+        assert "_launch(dev" in inspect.getsource(f)
