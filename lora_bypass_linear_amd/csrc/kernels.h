@@ -139,22 +139,24 @@ hipError_t launch_hdot(int c_dt, const HdotParams& p, hipStream_t s);
 // Compute-dtype copies of down [rank,K] -> [r_pad,K] (+ its hi/lo split per
 // 64-k block and row norms) and up [N,rank] -> [N,r_pad]; zero padding;
 // clears *flagged (if not null); and the fp32 operand casts, in one launch.
+// Every part is optional: r_pad 0 and uc null where there are no factors to
+// prepare, so a fresh one prepares and casts nothing.
 struct PrepParams {
-    const void* down;
-    int down_dt;
-    const void* up;
-    int up_dt;
-    void* dc;
-    void* dh;   // hi part of down_c (16-bit compute), else unused
-    void* dl;   // lo part
-    void* uc;
-    double2* dnorm;   // {|down_c,j|, |lo_j|}
-    int vec;          // down rows start 16-byte aligned: vector loads
-    unsigned* flagged;        // guard counts, all flag_slots of them cleared
+    const void* down = nullptr;
+    int down_dt = 0;
+    const void* up = nullptr;
+    int up_dt = 0;
+    void* dc = nullptr;
+    void* dh = nullptr;   // hi part of down_c (16-bit compute), else unused
+    void* dl = nullptr;   // lo part
+    void* uc = nullptr;
+    double2* dnorm = nullptr;   // {|down_c,j|, |lo_j|}
+    int vec = 0;                // down rows start 16-byte aligned: vector loads
+    unsigned* flagged = nullptr;   // guard counts, all flag_slots of them cleared
     int64_t flag_slots = 1;
-    int64_t N, K, rank;
-    int r_pad;
-    int c_dt;
+    int64_t N = 0, K = 0, rank = 0;
+    int r_pad = 0;
+    int c_dt = 0;
     // fp32 operands narrowed to the 16-bit compute dtype in the same launch
     // (cast_n[i] == 0: none); dst 256-byte aligned
     const float* cast_src[2] = {nullptr, nullptr};
