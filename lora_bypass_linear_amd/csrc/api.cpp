@@ -439,6 +439,7 @@ int forward(const Problem& P, const void* x, const void* w, const void* bias, co
         hp.guard = P.c_dt != LYC_F32 ? 1 : 0;
         hp.flagged = (unsigned*)(W + L.flagged);
         hp.mode = lyc::XR_H;
+        hp.columns(P.rank, P.r_pad);
         hp.out = W + L.h;
         hp.ld_out = P.r_pad;
         hp.scale = 1.0;
@@ -798,6 +799,7 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
         hp.guard = split ? 1 : 0;
         hp.flagged = (unsigned*)(W + L.flag_h);
         hp.mode = lyc::XR_H;
+        hp.columns(P.rank, P.r_pad);
         hp.out = W + L.h;
         hp.ld_out = P.r_pad;
         hp.scale = 1.0;
@@ -853,6 +855,7 @@ int backward(const Bwd& B, const void* x, const void* w, const void* down, const
             gp.guard = split ? 1 : 0;
             gp.flagged = (unsigned*)(W + L.flag_g);
             gp.mode = lyc::XR_H;
+            gp.columns(P.rank, P.r_pad);
             gp.out = W + L.gh;
             gp.ld_out = P.r_pad;
             gp.scale = scale;
@@ -1102,6 +1105,7 @@ int pair_h(const Problem& P, const PairH& H, const float* const (&cast_src)[3], 
         hp[i].guard = P.c_dt != LYC_F32 ? 1 : 0;
         hp[i].flagged = H.flagged;
         hp[i].mode = lyc::XR_H;
+        hp[i].columns(P.rank, P.r_pad);
         hp[i].out = (char*)H.h + (size_t)(i * P.r_pad) * esize(P.c_dt);
         hp[i].ld_out = 2 * P.r_pad;
         hp[i].scale = 1.0;
@@ -1461,6 +1465,7 @@ int gated_backward(const Bwd& B, const void* x, const void* const (&w)[2], const
                 gp[i].guard = split ? 1 : 0;
                 gp[i].flagged = (unsigned*)(W + L.flag_g);
                 gp[i].mode = lyc::XR_H;
+                gp[i].columns(P.rank, P.r_pad);
                 gp[i].out = W + L.gh[i];
                 gp[i].ld_out = P.r_pad;
                 gp[i].scale = scale;

@@ -42,7 +42,9 @@
 // listed output with the value rounded from the fp64 dot product of its x row
 // and b row (products exact, batched 16-byte loads).  fp32 compute, or an
 // fp32 rounding target, needs no guard: a flip there moves the result by
-// 2^-24 relative.
+// 2^-24 relative.  A NaN goes on the list as well: where a block's fp32 sums
+// leave the fp32 range (h above 2^127) or x holds an infinity, infinities of
+// both signs meet in them while the fp64 dot product is an infinity.
 //
 // Work split: a workgroup owns RW*16 rows and RP = 16*JB*CG columns; its
 // waves form RW row groups x KS k groups x CG column groups (k group g takes
@@ -196,6 +198,10 @@ __device__ __forceinline__ uint16_t round16(double v) {
     return CT::dt == DT_F16 ? f64_to_f16(v) : f64_to_bf16(v);
 }
 
+// the bits of the format's infinity
+template <class CT>
+constexpr uint32_t INF16 = CT::dt == DT_F16 ? 0x7c00u : 0x7f80u;
+
 // the projection rounded to the output dtype (exactly, from the fp64 value), as fp32
 template <class CT>
 __device__ __forceinline__ float affine_value(double acc, int out_dt) {
@@ -318,7 +324,8 @@ __device__ __forceinline__ void xr_epilogue(const XrParams& p, double (&acc)[JB]
                 // (the second conversion stays conditional: computed for every
                 // element up front, the 8-block instance runs out of registers)
                 const bool bwide = !(pq[e].x < 1e300);   // a block of b could not be split
-                const bool flag = (guard & row_ok & (jl < cols_wg)) && (wide || bwide || lo != round16<CT>(h + E));
+                const bool nan = (lo & 0x7fffu) > INF16<CT>;
+                const bool flag = (guard & row_ok & (jl < cols_wg)) && (wide || bwide || nan || lo != round16<CT>(h + E));
                 flags |= (uint32_t)flag << (jb * 4 + e);
             }
         }
@@ -341,8 +348,11 @@ __device__ __forceinline__ void xr_epilogue(const XrParams& p, double (&acc)[JB]
                 const int64_t jg = j0 + c0 + jb * 16 + 4 * (lane >> 4);
                 if (CT::dt == DT_F32) {
                     float* hp = (float*)p.out + m * p.ld_out + jg;
-                    *(f32x4*)hp = f32x4{(float)(acc[jb][0] * p.scale), (float)(acc[jb][1] * p.scale),
-                                        (float)(acc[jb][2] * p.scale), (float)(acc[jb][3] * p.scale)};
+                    f32x4 o;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        o[e] = (((int)jg + e) & p.col_mask) < p.cols ? (float)(acc[jb][e] * p.scale) : 0.f;
+                    *(f32x4*)hp = o;
                 } else {
                     uint16_t* hp = (uint16_t*)p.out + m * p.ld_out + jg;
                     *(i32x2*)hp = i32x2{(int)(r16[jb][0] | ((uint32_t)r16[jb][1] << 16)),
@@ -859,7 +869,9 @@ __device__ __forceinline__ void xr_body(const XrParams& p) {
             if (mine && j == 0) {
                 const int64_t m = wg_m0 + row, j = j0 + col;
                 if (p.mode == XR_H) {
-                    ((uint16_t*)p.out)[m * p.ld_out + j] = round16<CT>(d * p.scale);
+                    // (a column past the rank is zero, though a zero row of b times an infinity is not)
+                    const bool real = ((int)j & p.col_mask) < p.cols;
+                    ((uint16_t*)p.out)[m * p.ld_out + j] = round16<CT>(real ? d * p.scale : 0.0);
                 } else {
                     const float bias = p.bias != nullptr ? load_as_f32(p.bias, p.bias_dt, j) : 0.f;
                     const float v = affine_value<CT>(d, p.out_dt) + bias;
@@ -1106,7 +1118,9 @@ __device__ __forceinline__ void hdot_body(const HdotParams& p, int64_t wg, unsig
             if constexpr (CT::dt == DT_F32) cross = (float)(s - E) != (float)(s + E);
             else cross = round16<CT>(s - E) != round16<CT>(s + E);
             v = s;
-            if (cross) {
+            // (16-bit or fp32 operands' products do not overflow fp64: a dot that is not
+            // finite comes from operands that are not, and is what it is)
+            if (cross && __builtin_fabs(s) < __builtin_inf()) {
                 straddled = 1;
                 double S = 0.0, C = 0.0, t, err;
                 if (p.vec) {

@@ -113,6 +113,10 @@ struct XrParams {
     int bias_dt;
     int vec_store;          // XR_AFFINE: rows allow 4-element vector stores
     double scale;           // XR_H: the value rounded is scale * C (1 in the forward)
+    // XR_H: columns j with (j & col_mask) >= cols are written as zeros (by
+    // default none); columns() for a rank padded to r_pad, a power of two
+    int col_mask = 0, cols = 1;
+    void columns(int64_t rank, int r_pad) { col_mask = r_pad - 1, cols = (int)rank; }
     // XR_H, 16-bit compute, Nc = 16: b = down as stored, split in the kernel
     // and its norms taken there (b_lo and bnorm unused); the guard's count is
     // then written per workgroup (flag_slots of them)
