@@ -112,7 +112,8 @@ struct Feed {
         pa0 = (const char*)a0 + n0 * ka;
         na0 = ext;
         if constexpr (SH::TWO) {
-            // a fold step multiplies one factor pair: the other half's rows read zeros
+            // a fold step multiplies one factor pair: the other half's rows, which take no
+            // part in it, read zeros (every step issues the same loads)
             pa1 = fold ? pa0 : (const char*)p.a[1] + n0 * ka;
             na1 = fold && h == 0 ? 0u : ext;
             na0 = fold && h == 1 ? 0u : ext;
@@ -333,7 +334,12 @@ __global__ __launch_bounds__(TL::NT, 1) void pair_kernel(PairParams p, int tiles
         // first MFMAs of substep 1 are issued before the wait for step kt+1 and
         // the barrier; after it the loads of step kt+NS into the stage just
         // consumed and the next fragments go between the others.
-        auto k_step = [&](int kt) {
+        // A fold step of the gated block belongs to one projection: only that one's
+        // blocks (HALF 0 or 1) take part, since zeros for the other's rows would turn
+        // an h that is not finite into NaNs there (HALF 2: every block).
+        auto k_step = [&](int kt, auto half) {
+            constexpr int HALF = decltype(half)::value;
+            constexpr int I0 = HALF == 1 ? SH::FI : 0, I1 = HALF == 0 ? SH::FI : FN;
             constexpr int ND = FN + FM;
             constexpr int G = FN % 4 == 0 ? 4 : 2, FNG = FN / G;
             char* st = smem + (kt % NS) * TL::STAGE;
@@ -343,22 +349,25 @@ __global__ __launch_bounds__(TL::NT, 1) void pair_kernel(PairParams p, int tiles
 #pragma unroll
             for (int j = 0; j < FM; ++j) f1b[j] = frag_b(st, 1, j);
 #pragma unroll
-            for (int i = 0; i < FN; ++i)
+            for (int i = I0; i < I1; ++i)
 #pragma unroll
                 for (int j = 0; j < FM; ++j) acc[i][j] = CT::step(f0a[i], f0b[j], acc[i][j]);
-            constexpr int PER = FN * FM / (ND + 1);
+            constexpr int NF = (I1 - I0) * FM, PER = NF / (ND + 1);
+            if constexpr (PER > 0) {
 #pragma unroll
-            for (int g = 0; g < ND; ++g) {
-                __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-                __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+                for (int g = 0; g < ND; ++g) {
+                    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+                    __builtin_amdgcn_sched_group_barrier(0x008, PER, 0);
+                }
+                __builtin_amdgcn_sched_group_barrier(0x008, NF - ND * PER, 0);
             }
-            __builtin_amdgcn_sched_group_barrier(0x008, FN * FM - ND * PER, 0);
             __builtin_amdgcn_sched_barrier(0);
             __builtin_amdgcn_s_waitcnt(0xC07F);
 #pragma unroll
             for (int i = 0; i < FNG; ++i)
 #pragma unroll
-                for (int j = 0; j < FM; ++j) acc[i][j] = CT::step(f1a[i], f1b[j], acc[i][j]);
+                for (int j = 0; j < FM; ++j)
+                    if (i >= I0 && i < I1) acc[i][j] = CT::step(f1a[i], f1b[j], acc[i][j]);
             __builtin_amdgcn_sched_barrier(0);
             wait_vm<(NS - 2) * Q>();
             lds_barrier();
@@ -379,13 +388,20 @@ __global__ __launch_bounds__(TL::NT, 1) void pair_kernel(PairParams p, int tiles
                 }
 #pragma unroll
                 for (int m = FNG * FM + z * NM / Q; m < FNG * FM + (z + 1) * NM / Q; ++m)
-                    acc[m / FM][m % FM] = CT::step(f1a[m / FM], f1b[m % FM], acc[m / FM][m % FM]);
+                    if (m / FM >= I0 && m / FM < I1)
+                        acc[m / FM][m % FM] = CT::step(f1a[m / FM], f1b[m % FM], acc[m / FM][m % FM]);
                 __builtin_amdgcn_sched_barrier(0);
             }
             advance();
         };
         if constexpr (!I8) {
-            for (int kt = 0; kt < RF; ++kt) k_step(kt);
+            if constexpr (SH::TWO) {
+                int kt = 0;
+                for (; kt < RF / 2; ++kt) k_step(kt, std::integral_constant<int, 0>{});
+                for (; kt < RF; ++kt) k_step(kt, std::integral_constant<int, 1>{});
+            } else {
+                for (int kt = 0; kt < RF; ++kt) k_step(kt, std::integral_constant<int, 2>{});
+            }
             if (RF > 0) {
 #pragma unroll
                 for (int i = 0; i < FN; ++i)
@@ -393,7 +409,7 @@ __global__ __launch_bounds__(TL::NT, 1) void pair_kernel(PairParams p, int tiles
                     for (int j = 0; j < FM; ++j) acc[i][j] *= p.scale;
             }
         }
-        for (int kt = RF; kt < KT; ++kt) k_step(kt);
+        for (int kt = RF; kt < KT; ++kt) k_step(kt, std::integral_constant<int, 2>{});
         wait_vm<0>();   // the out-of-range loads past the last step still write LDS
     }
 
