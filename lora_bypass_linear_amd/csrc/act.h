@@ -57,15 +57,16 @@ __device__ __forceinline__ float act_logistic16(float a, float b, float g) {
 // relative (fp32 ulps at most), n_slope relative to mass = |t| + p, slope = t + p:
 // the exponent's rounding 1.2 |u| (the tanh form's u 3 |u| more), which counts
 // q-fold in p and p-fold in q = 1 - p; exp2 2, the sum 1, the reciprocal 2, so p 5
-// and q 6; g p one more, t 16 with its products and u'.  e is kept finite, so
-// that q = e r is 1, not a product of infinity and 0, where p is 0.
+// and q 6; g p one more, t 16 with its products and u'.  Below u = -87, where p
+// nears fp32's smallest normal value, both bounds are infinite (and e is kept
+// finite, or q = e r would be a product of infinity and 0).
 __device__ __forceinline__ float act_logistic16_grad(float a, float b, float g, float* slope, float* mass,
                                                      float* n_act, float* n_slope) {
     const float g2 = __builtin_fminf(g * g, 1e30f), u = g * __builtin_fmaf(b, g2, a);
     const float e = __builtin_fminf(__builtin_amdgcn_exp2f(u * -1.44269502f), 3e38f);
     const float p = __builtin_amdgcn_rcpf(1.f + e), v = g * p;
     const float t = v * (e * p) * __builtin_fmaf(3.f * b, g2, a);
-    const float nu = (b != 0.f ? 4.25f : 1.25f) * __builtin_fabsf(u);
+    const float nu = u < -87.f ? __builtin_inff() : (b != 0.f ? 4.25f : 1.25f) * __builtin_fabsf(u);
     *slope = t + p;
     *mass = __builtin_fabsf(t) + p;
     *n_act = nu + 6.f;

@@ -51,7 +51,8 @@ template <int DT>
 __device__ __forceinline__ uint16_t to16(float v) { return DT == DT_F16 ? f32_to_f16(v) : f32_to_bf16(v); }
 
 // whether x, off by up to n units of 2^-24 of itself (at most as many fp32
-// ulps), may lie on the other side of a border of the 16-bit type
+// ulps), may lie on the other side of a border of the 16-bit type; an n that is
+// no finite number says nothing of x, which then counts as undecided
 template <int DT>
 __device__ __forceinline__ bool near16(float x, float n) {
     if constexpr (DT == DT_BF16) {
@@ -60,7 +61,7 @@ __device__ __forceinline__ bool near16(float x, float n) {
         return ((__builtin_bit_cast(uint32_t, x) - 0x8000u + t) & 0xFFFFu) <= 2u * t;
     } else {
         const float e = n * 0x1p-24f * __builtin_fabsf(x);   // (fp16's borders move below 2^-14)
-        return !(to16<DT>(x - e) == to16<DT>(x + e));
+        return !(n < __builtin_inff()) || to16<DT>(x - e) != to16<DT>(x + e);
     }
 }
 
@@ -80,7 +81,8 @@ __device__ __forceinline__ uint32_t grads_f64(int act, float dy, float g, float 
 // transposed, which gh and dx read (a launch of their own for those cost a short
 // batch 5 of 52 us).
 //
-// dg and dv round to 16 bits as their exact values do: what is built on them
+// dg and dv round to 16 bits as their values in 64 bits do (the exact ones but
+// for ties of dy v / 2 beside a gate below 2^-53): what is built on them
 // (gh, itself rounded, then dx and the factors' gradients) would carry a step
 // taken the other way into every sum, and fp32 gradients with it (1e-4 of
 // their norm).  fp32 decides all but the few in a thousand that lie within its
@@ -131,17 +133,21 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateGradParams p, unsign
             for (int e = 0; e < 8; ++e) {
                 float slope, mass, na, ns;
                 const float r = act(g[e], &slope, &mass, &na, &ns);
-                dg[e] = dy[e] * v[e] * slope;
+                const float w = dy[e] * v[e];
+                dg[e] = w * slope;
                 dv[e] = dy[e] * r;
                 // (two more units for the products with dy and value; at slope 0 the bound is infinite)
                 const float nv = na + 2.f;
                 const float ng = __builtin_fmaf(ns * mass, __builtin_amdgcn_rcpf(__builtin_fabsf(slope)), 2.f);
-                open |= near16<C>(dg[e], ng) || near16<C>(dv[e], nv) ? 1u << e : 0u;
+                // dy v past fp32's range, which a small slope brings back (two fp16 values never)
+                const bool past = (C != DT_F16 || G != DT_F16) && __builtin_fabsf(w) == __builtin_inff();
+                open |= near16<C>(dg[e], ng) || near16<C>(dv[e], nv) || past ? 1u << e : 0u;
             }
         };
         if (p.act == ACT_GELU) {
+            // (below -13 exp(-g^2 / 2) nears fp32's smallest normal value)
             grads([](float x, float* s, float* m, float* na, float* ns) {
-                *na = *ns = 16.f;
+                *na = *ns = x < -13.f ? __builtin_inff() : 16.f;
                 return act_gelu<true>(x, s, m);
             });
         } else {
