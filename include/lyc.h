@@ -499,6 +499,8 @@ int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const flo
  * LYC_ACT_GELU g Phi(g), LYC_ACT_GELU_TANH g (1 + tanh(sqrt(2/pi) (g + 0.044715
  * g^3))) / 2, in fp32 (a few units of 2^-23 of the result; the tanh form's
  * tail of negative g, where it falls to 0 as exp(u), also 2^-22 |u| of it).
+ * Results below fp32's smallest normal value may be 0, and under a 16-bit y
+ * act(g) below 2^-119.
  *  - Shapes as lyc_lora_linear_fwd for each projection; both have the same
  *    sizes, dtypes and rank.  The dtype policy runs over (x, W, b, down, up);
  *    both biases or neither.  rank == 0: no bypass (factors may be NULL).

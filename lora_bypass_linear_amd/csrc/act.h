@@ -7,13 +7,15 @@
 
 namespace lyc {
 
-// exp(t), t below 88, to about two ulps: the product t log2(e) in two pieces, so
-// that the exponent's own rounding (2^-24 of up to 128) does not reach the result
-__device__ __forceinline__ float exp_f32(float t) {
+// exp(t) 2^s, t below 88 + s log(2), to about two ulps: the product t log2(e) in
+// two pieces, so that the exponent's own rounding (2^-24 of up to 128) does not
+// reach the result.  (hi + s has no rounding: s is 0, or 64 against a hi of 112 to
+// 192 of the other sign)
+__device__ __forceinline__ float exp_f32(float t, float s = 0.f) {
     constexpr float L = 1.44269502f, LL = 1.92596303e-8f;   // log2(e) = L + LL
     const float hi = t * L;
     const float lo = __builtin_fmaf(t, LL, __builtin_fmaf(t, L, -hi));
-    const float e = __builtin_amdgcn_exp2f(hi);
+    const float e = __builtin_amdgcn_exp2f(hi + s);
     return __builtin_fmaf(e, lo * 0.693147182f, e);
 }
 
@@ -26,21 +28,21 @@ __device__ __forceinline__ float rcp_f32(float d) {
 //   silu       g p(g)                                           slope p + g p (1 - p)
 //   gelu_tanh  g p(u), u = 2 sqrt(2/pi) (g + 0.044715 g^3)      slope p + g p (1 - p) u'
 // with p(u) = 1 / (1 + exp(-u)) (1/2 (1 + tanh z) is p(2 z)): u = g (b g^2 + a).
-// exp(-u) leaves the fp32 range below u = -87: there p is 0 (it is under 2e-38)
-// and 1 - p is 1.  u is taken of g within +-1e6, where p has long been 0 or 1, so
-// that no infinity meets another; a NaN passes through the factor g.
+// exp(-u) leaves the fp32 range below u = -87, where g p is still a normal value:
+// there it is taken 2^-64 fold (1 + e is e, so r is p 2^64) and the factor put
+// back at the end.  Below -112 both results are under fp32's smallest value.  u is
+// taken of g within +-1e6, where p has long been 0 or 1, so that no infinity
+// meets another; a NaN passes through the factor g.
 template <bool GRAD>
 __device__ __forceinline__ float act_logistic(float a, float b, float g, float* slope) {
     const float c = __builtin_amdgcn_fmed3f(g, -1e6f, 1e6f), c2 = c * c;
     const float u = c * __builtin_fmaf(b, c2, a);
-    const float e = exp_f32(-u);
+    const bool far = u < -87.f;
+    const float back = u < -112.f ? 0.f : far ? 0x1p-64f : 1.f;
+    const float e = exp_f32(__builtin_fminf(-u, 112.f), far ? -64.f : 0.f);
     const float r = rcp_f32(1.f + e);
-    const float p = u < -87.f ? 0.f : r;
-    if constexpr (GRAD) {
-        const float q = u < -87.f ? 1.f : e * r;
-        *slope = __builtin_fmaf(g * p * q, __builtin_fmaf(3.f * b, c2, a), p);
-    }
-    return g * p;
+    if constexpr (GRAD) *slope = __builtin_fmaf(g * r * (e * r), __builtin_fmaf(3.f * b, c2, a), r) * back;
+    return g * r * back;
 }
 
 // The same for 16-bit results: exp2 and the reciprocal as the hardware gives them
@@ -79,12 +81,15 @@ __device__ __forceinline__ float act_logistic16_grad(float a, float b, float g, 
 // accuracy where 1 + erf cancels.  (1 + 2 z) erfcx(z) is smooth in s = (z - 5/2) /
 // (z + 5/2): a polynomial of degree 9 fitted at Chebyshev nodes of z up to 13.5
 // (beyond, exp(-z^2) is 0) is within 3e-8 of it, 4e-7 with fp32's roundings.
-// exp(-z^2) takes z^2 = g^2 / 2 in two pieces.
-template <bool GRAD>
+// exp(-z^2) takes z^2 = g^2 / 2 in two pieces.  FAR: the slope keeps its accuracy
+// where exp(-z^2) is below fp32's smallest normal value (it is taken 2^64 fold).
+template <bool GRAD, bool FAR = false>
 __device__ __forceinline__ float act_gelu(float g, float* slope, float* mass) {
     const float c = __builtin_amdgcn_fmed3f(g, -1e6f, 1e6f), h = 0.5f * c;
     const float hi = h * c, lo = __builtin_fmaf(h, c, -hi);
-    float e = exp_f32(-hi);
+    const bool far = FAR && hi > 80.f;
+    const float back = far ? 0x1p-64f : 1.f;
+    float e = exp_f32(-hi, far ? 64.f : 0.f);
     e = __builtin_fmaf(-e, lo, e);
     const float z = __builtin_fabsf(c) * 0.707106769f;
     const float d = __builtin_fmaf(2.f, z, 1.f), k = z + 2.5f;
@@ -100,10 +105,10 @@ __device__ __forceinline__ float act_gelu(float g, float* slope, float* mass) {
     y = __builtin_fmaf(y, s, -0.0990233123f);
     y = __builtin_fmaf(y, s, -0.122356921f);
     y = __builtin_fmaf(y, s, 1.26483822f);
-    const float tail = 0.5f * e * (y * k * r);
+    const float tail = 0.5f * e * (y * k * r) * back;
     const float cdf = g < 0.f ? tail : 1.f - tail;
     if constexpr (GRAD) {
-        const float t = g * 0.398942292f * e;
+        const float t = g * 0.398942292f * e * back;
         *slope = t + cdf;
         *mass = __builtin_fabsf(t) + cdf;   // (both off by less than 16 units of 2^-24)
     }

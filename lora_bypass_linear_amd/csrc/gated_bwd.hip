@@ -125,7 +125,7 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(GateGradParams p, unsign
                 dg[e] = dy[e] * v[e] * slope;
             }
         };
-        if (p.act == ACT_GELU) grads([](float x, float* s) { float m; return act_gelu<true>(x, s, &m); });
+        if (p.act == ACT_GELU) grads([](float x, float* s) { float m; return act_gelu<true, true>(x, s, &m); });
         else grads([=](float x, float* s) { return act_logistic<true>(a, b, x, s); });
     } else {
         auto grads = [&](auto act) {
