@@ -244,7 +244,7 @@ int forward(const Problem& P, const void* x, const void* w, const void* bias, co
     // (P.w_kept: w is W_c, W already rounded to the compute dtype; P.w8: w is
     // its e4m3 codes and w_s their tile scales)
     if (y_dt != P.o_dt) return LYC_ERR_DTYPE_MISMATCH;
-    if ((bias == nullptr) != (P.b_dt == 0)) return LYC_ERR_INVALID_ARG;
+    if (P.N > 0 && (bias == nullptr) != (P.b_dt == 0)) return LYC_ERR_INVALID_ARG;
     if (P.M == 0 || P.N == 0) return LYC_OK;
     if (y == nullptr) return LYC_ERR_INVALID_ARG;
     if (P.K > 0) {
@@ -1147,7 +1147,7 @@ int gated_forward(const Problem& P, const void* x, const void* const (&w)[2], co
     if (y_dt != P.o_dt) return LYC_ERR_DTYPE_MISMATCH;
     if (bad_scale(scale)) return LYC_ERR_INVALID_ARG;
     for (int i = 0; i < 2; ++i)
-        if ((bias[i] == nullptr) != (P.b_dt == 0)) return LYC_ERR_INVALID_ARG;
+        if (P.N > 0 && (bias[i] == nullptr) != (P.b_dt == 0)) return LYC_ERR_INVALID_ARG;
     if ((keep[0] == nullptr) != (keep[1] == nullptr)) return LYC_ERR_INVALID_ARG;
     if (P.M == 0 || P.N == 0) return LYC_OK;
     if (y == nullptr) return LYC_ERR_INVALID_ARG;
@@ -1927,7 +1927,7 @@ int lyc_fp8_linear_fwd(const void* q_x, const float* s_x, const void* q_w, const
     const int st = check_fp8_linear(M, N, K);
     if (st != LYC_OK) return st;
     if (!valid_dt(y_dt) || (bias_dt != 0 && !valid_dt(bias_dt))) return LYC_ERR_INVALID_ARG;
-    if ((bias == nullptr) != (bias_dt == 0)) return LYC_ERR_INVALID_ARG;
+    if (N > 0 && (bias == nullptr) != (bias_dt == 0)) return LYC_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return LYC_OK;
     if (y == nullptr) return LYC_ERR_INVALID_ARG;
     if (K > 0 && (q_x == nullptr || s_x == nullptr || q_w == nullptr || s_w == nullptr)) return LYC_ERR_INVALID_ARG;
@@ -2088,7 +2088,7 @@ static int int8_forward(int mode, const void* q_x, const float* s_x, const void*
     if (!valid_dt(y_dt) || (bias_dt != 0 && !valid_dt(bias_dt))) return LYC_ERR_INVALID_ARG;
     if (act < 0 || act >= lyc::ACT_COUNT) return LYC_ERR_INVALID_ARG;
     for (int i = 0; i < H; ++i)
-        if ((bias[i] == nullptr) != (bias_dt == 0)) return LYC_ERR_INVALID_ARG;
+        if (N > 0 && (bias[i] == nullptr) != (bias_dt == 0)) return LYC_ERR_INVALID_ARG;
     if (M == 0 || N == 0) return LYC_OK;
     if (y == nullptr || s_x == nullptr || (K > 0 && q_x == nullptr)) return LYC_ERR_INVALID_ARG;
     if (!aligned(q_x, 16) || !aligned(s_x, 4) || !aligned(y, esize(y_dt))) return LYC_ERR_UNSUPPORTED;

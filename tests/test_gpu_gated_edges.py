@@ -90,3 +90,54 @@ def test_an_infinite_h_stays_with_its_projection(size, dt, hit):
         ref = torch.where(value[rows] == 0, float("nan"), float("inf") * value[rows].double().sign())
         assert torch.equal(y[rows][:, up].double().nan_to_num(nan=7.0), ref[:, up].nan_to_num(nan=7.0))
         assert torch.isnan(y[rows][:, ~up]).all()
+
+
+def _z(*s, dt):
+    return torch.zeros(*s, dtype=dt, device="cuda")
+
+
+@pytest.mark.parametrize("dt", [BF16, F32])
+@pytest.mark.parametrize("M", [3, 200])
+@pytest.mark.parametrize("given", ["", "h", "w", "wh"])
+def test_backward_without_features(dt, M, given):
+    """K = 0: no dx, no gradient of the downs, zeros for the ups (h is zero).  N = 0: zeros for dx and the downs."""
+    say("gated backward, empty axes", dt, M, given)
+    rp = 16 if dt == BF16 else 32
+
+    def call(N, K):
+        w = (_z(N, K, dt=dt), _z(N, K, dt=dt))
+        factors = (_z(4, K, dt=dt) + 1, _z(N, 4, dt=dt) + 1) * 2
+        kw = {"w_gate_t": _z(K, N, dt=dt), "w_value_t": _z(K, N, dt=dt)} if "w" in given else {}
+        if "h" in given:
+            kw["h"] = _z(M, 2 * rp, dt=dt)
+        d = _z(M, N, dt=dt) + 1
+        return L.lora_gated_linear_backward(_z(M, K, dt=dt) + 1, *w, *factors, 1.5, d, d, d, **kw)
+
+    dx, ddg, dug, ddv, duv = call(48, 0)
+    assert dx.shape == (M, 0) and ddg.shape == (4, 0) and ddv.shape == (4, 0)
+    assert torch.equal(dug, _z(48, 4, dt=dt)) and torch.equal(duv, _z(48, 4, dt=dt))
+    dx, ddg, dug, ddv, duv = call(0, 64)
+    assert dug.shape == (0, 4) and duv.shape == (0, 4)
+    assert torch.equal(dx, _z(M, 64, dt=dt)) and torch.equal(ddg, _z(4, 64, dt=dt)) and torch.equal(ddv, _z(4, 64, dt=dt))
+
+
+def test_nothing_wanted():
+    t = G._inputs(70, 72, 64, 4, BF16, BF16, BF16)
+    _, gate, value, h = L.lora_gated_linear(*G._args(t), 1.0, keep=True)
+    got = L.lora_gated_linear_backward(*G._args(t), 1.0, gate, gate, value, h=h, want_dx=False, want_ddown=False,
+                                       want_dup=False)
+    assert got == (None,) * 5
+
+
+@pytest.mark.parametrize("M,N,K", [(0, 48, 64), (5, 0, 64), (5, 48, 0), (200, 48, 0), (200, 0, 64)])
+def test_int8_without_rows_or_features(M, N, K):
+    say("int8, empty axes", M, N, K)
+    q, s = L.int8_quantize_rows(_z(M, K, dt=BF16))
+    assert q.shape == (M, K) and torch.equal(s, torch.full_like(s, 2.0 ** -100 / 127.0))
+    a, sa = L.int8_quantize_rows(_z(N, K, dt=F32))
+    b = torch.randn(N, device="cuda").to(BF16)
+    y = L.int8_linear(q, s, a, sa, b)
+    assert torch.equal(y, b.expand(M, N))
+    y = L.int8_gated_linear(q, s, a, sa, a, sa, b, b, activation="silu", out_dtype=F32)
+    want = (b.double() * b.double().sigmoid() * b.double()).expand(M, N)
+    assert ((y.double() - want).abs() <= 2.0 ** -19 * want.abs()).all()
