@@ -512,8 +512,8 @@ int lyc_fp8_lora_linear_bwd(const void* x, int x_dt, const void* q_wt, const flo
  *  - No output may overlap an input, the workspace or another output
  *    (LYC_ERR_INVALID_ARG).  One launch covers y: sizes whose tiles need 2^32
  *    threads or more (N = 2^28 for few rows; far past the memory otherwise) are
- *    LYC_ERR_UNSUPPORTED, with a rank M > 2^26 too.  Everything else, the workspace (lyc_lora_gated_workspace_size) and errors as
- *    lyc_lora_linear_fwd.
+ *    LYC_ERR_UNSUPPORTED, with a rank M > 2^26 too.  Everything else, the
+ *    workspace (lyc_lora_gated_workspace_size) and errors as lyc_lora_linear_fwd.
  * lyc_lora_gated_plan (host only): output tile (features x rows) and K split of
  * the block's product, or with backward = 1 of dx's (N and K as the forward's);
  * up to 32 rows the features and rows of one workgroup of the few-row kernel.
@@ -538,7 +538,10 @@ int lyc_lora_gated_fwd(const void* x, int x_dt, const void* w_gate, const void* 
  *                                                     once from its exact value
  *   dx    = round_x( sum_p d_p . W_p_c + gh_p . down_p_c )
  *   d_down_p = round_down( gh_p^T . x_c ),  d_up_p = round_up( scale * d_p^T . h_p )
- * fp32 accumulation; dx's two products run in one kernel.
+ * fp32 accumulation; dx's two products run in one kernel.  In 16 bits dg and dv
+ * are rounded once from their values in 64 bits (which differ from the exact
+ * ones at ties of dy value or dy gate only, where act' or act / gate is within
+ * 2^-53 of 1 or 1/2); in fp32 they are products of fp32, left to right.
  *  - w_gate, w_value or the caller-kept transposes w_gate_t, w_value_t [K][N] in
  *    c (16-byte aligned): exactly one pair, read only when dx is wanted.
  *  - h: the forward's [M][2 r_pad], or NULL (recomputed); read for d_up.
@@ -573,7 +576,9 @@ int lyc_lora_gated_bwd(const void* x, int x_dt, const void* w_gate, const void* 
  * lyc_int8_gated_fwd: the gated block over such weights, y = round_out( act(g) *
  *   v ) with g and v as above before their rounding, in one kernel.
  *  - K a multiple of 16, at most 131056; M, N <= 2^30 and, of the products, sizes
- *    that one launch covers, as lyc_lora_gated_fwd (else LYC_ERR_UNSUPPORTED).  x and codes 16-byte aligned.  y_dt and the bias's
+ *    that one launch covers, as lyc_lora_gated_fwd (else LYC_ERR_UNSUPPORTED).
+ *    Rows of another length are padded with zeros, on both sides: zeros change
+ *    no scale and no sum.  x and codes 16-byte aligned.  y_dt and the bias's
  *    dtype are the caller's choice (8-bit operands enter no dtype policy).
  *    Outputs and workspace must not overlap inputs or each other
  *    (LYC_ERR_INVALID_ARG).  Scales are read, and written by the quantization,

@@ -82,10 +82,10 @@ __device__ __forceinline__ uint32_t grads_f64(int act, float dy, float g, float 
 // batch 5 of 52 us).
 //
 // dg and dv round to 16 bits as their values in 64 bits do (the exact ones but
-// for ties of dy v / 2 beside a gate below 2^-53): what is built on them
-// (gh, itself rounded, then dx and the factors' gradients) would carry a step
-// taken the other way into every sum, and fp32 gradients with it (1e-4 of
-// their norm).  fp32 decides all but the few in a thousand that lie within its
+// for ties of dy v or dy g where act' or act / g is within 2^-53 of 1 or 1/2):
+// what is built on them (gh, itself rounded, then dx and the factors' gradients)
+// would carry a step taken the other way into every sum, and fp32 gradients with
+// it (1e-4 of their norm).  fp32 decides all but the few in a thousand that lie within its
 // error of a border; those are marked, a bit an element, and a second kernel
 // evaluates them in 64 bits.  (In this one that code's registers halved the
 // waves in flight: bf16 8192 x 8192 177 us with it, 113 and 32 apart.)

@@ -9,9 +9,11 @@
 // fused multiply-add ((f + 1/2) s has no rounding of its own there), says on
 // which side of the border between two codes x lies; 0 is the tie.
 //
-// Bound by memory: a workgroup a row (rows of up to 1024: a few lanes), up to 8192 elements of it in registers
-// between its maximum and its codes, so that x is read once.  bf16 16384 x 8192:
-// 70 us, 5.7 TB/s; fp32 4096 x 4096: 13.6 us.
+// Bound by memory: a workgroup a row (rows of up to 1024: a few lanes), up to
+// 8192 elements of it in registers between its maximum and its codes, so that x
+// is read once (the rest of a longer row a second time, from L2).  bf16 16384 x
+// 8192: 70 us, 5.7 TB/s; 16384 x 16384: 152 us, 5.3 TB/s; 8192 x 14336: 70 us,
+// 5.0 TB/s; fp32 4096 x 4096: 13.6 us.
 #include "pair_tile.h"
 #include "quant_device.h"
 
@@ -129,7 +131,7 @@ static dim3 rows_grid(int64_t n) {
 template <int DT>
 static hipError_t run_quant_int8(const QuantInt8Params& p, hipStream_t s) {
     // a workgroup a row, however short, is late with its loads: bf16 2^20 x 128 939 us,
-    // 72 so; 2^17 x 1024 130, 69
+    // 69-72 so; 2^17 x 1024 130, 69
     if (p.K <= 1024) {
         int lsh = 0;
         while (p.K > 16 << lsh) ++lsh;

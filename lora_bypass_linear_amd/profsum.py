@@ -9,13 +9,13 @@
     # HBM traffic of one kernel (from one --pmc FETCH_SIZE run and one --pmc
     # WRITE_SIZE run of a command that also performs a plain copy of a known size)
     python -m lora_bypass_linear_amd.profsum traffic --fetch DIR_F --write DIR_W --kernel SUBSTR \\
-        --sources gemm|hpass|merge|fp8|quant|ortho --calib-kernel copyBuffer --calib-bytes N --cmd "<commands>" --out profiles/NAME.txt
+        --sources KIND --calib-kernel copyBuffer --calib-bytes N --cmd "<commands>" --out profiles/NAME.txt
 
 FETCH_SIZE and WRITE_SIZE are reported in KiB per dispatch.  Each is scaled by
 the ratio (known bytes of the copy) / (what the same counter reports for the
 copy kernel), so the figures are bytes as the copy kernel defines them.  The
-traffic summary records a hash of the profiled kernel's sources; bench.py uses
-the figure only while the sources still hash to it.
+traffic summary records a hash of the profiled kernel's sources (a KIND of
+SOURCES); bench.py uses the figure only while the sources still hash to it.
 """
 from __future__ import annotations
 
@@ -37,6 +37,7 @@ SOURCES = {"gemm": ("csrc/gemm.hip", "csrc/fp8.h", "csrc/gemm_tile.h", "csrc/ker
            "gated": ("csrc/gated.hip", "csrc/pair_tile.h", "csrc/act.h", "csrc/pair.h", "csrc/bwd.h", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h"),
            "gated_bwd": ("csrc/gated_bwd.hip", "csrc/pair_tile.h", "csrc/act.h", "csrc/pair.h", "csrc/bwd.h", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h", "csrc/transpose_device.h"),
            "int8": ("csrc/int8.hip", "csrc/pair_tile.h", "csrc/act.h", "csrc/pair.h", "csrc/bwd.h", "csrc/gemm_tile.h", "csrc/quant_device.h", "csrc/fp8.h", "csrc/kernels.h", "csrc/lyc_device.h"),
+           "tokens": ("csrc/tokens.hip", "csrc/tokens.h", "csrc/kernels.h", "csrc/lyc_device.h"),
            "ortho": ("csrc/ortho.hip", "csrc/ortho.h", "csrc/gemm_tile.h", "csrc/kernels.h", "csrc/lyc_device.h")}
 
 

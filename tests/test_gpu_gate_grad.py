@@ -42,7 +42,8 @@ def _check(act, dy, gate, value):
     # What 64 bits leave open: each evaluation (a quotient, an exponential, a few products and one sum, whose terms
     # are at most 1.2 near its zero) is off by some 2^-53 of itself, 2^-48 bounds it, and 2^-50 of dy value where the
     # sum's terms cancel.  It matters at ties only: beside a gate g below 2^-53 the slope is 1/2 + g / 2 (gelu: + 0.8 g),
-    # which 64 bits round to 1/2, while dy value / 2 has 16 bits and is a tie of bf16 once in 2^8.
+    # which 64 bits round to 1/2, while dy value / 2 has 16 bits and is a tie of bf16 once in 2^8 (the same above the
+    # gates where the slope or act(g) / g is 1 to 64 bits).
     off = 2.0 ** -48 * d64[0].abs() + torch.where(gate.double().abs() < 2.0, 2.0 ** -50 * w, 0.0), 2.0 ** -48 * d64[1].abs()
     top = torch.finfo(c).max
     assert all((R.nearest(d, c).abs() <= top).all() for d in d64)
