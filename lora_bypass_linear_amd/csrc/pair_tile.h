@@ -17,6 +17,12 @@
 // int8 sums are exact 32-bit integers (127^2 K < 2^31), so neither the order of
 // the K steps nor a K split changes a result; they become fp32 once, at the end.
 //
+// fp32 products are summed in blocks of SUM_K: one chain of n fused steps is off
+// by about sqrt(n / 2) 2^-25 of the result (independent terms, partial sums that
+// grow as sqrt(k)), n / b blocks of b by sqrt(b / 2 + n / 2b) 2^-25.  (16-bit
+// products enter the chain 32 at a time, so theirs is short.)  20 x 512 x 8192:
+// 1.1e-6 of the norm as chains of 2048, 5.6e-7 so, in the same time.
+//
 // What bounds it: at the large sizes the matrix pipe (busy about 65 % of the
 // cycles, clocked down under its load) with the stream of operands from L2 into
 // LDS behind it: a 256 x 256 step takes 1.4 us, its loads alone 1.1, its MFMAs
@@ -47,6 +53,8 @@ struct CI8 {
 };
 template <class CT>
 using Acc = std::conditional_t<CT::dt == DT_I8, i32x4, f32x4>;
+
+constexpr int SUM_K = 512;   // products of a block of an fp32 sum
 
 __device__ __forceinline__ f32x4 to_f32(f32x4 v) { return v; }
 __device__ __forceinline__ f32x4 to_f32(i32x4 v) { return f32x4{(float)v[0], (float)v[1], (float)v[2], (float)v[3]}; }
@@ -409,7 +417,28 @@ __global__ __launch_bounds__(TL::NT, 1) void pair_kernel(PairParams p, int tiles
                     for (int j = 0; j < FM; ++j) acc[i][j] *= p.scale;
             }
         }
-        for (int kt = RF; kt < KT; ++kt) k_step(kt, std::integral_constant<int, 2>{});
+        if constexpr (CT::dt == DT_F32) {
+            // (a block's end as a condition in one loop: 77.5 us where this takes 76.5)
+            constexpr int BS = SUM_K * CT::es / TL::BKB;   // K steps of a block
+            f32x4 done[FN][FM] = {};
+            for (int kt = RF; kt < KT;) {
+                const int end = KT - kt < BS ? KT : kt + BS;
+                for (; kt < end; ++kt) k_step(kt, std::integral_constant<int, 2>{});
+#pragma unroll
+                for (int i = 0; i < FN; ++i)
+#pragma unroll
+                    for (int j = 0; j < FM; ++j) {
+                        done[i][j] += acc[i][j];
+                        acc[i][j] = f32x4{};
+                    }
+            }
+#pragma unroll
+            for (int i = 0; i < FN; ++i)
+#pragma unroll
+                for (int j = 0; j < FM; ++j) acc[i][j] += done[i][j];
+        } else {
+            for (int kt = RF; kt < KT; ++kt) k_step(kt, std::integral_constant<int, 2>{});
+        }
         wait_vm<0>();   // the out-of-range loads past the last step still write LDS
     }
 
@@ -617,6 +646,10 @@ __global__ __launch_bounds__(64 * NW) void pair_skinny_kernel(PairParams p) {
     const int steps = (int)((kb + 63) / 64);
     const int s0 = steps * wave / NW, s1 = steps * (wave + 1) / NW;
     const int se = s0 + ((s1 - s0 + D - 1) / D) * D;
+    constexpr bool BLOCKS = CT::dt == DT_F32;
+    constexpr int BS = SUM_K * CT::es / 64;   // steps of a block
+    static_assert((BS & (BS - 1)) == 0 && BS % D == 0, "steps of a block");
+    Acc<CT> done[BLOCKS ? H : 1][BLOCKS ? MT : 1] = {};
 #pragma unroll
     for (int sg = 0; sg < SEGS; ++sg) {
         const auto rx = make_rsrc_uniform(p.b[sg], (uint32_t)p.M * kb);
@@ -643,8 +676,21 @@ __global__ __launch_bounds__(64 * NW) void pair_skinny_kernel(PairParams p) {
                     for (int t = 0; t < MT; ++t) acc[h][t] = CT::step(wa[u][h], xa[u][t], acc[h][t]);
                 load(u, sb + u + D);
             }
+            if (BLOCKS && ((sb - s0) & (BS - 1)) == BS - D) {
+#pragma unroll
+                for (int h = 0; h < (BLOCKS ? H : 0); ++h)
+#pragma unroll
+                    for (int t = 0; t < MT; ++t) {
+                        done[h][t] += acc[h][t];
+                        acc[h][t] = Acc<CT>{};
+                    }
+            }
         }
     }
+#pragma unroll
+    for (int h = 0; h < (BLOCKS ? H : 0); ++h)
+#pragma unroll
+        for (int t = 0; t < MT; ++t) acc[h][t] += done[h][t];
 #pragma unroll
     for (int h = 0; h < H; ++h)
 #pragma unroll
