@@ -141,3 +141,30 @@ def test_int8_without_rows_or_features(M, N, K):
     y = L.int8_gated_linear(q, s, a, sa, a, sa, b, b, activation="silu", out_dtype=F32)
     want = (b.double() * b.double().sigmoid() * b.double()).expand(M, N)
     assert ((y.double() - want).abs() <= 2.0 ** -19 * want.abs()).all()
+
+
+@pytest.mark.parametrize("c", [F16, BF16])
+@pytest.mark.parametrize("wide", ["down", "up"])
+@pytest.mark.parametrize("M", [1, 20, 200])
+@pytest.mark.parametrize("r", [5, 16])
+def test_factors_of_two_dtypes(c, wide, M, r):
+    """One factor of each projection in fp32, the other in 16 bits: what is kept and the gradients are those of the
+    rounded factor, but for the dtype of the fp32 factor's gradient."""
+    say("factors of two dtypes", c, wide, M, r)
+    t = G._inputs(M, 136, 72, r, c, c, F32)
+    for n in ("gate", "value"):
+        k = ("up_" if wide == "down" else "down_") + n
+        t[k] = t[k].to(c)
+    low = {k: v.to(c) if v is not None else None for k, v in t.items()}
+    y, gate, value, h = L.lora_gated_linear(*G._args(t), 1.5, keep=True)
+    y0, gate0, value0, h0 = L.lora_gated_linear(*G._args(low), 1.5, keep=True)
+    assert y.dtype == F32 and y0.dtype == c
+    for a, b in ((gate, gate0), (value, value0), (h, h0)):
+        assert torch.equal(a, b)
+    dy = G._rand(3, M, 136).to(c)
+    for kept in (None, h):
+        got = L.lora_gated_linear_backward(*G._args(t), 1.5, dy, gate, value, h=kept)
+        want = L.lora_gated_linear_backward(*G._args(low), 1.5, dy, gate, value, h=kept)
+        dts = (c,) + ((F32, c) if wide == "down" else (c, F32)) * 2
+        for g, w, dt in zip(got, want, dts):
+            assert g.dtype == dt and torch.equal(g.to(c), w)
